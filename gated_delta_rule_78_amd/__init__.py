@@ -12,6 +12,11 @@ library is missing or fails, the call raises.
         -> (o, S_T, S_ckpt, ckpt_offsets)                         state checkpoints every E tokens
     chunk_bwd(q, k, v, log_alpha, beta, S0, dO, dS_T) -> grads    backward of chunkwise prefill
     decode_step(q, k, v, log_alpha, beta, S) -> o                 one token, S updated in place
+
+The elementwise operators around the core (``include/kda_glr.h``, ``include/kda_norm.h``):
+
+    glr_fwd, glr_bwd, glr_step          gated linear recurrence: prefill, backward, one token
+    block_norm_fwd, block_norm_bwd      post-norm, gate, residual and pre-norm; their backward
 """
 import contextlib
 import ctypes
@@ -20,7 +25,8 @@ import os
 import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "SCRATCH_BYTES", "chunk_fwd_varlen", "chunk_bwd", "chunk_bwd_workspace_bytes", "decode_step", "chunk_workspace_bytes", "varlen_workspace_bytes",
-           "library", "KDAError", "LIB_PATH"]
+           "library", "KDAError", "LIB_PATH", "glr_fwd", "glr_bwd", "glr_step", "GLR_CHUNK", "block_norm_fwd", "block_norm_bwd",
+           "NORM_MAX_D"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -457,3 +463,8 @@ def decode_step(q, k, v, log_alpha, beta, S, *, out_dtype=None, o=None, z=None, 
             fn = "kda_decode_step_gated"
     _check(fn, st)
     return o
+
+
+# The elementwise operators build on the helpers above.
+from .block_norm import NORM_MAX_D, block_norm_bwd, block_norm_fwd  # noqa: E402
+from .glr import GLR_CHUNK, glr_bwd, glr_fwd, glr_step  # noqa: E402

@@ -1,0 +1,160 @@
+"""Norms around a block with its gate, residual and residual scale (``include/kda_norm.h``).
+
+    block_norm_fwd(f, x=None, ...) -> (x_out, n)      post-norm, gate, residual, next pre-norm
+    block_norm_bwd(f, x, dx_out, dn, ...)             gradients of every input
+        -> (df, dx, dgate, dnorm_weight, dscale_weight, dpre_weight)
+"""
+import ctypes
+
+import torch
+
+from . import _alloc_on, _check, _check_device, _check_tensor, _check_workspace, _nbytes, _workspace, library
+from . import _DTYPES
+from ._launch import data_ptr, on_device, raw_stream
+
+NORM_MAX_D = 16384   # KDA_NORM_MAX_D of include/kda_norm.h
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("pre_norm", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("pre_eps", ctypes.c_float)]
+
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = library()
+        P, D, Z, I = ctypes.c_void_p, ctypes.POINTER(NormDesc), ctypes.c_size_t, ctypes.c_int32
+        lib.kda_block_norm_fwd.argtypes = [D] + [P] * 9
+        lib.kda_block_norm_fwd.restype = I
+        lib.kda_block_norm_bwd_workspace_bytes.argtypes = [D]
+        lib.kda_block_norm_bwd_workspace_bytes.restype = Z
+        lib.kda_block_norm_bwd.argtypes = [D] + [P] * 15 + [Z, P]
+        lib.kda_block_norm_bwd.restype = I
+        _lib = lib
+    return _lib
+
+
+def _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight):
+    """Checks the inputs both directions share; returns (rows, D)."""
+    dev, shape = f.device, f.shape
+    if f.dtype not in _DTYPES:
+        raise ValueError("unsupported input dtype %s" % f.dtype)
+    if f.dim() < 1:
+        raise ValueError("f must have at least one dimension")
+    D = shape[-1]
+    _check_tensor("f", f, dev, f.dtype, shape)
+    if x is not None:
+        if x.dtype not in _DTYPES:
+            raise ValueError("unsupported residual dtype %s" % x.dtype)
+        _check_tensor("x", x, dev, x.dtype, shape)
+    if gate is not None:
+        _check_tensor("gate", gate, dev, f.dtype, shape)
+    for name, w in (("norm_weight", norm_weight), ("scale_weight", scale_weight), ("pre_weight", pre_weight)):
+        if w is not None:
+            _check_tensor(name, w, dev, torch.float32, (D,))
+    if norm_weight is not None and not post_norm:
+        raise ValueError("norm_weight goes with post_norm")
+    if pre_weight is not None and not pre_norm:
+        raise ValueError("pre_weight goes with pre_norm")
+    return (f.numel() // D if D else 0), D
+
+
+def block_norm_fwd(f, x=None, *, gate=None, norm_weight=None, post_norm=True, eps=1e-6, scale=1.0, scale_weight=None,
+                   pre_norm=True, pre_weight=None, pre_eps=1e-6, res_dtype=None, out_dtype=None, x_out=None, n=None,
+                   store_x=True, stream=None):
+    """Post-norm, gate, residual and the next pre-norm through ``kda_block_norm_fwd``.
+
+    f: [..., D] bf16 or fp32, the block's output; x: the residual stream, f's shape (bf16 or fp32),
+    or None; gate: f's shape and type, or None; weights [D] fp32, or None (ones).
+        u = sigmoid(gate) * norm_weight * f / sqrt(mean(f^2) + eps)     (post_norm False: f itself)
+        x_out = x + scale * scale_weight * u
+        n = pre_weight * x_out / sqrt(mean(x_out^2) + pre_eps)
+    Returns (x_out, n): x_out in x's type (``res_dtype``, default f's type, without x), None with
+    ``store_x=False``; n in ``out_dtype`` (default f's type), None with ``pre_norm=False``.
+    ``x_out=x`` updates the residual stream in place. Caller-supplied outputs are checked like the
+    inputs; the others are allocated on ``stream``."""
+    dev = f.device
+    rows, D = _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight)
+    res_dtype = x.dtype if x is not None else (res_dtype or (x_out.dtype if x_out is not None else f.dtype))
+    out_dtype = out_dtype or (n.dtype if n is not None else f.dtype)
+    for dt in (res_dtype, out_dtype):
+        if dt not in _DTYPES:
+            raise ValueError("unsupported output dtype %s" % dt)
+    if x_out is not None:
+        _check_tensor("x_out", x_out, dev, res_dtype, f.shape)
+    if n is not None:
+        if not pre_norm:
+            raise ValueError("n goes with pre_norm")
+        _check_tensor("n", n, dev, out_dtype, f.shape)
+    if not pre_norm and x_out is None and not store_x:
+        raise ValueError("nothing to compute: neither x_out nor n is wanted")
+    _check_device("block_norm_fwd", dev)
+    desc = NormDesc(rows, D, _DTYPES[f.dtype], _DTYPES[res_dtype], _DTYPES[out_dtype], bool(post_norm), bool(pre_norm),
+                    scale, eps, pre_eps)
+    with on_device(dev), _alloc_on(stream):
+        if x_out is None and store_x:
+            x_out = torch.empty(f.shape, device=dev, dtype=res_dtype)
+        if n is None and pre_norm:
+            n = torch.empty(f.shape, device=dev, dtype=out_dtype)
+        st = _library().kda_block_norm_fwd(desc, data_ptr(f), data_ptr(gate), data_ptr(x), data_ptr(norm_weight),
+                                           data_ptr(scale_weight), data_ptr(pre_weight), data_ptr(x_out), data_ptr(n),
+                                           raw_stream(dev, stream))
+    _check("kda_block_norm_fwd", st)
+    return x_out, n
+
+
+def block_norm_bwd(f, x, dx_out, dn, *, gate=None, norm_weight=None, post_norm=True, eps=1e-6, scale=1.0,
+                   scale_weight=None, pre_norm=True, pre_weight=None, pre_eps=1e-6, dx=None, workspace=None,
+                   stream=None):
+    """Backward of ``block_norm_fwd`` through ``kda_block_norm_bwd``.
+
+    Inputs as the forward (x as it was before an in-place forward); dx_out: gradient of x_out (x's
+    type, or bf16 / fp32 without x), or None; dn: gradient of n (bf16 or fp32), or None.
+    Returns (df, dx, dgate, dnorm_weight, dscale_weight, dpre_weight): tensors in their input's
+    type, weight gradients [D] fp32; None for each input that was not given. ``dx=dx_out`` updates
+    the residual stream's gradient in place."""
+    dev = f.device
+    rows, D = _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight)
+    if dx_out is None and dn is None:
+        raise ValueError("one of dx_out and dn is required")
+    res_dtype = x.dtype if x is not None else (dx_out.dtype if dx_out is not None else f.dtype)
+    out_dtype = dn.dtype if dn is not None else f.dtype
+    for dt in (res_dtype, out_dtype):
+        if dt not in _DTYPES:
+            raise ValueError("unsupported gradient dtype %s" % dt)
+    if dx_out is not None:
+        _check_tensor("dx_out", dx_out, dev, res_dtype, f.shape)
+    if dn is not None:
+        if not pre_norm:
+            raise ValueError("dn goes with pre_norm")
+        _check_tensor("dn", dn, dev, out_dtype, f.shape)
+    if dx is not None:
+        if x is None:
+            raise ValueError("dx goes with x")
+        _check_tensor("dx", dx, dev, res_dtype, f.shape)
+    _check_workspace(workspace, dev)
+    _check_device("block_norm_bwd", dev)
+    desc = NormDesc(rows, D, _DTYPES[f.dtype], _DTYPES[res_dtype], _DTYPES[out_dtype], bool(post_norm), bool(pre_norm),
+                    scale, eps, pre_eps)
+    lib = _library()
+    sums = norm_weight is not None or scale_weight is not None or pre_weight is not None
+    need = lib.kda_block_norm_bwd_workspace_bytes(desc) if sums else 0
+    with on_device(dev), _alloc_on(stream):
+        df = torch.empty_like(f)
+        dgate = torch.empty_like(f) if gate is not None else None
+        if dx is None and x is not None:
+            dx = torch.empty_like(x)
+        dws = [torch.empty_like(w) if w is not None else None for w in (norm_weight, scale_weight, pre_weight)]
+        workspace = _workspace(need, workspace, dev)
+        st = lib.kda_block_norm_bwd(desc, data_ptr(f), data_ptr(gate), data_ptr(x), data_ptr(norm_weight),
+                                    data_ptr(scale_weight), data_ptr(pre_weight), data_ptr(dx_out), data_ptr(dn),
+                                    data_ptr(df), data_ptr(dgate), data_ptr(dx), *map(data_ptr, dws),
+                                    data_ptr(workspace), _nbytes(workspace), raw_stream(dev, stream))
+    _check("kda_block_norm_bwd", st)
+    return (df, dx, dgate, *dws)

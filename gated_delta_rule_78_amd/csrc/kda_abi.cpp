@@ -7,6 +7,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include "kda_check.h"
 #include "kda_internal.h"
 #include "kda_plan.h"
 #include "kda_record.h"
@@ -16,23 +17,15 @@ namespace {
 using kda::kChunk;
 using kda::Geometry;
 using kda::Plan;
+using kda::Range;
+using kda::aligned;
 using kda::ceil_div;
+using kda::elem_bytes;
 using kda::make_plan;
+using kda::overlaps;
+using kda::range_of;
 using kda::run_bf16;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range_of(const void* p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + (uintptr_t)bytes};
-}
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-bool valid_dtype(int32_t d) { return d == KDA_F32 || d == KDA_BF16; }
-int64_t elem_bytes(int32_t d) { return d == KDA_BF16 ? 2 : 4; }
+using kda::valid_dtype;
 
 // The plan (and so the workspace) depends on the compute-unit count of the device: a call plans
 // for its stream's device, a workspace query for the current device.

@@ -1,0 +1,41 @@
+// Internal launcher interface of the gated linear recurrence (include/kda_glr.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+// Rows come in blocks: N*H blocks of T rows (block n*H + h), or, packed, H blocks of T rows that
+// hold every sequence. A block's rows split into nch chunks.
+struct GlrArgs {
+    int64_t N, H, T, d;
+    int64_t blocks, nch;
+    bool in_bf16, out_bf16, packed;
+    int scale;               // kda_glr_scale
+    float g_min;
+    const void *x, *la, *z;  // one of la and z
+    const float* A_log;
+    const void* u;           // input gate pre-activation or NULL
+    const int32_t* cu;       // packed: [N+1]
+    const float* S0;         // [N,H,d] or NULL
+    void* y;
+    float* S_T;
+    float* entry;            // [blocks][nch][d]: forward writes (may be NULL), backward reads
+    // backward
+    const void* dy;
+    const float* dST;
+    void *dx, *dd, *du;
+    float *dA, *dS0;
+    unsigned char* ws;
+    // step: x, gates and y as [N,H,d], S updated in place
+    float* S;
+};
+
+size_t glr_fwd_ws_bytes(const GlrArgs& a);
+size_t glr_bwd_ws_bytes(const GlrArgs& a);
+hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t st);
+hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t st);
+hipError_t launch_glr_step(const GlrArgs& a, hipStream_t st);
+
+}  // namespace kda

@@ -1,0 +1,245 @@
+"""Host-side checks of include/kda_glr.h and include/kda_norm.h (no GPU): every declared function is
+exported, and bad arguments are refused before any device work."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import gated_delta_rule_78_amd as kda
+from gated_delta_rule_78_amd.block_norm import NormDesc
+from gated_delta_rule_78_amd import block_norm, glr
+from gated_delta_rule_78_amd.glr import GlrDesc, GlrGates
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
+FAKE = 0x7F0000000000  # never dereferenced: every call below fails validation first
+GB = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.LIB_PATH):
+        from gated_delta_rule_78_amd import build
+        build.build()
+    glr._library()
+    return block_norm._library()
+
+
+@pytest.mark.parametrize("header", ["kda_glr.h", "kda_norm.h"])
+def test_library_exports_every_declared_symbol(lib, header):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", header)).read(), flags=re.S)
+    names = set(re.findall(r"\b(kda_[a-z_]+)\s*\(", text))
+    assert len(names) >= 3
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def desc(N=2, H=2, T=600, d=64, ind=1, outd=1, packed=0, scale=0, g_min=-5.0):
+    return GlrDesc(N, H, T, d, ind, outd, packed, scale, g_min)
+
+
+def p(i, off=0):
+    return FAKE + i * GB + off
+
+
+def fwd(lib, d, x=p(0), la=p(1), z=None, A=None, u=None, cu=None, S0=None, y=p(2), ST=None, entry=None, ws=p(3),
+        ws_bytes=1 << 40, no_gates=False):
+    g = GlrGates(la, z, A, u)
+    return lib.kda_glr_fwd(d, x, None if no_gates else g, cu, S0, y, ST, entry, ws, ws_bytes, None)
+
+
+def test_glr_fwd_refusals(lib):
+    assert fwd(lib, None) == INVALID
+    for bad in (dict(N=0), dict(H=0), dict(T=-1), dict(d=0), dict(ind=7), dict(outd=-1), dict(packed=2), dict(scale=3),
+                dict(scale=-1)):
+        assert fwd(lib, desc(**bad)) == INVALID, bad
+    assert fwd(lib, desc(T=(1 << 31) - 256)) == UNSUPPORTED
+    assert fwd(lib, desc(N=1 << 20, H=1 << 20)) == UNSUPPORTED
+    assert fwd(lib, desc(), no_gates=True) == INVALID
+    assert fwd(lib, desc(), la=None) == INVALID                               # neither decay
+    assert fwd(lib, desc(), z=p(4), A=p(5)) == INVALID                        # both
+    assert fwd(lib, desc(), la=None, z=p(4)) == INVALID                       # z without A_log
+    assert fwd(lib, desc(), A=p(5)) == INVALID                                # A_log without z
+    for g_min in (0.0, 1.0, float("nan"), float("-inf")):
+        assert fwd(lib, desc(g_min=g_min), la=None, z=p(4), A=p(5)) == INVALID
+    assert fwd(lib, desc(), x=None) == INVALID
+    assert fwd(lib, desc(), y=None) == INVALID
+    assert fwd(lib, desc(packed=1)) == INVALID                                # packed needs cu_seqlens
+    assert fwd(lib, desc(), cu=p(4)) == INVALID                               # and only packed
+    assert fwd(lib, desc(packed=1), cu=p(4, 2)) == INVALID                    # misaligned
+    for k in ("x", "la", "u", "S0", "y", "ST", "entry"):
+        assert fwd(lib, desc(), **{k: p(6, 1)}) == INVALID, k                 # off its element
+    assert fwd(lib, desc(), y=p(0, 64)) == INVALID                            # y inside x
+    assert fwd(lib, desc(), ST=p(1, 64)) == INVALID                           # S_T inside log_alpha
+    assert fwd(lib, desc(), S0=p(5), ST=p(5, 64)) == INVALID                  # partial overlap
+    assert fwd(lib, desc(), entry=p(2, 64)) == INVALID                        # entry states inside y
+    assert fwd(lib, desc(packed=1), cu=p(2, 64)) == INVALID                   # cu_seqlens inside y
+    need = lib.kda_glr_fwd_workspace_bytes(desc())
+    if need:
+        assert fwd(lib, desc(), ws=None) == WORKSPACE
+        assert fwd(lib, desc(), ws_bytes=need - 1) == WORKSPACE
+        assert fwd(lib, desc(), ws=p(3, 8)) == INVALID
+        assert fwd(lib, desc(), ws=p(0, 256)) == INVALID                      # workspace inside x
+    assert lib.kda_glr_fwd_workspace_bytes(None) == 0
+    assert lib.kda_glr_fwd_workspace_bytes(desc(T=0)) == 0
+    assert lib.kda_glr_fwd_workspace_bytes(desc(d=0)) == 0
+
+
+def bwd(lib, d, x=p(0), la=p(1), z=None, A=None, u=None, cu=None, S0=None, entry=None, dy=p(2), dST=None, dx=p(3),
+        dd=p(4), du=None, dA=None, dS0=None, ws=p(5), ws_bytes=1 << 40):
+    return lib.kda_glr_bwd(d, x, GlrGates(la, z, A, u), cu, S0, entry, dy, dST, dx, dd, du, dA, dS0, ws, ws_bytes, None)
+
+
+def test_glr_bwd_refusals(lib):
+    assert bwd(lib, None) == INVALID
+    assert bwd(lib, desc(scale=9)) == INVALID
+    for k in ("x", "dy", "dx", "dd"):
+        assert bwd(lib, desc(), **{k: None}) == INVALID, k
+    assert bwd(lib, desc(), u=p(6)) == INVALID                                # in_gate without its gradient
+    assert bwd(lib, desc(), du=p(6)) == INVALID                               # and the reverse
+    assert bwd(lib, desc(), la=None, z=p(6), A=p(7)) == INVALID               # z without dA_log
+    assert bwd(lib, desc(), dA=p(6)) == INVALID
+    for k in ("x", "la", "S0", "entry", "dy", "dST", "dx", "dd", "dS0"):
+        assert bwd(lib, desc(), **{k: p(8, 1)}) == INVALID, k
+    assert bwd(lib, desc(), dx=p(0)) == INVALID                               # no gradient in place of an input
+    assert bwd(lib, desc(), dd=p(3, 128)) == INVALID
+    assert bwd(lib, desc(), dST=p(8), dS0=p(8)) == INVALID
+    assert bwd(lib, desc(packed=1)) == INVALID
+    need = lib.kda_glr_bwd_workspace_bytes(desc(), 0, 0)
+    assert need > 0
+    assert bwd(lib, desc(), ws=None) == WORKSPACE
+    assert bwd(lib, desc(), ws_bytes=need - 1) == WORKSPACE
+    assert bwd(lib, desc(), ws=p(5, 8)) == INVALID
+    assert bwd(lib, desc(), ws=p(2, 16)) == INVALID                           # workspace inside dy
+    assert lib.kda_glr_bwd_workspace_bytes(None, 0, 0) == 0
+
+
+def test_glr_step_refusals(lib):
+    step = lambda d, x=p(0), la=p(1), z=None, A=None, S=p(2), y=p(3): lib.kda_glr_step(
+        d, x, GlrGates(la, z, A, None), S, y, None)
+    assert step(None) == INVALID
+    assert step(desc(N=0)) == INVALID
+    assert step(desc(), la=None) == INVALID
+    for k in ("x", "S", "y"):
+        assert step(desc(), **{k: None}) == INVALID
+        assert step(desc(), **{k: p(6, 1)}) == INVALID
+    assert step(desc(), y=p(2, 16)) == INVALID
+    assert step(desc(), S=p(0)) == INVALID
+
+
+def ndesc(rows=8, D=64, ind=1, res=1, out=1, post=1, pre=1, scale=1.0, eps=1e-6, pre_eps=1e-6):
+    return NormDesc(rows, D, ind, res, out, post, pre, scale, eps, pre_eps)
+
+
+def nfwd(lib, d, f=p(0), gate=None, x=p(1), wp=None, lam=None, wr=None, xo=p(2), n=p(3)):
+    return lib.kda_block_norm_fwd(d, f, gate, x, wp, lam, wr, xo, n, None)
+
+
+BAD_NORM = (dict(rows=-1), dict(D=0), dict(ind=5), dict(res=-1), dict(out=2), dict(post=2), dict(pre=-1),
+            dict(scale=float("nan")), dict(scale=float("inf")), dict(eps=0.0), dict(eps=float("nan")), dict(pre_eps=-1.0),
+            dict(pre_eps=float("inf")))
+
+
+def test_norm_fwd_refusals(lib):
+    assert nfwd(lib, None) == INVALID
+    for bad in BAD_NORM:
+        assert nfwd(lib, ndesc(**bad)) == INVALID, bad
+    assert nfwd(lib, ndesc(D=16385)) == UNSUPPORTED
+    assert nfwd(lib, ndesc(rows=1 << 31)) == UNSUPPORTED
+    assert nfwd(lib, ndesc(), f=None) == INVALID
+    assert nfwd(lib, ndesc(), n=None) == INVALID                              # pre-norm without n
+    assert nfwd(lib, ndesc(pre=0)) == INVALID                                 # n without pre-norm
+    assert nfwd(lib, ndesc(pre=0), xo=None, n=None) == INVALID
+    assert nfwd(lib, ndesc(post=0), wp=p(4)) == INVALID
+    assert nfwd(lib, ndesc(pre=0), n=None, wr=p(4)) == INVALID
+    for k in ("f", "gate", "x", "wp", "lam", "wr", "xo", "n"):
+        assert nfwd(lib, ndesc(), **{k: p(6, 1)}) == INVALID, k
+    assert nfwd(lib, ndesc(), xo=p(0)) == INVALID                             # x_out in place of f
+    assert nfwd(lib, ndesc(), xo=p(1, 16)) == INVALID                         # a shifted x
+    assert nfwd(lib, ndesc(), n=p(1)) == INVALID                              # n in place of x
+    assert nfwd(lib, ndesc(), n=p(2, 16)) == INVALID
+    assert nfwd(lib, ndesc(rows=0), f=None, xo=None, n=None) == OK            # nothing to do
+
+
+def nbwd(lib, d, f=p(0), gate=None, x=p(1), wp=None, lam=None, wr=None, dxo=p(2), dn=p(3), df=p(4), dgate=None, dx=p(5),
+         dwp=None, dlam=None, dwr=None, ws=p(6), ws_bytes=1 << 40):
+    return lib.kda_block_norm_bwd(d, f, gate, x, wp, lam, wr, dxo, dn, df, dgate, dx, dwp, dlam, dwr, ws, ws_bytes, None)
+
+
+def test_norm_bwd_refusals(lib):
+    assert nbwd(lib, None) == INVALID
+    for bad in BAD_NORM:
+        assert nbwd(lib, ndesc(**bad)) == INVALID, bad
+    assert nbwd(lib, ndesc(), f=None) == INVALID
+    assert nbwd(lib, ndesc(), df=None) == INVALID
+    assert nbwd(lib, ndesc(), dxo=None, dn=None) == INVALID
+    assert nbwd(lib, ndesc(), gate=p(7)) == INVALID                           # gate without its gradient
+    assert nbwd(lib, ndesc(), dgate=p(7)) == INVALID
+    assert nbwd(lib, ndesc(), x=None) == INVALID                              # dx without x
+    assert nbwd(lib, ndesc(pre=0)) == INVALID                                 # dn without pre-norm
+    assert nbwd(lib, ndesc(pre=0), dn=None, dwr=p(7)) == INVALID
+    assert nbwd(lib, ndesc(post=0), dwp=p(7)) == INVALID
+    for k in ("f", "x", "wp", "lam", "wr", "dxo", "dn", "df", "dx", "dwp", "dlam", "dwr"):
+        assert nbwd(lib, ndesc(), **{k: p(8, 1)}) == INVALID, k
+    assert nbwd(lib, ndesc(), dx=p(2, 16)) == INVALID                         # a shifted dx_out
+    assert nbwd(lib, ndesc(), df=p(0)) == INVALID
+    assert nbwd(lib, ndesc(), dwp=p(7), dlam=p(7)) == INVALID
+    need = lib.kda_block_norm_bwd_workspace_bytes(ndesc())
+    assert need > 0
+    assert nbwd(lib, ndesc(), dlam=p(7), ws=None) == WORKSPACE
+    assert nbwd(lib, ndesc(), dlam=p(7), ws_bytes=need - 1) == WORKSPACE
+    assert nbwd(lib, ndesc(), dlam=p(7), ws=p(0)) == INVALID
+    assert nbwd(lib, ndesc(rows=0), f=None, df=None, dx=None) == OK
+
+
+# ---- the bindings refuse on the host what the C call cannot see ----
+
+def test_bindings_refuse():
+    x = torch.zeros(2, 3, 5, 8)
+    la = torch.zeros(2, 3, 5, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.glr_fwd(x, la)
+    with pytest.raises(ValueError, match="exactly one"):
+        kda.glr_fwd(x)
+    with pytest.raises(ValueError, match="exactly one"):
+        kda.glr_fwd(x, la, z=la, A_log=torch.zeros(3, 8))
+    with pytest.raises(ValueError, match="A_log"):
+        kda.glr_fwd(x, z=la)
+    with pytest.raises(ValueError, match="log_alpha"):
+        kda.glr_fwd(x, la.bfloat16())
+    with pytest.raises(ValueError, match="x must be"):
+        kda.glr_fwd(x[..., ::2], la[..., ::2].contiguous())
+    with pytest.raises(ValueError, match="input dtype"):
+        kda.glr_fwd(x.half(), la.half())
+    with pytest.raises(ValueError, match="input_scale"):
+        glr._scale("other")
+    with pytest.raises(ValueError, match=r"\[H,T,d\]"):
+        kda.glr_fwd(x, la, cu_seqlens=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        kda.glr_fwd(x[0], la[0], cu_seqlens=torch.zeros(2))
+    with pytest.raises(ValueError, match="S0"):
+        kda.glr_fwd(x, la, torch.zeros(2, 3, 9))
+    with pytest.raises(ValueError, match="entry_states"):
+        kda.glr_bwd(x, la, None, x, entry_states=torch.zeros(6, 2, 8))
+    with pytest.raises(ValueError, match=r"\[N,H,d\]"):
+        kda.glr_step(x, la, torch.zeros(2, 3, 8))
+    with pytest.raises(ValueError, match="S must be"):
+        kda.glr_step(x[0], la[0], torch.zeros(3, 5, 8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.block_norm_fwd(x)
+    with pytest.raises(ValueError, match="gate"):
+        kda.block_norm_fwd(x, gate=x.bfloat16())
+    with pytest.raises(ValueError, match="norm_weight goes"):
+        kda.block_norm_fwd(x, norm_weight=torch.ones(8), post_norm=False)
+    with pytest.raises(ValueError, match="pre_weight goes"):
+        kda.block_norm_fwd(x, pre_weight=torch.ones(8), pre_norm=False)
+    with pytest.raises(ValueError, match="scale_weight"):
+        kda.block_norm_fwd(x, scale_weight=torch.ones(9))
+    with pytest.raises(ValueError, match="nothing to compute"):
+        kda.block_norm_fwd(x, pre_norm=False, store_x=False)
+    with pytest.raises(ValueError, match="one of dx_out and dn"):
+        kda.block_norm_bwd(x, None, None, None)
+    with pytest.raises(ValueError, match="dx goes with x"):
+        kda.block_norm_bwd(x, None, x, None, dx=x)

@@ -1,0 +1,361 @@
+"""GPU parity of the gated linear recurrence (kda_glr_fwd, kda_glr_bwd, kda_glr_step) with the fp64
+token loop. Every output element is held to the bound that oracle.glr derives from counting fp32
+roundings along its path, plus half a step of the output type."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_78_amd as kda
+from oracle import glr
+from tests.parity import host32, say
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
+BF16, F32 = torch.bfloat16, torch.float32
+HALF_STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+TINY = {BF16: 2.0 ** -133, F32: 2.0 ** -149}    # a subnormal result is off by a whole step at most
+G_MIN = -5.0
+GUARD = 7.0
+
+
+def make(N, H, T, d, dt, *, lens=None, z=False, u=False, s0=False, tail=0, seed=0, la_range=(-0.5, -0.001)):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed * 1000003 + 17 * N + 31 * H + T + d)
+    cu = None
+    if lens is not None:
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=DEV)
+        N, T = len(lens), int(sum(lens)) + tail
+    lead = (H, T) if lens is not None else (N, H, T)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    lo, hi = la_range
+    c = dict(N=N, H=H, T=T, d=d, dt=dt, cu=cu, x=rn(*lead, d).to(dt), la=None, z=None, A=None, u=None, S0=None)
+    if z:
+        c["z"] = (rn(*lead, d) * 1.5 - 3.0).to(dt)
+        c["A"] = torch.rand(H, d, generator=g, device=DEV) - 0.5
+    else:
+        c["la"] = (torch.rand(*lead, d, generator=g, device=DEV) * (lo - hi) + hi).to(dt)
+    if u:
+        c["u"] = rn(*lead, d).to(dt)
+    if s0:
+        c["S0"] = rn(N, H, d)
+    c["dy"], c["dS_T"] = rn(*lead, d), rn(N, H, d)
+    return c
+
+
+def kw(c, scale):
+    return dict(z=c["z"], A_log=c["A"], g_min=G_MIN, in_gate=c["u"], input_scale=scale, cu_seqlens=c["cu"])
+
+
+def reference(c, scale, dy=None, dS_T=None):
+    """fp64 outputs and bounds: dict name -> (value, bound), rows in no sequence NaN."""
+    shape, sshape = tuple(c["x"].shape), (c["N"], c["H"], c["d"])
+    host = {k: (None if c[k] is None else host32(c[k]).astype(np.float64)) for k in ("x", "la", "z", "A", "u", "S0")}
+    ref = {k: (np.full(shape, np.nan), np.full(shape, np.nan)) for k in ("y", "dx", "dd", "du")}
+    ref.update({k: (np.zeros(sshape), np.zeros(sshape)) for k in ("S_T", "dS0")})
+    ref["dA"] = (np.zeros(sshape[1:]), np.zeros(sshape[1:]))
+    zero = np.zeros(c["d"])
+    cu = None if c["cu"] is None else c["cu"].cpu().numpy()
+    for n, h, at in glr.sequences(c["N"], c["H"], c["T"], cu):
+        part = lambda k: None if host[k] is None else host[k][at]
+        q = glr.gates(part("x"), part("la"), part("z"), None if host["A"] is None else host["A"][h], G_MIN, part("u"), scale)
+        s0 = zero if host["S0"] is None else host["S0"][n, h]
+        hs, prev, last = glr.forward(q, s0)
+        hb, lb = glr.forward_bound(q, s0, scale)
+        ref["y"][0][at], ref["y"][1][at] = hs, hb
+        ref["S_T"][0][n, h], ref["S_T"][1][n, h] = last, lb
+        if dy is None:
+            continue
+        dyr = host32(dy).astype(np.float64)[at]
+        ds = zero if dS_T is None else host32(dS_T).astype(np.float64)[n, h]
+        r = glr.backward(q, prev, dyr, ds, G_MIN)
+        b = glr.backward_bounds(q, prev, hb, dyr, ds, scale, s0, G_MIN)
+        for k in ("dx", "dd") + (("du",) if host["u"] is not None else ()):
+            ref[k][0][at], ref[k][1][at] = r[k], b[k]
+        ref["dS0"][0][n, h], ref["dS0"][1][n, h] = r["dS0"], b["dS0"]
+        if host["z"] is not None:
+            ref["dA"][0][h] += r["dA"]
+            ref["dA"][1][h] += b["dA"]
+    return ref
+
+
+def check(tag, got, ref, dt):
+    """Every element within its bound plus half a step of its type; where the reference is NaN
+    (rows in no sequence), the element is not looked at."""
+    val, bound = ref
+    g = host32(got).astype(np.float64)
+    assert g.shape == val.shape, tag
+    if g.size == 0:
+        return
+    ok = ~np.isnan(val)
+    tol = bound + HALF_STEP[dt] * (np.abs(val) + bound) + TINY[dt]
+    err = np.abs(g - val)
+    worst = float(np.max(np.where(ok, err / tol, 0.0)))
+    say("%s: worst error / bound %.3f" % (tag, worst))
+    assert np.all(np.isfinite(g[ok])) and worst <= 1.0, tag
+
+
+def run_fwd(c, scale, odt):
+    y = torch.full(tuple(c["x"].shape), GUARD, device=DEV, dtype=odt)
+    y, S_T, entry = kda.glr_fwd(c["x"], c["la"], c["S0"], out_dtype=odt, y=y, store_entry_states=True, **kw(c, scale))
+    torch.cuda.synchronize()
+    return y, S_T, entry
+
+
+CASES = [
+    # (N, H, T, d, lens), dtype, out dtype, z, u, scale, S0
+    ((1, 1, 1, 1, None), BF16, BF16, False, False, "one", False),
+    ((2, 3, 2, 3, None), F32, F32, True, True, "norm", True),
+    ((1, 2, 255, 64, None), BF16, F32, False, True, "leaky", True),
+    ((1, 2, 256, 8, None), F32, BF16, True, False, "one", False),
+    ((2, 2, 257, 128, None), BF16, BF16, True, True, "norm", True),
+    ((3, 1, 777, 77, None), F32, F32, False, False, "one", True),
+    ((1, 3, 1300, 40, None), BF16, BF16, False, True, "norm", False),
+    ((1, 1, 600, 300, None), F32, F32, True, True, "leaky", False),
+    ((2, 1, 33, 1001, None), BF16, BF16, True, False, "norm", True),
+    ((0, 2, 0, 64, [3, 0, 300, 1, 256, 0]), BF16, BF16, True, True, "norm", True),
+    ((0, 3, 0, 100, [0, 0, 1000, 1, 500]), F32, F32, False, False, "leaky", True),
+    ((0, 1, 0, 72, [1] * 40), BF16, F32, True, False, "one", False),
+    ((0, 2, 0, 5, [255, 1, 256, 257, 2, 510]), F32, F32, False, True, "norm", False),
+    ((0, 1, 0, 16, [0, 0, 0]), F32, F32, False, False, "one", True),
+]
+
+
+def build(case, seed=1, tail=0):
+    (N, H, T, d, lens), dt, odt, z, u, scale, s0 = case
+    c = make(N, H, T, d, dt, lens=lens, z=z, u=u, s0=s0, tail=tail if lens is not None else 0, seed=seed)
+    return c, scale, dt, odt
+
+
+def name(case):
+    (N, H, T, d, lens), dt, odt, z, u, scale, s0 = case
+    return "%s-%s-%s%s%s" % ("packed%d" % sum(lens) if lens is not None else "%dx%dx%d" % (N, H, T), d,
+                             "bf16" if dt == BF16 else "fp32", "-z" if z else "", "-u" if u else "") + "-" + scale
+
+
+@pytest.mark.parametrize("case", CASES, ids=name)
+def test_forward(case):
+    c, scale, dt, odt = build(case)
+    say("forward", name(case))
+    y, S_T, entry = run_fwd(c, scale, odt)
+    ref = reference(c, scale)
+    check("y", y, ref["y"], odt)
+    check("S_T", S_T, ref["S_T"], F32)
+    # entry states: the state before row c * 256 of its block of rows
+    if c["cu"] is None and c["T"] > 256:
+        val, bound = ref["y"]
+        rows = np.arange(256, c["T"], 256) - 1
+        shape = (c["N"] * c["H"], len(rows), c["d"])
+        check("entry states", entry[:, 1:], (val[:, :, rows].reshape(shape), bound[:, :, rows].reshape(shape)), F32)
+
+
+@pytest.mark.parametrize("with_entry", [True, False])
+@pytest.mark.parametrize("case", CASES, ids=name)
+def test_backward(case, with_entry):
+    c, scale, dt, odt = build(case, seed=2)
+    say("backward", name(case), "entry states given" if with_entry else "recomputed")
+    dy = c["dy"].to(odt)
+    dS_T = c["dS_T"] if case[-1] else None
+    entry = run_fwd(c, scale, odt)[2] if with_entry else None
+    dx, dd, du, dS0, dA = kda.glr_bwd(c["x"], c["la"], c["S0"], dy, dS_T, entry_states=entry, **kw(c, scale))
+    torch.cuda.synchronize()
+    ref = reference(c, scale, dy, dS_T)
+    check("dx", dx, ref["dx"], dt)
+    check("ddecay", dd, ref["dd"], dt)
+    check("dS0", dS0, ref["dS0"], F32)
+    assert (du is None) == (c["u"] is None) and (dA is None) == (c["z"] is None)
+    if du is not None:
+        check("din_gate", du, ref["du"], dt)
+    if dA is not None:
+        check("dA_log", dA, ref["dA"], F32)
+
+
+@pytest.mark.parametrize("N,H,d,dt,odt,z,u,scale", [
+    (1, 1, 1, BF16, BF16, False, False, "one"),
+    (1, 32, 128, BF16, BF16, True, True, "norm"),
+    (5, 3, 77, F32, F32, False, True, "leaky"),
+    (64, 4, 40, BF16, F32, True, False, "leaky"),
+    (7, 2, 1001, F32, BF16, False, False, "norm"),
+])
+def test_step_chain(N, H, d, dt, odt, z, u, scale):
+    """Six tokens through glr_step give the forward's outputs, the state carried in place."""
+    T = 6
+    c = make(N, H, T, d, dt, z=z, u=u, s0=True, seed=3)
+    ref = reference(c, scale)
+    S = c["S0"].clone()
+    cut = lambda t, i: None if t is None else t[:, :, i].contiguous()
+    for i in range(T):
+        y = kda.glr_step(cut(c["x"], i), cut(c["la"], i), S, z=cut(c["z"], i), A_log=c["A"], g_min=G_MIN,
+                         in_gate=cut(c["u"], i), input_scale=scale, out_dtype=odt)
+        check("step %d" % i, y, (ref["y"][0][:, :, i], ref["y"][1][:, :, i]), odt)
+    check("S", S, ref["S_T"], F32)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_bases_off_the_wide_alignment(dt):
+    """Tensors that start one element into their storage."""
+    c = make(1, 3, 300, 64, dt, z=True, u=True, s0=True, seed=12)
+
+    def off(t):
+        r = torch.empty(t.numel() + 1, device=DEV, dtype=t.dtype)[1:].view(t.shape)
+        return r.copy_(t)
+
+    o = {k: off(v) if torch.is_tensor(v) else v for k, v in c.items()}
+    y, S_T, entry = kda.glr_fwd(o["x"], None, o["S0"], y=off(torch.zeros_like(o["x"])), S_T=off(torch.zeros_like(o["S0"])),
+                                store_entry_states=True, **kw(o, "norm"))
+    dy = off(c["dy"].to(dt))
+    grads = kda.glr_bwd(o["x"], None, o["S0"], dy, o["dS_T"], entry_states=entry, **kw(o, "norm"))
+    ref = reference(c, "norm", dy, c["dS_T"])
+    check("y", y, ref["y"], dt)
+    check("S_T", S_T, ref["S_T"], F32)
+    for k, g in zip(("dx", "dd", "du", "dS0", "dA"), grads):
+        check(k, g, ref[k], F32 if k in ("dS0", "dA") else dt)
+    S = o["S0"].clone()
+    one = lambda k: off(c[k][:, :, 0])
+    ys = kda.glr_step(one("x"), None, S, z=one("z"), A_log=o["A"], g_min=G_MIN, in_gate=one("u"), input_scale="norm")
+    check("step", ys, (ref["y"][0][:, :, 0], ref["y"][1][:, :, 0]), dt)
+
+
+def test_rows_behind_the_last_sequence_stay():
+    lens = [70, 300]
+    c = make(0, 2, 0, 48, F32, lens=lens, z=True, u=True, s0=True, tail=90, seed=4)
+    for k in ("x", "z", "u"):                       # what lies there must not matter
+        c[k][:, 370:] = float("nan")
+    y, S_T, entry = run_fwd(c, "norm", F32)
+    ref = reference(c, "norm", c["dy"], c["dS_T"])
+    check("y", y, ref["y"], F32)
+    check("S_T", S_T, ref["S_T"], F32)
+    assert bool((y[:, 370:] == GUARD).all())
+    dy = c["dy"].clone()
+    dy[:, 370:] = float("nan")
+    grads = kda.glr_bwd(c["x"], None, c["S0"], dy, c["dS_T"], entry_states=entry, **kw(c, "norm"))
+    for k, g in zip(("dx", "dd", "du", "dS0", "dA"), grads):
+        check(k, g, ref[k], F32)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_packed_equals_sequences_alone(dt):
+    """A packed batch gives what each sequence alone gives, to the bound of both: no state leaks
+    over a boundary, not even a non-finite one."""
+    lens = [300, 5, 256, 0, 190]
+    c = make(0, 2, 0, 64, dt, lens=lens, u=True, seed=5)
+    c["x"][:, 100] = float("inf")                   # sequence 0 from its row 100 on
+    y, S_T, _ = run_fwd(c, "leaky", F32)
+    cu = c["cu"].tolist()
+    assert not bool(torch.isfinite(y[:, 100:300]).any())
+    assert not bool(torch.isfinite(S_T[0]).any())
+    clean = dict(c, x=c["x"].clone())
+    clean["x"][:, 100] = 1.0
+    ref = reference(clean, "leaky")
+    for n in range(1, len(lens)):
+        at = (slice(None), slice(cu[n], cu[n + 1]))
+        check("sequence %d" % n, y[at], (ref["y"][0][at], ref["y"][1][at]), F32)
+    check("states", S_T[1:], (ref["S_T"][0][1:], ref["S_T"][1][1:]), F32)
+
+
+@pytest.mark.parametrize("scale", ["one", "leaky", "norm"])
+def test_decay_at_its_ends(scale):
+    """alpha = 1 (log decay 0) and alpha = 0 (-inf) among ordinary ones, and long runs of either."""
+    c = make(1, 2, 700, 24, F32, s0=True, seed=6)
+    c["la"][..., 3::7, :] = 0.0
+    c["la"][..., 5::11, :] = float("-inf")
+    c["la"][:, 0, 100:400] = 0.0
+    c["la"][:, 1, 100:400] = float("-inf")
+    y, S_T, entry = run_fwd(c, scale, F32)
+    ref = reference(c, scale, c["dy"], c["dS_T"])
+    check("y", y, ref["y"], F32)
+    check("S_T", S_T, ref["S_T"], F32)
+    grads = kda.glr_bwd(c["x"], c["la"], c["S0"], c["dy"], c["dS_T"], entry_states=entry, **kw(c, scale))
+    for k, g in zip(("dx", "dd", "du", "dS0"), grads):
+        if g is not None:
+            check(k, g, ref[k], F32)
+
+
+def test_slow_decay_over_many_chunks():
+    """Decays so near 1 that a state lives through every chunk."""
+    c = make(1, 2, 3000, 64, F32, s0=True, seed=7, la_range=(-2e-4, 0.0))
+    y, S_T, entry = run_fwd(c, "one", F32)
+    ref = reference(c, "one", c["dy"], c["dS_T"])
+    check("y", y, ref["y"], F32)
+    check("S_T", S_T, ref["S_T"], F32)
+    grads = kda.glr_bwd(c["x"], c["la"], c["S0"], c["dy"], c["dS_T"], entry_states=entry, **kw(c, "one"))
+    for k, g in zip(("dx", "dd", "du", "dS0"), grads):
+        if g is not None:
+            check(k, g, ref[k], F32)
+
+
+def test_split_and_resume():
+    """Prefill of a prefix, then of the rest from its state, then tokens one by one."""
+    c = make(2, 2, 603, 128, BF16, z=True, u=True, s0=True, seed=8)
+    ref = reference(c, "norm")
+    cut = lambda t, a, b: None if t is None else t[:, :, a:b].contiguous()
+    S = c["S0"].clone()
+    for a, b in ((0, 256), (256, 600)):
+        y, S, _ = kda.glr_fwd(cut(c["x"], a, b), None, S, S_T=S, z=cut(c["z"], a, b), A_log=c["A"], g_min=G_MIN,
+                              in_gate=cut(c["u"], a, b), input_scale="norm")
+        check("rows %d..%d" % (a, b), y, (ref["y"][0][:, :, a:b], ref["y"][1][:, :, a:b]), BF16)
+    for t in range(600, 603):
+        one = lambda k: c[k][:, :, t].contiguous()
+        y = kda.glr_step(one("x"), None, S, z=one("z"), A_log=c["A"], g_min=G_MIN, in_gate=one("u"), input_scale="norm")
+        check("token %d" % t, y, (ref["y"][0][:, :, t], ref["y"][1][:, :, t]), BF16)
+    check("S_T", S, ref["S_T"], F32)
+
+
+def test_same_bits_every_call():
+    c = make(0, 4, 0, 128, BF16, lens=[1500, 20, 3000, 700], z=True, u=True, s0=True, seed=9)
+    first = None
+    for _ in range(5):
+        y, S_T, entry = run_fwd(c, "norm", BF16)
+        grads = kda.glr_bwd(c["x"], None, c["S0"], c["dy"].to(BF16), c["dS_T"], entry_states=entry, **kw(c, "norm"))
+        out = [y, S_T] + list(grads)
+        if first is None:
+            first = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+def test_captured_replay_and_side_stream():
+    """One workspace and one graph: replays with new inputs copied in give the eager results; the
+    eager call on another stream gives them too."""
+    c = make(1, 4, 1500, 128, BF16, z=True, u=True, s0=True, seed=10)
+    c2 = make(1, 4, 1500, 128, BF16, z=True, u=True, s0=True, seed=11)
+    y, S_T = torch.empty_like(c["x"]), torch.empty_like(c["S0"])
+    k = kw(c, "norm")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kda.glr_fwd(c["x"], None, c["S0"], y=y, S_T=S_T, stream=side, **k)
+    side.synchronize()
+    want = y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.glr_fwd(c["x"], None, c["S0"], y=y, S_T=S_T, **k)
+        grads = kda.glr_bwd(c["x"], None, c["S0"], y, S_T, **k)
+    eager = None
+    for i in range(4):
+        if i == 2:
+            for n in ("x", "z", "u", "S0"):
+                c[n].copy_(c2[n])
+        y.fill_(GUARD)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [y.clone(), S_T.clone()] + [t.clone() for t in grads]
+        ye, Se, _ = kda.glr_fwd(c["x"], None, c["S0"], **k)
+        eager = [ye, Se] + list(kda.glr_bwd(c["x"], None, c["S0"], ye, Se, **k))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, eager))
+        if i < 2:
+            assert torch.equal(got[0], want)
+
+
+def test_two_streams_at_once():
+    cs = [make(1, 8, 4000, 128, BF16, z=True, u=True, s0=True, seed=20 + i) for i in range(2)]
+    want = [kda.glr_fwd(c["x"], None, c["S0"], **kw(c, "norm"))[:2] for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [None, None]
+    for _ in range(8):
+        for i, c in enumerate(cs):
+            got[i] = kda.glr_fwd(c["x"], None, c["S0"], stream=streams[i], **kw(c, "norm"))[:2]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
