@@ -20,6 +20,8 @@ kda_status check_desc(const kda_glr_desc* d, bool step) {
     if (!kda::valid_dtype(d->in_dtype) || !kda::valid_dtype(d->out_dtype)) return KDA_ERR_INVALID_ARG;
     if (d->scale < KDA_GLR_ONE || d->scale > KDA_GLR_NORM) return KDA_ERR_INVALID_ARG;
     if (!step && d->T >= ((int64_t)1 << 31) - KDA_GLR_CHUNK) return KDA_ERR_UNSUPPORTED;
+    // a tile's elements are addressed with 32 bits
+    if (d->d > KDA_GLR_MAX_D) return KDA_ERR_UNSUPPORTED;
     // element counts must fit comfortably in 64-bit byte offsets
     const double T = step ? 1.0 : (double)(d->T > 0 ? d->T : 1);
     if ((double)d->N * (double)d->H * T * (double)d->d > 1e17) return KDA_ERR_INVALID_ARG;
@@ -78,8 +80,8 @@ kda_status kda_glr_fwd(const kda_glr_desc* d, const void* x, const kda_glr_gates
     const size_t need = rows ? kda::glr_fwd_ws_bytes(a) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (cu_seqlens && !kda::aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
-    const Operand in[] = {{S0, states, 4}, {rows ? x : nullptr, n * ein, ein}, {a.la, n * ein, ein}, {a.z, n * ein, ein}, {a.u, n * ein, ein},
-                          {a.A_log, d->H * d->d * 4, 4}};
+    const Operand in[] = {{S0, states, 4}, {rows ? x : nullptr, n * ein, ein}, {a.la, n * ein, ein},
+                          {a.z, n * ein, ein}, {a.u, n * ein, ein}, {a.A_log, d->H * d->d * 4, 4}};
     const Operand out[] = {{S_T, states, 4}, {rows ? y : nullptr, n * eout, eout},
                            {rows ? entry_states : nullptr, a.blocks * a.nch * d->d * 4, 4},
                            {need > 0 ? workspace : nullptr, (int64_t)need, 16}};
@@ -126,8 +128,8 @@ kda_status kda_glr_bwd(const kda_glr_desc* d, const void* x, const kda_glr_gates
     const size_t need = rows ? kda::glr_bwd_ws_bytes(a) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (cu_seqlens && !kda::aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
-    const Operand in[] = {{S0, states, 4}, {dS_T, states, 4}, {x, n * ein, ein}, {a.la, n * ein, ein}, {a.z, n * ein, ein}, {a.u, n * ein, ein},
-                          {a.A_log, d->H * d->d * 4, 4}, {dy, n * eout, eout}, {a.entry, a.blocks * a.nch * d->d * 4, 4}};
+    const Operand in[] = {{S0, states, 4}, {dS_T, states, 4}, {x, n * ein, ein}, {a.la, n * ein, ein},
+                          {a.z, n * ein, ein}, {a.u, n * ein, ein}, {a.A_log, d->H * d->d * 4, 4}, {dy, n * eout, eout}, {a.entry, a.blocks * a.nch * d->d * 4, 4}};
     const Operand out[] = {{dS0, states, 4}, {dx, n * ein, ein}, {ddecay, n * ein, ein}, {din_gate, n * ein, ein},
                            {dA_log, d->H * d->d * 4, 4}, {need > 0 ? workspace : nullptr, (int64_t)need, 16}};
     if (!kda::operands_ok(in, out)) return KDA_ERR_INVALID_ARG;
@@ -151,7 +153,8 @@ kda_status kda_glr_step(const kda_glr_desc* d, const void* x, const kda_glr_gate
     one.T = 1; one.packed = 0;
     GlrArgs a = to_args(&one, gates);
     const int64_t n = d->N * d->H * d->d, ein = elem_bytes(d->in_dtype), eout = elem_bytes(d->out_dtype);
-    const Operand in[] = {{x, n * ein, ein}, {a.la, n * ein, ein}, {a.z, n * ein, ein}, {a.u, n * ein, ein}, {a.A_log, d->H * d->d * 4, 4}};
+    const Operand in[] = {{x, n * ein, ein}, {a.la, n * ein, ein}, {a.z, n * ein, ein}, {a.u, n * ein, ein},
+                          {a.A_log, d->H * d->d * 4, 4}};
     const Operand out[] = {{S, n * 4, 4}, {y, n * eout, eout}};
     if (!kda::operands_ok(in, out)) return KDA_ERR_INVALID_ARG;
     a.x = x; a.S = S; a.y = y;

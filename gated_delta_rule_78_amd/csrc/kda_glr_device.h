@@ -1,44 +1,190 @@
-// Elementwise arithmetic of the gated linear recurrence: the gates and their derivatives.
+// Device code shared by the gated linear recurrence's kernels: the gates and their derivatives, the
+// composition of row spans, the tile geometry and the chain that carries states between tiles.
 #pragma once
 
 #include "kda_glr.h"
+#include "kda_glr_internal.h"
 #include "kda_math.h"
 
 namespace kda {
 namespace glr {
 
-// alpha = e^la and, with W, 1 - alpha without the cancellation near alpha = 1: for la > -0.35 from
-// e^la - 1 = la (1 + la/2 (1 + la/3 (...))), cut after la^8 / 8! (relative error 0.35^8 / 9! < 1e-9).
-template <bool W>
-__device__ __forceinline__ void decay_f(float la, float& alpha, float& one_minus) {
-    alpha = exp_f(la);
-    if constexpr (W) {
-        float p = fmaf(la, 1.f / 8.f, 1.f);
-        p = fmaf(p * la, 1.f / 7.f, 1.f);
-        p = fmaf(p * la, 1.f / 6.f, 1.f);
-        p = fmaf(p * la, 1.f / 5.f, 1.f);
-        p = fmaf(p * la, 1.f / 4.f, 1.f);
-        p = fmaf(p * la, 1.f / 3.f, 1.f);
-        p = fmaf(p * la, 1.f / 2.f, 1.f);
-        one_minus = la > -0.35f ? -la * p : 1.f - alpha;
+// 1 - e^la without the cancellation near la = 0: for la > -0.35 the series
+// -la (1 + la/2 + la^2/6 + ... + la^6/5040), cut at a relative error of 0.35^7 / 8! < 2^-25.
+__device__ __forceinline__ float one_minus_exp(float la, float alpha) {
+    float p = fmaf(la, 1.f / 5040.f, 1.f / 720.f);
+    p = fmaf(p, la, 1.f / 120.f);
+    p = fmaf(p, la, 1.f / 24.f);
+    p = fmaf(p, la, 1.f / 6.f);
+    p = fmaf(p, la, 0.5f);
+    p = fmaf(p, la, 1.f);
+    return la > -0.35f ? -la * p : 1.f - alpha;
+}
+
+// The input scale w(alpha).
+template <int SCALE>
+__device__ __forceinline__ float scale_w(float la, float alpha) {
+    if constexpr (SCALE == KDA_GLR_ONE) return 1.f;
+    const float om = one_minus_exp(la, alpha);
+    if constexpr (SCALE == KDA_GLR_LEAKY) return om;
+    return __builtin_amdgcn_sqrtf(fmaf(om, alpha, om));   // (1 - alpha)(1 + alpha)
+}
+
+// w and dw / dlog_alpha: 0, -alpha, -alpha^2 / w (taken as 0 where w = 0).
+template <int SCALE>
+__device__ __forceinline__ void scale_w_dw(float la, float alpha, float& w, float& dw) {
+    if constexpr (SCALE == KDA_GLR_ONE) {
+        w = 1.f; dw = 0.f;
+    } else {
+        const float om = one_minus_exp(la, alpha);
+        if constexpr (SCALE == KDA_GLR_LEAKY) {
+            w = om; dw = -alpha;
+        } else {
+            const float w2 = fmaf(om, alpha, om);
+            const float rw = w2 > 0.f ? __builtin_amdgcn_rsqf(w2) : 0.f;
+            w = w2 * rw; dw = -alpha * alpha * rw;
+        }
     }
 }
 
-// The input scale w(alpha) from alpha and 1 - alpha.
-template <int SCALE>
-__device__ __forceinline__ float scale_w(float alpha, float one_minus) {
-    if constexpr (SCALE == KDA_GLR_ONE) return 1.f;
-    if constexpr (SCALE == KDA_GLR_LEAKY) return one_minus;
-    return __builtin_amdgcn_sqrtf(one_minus * (1.f + alpha));
+// A span of rows maps the state before it to the state after it: h -> A h + b. The sign bit of A
+// says that a sequence starts inside the span, which then does not see the state before it at all
+// (A's magnitude is not read); log decays give A >= 0 otherwise.
+struct Span {
+    float A, h;
+};
+template <bool CUTS>
+__device__ __forceinline__ float apply(Span s, float h) {
+    const float r = fmaf(s.A, h, s.h);
+    if constexpr (!CUTS) return r;
+    return __float_as_int(s.A) < 0 ? s.h : r;
+}
+// First l, then r: a cut in l keeps the sign of the product negative.
+template <bool CUTS>
+__device__ __forceinline__ Span compose(Span l, Span r) {
+    Span o{l.A * r.A, apply<CUTS>(r, l.h)};
+    if constexpr (CUTS)
+        if (__float_as_int(r.A) < 0) o.A = r.A;
+    return o;
 }
 
-// dw / dlog_alpha: 0, -alpha, -alpha^2 / w (taken as 0 where w = 0).
-template <int SCALE>
-__device__ __forceinline__ float scale_dw(float alpha, float one_minus) {
-    if constexpr (SCALE == KDA_GLR_ONE) return 0.f;
-    if constexpr (SCALE == KDA_GLR_LEAKY) return -alpha;
-    const float w2 = one_minus * (1.f + alpha);
-    return w2 > 0.f ? -alpha * alpha * __builtin_amdgcn_rsqf(w2) : 0.f;
+// A tile is kRows rows of kCW channels: lane ct of a sub-chunk's CT lanes owns VEC channels, a
+// thread L consecutive rows. CT = 16 and VEC = 4, or 64 and 1 where rows are not aligned for 4.
+constexpr int kThreads = 256;
+constexpr int kCW = 64;
+template <int VEC>
+struct Tile {
+    static constexpr int CT = kCW / VEC;            // threads across the channels
+    static constexpr int SPW = 64 / CT;             // sub-chunks per wave
+    static constexpr int W = kThreads / 64;         // waves
+};
+
+// ---- the chain -------------------------------------------------------------------------------
+// Tiles of one block of rows and channel tile form a chain. A tile publishes its span as one
+// 64-bit word per channel as soon as it has read its rows, and the state behind it as another once
+// it knows the state before it. Each word holds all a reader needs (all ones: not there yet), so
+// relaxed agent-scope accesses suffice: nothing is ordered against anything else. A workgroup
+// takes its tile from a counter, in chain order, so every tile it waits for is held by a workgroup
+// that started earlier and itself only waits for earlier ones: every wait ends.
+typedef unsigned long long u64;
+constexpr u64 kNone = ~0ull;
+
+__device__ __forceinline__ void publish(u64* p, uint32_t hi, float lo) {
+    const u64 v = ((u64)hi << 32) | __float_as_uint(lo);
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ u64 peek(const u64* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish_span(u64* p, Span s) {
+    uint32_t a = __float_as_uint(s.A);
+    if (a == 0xffffffffu) a = 0xffc00000u;          // a NaN: any other one, the word must not be kNone
+    publish(p, a, s.h);
+}
+
+// The state before the tile whose words are span[i * step], state[i * step] at i = 0, from the
+// `avail` tiles before it (i = -1, -2, ...): the nearest published state, carried forward over the
+// spans in between one by one. A tile's own published state is the same operations on the same
+// numbers, so the result does not depend on which one was found.
+constexpr int kWindow = 6;
+template <bool CUTS>
+__device__ __forceinline__ float look_back(const u64* span, const u64* state, int64_t step, int64_t avail) {
+    const int n = avail < kWindow ? (int)avail : kWindow;
+    for (int spin = 0; spin < (1 << 26); ++spin) {
+        u64 sp[kWindow], st[kWindow];
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i)
+            if (i < n) {
+                st[i] = peek(state - (int64_t)(i + 1) * step);
+                if (i + 1 < kWindow) sp[i] = peek(span - (int64_t)(i + 1) * step);
+            }
+        int found = -1;
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i)
+            if (i < n && found < 0 && ok) {
+                if (st[i] != kNone) found = i;
+                else if (i + 1 < kWindow) ok = sp[i] != kNone;
+            }
+        if (found >= 0) {
+            float h = 0.f;
+#pragma unroll
+            for (int i = kWindow - 1; i >= 0; --i) {
+                if (i == found) h = __uint_as_float((uint32_t)st[i]);
+                else if (i < found) h = apply<CUTS>(Span{__uint_as_float((uint32_t)(sp[i] >> 32)), __uint_as_float((uint32_t)sp[i])}, h);
+            }
+            return h;
+        }
+        __builtin_amdgcn_s_sleep(2);
+    }
+    return __uint_as_float(0x7fc00000u);
+}
+
+// VEC consecutive elements of a row as they lie in memory.
+template <typename T, int VEC>
+struct RawRow;
+template <> struct RawRow<bf16_t, 4> { uint2 v; };
+template <> struct RawRow<float, 4> { float4 v; };
+template <> struct RawRow<bf16_t, 1> { bf16_t v; };
+template <> struct RawRow<float, 1> { float v; };
+
+__device__ __forceinline__ void unpack(const RawRow<bf16_t, 4>& r, float* o) {
+    o[0] = __uint_as_float(r.v.x << 16); o[1] = __uint_as_float(r.v.x & 0xffff0000u);
+    o[2] = __uint_as_float(r.v.y << 16); o[3] = __uint_as_float(r.v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack(const RawRow<float, 4>& r, float* o) {
+    o[0] = r.v.x; o[1] = r.v.y; o[2] = r.v.z; o[3] = r.v.w;
+}
+__device__ __forceinline__ void unpack(const RawRow<bf16_t, 1>& r, float* o) { o[0] = bf16_bits_to_f32(r.v); }
+__device__ __forceinline__ void unpack(const RawRow<float, 1>& r, float* o) { o[0] = r.v; }
+
+template <int VEC, typename T>
+__device__ __forceinline__ void store_row(T* p, const float* x) {
+    if constexpr (VEC == 4) store4(p, x[0], x[1], x[2], x[3]);
+    else st_f(p, x[0]);
+}
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float* p, float* o) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) o[v] = p[v];
+}
+
+// Which sequences start and end in a packed tile's rows: start[r], end[r] = sequence or -1, from
+// the tile's first sequence (kept per tile by the prepare kernel). Empty sequences mark nothing.
+template <int ROWS>
+__device__ __forceinline__ void mark_rows(const GlrArgs& a, int64_t row0, int32_t s_lo, int32_t s_hi, int32_t* start,
+                                          int32_t* end) {
+    for (int r = threadIdx.x; r < ROWS; r += kThreads) { start[r] = -1; end[r] = -1; }
+    __syncthreads();
+    const int32_t last = s_hi < (int32_t)a.N - 1 ? s_hi : (int32_t)a.N - 1;
+    for (int32_t s = s_lo + (int32_t)threadIdx.x; s <= last; s += kThreads) {
+        const int64_t c0 = a.cu[s], c1 = a.cu[s + 1];
+        if (c1 > c0) {
+            if (c0 >= row0 && c0 < row0 + ROWS) start[c0 - row0] = s;
+            if (c1 - 1 >= row0 && c1 - 1 < row0 + ROWS) end[c1 - 1 - row0] = s;
+        }
+    }
+    __syncthreads();
 }
 
 }  // namespace glr

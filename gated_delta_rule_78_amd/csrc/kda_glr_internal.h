@@ -32,6 +32,24 @@ struct GlrArgs {
     float* S;
 };
 
+namespace glr {
+
+// Workspace of a tiled launch, carved by kda_glr.hip: the tile counter, the first sequence of every
+// tile (packed), the chain's two words per tile and channel, the tiles' parts of dA_log.
+struct GlrWs {
+    uint32_t* ticket;
+    int32_t* seq;                        // [nt + 1]
+    unsigned long long *span, *state;    // [blocks][nt][d]
+    float* dA;                           // [blocks][nt][d]
+    int64_t nt, rows;                    // tiles per block, rows per tile
+    int vec;                             // channels per thread: 4 or 1
+};
+hipError_t launch_prepare(const GlrArgs& a, const GlrWs& ws, const float* src, float* dst, hipStream_t st);
+hipError_t launch_fwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
+hipError_t launch_bwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
+
+}  // namespace glr
+
 size_t glr_fwd_ws_bytes(const GlrArgs& a);
 size_t glr_bwd_ws_bytes(const GlrArgs& a);
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t st);

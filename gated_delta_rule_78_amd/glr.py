@@ -14,7 +14,7 @@ from . import _alloc_on, _check, _check_device, _check_tensor, _check_workspace,
 from . import _DTYPES
 from ._launch import data_ptr, on_device, raw_stream
 
-GLR_CHUNK = 256   # KDA_GLR_CHUNK of include/kda_glr.h
+GLR_CHUNK = 128   # KDA_GLR_CHUNK of include/kda_glr.h
 _SCALES = {"one": 0, "leaky": 1, "norm": 2}
 
 

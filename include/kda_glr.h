@@ -34,8 +34,11 @@
 extern "C" {
 #endif
 
+/* Channels per head at most. */
+#define KDA_GLR_MAX_D (1 << 20)
+
 /* Rows per chunk of the sequence split: entry states are stored every KDA_GLR_CHUNK rows. */
-#define KDA_GLR_CHUNK 256
+#define KDA_GLR_CHUNK 128
 
 typedef enum kda_glr_scale {
     KDA_GLR_ONE = 0,    /* w = 1                                                                */
@@ -48,8 +51,8 @@ typedef enum kda_glr_scale {
 typedef struct kda_glr_desc {
     int64_t N;          /* sequences, >= 1                                                     */
     int64_t H;          /* heads, >= 1                                                         */
-    int64_t T;          /* packed: rows per head; else tokens per sequence. 0 <= T < 2^31 - 256 */
-    int64_t d;          /* channels per head, >= 1                                             */
+    int64_t T;          /* packed: rows per head; else tokens per sequence. 0 <= T < 2^31 - 128 */
+    int64_t d;          /* channels per head, 1 .. KDA_GLR_MAX_D                               */
     int32_t in_dtype;   /* kda_dtype of x, log_alpha / z, in_gate and of their gradients       */
     int32_t out_dtype;  /* kda_dtype of y and dy                                               */
     int32_t packed;     /* 1: sequence s is rows cu_seqlens[s] .. cu_seqlens[s+1]-1 of every

@@ -79,7 +79,7 @@ def backward(q, prev, dy, dS_T, g_min=-5.0):
 # root of the hardware by at most 2 U32. Counting them along each path:
 #   sigmoid(v)      exponent's argument |v| U32, exp 3, sum 1, reciprocal 2: (6 + |v|) U32
 #   la from z       e^A 3, e^A z 1 (an absolute error 4 |e^A z| of sigmoid's argument), sigmoid, g_min: ra U32
-#   a               exp 3, and la's error |la| ra
+#   a               exp 3 and its argument |la|, and la's error |la| ra
 #   w               1 - a: the series 4 + ra, or past -0.35 the difference, a / (1 - a) <= 2.4 times a's error;
 #                   the root of it adds 1 + a, product and root
 # The recurrence adds one rounding a step, and a split over chunks at most doubles each count (the
@@ -88,7 +88,7 @@ def backward(q, prev, dy, dS_T, g_min=-5.0):
 def _counts(q, scale):
     ra = 8.0 + 5.0 * np.abs(q["eA"] * q["z"]) if "z" in q else np.zeros_like(q["x"])
     with np.errstate(invalid="ignore"):
-        ca = 3.0 + np.where(np.isinf(q["la"]), 0.0, np.abs(q["la"]) * ra)
+        ca = 3.0 + np.where(np.isinf(q["la"]), 0.0, np.abs(q["la"]) * (1.0 + ra))
     cw = np.zeros_like(ca) if scale == "one" else 6.0 + ra + 2.4 * ca
     if scale == "norm":
         cw = cw + ca + 4.0

@@ -55,8 +55,9 @@ def test_glr_fwd_refusals(lib):
     for bad in (dict(N=0), dict(H=0), dict(T=-1), dict(d=0), dict(ind=7), dict(outd=-1), dict(packed=2), dict(scale=3),
                 dict(scale=-1)):
         assert fwd(lib, desc(**bad)) == INVALID, bad
-    assert fwd(lib, desc(T=(1 << 31) - 256)) == UNSUPPORTED
+    assert fwd(lib, desc(T=(1 << 31) - kda.GLR_CHUNK)) == UNSUPPORTED
     assert fwd(lib, desc(N=1 << 20, H=1 << 20)) == UNSUPPORTED
+    assert fwd(lib, desc(T=1, d=(1 << 20) + 1)) == UNSUPPORTED
     assert fwd(lib, desc(), no_gates=True) == INVALID
     assert fwd(lib, desc(), la=None) == INVALID                               # neither decay
     assert fwd(lib, desc(), z=p(4), A=p(5)) == INVALID                        # both

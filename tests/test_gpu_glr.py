@@ -140,10 +140,10 @@ def test_forward(case):
     ref = reference(c, scale)
     check("y", y, ref["y"], odt)
     check("S_T", S_T, ref["S_T"], F32)
-    # entry states: the state before row c * 256 of its block of rows
-    if c["cu"] is None and c["T"] > 256:
+    # entry states: the state before row c * GLR_CHUNK of its block of rows
+    if c["cu"] is None and c["T"] > kda.GLR_CHUNK:
         val, bound = ref["y"]
-        rows = np.arange(256, c["T"], 256) - 1
+        rows = np.arange(kda.GLR_CHUNK, c["T"], kda.GLR_CHUNK) - 1
         shape = (c["N"] * c["H"], len(rows), c["d"])
         check("entry states", entry[:, 1:], (val[:, :, rows].reshape(shape), bound[:, :, rows].reshape(shape)), F32)
 
@@ -230,6 +230,17 @@ def test_rows_behind_the_last_sequence_stay():
     grads = kda.glr_bwd(c["x"], None, c["S0"], dy, c["dS_T"], entry_states=entry, **kw(c, "norm"))
     for k, g in zip(("dx", "dd", "du", "dS0", "dA"), grads):
         check(k, g, ref[k], F32)
+
+
+def test_packed_states_in_place():
+    """S_T in place of S0, sequences that start and end inside a tile, over tiles, and empty ones."""
+    c = make(0, 2, 0, 200, F32, lens=[0, 5, 3, 1, 0, 900, 127, 1, 300, 0], z=True, u=True, s0=True, seed=13)
+    ref = reference(c, "norm")
+    S = c["S0"].clone()
+    y, S_T, _ = kda.glr_fwd(c["x"], None, S, S_T=S, **kw(c, "norm"))
+    assert S_T is S
+    check("y", y, ref["y"], F32)
+    check("S_T", S, ref["S_T"], F32)
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
