@@ -39,7 +39,7 @@ static hipError_t launch_step_s(const GlrArgs& a, hipStream_t st) {
     return launch_step_t<SCALE, float, float>(a, st);
 }
 
-// Workspace in order: counter (256 bytes), first sequences, chain words, dA_log parts, entry states.
+// Workspace in order: counters, first sequences, chain words, dA_log parts, entry states.
 struct Plan {
     GlrWs ws;
     float* entry;
@@ -57,7 +57,9 @@ static Plan make_plan(const GlrArgs& a, unsigned char* base, bool with_dA, bool 
         return r;
     };
     const size_t words = (size_t)(a.blocks * p.ws.nt * a.d);
-    if (p.ws.nt > 1) p.ws.ticket = reinterpret_cast<uint32_t*>(take(4));
+    const int64_t chains = a.blocks * ((a.d + kCW - 1) / kCW);
+    p.ws.counters = chains < (int64_t)kCounters ? chains : (int64_t)kCounters;
+    if (p.ws.nt > 1) p.ws.ticket = reinterpret_cast<uint32_t*>(take((size_t)p.ws.counters * kCounterStride * 4));
     if (a.packed) p.ws.seq = reinterpret_cast<int32_t*>(take((size_t)(p.ws.nt + 1) * 4));
     if (p.ws.nt > 1) {
         p.ws.span = reinterpret_cast<u64*>(take(words * 8));

@@ -28,13 +28,13 @@ __global__ __launch_bounds__(kThreads) void glr_bwd_kernel(GlrArgs a, GlrWs ws) 
     const int ct = tid % CT, sub = tid / CT;
     const uint32_t ntc = (uint32_t)((a.d + kCW - 1) / kCW), chains = (uint32_t)a.blocks * ntc;
     const bool chained = ws.nt > 1;
-    uint32_t t = blockIdx.x;
+    uint32_t c = blockIdx.x / chains, chain = blockIdx.x % chains;
     if (chained) {
-        if (tid == 0) ticket = atomicAdd(ws.ticket, 1u);
+        if (tid == 0) ticket = atomicAdd(ws.ticket + chain % kCounters * kCounterStride, 1u);
         __syncthreads();
-        t = __builtin_amdgcn_readfirstlane(ticket);
+        next_tile(__builtin_amdgcn_readfirstlane(ticket), chains, c, chain);
     }
-    const uint32_t c = (uint32_t)ws.nt - 1 - t / chains, chain = t % chains;
+    c = (uint32_t)ws.nt - 1 - c;   // the last tile first
     const int64_t block = chain / ntc;
     const int ch_tile = (int)(chain % ntc) * kCW;
     const int ch0 = ch_tile + ct * VEC;

@@ -29,13 +29,12 @@ __global__ __launch_bounds__(kThreads) void glr_fwd_kernel(GlrArgs a, GlrWs ws) 
     const int ct = tid % CT, sub = tid / CT;
     const uint32_t ntc = (uint32_t)((a.d + kCW - 1) / kCW), chains = (uint32_t)a.blocks * ntc;
     const bool chained = ws.nt > 1;
-    uint32_t t = blockIdx.x;
+    uint32_t c = blockIdx.x / chains, chain = blockIdx.x % chains;
     if (chained) {
-        if (tid == 0) ticket = atomicAdd(ws.ticket, 1u);
+        if (tid == 0) ticket = atomicAdd(ws.ticket + chain % kCounters * kCounterStride, 1u);
         __syncthreads();
-        t = __builtin_amdgcn_readfirstlane(ticket);
+        next_tile(__builtin_amdgcn_readfirstlane(ticket), chains, c, chain);
     }
-    const uint32_t c = t / chains, chain = t % chains;
     const int64_t block = chain / ntc;
     const int ch_tile = (int)(chain % ntc) * kCW;
     const int ch0 = ch_tile + ct * VEC;
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void glr_fwd_kernel(GlrArgs a, GlrWs ws) 
 __global__ __launch_bounds__(256) void glr_prepare_kernel(GlrArgs a, GlrWs ws, const float* src, float* dst) {
     const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
     if (ws.nt > 1) {
-        if (i0 == 0) *ws.ticket = 0;
+        for (int64_t i = i0; i < ws.counters; i += step) ws.ticket[i * kCounterStride] = 0;
         const int64_t words = a.blocks * ws.nt * a.d;
         for (int64_t i = i0; i < words; i += step) {
             ws.span[i] = kNone;

@@ -37,7 +37,8 @@ namespace glr {
 // Workspace of a tiled launch, carved by kda_glr.hip: the tile counter, the first sequence of every
 // tile (packed), the chain's two words per tile and channel, the tiles' parts of dA_log.
 struct GlrWs {
-    uint32_t* ticket;
+    uint32_t* ticket;                    // counters, a cache line each
+    int64_t counters;
     int32_t* seq;                        // [nt + 1]
     unsigned long long *span, *state;    // [blocks][nt][d]
     float* dA;                           // [blocks][nt][d]

@@ -303,15 +303,27 @@ __global__ __launch_bounds__(Geo<TPR>::threads) void norm_bwd_kernel(NormArgs a)
     }
 }
 
-// Column sums of the workgroups' partials [groups][3][D], in order.
-__global__ __launch_bounds__(256) void norm_colsum_kernel(NormArgs a, int groups) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int k = blockIdx.y;
+// Column sums of the workgroups' partials [groups][3][D]: 16 runs of workgroups a column, each
+// summed in order by a thread, joined in LDS in order.
+__global__ __launch_bounds__(1024) void norm_colsum_kernel(NormArgs a, int groups) {
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, k = blockIdx.y;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float* out = k == 0 ? a.dw_post : k == 1 ? a.dlam : a.dw_pre;
-    if (!out || c >= a.D) return;
+    if (!out) return;
+    const int each = (groups + 15) / 16, g1 = (run + 1) * each < groups ? (run + 1) * each : groups;
     float s = 0.f;
-    for (int g = 0; g < groups; ++g) s += a.ws[((int64_t)g * 3 + k) * a.D + c];
-    out[c] = k == 1 ? s * a.scale : s;
+    if (c < a.D) {
+#pragma unroll 8
+        for (int g = run * each; g < g1; ++g) s += a.ws[((int64_t)g * 3 + k) * a.D + c];
+    }
+    part[run][lane] = s;
+    __syncthreads();
+    if (run == 0 && c < a.D) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += part[i][lane];
+        out[c] = k == 1 ? s * a.scale : s;
+    }
 }
 
 template <typename TI, typename TR, typename TO, int VEC, int NV, int TPR>
@@ -327,7 +339,8 @@ static hipError_t launch_g(const NormArgs& a, bool bwd, hipStream_t st) {
     if (groups > 0)
         hipLaunchKernelGGL((norm_bwd_kernel<TI, TR, TO, VEC, NV, TPR>), dim3(groups), dim3(Geo<TPR>::threads), 0, st, a);
     if (a.dw_post || a.dlam || a.dw_pre)
-        hipLaunchKernelGGL(norm_colsum_kernel, dim3((unsigned)((a.D + 255) / 256), 3), dim3(256), 0, st, a, groups);
+        hipLaunchKernelGGL(norm_colsum_kernel, dim3((unsigned)((a.D + 63) / 64), 3), dim3(1024), 0, st, a,
+                           groups);
     return hipGetLastError();
 }
 
