@@ -39,36 +39,92 @@ static hipError_t launch_step_s(const GlrArgs& a, hipStream_t st) {
     return launch_step_t<SCALE, float, float>(a, st);
 }
 
-// Workspace in order: counters, first sequences, chain words, dA_log parts, entry states.
-struct Plan {
-    GlrWs ws;
-    float* entry;
-    size_t bytes;
-};
-
-static Plan make_plan(const GlrArgs& a, unsigned char* base, bool with_dA, bool with_entry) {
-    Plan p{};
-    p.ws.rows = KDA_GLR_CHUNK;
-    p.ws.nt = (a.T + KDA_GLR_CHUNK - 1) / KDA_GLR_CHUNK;
-    size_t at = 0;
-    auto take = [&](size_t bytes) {
-        unsigned char* r = base ? base + at : nullptr;
-        at += (bytes + 255) & ~(size_t)255;
-        return r;
-    };
-    const size_t words = (size_t)(a.blocks * p.ws.nt * a.d);
-    const int64_t chains = a.blocks * ((a.d + kCW - 1) / kCW);
-    p.ws.counters = chains < (int64_t)kCounters ? chains : (int64_t)kCounters;
-    if (p.ws.nt > 1) p.ws.ticket = reinterpret_cast<uint32_t*>(take((size_t)p.ws.counters * kCounterStride * 4));
-    if (a.packed) p.ws.seq = reinterpret_cast<int32_t*>(take((size_t)(p.ws.nt + 1) * 4));
-    if (p.ws.nt > 1) {
-        p.ws.span = reinterpret_cast<u64*>(take(words * 8));
-        p.ws.state = reinterpret_cast<u64*>(take(words * 8));
+// The first sequence that ends behind row (N if none does).
+__device__ __forceinline__ int64_t sequence_behind(const GlrArgs& a, int64_t row) {
+    int64_t lo = 0, hi = a.N;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if ((int64_t)a.cu[mid + 1] > row) hi = mid;
+        else lo = mid + 1;
     }
-    if (with_dA) p.ws.dA = reinterpret_cast<float*>(take(words * 4));
-    if (with_entry) p.entry = reinterpret_cast<float*>(take((size_t)(a.blocks * a.nch * a.d) * 4));
-    p.bytes = at;
-    return p;
+    return lo;
+}
+
+// Before a chained or packed launch: the chain's words and counters, the rows where sequences start
+// and end, and the states of empty sequences (dst = src or zero).
+__global__ __launch_bounds__(256) void glr_prepare_kernel(GlrArgs a, GlrWs ws, const float* src, float* dst) {
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    if (a.packed) {
+        // 32 rows a thread, from sequence to sequence; an empty one (they may be many) is left by search
+        for (int64_t i = i0; i < ws.nt * ws.rows / 32; i += step) {
+            const int64_t r0 = i * 32, r1 = r0 + 32 < a.T ? r0 + 32 : a.T;
+            uint32_t sb = 0, eb = 0;
+            int64_t s = r0 < a.T ? sequence_behind(a, r0) : a.N;
+            while (s < a.N) {
+                const int64_t c0 = a.cu[s], c1 = a.cu[s + 1];
+                if (c0 >= r1) break;
+                if (c1 <= c0) {
+                    const int64_t next = sequence_behind(a, c0);
+                    if (next <= s) break;   // lengths out of order
+                    s = next;
+                    continue;
+                }
+                if (c0 >= r0) { sb |= 1u << (c0 - r0); ws.start[c0] = (int32_t)s; }
+                if (c1 - 1 >= r0 && c1 - 1 < r1) { eb |= 1u << (c1 - 1 - r0); ws.end[c1 - 1] = (int32_t)s; }
+                ++s;
+            }
+            ws.sbits[i] = sb;
+            ws.ebits[i] = eb;
+        }
+        const int64_t per = a.H * a.d;
+        for (int64_t i = dst ? i0 : a.N * per; i < a.N * per; i += step) {
+            const int64_t s = i / per;
+            if (a.cu[s + 1] <= a.cu[s] && src != dst) dst[i] = src ? src[i] : 0.f;
+        }
+    }
+    if (ws.nt <= 1) return;
+    for (int64_t i = i0; i < ws.counters; i += step) ws.ticket[i * kCounterStride] = 0;
+    const int64_t words = a.blocks * ws.nt * a.d;
+    for (int64_t i = i0; i < words; i += step) {
+        ws.span[i] = kNone;
+        ws.state[i] = kNone;
+    }
+}
+
+static hipError_t launch_prepare(const GlrArgs& a, const GlrWs& ws, const float* src, float* dst, hipStream_t st) {
+    if (ws.nt <= 1 && !a.packed) return hipSuccess;
+    int64_t n = ws.nt > 1 ? a.blocks * ws.nt * a.d : 1;
+    if (a.packed && ws.nt * ws.rows / 32 > n) n = ws.nt * ws.rows / 32;
+    if (a.packed && dst && a.N * a.H * a.d > n) n = a.N * a.H * a.d;
+    int64_t grid = (n + 255) / 256;
+    if (grid > 2048) grid = 2048;
+    hipLaunchKernelGGL(glr_prepare_kernel, dim3((unsigned)grid), dim3(256), 0, st, a, ws, src, dst);
+    return hipGetLastError();
+}
+
+// dA_log [H,d] from the tiles' parts [blocks][nt][d], in order: 16 groups of tiles a channel, each
+// summed by a thread, joined in LDS.
+__global__ __launch_bounds__(1024) void glr_dA_kernel(GlrArgs a, GlrWs ws) {
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    const int64_t ntc = (a.d + 63) / 64, head = blockIdx.x / ntc, ch = (int64_t)(blockIdx.x % ntc) * 64 + lane;
+    const int64_t per = a.packed ? 1 : a.N, n = per * ws.nt, each = (n + 15) / 16;
+    float s = 0.f;
+    if (ch < a.d) {
+        const int64_t k1 = (grp + 1) * each < n ? (grp + 1) * each : n;
+#pragma unroll 8
+        for (int64_t k = grp * each; k < k1; ++k) {
+            const int64_t block = (k / ws.nt) * a.H + head, c = k % ws.nt;
+            s += ws.dA[(block * ws.nt + c) * a.d + ch];
+        }
+    }
+    part[grp][lane] = s;
+    __syncthreads();
+    if (grp == 0 && ch < a.d) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += part[i][lane];
+        a.dA[head * a.d + ch] = s;
+    }
 }
 
 // Whether every row of these tensors starts on 4 elements of its type.
@@ -81,19 +137,92 @@ static bool rows_of_4(const GlrArgs& a) {
     return (in & (a.in_bf16 ? 7 : 15)) == 0 && (out & (a.out_bf16 ? 7 : 15)) == 0;
 }
 
+// Workspace in order: counters, marked rows, chain words, dA_log parts.
+struct Plan {
+    GlrWs ws;
+    size_t bytes;
+};
+
+static Plan make_plan(const GlrArgs& a, unsigned char* base, int rows, bool with_dA) {
+    Plan p{};
+    p.ws.rows = rows;
+    p.ws.nt = (a.T + rows - 1) / rows;
+    p.ws.vec = rows_of_4(a) ? 4 : 1;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char* r = base ? base + at : nullptr;
+        at += (bytes + 255) & ~(size_t)255;
+        return r;
+    };
+    const size_t words = (size_t)(a.blocks * p.ws.nt * a.d);
+    const int64_t chains = a.blocks * ((a.d + kCW - 1) / kCW);
+    p.ws.counters = chains < (int64_t)kCounters ? chains : (int64_t)kCounters;
+    if (p.ws.nt > 1) p.ws.ticket = reinterpret_cast<uint32_t*>(take((size_t)p.ws.counters * kCounterStride * 4));
+    if (a.packed) {
+        p.ws.sbits = reinterpret_cast<uint32_t*>(take((size_t)(p.ws.nt * rows / 8)));
+        p.ws.ebits = reinterpret_cast<uint32_t*>(take((size_t)(p.ws.nt * rows / 8)));
+        p.ws.start = reinterpret_cast<int32_t*>(take((size_t)a.T * 4));
+        p.ws.end = reinterpret_cast<int32_t*>(take((size_t)a.T * 4));
+    }
+    if (p.ws.nt > 1) {
+        p.ws.span = reinterpret_cast<u64*>(take(words * 8));
+        p.ws.state = reinterpret_cast<u64*>(take(words * 8));
+    }
+    if (with_dA) p.ws.dA = reinterpret_cast<float*>(take(words * 4));
+    p.bytes = at;
+    return p;
+}
+
+template <bool PACKED, typename TIn>
+static hipError_t launch_fwd_s(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    if (a.scale == KDA_GLR_ONE) return launch_fwd_t<KDA_GLR_ONE, PACKED, TIn>(a, ws, st);
+    if (a.scale == KDA_GLR_LEAKY) return launch_fwd_t<KDA_GLR_LEAKY, PACKED, TIn>(a, ws, st);
+    return launch_fwd_t<KDA_GLR_NORM, PACKED, TIn>(a, ws, st);
+}
+
+static hipError_t launch_fwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    const hipError_t e = launch_prepare(a, ws, a.S0, a.S_T, st);
+    if (e != hipSuccess) return e;
+    if (a.in_bf16) return a.packed ? launch_fwd_s<true, bf16_t>(a, ws, st) : launch_fwd_s<false, bf16_t>(a, ws, st);
+    return a.packed ? launch_fwd_s<true, float>(a, ws, st) : launch_fwd_s<false, float>(a, ws, st);
+}
+
+template <bool PACKED, typename TIn>
+static hipError_t launch_bwd_s(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    if (a.scale == KDA_GLR_ONE) return launch_bwd_t<KDA_GLR_ONE, PACKED, TIn>(a, ws, st);
+    if (a.scale == KDA_GLR_LEAKY) return launch_bwd_t<KDA_GLR_LEAKY, PACKED, TIn>(a, ws, st);
+    return launch_bwd_t<KDA_GLR_NORM, PACKED, TIn>(a, ws, st);
+}
+
+static hipError_t launch_bwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    hipError_t e = launch_prepare(a, ws, a.dST, a.dS0, st);
+    if (e != hipSuccess) return e;
+    if (a.in_bf16) e = a.packed ? launch_bwd_s<true, bf16_t>(a, ws, st) : launch_bwd_s<false, bf16_t>(a, ws, st);
+    else e = a.packed ? launch_bwd_s<true, float>(a, ws, st) : launch_bwd_s<false, float>(a, ws, st);
+    if (e != hipSuccess || !a.z) return e;
+    hipLaunchKernelGGL(glr_dA_kernel, dim3((unsigned)((a.d + 63) / 64 * a.H)), dim3(1024), 0, st, a, ws);
+    return hipGetLastError();
+}
+
 }  // namespace glr
 
-size_t glr_fwd_ws_bytes(const GlrArgs& a) { return glr::make_plan(a, nullptr, false, false).bytes; }
-size_t glr_bwd_ws_bytes(const GlrArgs& a) { return glr::make_plan(a, nullptr, a.z != nullptr, a.entry == nullptr).bytes; }
+size_t glr_fwd_ws_bytes(const GlrArgs& a) { return glr::make_plan(a, nullptr, glr::kFwdRows, false).bytes; }
+
+// The backward's own workspace, or, where it runs the forward first, one that holds either's (one
+// after the other) with the entry states behind.
+size_t glr_bwd_ws_bytes(const GlrArgs& a) {
+    const size_t own = glr::make_plan(a, nullptr, glr::kBwdRows, a.z != nullptr).bytes;
+    if (a.entry) return own;
+    const size_t fwd = glr::make_plan(a, nullptr, glr::kFwdRows, false).bytes;
+    return (own > fwd ? own : fwd) + (size_t)(a.blocks * a.nch * a.d) * 4;
+}
 
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t st) {
     if (a.T == 0) {   // no tokens: S_T = S0
         if (!a.S_T || a.S_T == a.S0) return hipSuccess;
         return launch_copy_or_zero(a.S_T, a.S0, a.N * a.H * a.d, st);
     }
-    glr::Plan p = glr::make_plan(a, a.ws, false, false);
-    p.ws.vec = glr::rows_of_4(a) ? 4 : 1;
-    return glr::launch_fwd_tiles(a, p.ws, st);
+    return glr::launch_fwd_tiles(a, glr::make_plan(a, a.ws, glr::kFwdRows, false).ws, st);
 }
 
 hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t st) {
@@ -104,13 +233,12 @@ hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t st) {
         }
         return a.dS0 ? launch_copy_or_zero(a.dS0, a.dST, a.N * a.H * a.d, st) : hipSuccess;
     }
-    glr::Plan p = glr::make_plan(a, a.ws, a.z != nullptr, a.entry == nullptr);
-    p.ws.vec = glr::rows_of_4(a) ? 4 : 1;
+    const glr::Plan p = glr::make_plan(a, a.ws, glr::kBwdRows, a.z != nullptr);
     GlrArgs b = a;
     if (!b.entry) {   // the forward again, for its entry states alone
-        b.entry = p.entry;
-        b.y = nullptr; b.S_T = nullptr;
-        const hipError_t e = glr::launch_fwd_tiles(b, p.ws, st);
+        const glr::Plan f = glr::make_plan(a, a.ws, glr::kFwdRows, false);
+        b.entry = reinterpret_cast<float*>(a.ws + (p.bytes > f.bytes ? p.bytes : f.bytes));
+        const hipError_t e = glr::launch_fwd_tiles(b, f.ws, st);
         if (e != hipSuccess) return e;
     }
     return glr::launch_bwd_tiles(b, p.ws, st);

@@ -1,0 +1,355 @@
+// Gated linear recurrence for gfx950, backward (include/kda_glr.h). With g_t = dL/dh_t:
+//     g_t = dy_t + alpha_{t+1} g_{t+1}  (dS_T in place of the carry at a sequence's last row),
+//     dx_t = g_t w_t i_t,  din_gate_t = g_t w_t x_t i_t (1 - i_t),
+//     dlog_alpha_t = g_t (alpha_t h_{t-1} + w'_t i_t x_t),
+//     dz_t = dlog_alpha_t log_alpha_t e^A (1 - s_t),  dA_log = sum_t dz_t z_t,  dS0 = alpha_1 g_1.
+//
+// The tiles, their chain and their bound are the forward's (kda_glr_fwd.h), the chain run from the
+// last tile to the first with spans g -> A g + b; the states h_{t-1} are run again inside the tile
+// from the entry state that the forward stored, so that every tensor is read once here too. Between
+// the passes over the rows the gates stay in registers (computing them twice costs more issue slots
+// than the memory leaves free) and x, z and dy wait in LDS as they were read: 128 registers a
+// thread hold no more, and 168 would leave one workgroup a CU.
+#pragma once
+
+#include "kda_glr_device.h"
+
+namespace kda {
+namespace glr {
+
+template <int SCALE, bool PACKED, int Z, int U, typename TIn, typename TOut, int VEC, int L, int THREADS>
+__global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrArgs a, GlrWs ws) {
+    using G = Tile<VEC, L, THREADS>;
+    constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
+    static_assert(ROWS == KDA_GLR_CHUNK, "a tile starts at an entry state");
+    __shared__ float wtA[W][kCW], wth[W][kCW], wtg[W][kCW], wtR[W][kCW], gin[kCW];
+    // fp32 rows are read from memory again instead: they would take all of LDS for one workgroup
+    constexpr bool STASH = sizeof(TIn) == 2 && sizeof(TOut) == 2;
+    __shared__ RawRow<TIn, VEC> xs[STASH ? L : 1][THREADS], zs[STASH && Z != 0 ? L : 1][THREADS];
+    __shared__ RawRow<TOut, VEC> ys[STASH ? L : 1][THREADS];
+    __shared__ uint32_t ticket;
+    const bool has_z = Z == 2 ? a.z != nullptr : Z == 1, has_u = U == 2 ? a.u != nullptr : U == 1;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int ct = tid % CT, sub = tid / CT, row_t = sub * L;
+    const uint32_t ntc = (uint32_t)((a.d + kCW - 1) / kCW), chains = (uint32_t)a.blocks * ntc;
+    const bool chained = ws.nt > 1;
+    uint32_t c = blockIdx.x / chains, chain = blockIdx.x % chains;
+    if (chained) {
+        if (tid == 0) ticket = atomicAdd(ws.ticket + chain % kCounters * kCounterStride, 1u);
+        lds_barrier();
+        next_tile(__builtin_amdgcn_readfirstlane(ticket), chains, c, chain);
+    }
+    c = (uint32_t)ws.nt - 1 - c;   // the last tile first
+    const int64_t block = chain / ntc;
+    const int ch_tile = (int)(chain % ntc) * kCW;
+    const uint32_t d = (uint32_t)a.d;
+    const bool on = ch_tile + ct * VEC < (int)d;
+    const uint32_t ch0 = on ? ch_tile + ct * VEC : d - VEC;   // lanes past the channels shadow the last ones
+    const int64_t row0 = (int64_t)c * ROWS;
+    const int rows_here = (int)(a.T - row0 < ROWS ? a.T - row0 : ROWS);
+    const int64_t base = (block * a.T + row0) * a.d;
+    const int head = (int)(PACKED ? block : block % a.H);
+
+    int lo = 0, hi = rows_here;     // rows of the tile that are in a sequence
+    uint32_t sbits = 0, ebits = 0;  // the thread's rows where one starts or ends
+    if constexpr (PACKED) {
+        sbits = bits_at<L>(ws.sbits, row0 + row_t);
+        ebits = bits_at<L>(ws.ebits, row0 + row_t);
+        live_rows(a, row0, ROWS, lo, hi);
+    }
+    const TIn* dec = (const TIn*)(has_z ? a.z : a.la) + base;
+    const TIn* xp = (const TIn*)a.x + base;
+    const TIn* up = (const TIn*)a.u + base;
+    const TOut* yp = (const TOut*)a.dy + base;
+
+    // decays and gates; the thread's spans, forwards (state) and backwards (a row maps the carry g to
+    // alpha (dy + g)), rows from the last to the first
+    float al[L][VEC], w[L][VEC], gi[L][VEC], s[L][VEC];
+    Span sf[VEC], sr[VEC];
+    {
+        RawRow<TIn, VEC> xr[L], dr[L], ur[L];
+        RawRow<TOut, VEC> yr[L];
+#pragma unroll
+        for (int r = 0; r < L; ++r) {
+            const uint32_t off = row_offset(row_t + r, rows_here, d, ch0);
+            dr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off);
+            xr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off);
+            if (has_u) ur[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(up + off);
+            yr[r] = *reinterpret_cast<const RawRow<TOut, VEC>*>(yp + off);
+        }
+        float cz[VEC];
+        if (has_z) {
+            load_f32<VEC>(a.A_log + (int64_t)head * a.d + ch0, cz);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) cz[v] = -kLog2e * exp_f(cz[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sf[v] = sr[v] = Span{1.f, 0.f};
+        const bool plain = !PACKED || (sbits | ebits) == 0;
+#pragma unroll
+        for (int r = L - 1; r >= 0; --r) {
+            float x[VEC], q[VEC], u[VEC], dy[VEC], b[VEC];
+            unpack(xr[r], x);
+            unpack(dr[r], q);
+            unpack(yr[r], dy);
+            if (has_u) unpack(ur[r], u);
+            if constexpr (STASH) {
+                xs[r][tid] = xr[r];
+                if (has_z) zs[r][tid] = dr[r];
+                ys[r][tid] = yr[r];
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float la = q[v];
+                if (has_z) {
+                    s[r][v] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(cz[v] * q[v]));
+                    la = a.g_min * s[r][v];
+                }
+                al[r][v] = exp_f(la);
+                b[v] = x[v];
+                if (has_u) {
+                    gi[r][v] = sigmoid_f(u[v]);
+                    b[v] *= gi[r][v];
+                }
+                if (SCALE != KDA_GLR_ONE) {
+                    w[r][v] = scale_w<SCALE>(la, al[r][v]);
+                    b[v] *= w[r][v];
+                }
+            }
+            if (row_t + r < lo || row_t + r >= hi) {   // rows in no sequence pass state and carry on
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) { al[r][v] = 1.f; b[v] = 0.f; dy[v] = 0.f; }
+            }
+            if (plain) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    sf[v].h = fmaf(sf[v].A, b[v], sf[v].h);
+                    sf[v].A *= al[r][v];
+                    sr[v].h = al[r][v] * (dy[v] + sr[v].h);
+                    sr[v].A *= al[r][v];
+                }
+            } else {
+                // S0 becomes part of a first row's input, dS_T takes the carry's place at a last row
+                const float* p0 = a.S0 && (sbits >> r & 1) ? a.S0 + ((int64_t)ws.start[row0 + row_t + r] * a.H + head) * a.d + ch0 : nullptr;
+                const float* p1 = a.dST && (ebits >> r & 1) ? a.dST + ((int64_t)ws.end[row0 + row_t + r] * a.H + head) * a.d + ch0 : nullptr;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    if (p0) b[v] = fmaf(al[r][v], p0[v], b[v]);
+                    if (p1) dy[v] += p1[v];
+                    sf[v] = compose<true>(Span{sbits >> r & 1 ? -1.f : al[r][v], b[v]}, sf[v]);
+                    sr[v] = ebits >> r & 1 ? Span{-1.f, al[r][v] * dy[v]}
+                                           : Span{sr[v].A * al[r][v], al[r][v] * (dy[v] + sr[v].h)};
+                }
+            }
+        }
+    }
+
+    // forward spans up to the thread, backward spans behind it: within the wave, then over the waves
+#pragma unroll
+    for (int m = 1; m < SPW; m <<= 1) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const Span l{__shfl_up(sf[v].A, m * CT), __shfl_up(sf[v].h, m * CT)};
+            const Span o = compose<PACKED>(l, sf[v]);
+            const Span rl{__shfl_down(sr[v].A, m * CT), __shfl_down(sr[v].h, m * CT)};
+            const Span ro = compose<PACKED>(rl, sr[v]);
+            if (lane >= m * CT) sf[v] = o;
+            if (lane < 64 - m * CT) sr[v] = ro;
+        }
+    }
+    if (lane >= 64 - CT) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { wtA[wave][ct * VEC + v] = sf[v].A; wth[wave][ct * VEC + v] = sf[v].h; }
+    }
+    if (lane < CT) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { wtR[wave][ct * VEC + v] = sr[v].A; wtg[wave][ct * VEC + v] = sr[v].h; }
+    }
+    lds_barrier();
+    if (wave == 0) {   // lane = channel: the tile's backward span, the chain
+        const uint32_t ch = ch_tile + lane;
+        Span tot{wtR[W - 1][lane], wtg[W - 1][lane]};
+#pragma unroll
+        for (int i = W - 2; i >= 0; --i) tot = compose<PACKED>(tot, Span{wtR[i][lane], wtg[i][lane]});
+        float g = 0.f;
+        if (ch < d) {
+            const bool first = (int64_t)c + 1 == ws.nt, more = c > 0;
+            if (!PACKED && first && a.dST) g = a.dST[block * a.d + ch];
+            if (chained) {
+                const int64_t word = (block * ws.nt + c) * a.d + ch;
+                const bool cut = PACKED && __float_as_int(tot.A) < 0;
+                if (cut && more) publish(ws.state + word, 0, tot.h);
+                if (!first) {
+                    if (!cut && more) publish_span(ws.span + word, tot);
+                    g = look_back<PACKED>(ws.span + word, ws.state + word, -a.d, ws.nt - 1 - c);
+                }
+                if (!cut && more) publish(ws.state + word, 0, apply<PACKED>(tot, g));
+            }
+            if (!PACKED && c == 0 && a.dS0) a.dS0[block * a.d + ch] = apply<PACKED>(tot, g);
+        }
+        gin[lane] = g;
+    }
+    lds_barrier();
+
+    // the state before the thread's rows and the carry behind them
+    float h[VEC], g[VEC];
+    load_f32<VEC>(a.entry + (block * a.nch + c) * a.d + ch0, h);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) g[v] = gin[ct * VEC + v];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i)
+        if (i < wave) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) h[v] = apply<PACKED>(Span{wtA[i][ct * VEC + v], wth[i][ct * VEC + v]}, h[v]);
+        }
+#pragma unroll
+    for (int i = W - 1; i > 0; --i)
+        if (i > wave) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) g[v] = apply<PACKED>(Span{wtR[i][ct * VEC + v], wtg[i][ct * VEC + v]}, g[v]);
+        }
+    if constexpr (SPW > 1) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const Span l{__shfl_up(sf[v].A, CT), __shfl_up(sf[v].h, CT)};
+            const Span rl{__shfl_down(sr[v].A, CT), __shfl_down(sr[v].h, CT)};
+            const float hl = apply<PACKED>(l, h[v]), gl = apply<PACKED>(rl, g[v]);
+            if (lane >= CT) h[v] = hl;
+            if (lane < 64 - CT) g[v] = gl;
+        }
+    }
+    // the state before each row
+    auto row_x = [&](int r, float* o) {
+        if constexpr (STASH) unpack(xs[r][tid], o);
+        else unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(xp + row_offset(row_t + r, rows_here, d, ch0)), o);
+    };
+    float prev[L][VEC];
+#pragma unroll
+    for (int r = 0; r < L; ++r) {
+        float x[VEC];
+        row_x(r, x);
+        if (PACKED && (sbits >> r & 1)) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                h[v] = a.S0 ? a.S0[((int64_t)ws.start[row0 + row_t + r] * a.H + head) * a.d + ch0 + v] : 0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) prev[r][v] = h[v];
+        if (row_t + r < lo || row_t + r >= hi) continue;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            float b = x[v];
+            if (has_u) b *= gi[r][v];
+            if (SCALE != KDA_GLR_ONE) b *= w[r][v];
+            h[v] = fmaf(al[r][v], h[v], b);
+        }
+    }
+    float eA[VEC], dA[VEC];
+    if (has_z) {
+        load_f32<VEC>(a.A_log + (int64_t)head * a.d + ch0, eA);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { eA[v] = a.g_min * exp_f(eA[v]); dA[v] = 0.f; }
+    }
+    TIn *dx = (TIn*)a.dx + base, *dd = (TIn*)a.dd + base, *du = (TIn*)a.du + base;
+    const uint32_t off0 = (uint32_t)row_t * d + ch0;
+#pragma unroll
+    for (int r = L - 1; r >= 0; --r) {
+        float x[VEC], q[VEC], dy[VEC], ox[VEC], od[VEC], ou[VEC];
+        const bool live = row_t + r >= lo && row_t + r < hi;
+        row_x(r, x);
+        if constexpr (STASH) {
+            if (has_z) unpack(zs[r][tid], q);
+            unpack(ys[r][tid], dy);
+        } else {
+            const uint32_t off = row_offset(row_t + r, rows_here, d, ch0);
+            if (has_z) unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off), q);
+            unpack(*reinterpret_cast<const RawRow<TOut, VEC>*>(yp + off), dy);
+        }
+        if (PACKED && (ebits >> r & 1)) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                g[v] = a.dST ? a.dST[((int64_t)ws.end[row0 + row_t + r] * a.H + head) * a.d + ch0 + v] : 0.f;
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float gr = g[v] + dy[v], alpha = al[r][v];
+            float ix = x[v];
+            ox[v] = SCALE == KDA_GLR_ONE ? gr : gr * w[r][v];
+            if (has_u) {
+                ix *= gi[r][v];
+                ox[v] *= gi[r][v];
+                ou[v] = ox[v] * x[v] * (1.f - gi[r][v]);
+            }
+            float e = alpha * prev[r][v];
+            if (SCALE == KDA_GLR_LEAKY) e = fmaf(-alpha, ix, e);
+            if (SCALE == KDA_GLR_NORM) {
+                // dw / dlog_alpha = -alpha^2 / w, taken as 0 where w = 0
+                const float aw = w[r][v] > 0.f ? alpha * __builtin_amdgcn_rcpf(w[r][v]) : 0.f;
+                e = fmaf(-alpha * aw, ix, e);
+            }
+            e *= gr;
+            if (has_z) {
+                e *= s[r][v] * (1.f - s[r][v]) * eA[v];
+                dA[v] = fmaf(e, q[v], dA[v]);
+            }
+            od[v] = e;
+            g[v] = alpha * gr;
+        }
+        if (on) {
+            store_row<VEC>(dx + (off0 + r * d), ox);
+            store_row<VEC>(dd + (off0 + r * d), od);
+            if (has_u) store_row<VEC>(du + (off0 + r * d), ou);
+            if (PACKED && a.dS0 && (sbits >> r & 1)) {
+                float* p = a.dS0 + ((int64_t)ws.start[row0 + row_t + r] * a.H + head) * a.d + ch0;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) p[v] = g[v];
+            }
+        }
+    }
+    if (!has_z) return;
+    // the tile's part of dA_log: over the sub-chunks of the wave, then the waves
+#pragma unroll
+    for (int m = CT; m < 64; m <<= 1)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) dA[v] += __shfl_xor(dA[v], m);
+    lds_barrier();
+    if (lane < CT) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) wth[wave][ct * VEC + v] = dA[v];
+    }
+    lds_barrier();
+    if (wave == 0 && ch_tile + lane < (int)d) {
+        float t = wth[0][lane];
+#pragma unroll
+        for (int i = 1; i < W; ++i) t += wth[i][lane];
+        ws.dA[(block * ws.nt + c) * a.d + ch_tile + lane] = t;
+    }
+}
+
+template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
+static hipError_t launch_bwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    static_assert(Tile<VEC, L, THREADS>::ROWS == kBwdRows, "the plan's tile");
+    const dim3 grid((unsigned)(a.blocks * ((a.d + kCW - 1) / kCW) * ws.nt));
+    if (a.out_bf16)
+        hipLaunchKernelGGL((glr_bwd_kernel<SCALE, PACKED, Z, U, TIn, bf16_t, VEC, L, THREADS>), grid, dim3(THREADS), 0, st, a, ws);
+    else
+        hipLaunchKernelGGL((glr_bwd_kernel<SCALE, PACKED, Z, U, TIn, float, VEC, L, THREADS>), grid, dim3(THREADS), 0, st, a, ws);
+    return hipGetLastError();
+}
+
+// 4 channels a thread where every row of every tensor starts on 4 elements (ws.vec), else 1.
+template <int SCALE, bool PACKED, typename TIn>
+hipError_t launch_bwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    if (ws.vec == 4) {
+        if (a.z && a.u) return launch_bwd_k<SCALE, PACKED, 1, 1, TIn, 4, 4, 512>(a, ws, st);
+        if (a.z) return launch_bwd_k<SCALE, PACKED, 1, 0, TIn, 4, 4, 512>(a, ws, st);
+        if (a.u) return launch_bwd_k<SCALE, PACKED, 0, 1, TIn, 4, 4, 512>(a, ws, st);
+        return launch_bwd_k<SCALE, PACKED, 0, 0, TIn, 4, 4, 512>(a, ws, st);
+    }
+    return launch_bwd_k<SCALE, PACKED, 2, 2, TIn, 1, 16, 512>(a, ws, st);
+}
+
+}  // namespace glr
+}  // namespace kda

@@ -1,0 +1,15 @@
+// The backward of the gated linear recurrence for bf16 inputs (kda_glr_bwd.h).
+#include "kda_glr_bwd.h"
+
+namespace kda {
+namespace glr {
+
+template hipError_t launch_bwd_t<KDA_GLR_ONE, false, bf16_t>(const GlrArgs&, const GlrWs&, hipStream_t);
+template hipError_t launch_bwd_t<KDA_GLR_LEAKY, false, bf16_t>(const GlrArgs&, const GlrWs&, hipStream_t);
+template hipError_t launch_bwd_t<KDA_GLR_NORM, false, bf16_t>(const GlrArgs&, const GlrWs&, hipStream_t);
+template hipError_t launch_bwd_t<KDA_GLR_ONE, true, bf16_t>(const GlrArgs&, const GlrWs&, hipStream_t);
+template hipError_t launch_bwd_t<KDA_GLR_LEAKY, true, bf16_t>(const GlrArgs&, const GlrWs&, hipStream_t);
+template hipError_t launch_bwd_t<KDA_GLR_NORM, true, bf16_t>(const GlrArgs&, const GlrWs&, hipStream_t);
+
+}  // namespace glr
+}  // namespace kda

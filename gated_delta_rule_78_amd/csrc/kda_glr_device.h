@@ -30,23 +30,6 @@ __device__ __forceinline__ float scale_w(float la, float alpha) {
     return __builtin_amdgcn_sqrtf(fmaf(om, alpha, om));   // (1 - alpha)(1 + alpha)
 }
 
-// w and dw / dlog_alpha: 0, -alpha, -alpha^2 / w (taken as 0 where w = 0).
-template <int SCALE>
-__device__ __forceinline__ void scale_w_dw(float la, float alpha, float& w, float& dw) {
-    if constexpr (SCALE == KDA_GLR_ONE) {
-        w = 1.f; dw = 0.f;
-    } else {
-        const float om = one_minus_exp(la, alpha);
-        if constexpr (SCALE == KDA_GLR_LEAKY) {
-            w = om; dw = -alpha;
-        } else {
-            const float w2 = fmaf(om, alpha, om);
-            const float rw = w2 > 0.f ? __builtin_amdgcn_rsqf(w2) : 0.f;
-            w = w2 * rw; dw = -alpha * alpha * rw;
-        }
-    }
-}
-
 // A span of rows maps the state before it to the state after it: h -> A h + b. The sign bit of A
 // says that a sequence starts inside the span, which then does not see the state before it at all
 // (A's magnitude is not read); log decays give A >= 0 otherwise.
@@ -68,15 +51,16 @@ __device__ __forceinline__ Span compose(Span l, Span r) {
     return o;
 }
 
-// A tile is kRows rows of kCW channels: lane ct of a sub-chunk's CT lanes owns VEC channels, a
-// thread L consecutive rows. CT = 16 and VEC = 4, or 64 and 1 where rows are not aligned for 4.
-constexpr int kThreads = 256;
+// A tile is some rows of kCW channels, in the registers of THREADS threads: CT lanes lie across the
+// channels with VEC channels each (VEC = 4, or 1 where rows are not aligned for 4), and each run of
+// CT lanes owns L consecutive rows, a sub-chunk.
 constexpr int kCW = 64;
-template <int VEC>
+template <int VEC, int L, int THREADS>
 struct Tile {
     static constexpr int CT = kCW / VEC;            // threads across the channels
     static constexpr int SPW = 64 / CT;             // sub-chunks per wave
-    static constexpr int W = kThreads / 64;         // waves
+    static constexpr int W = THREADS / 64;          // waves
+    static constexpr int ROWS = THREADS / CT * L;
 };
 
 // ---- the chain -------------------------------------------------------------------------------
@@ -116,8 +100,10 @@ __device__ __forceinline__ void publish_span(u64* p, Span s) {
 // The state before the tile whose words are span[i * step], state[i * step] at i = 0, from the
 // `avail` tiles before it (i = -1, -2, ...): the nearest published state, carried forward over the
 // spans in between one by one. A tile's own published state is the same operations on the same
-// numbers, so the result does not depend on which one was found.
-constexpr int kWindow = 6;
+// numbers, so the result does not depend on which one was found. A window of 3 takes 397 us at 64K
+// rows x 4096 channels (256-row tiles aside) where 6 takes 430: the words polled cost more than
+// the shorter wait gains.
+constexpr int kWindow = 3;
 template <bool CUTS>
 __device__ __forceinline__ float look_back(const u64* span, const u64* state, int64_t step, int64_t avail) {
     const int n = avail < kWindow ? (int)avail : kWindow;
@@ -180,22 +166,23 @@ __device__ __forceinline__ void load_f32(const float* p, float* o) {
     for (int v = 0; v < VEC; ++v) o[v] = p[v];
 }
 
-// Which sequences start and end in a packed tile's rows: start[r], end[r] = sequence or -1, from
-// the tile's first sequence (kept per tile by the prepare kernel). Empty sequences mark nothing.
-template <int ROWS>
-__device__ __forceinline__ void mark_rows(const GlrArgs& a, int64_t row0, int32_t s_lo, int32_t s_hi, int32_t* start,
-                                          int32_t* end) {
-    for (int r = threadIdx.x; r < ROWS; r += kThreads) { start[r] = -1; end[r] = -1; }
-    __syncthreads();
-    const int32_t last = s_hi < (int32_t)a.N - 1 ? s_hi : (int32_t)a.N - 1;
-    for (int32_t s = s_lo + (int32_t)threadIdx.x; s <= last; s += kThreads) {
-        const int64_t c0 = a.cu[s], c1 = a.cu[s + 1];
-        if (c1 > c0) {
-            if (c0 >= row0 && c0 < row0 + ROWS) start[c0 - row0] = s;
-            if (c1 - 1 >= row0 && c1 - 1 < row0 + ROWS) end[c1 - 1 - row0] = s;
-        }
-    }
-    __syncthreads();
+// Which sequences start and end in the rows of a packed batch (kda_glr_prepare_kernel): a bit per
+// row, and the sequence where the bit is set. bits_at: those of the L rows from row on (L divides
+// 32, row a multiple of L).
+template <int L>
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* bits, int64_t row) {
+    return (bits[row >> 5] >> (row & 31)) & (L == 32 ? ~0u : (1u << L) - 1u);
+}
+// The rows of a tile that are in a sequence: [lo, hi) (sequences lie back to back).
+__device__ __forceinline__ void live_rows(const GlrArgs& a, int64_t row0, int rows, int& lo, int& hi) {
+    const int64_t c0 = a.cu[0] - row0, c1 = a.cu[a.N] - row0;
+    lo = c0 > 0 ? (int)(c0 < rows ? c0 : rows) : 0;
+    hi = c1 < hi ? (int)(c1 > 0 ? c1 : 0) : hi;
+}
+
+// Byte offset of a thread's row inside a tile, kept inside the tile's rows and the row's channels.
+__device__ __forceinline__ uint32_t row_offset(uint32_t row, uint32_t rows_here, uint32_t d, uint32_t ch) {
+    return (row < rows_here ? row : rows_here - 1) * d + ch;
 }
 
 }  // namespace glr

@@ -1,0 +1,262 @@
+// Gated linear recurrence for gfx950, forward (include/kda_glr.h):
+//     h_t = alpha_t h_{t-1} + w(alpha_t) i_t x_t,   y_t = h_t.
+//
+// The operator moves one word in per tensor and one out per element, so HBM bounds it and every
+// input should be read once; the gates' exponentials and roots come close behind (about 50 issue
+// slots an element with every gate). The rows of a block are split into tiles: a workgroup holds
+// its tile's decays and inputs in registers, reduces them to the tile's span h -> A h + b (a scan
+// over threads, waves and LDS), gets the state before the tile from the chain of the tiles before
+// it (kda_glr_device.h), and runs the recurrence again from there with the rows still in registers.
+// The chain is waited for once per tile, when the spans of the tiles before it, which depend on
+// nothing, are usually there.
+#pragma once
+
+#include "kda_glr_device.h"
+
+namespace kda {
+namespace glr {
+
+constexpr int kCh = KDA_GLR_CHUNK;
+
+// Z, U: whether the decay comes from z and whether there is an input gate (2: looked up).
+template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
+__global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrArgs a, GlrWs ws) {
+    using G = Tile<VEC, L, THREADS>;
+    constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
+    static_assert(kCh % L == 0 && ROWS % kCh == 0, "a chunk starts at a thread's first row");
+    __shared__ float wtA[W][kCW], wth[W][kCW], hin[kCW];
+    __shared__ uint32_t ticket;
+    const bool has_z = Z == 2 ? a.z != nullptr : Z == 1, has_u = U == 2 ? a.u != nullptr : U == 1;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int ct = tid % CT, sub = tid / CT, row_t = sub * L;
+    const uint32_t ntc = (uint32_t)((a.d + kCW - 1) / kCW), chains = (uint32_t)a.blocks * ntc;
+    const bool chained = ws.nt > 1;
+    uint32_t c = blockIdx.x / chains, chain = blockIdx.x % chains;
+    if (chained) {
+        if (tid == 0) ticket = atomicAdd(ws.ticket + chain % kCounters * kCounterStride, 1u);
+        lds_barrier();
+        next_tile(__builtin_amdgcn_readfirstlane(ticket), chains, c, chain);
+    }
+    const int64_t block = chain / ntc;
+    const int ch_tile = (int)(chain % ntc) * kCW;
+    const uint32_t d = (uint32_t)a.d;
+    const bool on = ch_tile + ct * VEC < (int)d;
+    const uint32_t ch0 = on ? ch_tile + ct * VEC : d - VEC;   // lanes past the channels shadow the last ones
+    const int64_t row0 = (int64_t)c * ROWS;
+    const int rows_here = (int)(a.T - row0 < ROWS ? a.T - row0 : ROWS);
+    const int64_t base = (block * a.T + row0) * a.d;
+    const int head = (int)(PACKED ? block : block % a.H);
+
+    int lo = 0, hi = rows_here;     // rows of the tile that are in a sequence
+    uint32_t sbits = 0, ebits = 0;  // the thread's rows where one starts or ends
+    if constexpr (PACKED) {
+        sbits = bits_at<L>(ws.sbits, row0 + row_t);
+        ebits = bits_at<L>(ws.ebits, row0 + row_t);
+        live_rows(a, row0, ROWS, lo, hi);
+    }
+    RawRow<TIn, VEC> xr[L], dr[L], ur[L];
+    const TIn* dec = (const TIn*)(has_z ? a.z : a.la) + base;
+    const TIn* xp = (const TIn*)a.x + base;
+    const TIn* up = (const TIn*)a.u + base;
+#pragma unroll
+    for (int r = 0; r < L; ++r) {
+        const uint32_t off = row_offset(row_t + r, rows_here, d, ch0);
+        dr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off);
+        xr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off);
+        if (has_u) ur[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(up + off);
+    }
+    float cz[VEC];
+    if (has_z) {
+        load_f32<VEC>(a.A_log + (int64_t)head * a.d + ch0, cz);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) cz[v] = -kLog2e * exp_f(cz[v]);
+    }
+    // decays and scaled inputs
+    float al[L][VEC], b[L][VEC];
+#pragma unroll
+    for (int r = 0; r < L; ++r) {
+        float x[VEC], q[VEC], g[VEC];
+        unpack(xr[r], x);
+        unpack(dr[r], q);
+        if (has_u) unpack(ur[r], g);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            float la = q[v];
+            if (has_z) la = a.g_min * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(cz[v] * q[v]));
+            al[r][v] = exp_f(la);
+            b[r][v] = has_u ? x[v] * sigmoid_f(g[v]) : x[v];
+            if (SCALE != KDA_GLR_ONE) b[r][v] *= scale_w<SCALE>(la, al[r][v]);
+        }
+    }
+    if (lo > 0 || hi < ROWS) {      // rows in no sequence pass the state on
+#pragma unroll
+        for (int r = 0; r < L; ++r)
+            if (row_t + r < lo || row_t + r >= hi) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) { al[r][v] = 1.f; b[r][v] = 0.f; }
+            }
+    }
+    if (PACKED && sbits != 0) {     // a sequence's S0 becomes part of its first row's input
+#pragma unroll
+        for (int r = 0; r < L; ++r)
+            if (sbits >> r & 1) {
+                const float* s0 = a.S0 + ((int64_t)ws.start[row0 + row_t + r] * a.H + head) * a.d + ch0;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    if (a.S0) b[r][v] = fmaf(al[r][v], s0[v], b[r][v]);
+            }
+    }
+    // the thread's span
+    Span sp[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) sp[v] = Span{1.f, 0.f};
+    if (!PACKED || sbits == 0) {
+#pragma unroll
+        for (int r = 0; r < L; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sp[v] = compose<false>(sp[v], Span{al[r][v], b[r][v]});
+    } else {
+#pragma unroll
+        for (int r = 0; r < L; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sp[v].h = sbits >> r & 1 ? b[r][v] : fmaf(al[r][v], sp[v].h, b[r][v]);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sp[v].A = -1.f;
+    }
+
+    // spans over the sub-chunks of the wave (inclusive), then over the waves
+#pragma unroll
+    for (int m = 1; m < SPW; m <<= 1) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const Span l{__shfl_up(sp[v].A, m * CT), __shfl_up(sp[v].h, m * CT)};
+            const Span o = compose<PACKED>(l, sp[v]);
+            if (lane >= m * CT) sp[v] = o;
+        }
+    }
+    if (lane >= 64 - CT) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { wtA[wave][ct * VEC + v] = sp[v].A; wth[wave][ct * VEC + v] = sp[v].h; }
+    }
+    lds_barrier();
+    if (wave == 0) {   // lane = channel: the tile's span, the chain
+        const uint32_t ch = ch_tile + lane;
+        Span tot{wtA[0][lane], wth[0][lane]};
+#pragma unroll
+        for (int w = 1; w < W; ++w) tot = compose<PACKED>(tot, Span{wtA[w][lane], wth[w][lane]});
+        float h = 0.f;
+        if (ch < d) {
+            if (!PACKED && c == 0 && a.S0) h = a.S0[block * a.d + ch];
+            if (chained) {
+                const int64_t word = (block * ws.nt + c) * a.d + ch;
+                const bool more = (int64_t)c + 1 < ws.nt;
+                const bool cut = PACKED && __float_as_int(tot.A) < 0;
+                if (cut && more) publish(ws.state + word, 0, tot.h);
+                if (c > 0) {
+                    if (!cut && more) publish_span(ws.span + word, tot);
+                    h = look_back<PACKED>(ws.span + word, ws.state + word, a.d, c);
+                }
+                if (!cut && more) publish(ws.state + word, 0, apply<PACKED>(tot, h));
+            }
+        }
+        hin[lane] = h;
+    }
+    lds_barrier();
+    if (!on) return;
+
+    // the state before the thread's first row
+    float h[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = hin[ct * VEC + v];
+#pragma unroll
+    for (int w = 0; w < W - 1; ++w)
+        if (w < wave) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) h[v] = apply<PACKED>(Span{wtA[w][ct * VEC + v], wth[w][ct * VEC + v]}, h[v]);
+        }
+    if constexpr (SPW > 1) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const Span l{__shfl_up(sp[v].A, CT), __shfl_up(sp[v].h, CT)};
+            const float hl = apply<PACKED>(l, h[v]);
+            if (lane >= CT) h[v] = hl;
+        }
+    }
+    if (a.entry && row_t % kCh == 0 && row_t < rows_here) {
+        float* e = a.entry + (block * a.nch + (row0 + row_t) / kCh) * a.d + ch0;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) e[v] = h[v];
+    }
+    // the recurrence again, from there
+    if (!PACKED || sbits == 0) {
+#pragma unroll
+        for (int r = 0; r < L; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) h[v] = b[r][v] = fmaf(al[r][v], h[v], b[r][v]);
+    } else {
+#pragma unroll
+        for (int r = 0; r < L; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) h[v] = b[r][v] = sbits >> r & 1 ? b[r][v] : fmaf(al[r][v], h[v], b[r][v]);
+    }
+    if (a.y) {
+        const uint32_t off0 = (uint32_t)row_t * d + ch0;
+        if (a.out_bf16) {
+            bf16_t* y = (bf16_t*)a.y + base;
+#pragma unroll
+            for (int r = 0; r < L; ++r)
+                if (row_t + r >= lo && row_t + r < hi) store_row<VEC>(y + (off0 + r * d), b[r]);
+        } else {
+            float* y = (float*)a.y + base;
+#pragma unroll
+            for (int r = 0; r < L; ++r)
+                if (row_t + r >= lo && row_t + r < hi) store_row<VEC>(y + (off0 + r * d), b[r]);
+        }
+    }
+    if (!a.S_T) return;
+    if constexpr (PACKED) {
+        if (ebits != 0) {
+#pragma unroll
+            for (int r = 0; r < L; ++r)
+                if (ebits >> r & 1) {
+                    float* st = a.S_T + ((int64_t)ws.end[row0 + row_t + r] * a.H + head) * a.d + ch0;
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) st[v] = b[r][v];
+                }
+        }
+    } else {
+        // rows behind the last one pass the state on, so the last row's state is the thread's last
+        const int64_t last = a.T - 1 - row0;
+        if (row_t <= last && last < row_t + L) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) a.S_T[block * a.d + ch0 + v] = h[v];
+        }
+    }
+}
+
+template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
+static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    static_assert(Tile<VEC, L, THREADS>::ROWS == kFwdRows, "the plan's tile");
+    const int64_t ntc = (a.d + kCW - 1) / kCW;
+    hipLaunchKernelGGL((glr_fwd_kernel<SCALE, PACKED, Z, U, TIn, VEC, L, THREADS>),
+                       dim3((unsigned)(a.blocks * ntc * ws.nt)), dim3(THREADS), 0, st, a, ws);
+    return hipGetLastError();
+}
+
+// 4 channels a thread where every row of every tensor starts on 4 elements (ws.vec), else 1.
+// 512 threads of 8 rows: a tile of 256 rows halves the chain's links against 128 (64K rows x 4096
+// channels: 366 us against 397), and 8 rows a thread leave room for 4 waves a SIMD.
+template <int SCALE, bool PACKED, typename TIn>
+hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    if (ws.vec == 4) {
+        if (a.z && a.u) return launch_fwd_k<SCALE, PACKED, 1, 1, TIn, 4, 8, 512>(a, ws, st);
+        if (a.z) return launch_fwd_k<SCALE, PACKED, 1, 0, TIn, 4, 8, 512>(a, ws, st);
+        if (a.u) return launch_fwd_k<SCALE, PACKED, 0, 1, TIn, 4, 8, 512>(a, ws, st);
+        return launch_fwd_k<SCALE, PACKED, 0, 0, TIn, 4, 8, 512>(a, ws, st);
+    }
+    return launch_fwd_k<SCALE, PACKED, 2, 2, TIn, 1, 32, 512>(a, ws, st);
+}
+
+}  // namespace glr
+}  // namespace kda

@@ -34,20 +34,26 @@ struct GlrArgs {
 
 namespace glr {
 
-// Workspace of a tiled launch, carved by kda_glr.hip: the tile counter, the first sequence of every
-// tile (packed), the chain's two words per tile and channel, the tiles' parts of dA_log.
+// Workspace of a tiled launch, carved by kda_glr.hip: the tile counters, the rows where sequences
+// start and end (packed), the chain's two words per tile and channel, the tiles' parts of dA_log.
 struct GlrWs {
     uint32_t* ticket;                    // counters, a cache line each
     int64_t counters;
-    int32_t* seq;                        // [nt + 1]
+    uint32_t *sbits, *ebits;             // packed: a bit per row, [nt * rows / 32]
+    int32_t *start, *end;                // packed: the sequence of a marked row, [T]
     unsigned long long *span, *state;    // [blocks][nt][d]
     float* dA;                           // [blocks][nt][d]
     int64_t nt, rows;                    // tiles per block, rows per tile
     int vec;                             // channels per thread: 4 or 1
 };
-hipError_t launch_prepare(const GlrArgs& a, const GlrWs& ws, const float* src, float* dst, hipStream_t st);
-hipError_t launch_fwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
-hipError_t launch_bwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
+
+constexpr int kFwdRows = 256, kBwdRows = 128;   // rows of a tile
+
+// Instantiated per input type (kda_glr_fwd_*.hip, kda_glr_bwd_*.hip).
+template <int SCALE, bool PACKED, typename TIn>
+hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
+template <int SCALE, bool PACKED, typename TIn>
+hipError_t launch_bwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
 
 }  // namespace glr
 
