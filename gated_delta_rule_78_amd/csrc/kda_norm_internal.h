@@ -21,6 +21,21 @@ struct NormArgs {
     float* ws;
 };
 
+namespace norm {
+
+// Workgroups at most: what 256 CUs hold at a time (16 waves a CU in the backward, whose column sums
+// cost traffic per workgroup; 24 in the forward).
+inline int fwd_groups(int threads) { return 256 * 24 * 64 / threads; }
+inline int bwd_groups(int threads) { return 256 * 16 * 64 / threads; }
+
+// Instantiated per type of f (kda_norm_*.hip).
+template <typename TI>
+hipError_t launch_i(const NormArgs& a, bool bwd, hipStream_t st);
+// dnorm_weight, dscale_weight and dpre_weight from the sums of `groups` workgroups.
+hipError_t launch_colsum(const NormArgs& a, int groups, hipStream_t st);
+
+}  // namespace norm
+
 size_t norm_bwd_ws_bytes(int64_t rows, int64_t D);
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t st);

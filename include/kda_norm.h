@@ -16,8 +16,8 @@
  *    x_out before x_out is rounded; every output is rounded once.
  *  - 1 <= D <= KDA_NORM_MAX_D. The mean squares must be finite in fp32; a row that holds a
  *    non-finite value gives non-finite outputs in its own row (and weight gradients), no others.
- *  - Every tensor is dense, its base aligned to its element (16-byte bases and D a multiple of 8
- *    take wide accesses); workspaces are aligned to 16 bytes. Sums over rows run in a fixed order:
+ *  - Every tensor is dense, its base aligned to its element (16-byte bases take wide accesses);
+ *    workspaces are aligned to 16 bytes. Sums over rows run in a fixed order:
  *    the same inputs give the same bits on every call.
  */
 #ifndef KDA_NORM_H

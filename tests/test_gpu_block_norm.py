@@ -67,6 +67,14 @@ CASES = [
     (3, 11111, BF16, BF16, {}),
     (2, 16384, F32, F32, {}),
     (3, 12000, BF16, F32, dict(gate=False)),
+    # more rows than workgroups, rows off 8 elements
+    (2501, 1001, BF16, BF16, {}),
+    (40003, 65, BF16, F32, dict(lam=False)),
+    (17000, 12, F32, BF16, {}),
+    (1500, 2050, F32, F32, dict(pre=False)),
+    (300, 8190, BF16, BF16, {}),
+    (259, 9001, F32, F32, {}),
+    (4, 16380, BF16, BF16, {}),
 ]
 ids = lambda c: "%dx%d-%s-%s%s" % (c[0], c[1], "bf16" if c[2] == BF16 else "fp32", "bf16" if c[3] == BF16 else "fp32",
                                    "".join("-%s=%d" % kv for kv in c[4].items())) if isinstance(c, tuple) else None
