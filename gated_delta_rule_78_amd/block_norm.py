@@ -5,12 +5,12 @@
         -> (df, dx, dgate, dnorm_weight, dscale_weight, dpre_weight)
 """
 import ctypes
+import functools
 
 import torch
 
-from . import _alloc_on, _check, _check_device, _check_tensor, _check_workspace, _nbytes, _workspace, library
-from . import _DTYPES
-from ._launch import data_ptr, on_device, raw_stream
+from . import _DTYPES, _check, _check_device, _check_workspace, _nbytes, _workspace, library
+from ._launch import check, data_ptr, raw_stream, scope
 
 NORM_MAX_D = 16384   # KDA_NORM_MAX_D of include/kda_norm.h
 
@@ -40,6 +40,13 @@ def _library():
     return _lib
 
 
+@functools.lru_cache(maxsize=1024)
+def _desc(rows, D, in_dtype, res_dtype, out_dtype, post_norm, pre_norm, scale, eps, pre_eps):
+    """The call's descriptor: nothing but its arguments, so calls of one shape share it."""
+    return NormDesc(rows, D, _DTYPES[in_dtype], _DTYPES[res_dtype], _DTYPES[out_dtype], post_norm, pre_norm, scale, eps,
+                    pre_eps)
+
+
 def _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight):
     """Checks the inputs both directions share; returns (rows, D)."""
     dev, shape = f.device, f.shape
@@ -48,16 +55,16 @@ def _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weig
     if f.dim() < 1:
         raise ValueError("f must have at least one dimension")
     D = shape[-1]
-    _check_tensor("f", f, dev, f.dtype, shape)
+    check("f", f, dev, f.dtype, shape)
     if x is not None:
         if x.dtype not in _DTYPES:
             raise ValueError("unsupported residual dtype %s" % x.dtype)
-        _check_tensor("x", x, dev, x.dtype, shape)
+        check("x", x, dev, x.dtype, shape)
     if gate is not None:
-        _check_tensor("gate", gate, dev, f.dtype, shape)
+        check("gate", gate, dev, f.dtype, shape)
     for name, w in (("norm_weight", norm_weight), ("scale_weight", scale_weight), ("pre_weight", pre_weight)):
         if w is not None:
-            _check_tensor(name, w, dev, torch.float32, (D,))
+            check(name, w, dev, torch.float32, (D,))
     if norm_weight is not None and not post_norm:
         raise ValueError("norm_weight goes with post_norm")
     if pre_weight is not None and not pre_norm:
@@ -87,17 +94,17 @@ def block_norm_fwd(f, x=None, *, gate=None, norm_weight=None, post_norm=True, ep
         if dt not in _DTYPES:
             raise ValueError("unsupported output dtype %s" % dt)
     if x_out is not None:
-        _check_tensor("x_out", x_out, dev, res_dtype, f.shape)
+        check("x_out", x_out, dev, res_dtype, f.shape)
     if n is not None:
         if not pre_norm:
             raise ValueError("n goes with pre_norm")
-        _check_tensor("n", n, dev, out_dtype, f.shape)
+        check("n", n, dev, out_dtype, f.shape)
     if not pre_norm and x_out is None and not store_x:
         raise ValueError("nothing to compute: neither x_out nor n is wanted")
     _check_device("block_norm_fwd", dev)
-    desc = NormDesc(rows, D, _DTYPES[f.dtype], _DTYPES[res_dtype], _DTYPES[out_dtype], bool(post_norm), bool(pre_norm),
-                    scale, eps, pre_eps)
-    with on_device(dev), _alloc_on(stream):
+    desc = _desc(rows, D, f.dtype, res_dtype, out_dtype, bool(post_norm), bool(pre_norm), float(scale), float(eps),
+                 float(pre_eps))
+    with scope(dev, stream):
         if x_out is None and store_x:
             x_out = torch.empty(f.shape, device=dev, dtype=res_dtype)
         if n is None and pre_norm:
@@ -129,23 +136,23 @@ def block_norm_bwd(f, x, dx_out, dn, *, gate=None, norm_weight=None, post_norm=T
         if dt not in _DTYPES:
             raise ValueError("unsupported gradient dtype %s" % dt)
     if dx_out is not None:
-        _check_tensor("dx_out", dx_out, dev, res_dtype, f.shape)
+        check("dx_out", dx_out, dev, res_dtype, f.shape)
     if dn is not None:
         if not pre_norm:
             raise ValueError("dn goes with pre_norm")
-        _check_tensor("dn", dn, dev, out_dtype, f.shape)
+        check("dn", dn, dev, out_dtype, f.shape)
     if dx is not None:
         if x is None:
             raise ValueError("dx goes with x")
-        _check_tensor("dx", dx, dev, res_dtype, f.shape)
+        check("dx", dx, dev, res_dtype, f.shape)
     _check_workspace(workspace, dev)
     _check_device("block_norm_bwd", dev)
-    desc = NormDesc(rows, D, _DTYPES[f.dtype], _DTYPES[res_dtype], _DTYPES[out_dtype], bool(post_norm), bool(pre_norm),
-                    scale, eps, pre_eps)
+    desc = _desc(rows, D, f.dtype, res_dtype, out_dtype, bool(post_norm), bool(pre_norm), float(scale), float(eps),
+                 float(pre_eps))
     lib = _library()
     sums = norm_weight is not None or scale_weight is not None or pre_weight is not None
     need = lib.kda_block_norm_bwd_workspace_bytes(desc) if sums else 0
-    with on_device(dev), _alloc_on(stream):
+    with scope(dev, stream):
         df = torch.empty_like(f)
         dgate = torch.empty_like(f) if gate is not None else None
         if dx is None and x is not None:

@@ -7,12 +7,12 @@
     glr_step(x, log_alpha, S, ...) -> y                               one token, S updated in place
 """
 import ctypes
+import functools
 
 import torch
 
-from . import _alloc_on, _check, _check_device, _check_tensor, _check_workspace, _nbytes, _workspace, library
-from . import _DTYPES
-from ._launch import data_ptr, on_device, raw_stream
+from . import _DTYPES, _check, _check_device, _check_workspace, _nbytes, _workspace, library
+from ._launch import check, data_ptr, raw_stream, scope
 
 GLR_CHUNK = 128   # KDA_GLR_CHUNK of include/kda_glr.h
 _SCALES = {"one": 0, "leaky": 1, "norm": 2}
@@ -67,12 +67,12 @@ def _gates(x, log_alpha, z, A_log, in_gate, H, d):
     if (z is None) != (A_log is None):
         raise ValueError("A_log goes with z")
     if z is None:
-        _check_tensor("log_alpha", log_alpha, dev, dt, shape)
+        check("log_alpha", log_alpha, dev, dt, shape)
     else:
-        _check_tensor("z", z, dev, dt, shape)
-        _check_tensor("A_log", A_log, dev, torch.float32, (H, d))
+        check("z", z, dev, dt, shape)
+        check("A_log", A_log, dev, torch.float32, (H, d))
     if in_gate is not None:
-        _check_tensor("in_gate", in_gate, dev, dt, shape)
+        check("in_gate", in_gate, dev, dt, shape)
     return GlrGates(data_ptr(log_alpha), data_ptr(z), data_ptr(A_log), data_ptr(in_gate))
 
 
@@ -85,6 +85,12 @@ def _dtype(x, out_dtype):
     return out_dtype
 
 
+@functools.lru_cache(maxsize=1024)
+def _desc(N, H, T, d, in_dtype, out_dtype, packed, input_scale, g_min):
+    """The call's descriptor: nothing but its arguments, so calls of one shape share it."""
+    return GlrDesc(N, H, T, d, _DTYPES[in_dtype], _DTYPES[out_dtype], packed, _scale(input_scale), g_min)
+
+
 def _batch(x, cu_seqlens):
     """(N, H, T, d) of a fixed [N,H,T,d] or packed [H,T,d] batch."""
     if cu_seqlens is None:
@@ -93,7 +99,7 @@ def _batch(x, cu_seqlens):
         return tuple(x.shape)
     if x.dim() != 3:
         raise ValueError("x must be [H,T,d] with cu_seqlens (got %s)" % (tuple(x.shape),))
-    _check_tensor("cu_seqlens", cu_seqlens, x.device, torch.int32, (cu_seqlens.numel(),))
+    check("cu_seqlens", cu_seqlens, x.device, torch.int32, (cu_seqlens.numel(),))
     N = cu_seqlens.numel() - 1
     if N < 1:
         raise ValueError("cu_seqlens must have at least 2 entries")
@@ -125,22 +131,22 @@ def glr_fwd(x, log_alpha=None, S0=None, *, z=None, A_log=None, g_min=-5.0, in_ga
     dev = x.device
     N, H, T, d = _batch(x, cu_seqlens)
     packed = cu_seqlens is not None
-    _check_tensor("x", x, dev, x.dtype, x.shape)
+    check("x", x, dev, x.dtype, x.shape)
     gates = _gates(x, log_alpha, z, A_log, in_gate, H, d)
     for name, t in (("S0", S0), ("S_T", S_T)):
         if t is not None:
-            _check_tensor(name, t, dev, torch.float32, (N, H, d))
+            check(name, t, dev, torch.float32, (N, H, d))
     if y is not None:
-        _check_tensor("y", y, dev, out_dtype, x.shape)
+        check("y", y, dev, out_dtype, x.shape)
     eshape = _entry_shape(N, H, T, d, packed)
     if entry_states is not None:
-        _check_tensor("entry_states", entry_states, dev, torch.float32, eshape)
+        check("entry_states", entry_states, dev, torch.float32, eshape)
     _check_workspace(workspace, dev)
     _check_device("glr_fwd", dev)
-    desc = GlrDesc(N, H, T, d, _DTYPES[x.dtype], _DTYPES[out_dtype], packed, _scale(input_scale), g_min)
+    desc = _desc(N, H, T, d, x.dtype, out_dtype, packed, input_scale, float(g_min))
     lib = _library()
     need = lib.kda_glr_fwd_workspace_bytes(desc)
-    with on_device(dev), _alloc_on(stream):
+    with scope(dev, stream):
         if y is None:
             y = torch.empty(x.shape, device=dev, dtype=out_dtype)
         if S_T is None and store_state:
@@ -168,20 +174,20 @@ def glr_bwd(x, log_alpha, S0, dy, dS_T=None, *, z=None, A_log=None, g_min=-5.0, 
     dev = x.device
     N, H, T, d = _batch(x, cu_seqlens)
     packed = cu_seqlens is not None
-    _check_tensor("x", x, dev, x.dtype, x.shape)
+    check("x", x, dev, x.dtype, x.shape)
     gates = _gates(x, log_alpha, z, A_log, in_gate, H, d)
-    _check_tensor("dy", dy, dev, dy.dtype, x.shape)
+    check("dy", dy, dev, dy.dtype, x.shape)
     for name, t in (("S0", S0), ("dS_T", dS_T)):
         if t is not None:
-            _check_tensor(name, t, dev, torch.float32, (N, H, d))
+            check(name, t, dev, torch.float32, (N, H, d))
     if entry_states is not None:
-        _check_tensor("entry_states", entry_states, dev, torch.float32, _entry_shape(N, H, T, d, packed))
+        check("entry_states", entry_states, dev, torch.float32, _entry_shape(N, H, T, d, packed))
     _check_workspace(workspace, dev)
     _check_device("glr_bwd", dev)
-    desc = GlrDesc(N, H, T, d, _DTYPES[x.dtype], _DTYPES[dy.dtype], packed, _scale(input_scale), g_min)
+    desc = _desc(N, H, T, d, x.dtype, dy.dtype, packed, input_scale, float(g_min))
     lib = _library()
     need = lib.kda_glr_bwd_workspace_bytes(desc, entry_states is not None, z is not None)
-    with on_device(dev), _alloc_on(stream):
+    with scope(dev, stream):
         dx, dd = torch.empty_like(x), torch.empty_like(x)
         du = torch.empty_like(x) if in_gate is not None else None
         dA = torch.empty(H, d, device=dev, dtype=torch.float32) if z is not None else None
@@ -203,14 +209,14 @@ def glr_step(x, log_alpha, S, *, z=None, A_log=None, g_min=-5.0, in_gate=None, i
     if x.dim() != 3:
         raise ValueError("x must be [N,H,d] (got %s)" % (tuple(x.shape),))
     N, H, d = x.shape
-    _check_tensor("x", x, dev, x.dtype, x.shape)
+    check("x", x, dev, x.dtype, x.shape)
     gates = _gates(x, log_alpha, z, A_log, in_gate, H, d)
-    _check_tensor("S", S, dev, torch.float32, x.shape)
+    check("S", S, dev, torch.float32, x.shape)
     if y is not None:
-        _check_tensor("y", y, dev, out_dtype, x.shape)
+        check("y", y, dev, out_dtype, x.shape)
     _check_device("glr_step", dev)
-    desc = GlrDesc(N, H, 1, d, _DTYPES[x.dtype], _DTYPES[out_dtype], 0, _scale(input_scale), g_min)
-    with on_device(dev), _alloc_on(stream):
+    desc = _desc(N, H, 1, d, x.dtype, out_dtype, False, input_scale, float(g_min))
+    with scope(dev, stream):
         if y is None:
             y = torch.empty(x.shape, device=dev, dtype=out_dtype)
         st = _library().kda_glr_step(desc, data_ptr(x), gates, data_ptr(S), data_ptr(y), raw_stream(dev, stream))
