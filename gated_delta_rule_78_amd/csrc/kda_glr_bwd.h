@@ -23,6 +23,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
     constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
     static_assert(ROWS == KDA_GLR_CHUNK, "a tile starts at an entry state");
     __shared__ float wtA[W][kCW], wth[W][kCW], wtg[W][kCW], wtR[W][kCW], gin[kCW];
+    __shared__ __align__(16) float turn[W][SPW > 1 ? 2 * SPW * kCW : 1];
     // fp32 rows are read from memory again instead: they would take all of LDS for one workgroup
     constexpr bool STASH = sizeof(TIn) == 2 && sizeof(TOut) == 2;
     __shared__ RawRow<TIn, VEC> xs[STASH ? L : 1][THREADS], zs[STASH && Z != 0 ? L : 1][THREADS];
@@ -145,30 +146,20 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
         }
     }
 
-    // forward spans up to the thread, backward spans behind it: within the wave, then over the waves
-#pragma unroll
-    for (int m = 1; m < SPW; m <<= 1) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const Span l{__shfl_up(sf[v].A, m * CT), __shfl_up(sf[v].h, m * CT)};
-            const Span o = compose<PACKED>(l, sf[v]);
-            const Span rl{__shfl_down(sr[v].A, m * CT), __shfl_down(sr[v].h, m * CT)};
-            const Span ro = compose<PACKED>(rl, sr[v]);
-            if (lane >= m * CT) sf[v] = o;
-            if (lane < 64 - m * CT) sr[v] = ro;
-        }
-    }
-    if (lane >= 64 - CT) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) { wtA[wave][ct * VEC + v] = sf[v].A; wth[wave][ct * VEC + v] = sf[v].h; }
-    }
-    if (lane < CT) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) { wtR[wave][ct * VEC + v] = sr[v].A; wtg[wave][ct * VEC + v] = sr[v].h; }
-    }
+    // forward spans up to the thread, backward spans behind it: over the sub-chunks of the wave, then
+    // over the waves, lane = channel
+    WaveSpans<PACKED, false, VEC, SPW> wf;
+    WaveSpans<PACKED, true, VEC, SPW> wb;
+    wf.scan(sf, turn[wave], lane);
+    wtA[wave][lane] = wf.total.A;
+    wth[wave][lane] = wf.total.h;
+    wb.scan(sr, turn[wave], lane);
+    wtR[wave][lane] = wb.total.A;
+    wtg[wave][lane] = wb.total.h;
+    const uint32_t ch = ch_tile + lane;
+    float hw = a.entry[(block * a.nch + c) * a.d + (ch < d ? ch : d - 1)];
     lds_barrier();
     if (wave == 0) {   // lane = channel: the tile's backward span, the chain
-        const uint32_t ch = ch_tile + lane;
         Span tot{wtR[W - 1][lane], wtg[W - 1][lane]};
 #pragma unroll
         for (int i = W - 2; i >= 0; --i) tot = compose<PACKED>(tot, Span{wtR[i][lane], wtg[i][lane]});
@@ -192,33 +183,12 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
     }
     lds_barrier();
 
-    // the state before the thread's rows and the carry behind them
-    float h[VEC], g[VEC];
-    load_f32<VEC>(a.entry + (block * a.nch + c) * a.d + ch0, h);
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) g[v] = gin[ct * VEC + v];
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i)
-        if (i < wave) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = apply<PACKED>(Span{wtA[i][ct * VEC + v], wth[i][ct * VEC + v]}, h[v]);
-        }
-#pragma unroll
-    for (int i = W - 1; i > 0; --i)
-        if (i > wave) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) g[v] = apply<PACKED>(Span{wtR[i][ct * VEC + v], wtg[i][ct * VEC + v]}, g[v]);
-        }
-    if constexpr (SPW > 1) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const Span l{__shfl_up(sf[v].A, CT), __shfl_up(sf[v].h, CT)};
-            const Span rl{__shfl_down(sr[v].A, CT), __shfl_down(sr[v].h, CT)};
-            const float hl = apply<PACKED>(l, h[v]), gl = apply<PACKED>(rl, g[v]);
-            if (lane >= CT) h[v] = hl;
-            if (lane < 64 - CT) g[v] = gl;
-        }
-    }
+    // the state before the wave's rows and the carry behind them, then the thread's
+    float gw = gin[lane], h[VEC], g[VEC];
+    for (int i = 0; i < wave; ++i) hw = apply<PACKED>(Span{wtA[i][lane], wth[i][lane]}, hw);
+    for (int i = W - 1; i > wave; --i) gw = apply<PACKED>(Span{wtR[i][lane], wtg[i][lane]}, gw);
+    wf.spread(hw, turn[wave], lane, h);
+    wb.spread(gw, turn[wave], lane, g);
     // the state before each row
     auto row_x = [&](int r, float* o) {
         if constexpr (STASH) unpack(xs[r][tid], o);

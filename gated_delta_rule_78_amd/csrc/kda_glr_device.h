@@ -100,9 +100,11 @@ __device__ __forceinline__ void publish_span(u64* p, Span s) {
 // The state before the tile whose words are span[i * step], state[i * step] at i = 0, from the
 // `avail` tiles before it (i = -1, -2, ...): the nearest published state, carried forward over the
 // spans in between one by one. A tile's own published state is the same operations on the same
-// numbers, so the result does not depend on which one was found. A window of 3 takes 397 us at 64K
-// rows x 4096 channels (256-row tiles aside) where 6 takes 430: the words polled cost more than
-// the shorter wait gains.
+// numbers, so the result does not depend on which one was found. The words are nearly always there
+// at the first look, whose latency is what the chain costs (64K rows x 4096 channels: 352 us with a
+// single look and no wait, 357 as it is, 328 without the chain), so a wider window gains nothing (a
+// window of 5: 380), and neither does a look taken before the tile's own span is known (361): that
+// one is too early.
 constexpr int kWindow = 3;
 template <bool CUTS>
 __device__ __forceinline__ float look_back(const u64* span, const u64* state, int64_t step, int64_t avail) {
@@ -136,6 +138,50 @@ __device__ __forceinline__ float look_back(const u64* span, const u64* state, in
     }
     return __uint_as_float(0x7fc00000u);
 }
+
+// Spans of a wave's threads (SPW sub-chunks of CT threads, VEC channels each), turned through LDS so
+// that a lane holds one channel: before[s] spans the sub-chunks before s (behind it, BACK), total
+// all of them. `buf`: 2 * SPW * kCW floats of the wave's own; its accesses need no barrier.
+// Shuffles instead cost twice the LDS accesses and four times the arithmetic, every lane scanning
+// its four channels in log steps.
+template <bool CUTS, bool BACK, int VEC, int SPW>
+struct WaveSpans {
+    Span before[SPW], total;
+
+    __device__ __forceinline__ void scan(const Span (&sp)[VEC], float* buf, int lane) {
+        if constexpr (SPW == 1) {   // VEC = 1: the lane has its channel already
+            total = sp[0];
+        } else {
+            static_assert(VEC == 4 && SPW == 4, "16 lanes of 4 channels");
+            float* own = buf + (lane >> 4) * 2 * kCW + (lane & 15) * 4;
+            *reinterpret_cast<float4*>(own) = make_float4(sp[0].A, sp[1].A, sp[2].A, sp[3].A);
+            *reinterpret_cast<float4*>(own + kCW) = make_float4(sp[0].h, sp[1].h, sp[2].h, sp[3].h);
+            wave_lds_sync();
+#pragma unroll
+            for (int i = 0; i < SPW; ++i) {
+                const int s = BACK ? SPW - 1 - i : i;
+                const Span x{buf[2 * s * kCW + lane], buf[(2 * s + 1) * kCW + lane]};
+                before[s] = total;
+                total = i == 0 ? x : compose<CUTS>(total, x);
+            }
+        }
+    }
+    // h at the wave's first row (last, BACK) to h[VEC] at each thread's
+    __device__ __forceinline__ void spread(float at, float* buf, int lane, float (&h)[VEC]) const {
+        if constexpr (SPW == 1) {
+            h[0] = at;
+        } else {
+#pragma unroll
+            for (int i = 0; i < SPW; ++i) {
+                const int s = BACK ? SPW - 1 - i : i;
+                buf[s * kCW + lane] = i == 0 ? at : apply<CUTS>(before[s], at);
+            }
+            wave_lds_sync();
+            const float4 v = *reinterpret_cast<const float4*>(buf + (lane >> 4) * kCW + (lane & 15) * 4);
+            h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
+        }
+    }
+};
 
 // VEC consecutive elements of a row as they lie in memory.
 template <typename T, int VEC>

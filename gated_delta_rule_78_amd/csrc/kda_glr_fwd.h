@@ -25,6 +25,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
     constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
     static_assert(kCh % L == 0 && ROWS % kCh == 0, "a chunk starts at a thread's first row");
     __shared__ float wtA[W][kCW], wth[W][kCW], hin[kCW];
+    __shared__ __align__(16) float turn[W][SPW > 1 ? 2 * SPW * kCW : 1];
     __shared__ uint32_t ticket;
     const bool has_z = Z == 2 ? a.z != nullptr : Z == 1, has_u = U == 2 ? a.u != nullptr : U == 1;
 
@@ -72,10 +73,9 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
 #pragma unroll
         for (int v = 0; v < VEC; ++v) cz[v] = -kLog2e * exp_f(cz[v]);
     }
-    // decays and scaled inputs
-    float al[L][VEC], b[L][VEC];
-#pragma unroll
-    for (int r = 0; r < L; ++r) {
+    // decay and scaled input of a row of the thread
+    const bool edge = lo > 0 || hi < ROWS;
+    auto row_values = [&](int r, float (&al)[VEC], float (&b)[VEC]) {
         float x[VEC], q[VEC], g[VEC];
         unpack(xr[r], x);
         unpack(dr[r], q);
@@ -84,61 +84,43 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
         for (int v = 0; v < VEC; ++v) {
             float la = q[v];
             if (has_z) la = a.g_min * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(cz[v] * q[v]));
-            al[r][v] = exp_f(la);
-            b[r][v] = has_u ? x[v] * sigmoid_f(g[v]) : x[v];
-            if (SCALE != KDA_GLR_ONE) b[r][v] *= scale_w<SCALE>(la, al[r][v]);
+            al[v] = exp_f(la);
+            b[v] = has_u ? x[v] * sigmoid_f(g[v]) : x[v];
+            if (SCALE != KDA_GLR_ONE) b[v] *= scale_w<SCALE>(la, al[v]);
         }
-    }
-    if (lo > 0 || hi < ROWS) {      // rows in no sequence pass the state on
+        if (edge && (row_t + r < lo || row_t + r >= hi)) {   // a row in no sequence passes the state on
 #pragma unroll
-        for (int r = 0; r < L; ++r)
-            if (row_t + r < lo || row_t + r >= hi) {
+            for (int v = 0; v < VEC; ++v) { al[v] = 1.f; b[v] = 0.f; }
+        }
+        if (PACKED && (sbits >> r & 1) && a.S0) {   // a sequence's S0 becomes part of its first row's input
+            const float* s0 = a.S0 + ((int64_t)ws.start[row0 + row_t + r] * a.H + head) * a.d + ch0;
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) { al[r][v] = 1.f; b[r][v] = 0.f; }
-            }
-    }
-    if (PACKED && sbits != 0) {     // a sequence's S0 becomes part of its first row's input
+            for (int v = 0; v < VEC; ++v) b[v] = fmaf(al[v], s0[v], b[v]);
+        }
+    };
+    float al[L][VEC], b[L][VEC];
 #pragma unroll
-        for (int r = 0; r < L; ++r)
-            if (sbits >> r & 1) {
-                const float* s0 = a.S0 + ((int64_t)ws.start[row0 + row_t + r] * a.H + head) * a.d + ch0;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    if (a.S0) b[r][v] = fmaf(al[r][v], s0[v], b[r][v]);
-            }
-    }
+    for (int r = 0; r < L; ++r) row_values(r, al[r], b[r]);
     // the thread's span
     Span sp[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) sp[v] = Span{1.f, 0.f};
-    if (!PACKED || sbits == 0) {
 #pragma unroll
-        for (int r = 0; r < L; ++r)
+    for (int r = 0; r < L; ++r) {
+        if (PACKED && (sbits >> r & 1)) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sp[v] = Span{-1.f, b[r][v]};
+        } else {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) sp[v] = compose<false>(sp[v], Span{al[r][v], b[r][v]});
-    } else {
-#pragma unroll
-        for (int r = 0; r < L; ++r)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) sp[v].h = sbits >> r & 1 ? b[r][v] : fmaf(al[r][v], sp[v].h, b[r][v]);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) sp[v].A = -1.f;
-    }
-
-    // spans over the sub-chunks of the wave (inclusive), then over the waves
-#pragma unroll
-    for (int m = 1; m < SPW; m <<= 1) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const Span l{__shfl_up(sp[v].A, m * CT), __shfl_up(sp[v].h, m * CT)};
-            const Span o = compose<PACKED>(l, sp[v]);
-            if (lane >= m * CT) sp[v] = o;
         }
     }
-    if (lane >= 64 - CT) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) { wtA[wave][ct * VEC + v] = sp[v].A; wth[wave][ct * VEC + v] = sp[v].h; }
-    }
+
+    // spans over the sub-chunks of the wave, then over the waves: lane = channel
+    WaveSpans<PACKED, false, VEC, SPW> wave_spans;
+    wave_spans.scan(sp, turn[wave], lane);
+    wtA[wave][lane] = wave_spans.total.A;
+    wth[wave][lane] = wave_spans.total.h;
     lds_barrier();
     if (wave == 0) {   // lane = channel: the tile's span, the chain
         const uint32_t ch = ch_tile + lane;
@@ -163,72 +145,43 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
         hin[lane] = h;
     }
     lds_barrier();
+    // the state before the wave's first row, then before the thread's
+    float hw = hin[lane], h[VEC];
+    for (int w = 0; w < wave; ++w) hw = apply<PACKED>(Span{wtA[w][lane], wth[w][lane]}, hw);
+    wave_spans.spread(hw, turn[wave], lane, h);
     if (!on) return;
-
-    // the state before the thread's first row
-    float h[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = hin[ct * VEC + v];
-#pragma unroll
-    for (int w = 0; w < W - 1; ++w)
-        if (w < wave) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = apply<PACKED>(Span{wtA[w][ct * VEC + v], wth[w][ct * VEC + v]}, h[v]);
-        }
-    if constexpr (SPW > 1) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const Span l{__shfl_up(sp[v].A, CT), __shfl_up(sp[v].h, CT)};
-            const float hl = apply<PACKED>(l, h[v]);
-            if (lane >= CT) h[v] = hl;
-        }
-    }
     if (a.entry && row_t % kCh == 0 && row_t < rows_here) {
         float* e = a.entry + (block * a.nch + (row0 + row_t) / kCh) * a.d + ch0;
 #pragma unroll
         for (int v = 0; v < VEC; ++v) e[v] = h[v];
     }
     // the recurrence again, from there
-    if (!PACKED || sbits == 0) {
+    const uint32_t off0 = (uint32_t)row_t * d + ch0;
+    bf16_t* yh = (bf16_t*)a.y + base;
+    float* yf = (float*)a.y + base;
 #pragma unroll
-        for (int r = 0; r < L; ++r)
+    for (int r = 0; r < L; ++r) {
+        if (PACKED && (sbits >> r & 1)) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = b[r][v] = fmaf(al[r][v], h[v], b[r][v]);
-    } else {
-#pragma unroll
-        for (int r = 0; r < L; ++r)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = b[r][v] = sbits >> r & 1 ? b[r][v] : fmaf(al[r][v], h[v], b[r][v]);
-    }
-    if (a.y) {
-        const uint32_t off0 = (uint32_t)row_t * d + ch0;
-        if (a.out_bf16) {
-            bf16_t* y = (bf16_t*)a.y + base;
-#pragma unroll
-            for (int r = 0; r < L; ++r)
-                if (row_t + r >= lo && row_t + r < hi) store_row<VEC>(y + (off0 + r * d), b[r]);
+            for (int v = 0; v < VEC; ++v) h[v] = b[r][v];
         } else {
-            float* y = (float*)a.y + base;
 #pragma unroll
-            for (int r = 0; r < L; ++r)
-                if (row_t + r >= lo && row_t + r < hi) store_row<VEC>(y + (off0 + r * d), b[r]);
+            for (int v = 0; v < VEC; ++v) h[v] = fmaf(al[r][v], h[v], b[r][v]);
+        }
+        if (a.y && row_t + r >= lo && row_t + r < hi) {
+            if (a.out_bf16) store_row<VEC>(yh + (off0 + r * d), h);
+            else store_row<VEC>(yf + (off0 + r * d), h);
+        }
+        if (PACKED && (ebits >> r & 1) && a.S_T) {
+            float* st = a.S_T + ((int64_t)ws.end[row0 + row_t + r] * a.H + head) * a.d + ch0;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) st[v] = h[v];
         }
     }
-    if (!a.S_T) return;
-    if constexpr (PACKED) {
-        if (ebits != 0) {
-#pragma unroll
-            for (int r = 0; r < L; ++r)
-                if (ebits >> r & 1) {
-                    float* st = a.S_T + ((int64_t)ws.end[row0 + row_t + r] * a.H + head) * a.d + ch0;
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) st[v] = b[r][v];
-                }
-        }
-    } else {
+    if constexpr (!PACKED) {
         // rows behind the last one pass the state on, so the last row's state is the thread's last
         const int64_t last = a.T - 1 - row0;
-        if (row_t <= last && last < row_t + L) {
+        if (a.S_T && row_t <= last && last < row_t + L) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) a.S_T[block * a.d + ch0 + v] = h[v];
         }
