@@ -14,8 +14,8 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrArgs a) {
         float la;
         if (a.z) la = a.g_min * sigmoid_f(exp_f(a.A_log[at % (a.H * a.d)]) * ld_f((const TIn*)a.z + at));
         else la = ld_f((const TIn*)a.la + at);
-        const float alpha = exp_f(la);
-        float b = ld_f((const TIn*)a.x + at) * scale_w<SCALE>(la, alpha);
+        const float yl = la * kLog2e, alpha = __builtin_amdgcn_exp2f(yl);
+        float b = ld_f((const TIn*)a.x + at) * scale_w<SCALE>(yl, alpha);
         if (a.u) b *= sigmoid_f(ld_f((const TIn*)a.u + at));
         const float st = fmaf(alpha, a.S[at], b);
         a.S[at] = st;

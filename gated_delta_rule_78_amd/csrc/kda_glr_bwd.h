@@ -59,6 +59,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
         ebits = bits_at<L>(ws.ebits, row0 + row_t);
         live_rows(a, row0, ROWS, lo, hi);
     }
+    const uint32_t off0 = (uint32_t)row_t * d + ch0, last_off = (uint32_t)(rows_here - 1) * d + ch0;
     const TIn* dec = (const TIn*)(has_z ? a.z : a.la) + base;
     const TIn* xp = (const TIn*)a.x + base;
     const TIn* up = (const TIn*)a.u + base;
@@ -68,17 +69,19 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
     // alpha (dy + g)), rows from the last to the first
     float al[L][VEC], w[L][VEC], gi[L][VEC], s[L][VEC];
     Span sf[VEC], sr[VEC];
+    const bool plain = !PACKED || (sbits | ebits) == 0;
     {
         RawRow<TIn, VEC> xr[L], dr[L], ur[L];
         RawRow<TOut, VEC> yr[L];
 #pragma unroll
         for (int r = 0; r < L; ++r) {
-            const uint32_t off = row_offset(row_t + r, rows_here, d, ch0);
+            const uint32_t off = row_offset(off0, r, d, last_off);
             dr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off);
             xr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off);
             if (has_u) ur[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(up + off);
             yr[r] = *reinterpret_cast<const RawRow<TOut, VEC>*>(yp + off);
         }
+        const float gy = a.g_min * kLog2e;
         float cz[VEC];
         if (has_z) {
             load_f32<VEC>(a.A_log + (int64_t)head * a.d + ch0, cz);
@@ -87,7 +90,6 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) sf[v] = sr[v] = Span{1.f, 0.f};
-        const bool plain = !PACKED || (sbits | ebits) == 0;
 #pragma unroll
         for (int r = L - 1; r >= 0; --r) {
             float x[VEC], q[VEC], u[VEC], dy[VEC], b[VEC];
@@ -102,19 +104,21 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
             }
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                float la = q[v];
+                float y;
                 if (has_z) {
                     s[r][v] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(cz[v] * q[v]));
-                    la = a.g_min * s[r][v];
+                    y = gy * s[r][v];
+                } else {
+                    y = q[v] * kLog2e;
                 }
-                al[r][v] = exp_f(la);
+                al[r][v] = __builtin_amdgcn_exp2f(y);
                 b[v] = x[v];
                 if (has_u) {
                     gi[r][v] = sigmoid_f(u[v]);
                     b[v] *= gi[r][v];
                 }
                 if (SCALE != KDA_GLR_ONE) {
-                    w[r][v] = scale_w<SCALE>(la, al[r][v]);
+                    w[r][v] = scale_w<SCALE>(y, al[r][v]);
                     b[v] *= w[r][v];
                 }
             }
@@ -128,7 +132,6 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
                     sf[v].h = fmaf(sf[v].A, b[v], sf[v].h);
                     sf[v].A *= al[r][v];
                     sr[v].h = al[r][v] * (dy[v] + sr[v].h);
-                    sr[v].A *= al[r][v];
                 }
             } else {
                 // S0 becomes part of a first row's input, dS_T takes the carry's place at a last row
@@ -144,6 +147,11 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
                 }
             }
         }
+    }
+
+    if (plain) {   // no cut: the product is the same in both directions
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sr[v].A = sf[v].A;
     }
 
     // forward spans up to the thread, backward spans behind it: over the sub-chunks of the wave, then
@@ -192,7 +200,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
     // the state before each row
     auto row_x = [&](int r, float* o) {
         if constexpr (STASH) unpack(xs[r][tid], o);
-        else unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(xp + row_offset(row_t + r, rows_here, d, ch0)), o);
+        else unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(xp + row_offset(off0, r, d, last_off)), o);
     };
     float prev[L][VEC];
 #pragma unroll
@@ -222,7 +230,6 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
         for (int v = 0; v < VEC; ++v) { eA[v] = a.g_min * exp_f(eA[v]); dA[v] = 0.f; }
     }
     TIn *dx = (TIn*)a.dx + base, *dd = (TIn*)a.dd + base, *du = (TIn*)a.du + base;
-    const uint32_t off0 = (uint32_t)row_t * d + ch0;
 #pragma unroll
     for (int r = L - 1; r >= 0; --r) {
         float x[VEC], q[VEC], dy[VEC], ox[VEC], od[VEC], ou[VEC];
@@ -232,7 +239,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrA
             if (has_z) unpack(zs[r][tid], q);
             unpack(ys[r][tid], dy);
         } else {
-            const uint32_t off = row_offset(row_t + r, rows_here, d, ch0);
+            const uint32_t off = row_offset(off0, r, d, last_off);
             if (has_z) unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off), q);
             unpack(*reinterpret_cast<const RawRow<TOut, VEC>*>(yp + off), dy);
         }

@@ -9,23 +9,24 @@
 namespace kda {
 namespace glr {
 
-// 1 - e^la without the cancellation near la = 0: for la > -0.35 the series
-// -la (1 + la/2 + la^2/6 + ... + la^6/5040), cut at a relative error of 0.35^7 / 8! < 2^-25.
-__device__ __forceinline__ float one_minus_exp(float la, float alpha) {
-    float p = fmaf(la, 1.f / 5040.f, 1.f / 720.f);
-    p = fmaf(p, la, 1.f / 120.f);
-    p = fmaf(p, la, 1.f / 24.f);
-    p = fmaf(p, la, 1.f / 6.f);
-    p = fmaf(p, la, 0.5f);
-    p = fmaf(p, la, 1.f);
-    return la > -0.35f ? -la * p : 1.f - alpha;
+// Log decays are carried as y = log2(alpha) = log_alpha log2(e).
+// 1 - 2^y without the cancellation near y = 0: for y > -0.5 (log_alpha > -0.35) the series
+// -y (ln2 + y ln2^2/2 + ... + y^6 ln2^7/5040), cut at a relative error of 0.35^7 / 8! < 2^-25.
+__device__ __forceinline__ float one_minus_exp2(float y, float alpha) {
+    float p = fmaf(y, 1.5252733804059840e-5f, 1.5403530393381609e-4f);
+    p = fmaf(p, y, 1.3333558146428443e-3f);
+    p = fmaf(p, y, 9.6181291076284772e-3f);
+    p = fmaf(p, y, 5.5504108664821580e-2f);
+    p = fmaf(p, y, 2.4022650695910071e-1f);
+    p = fmaf(p, y, 6.9314718055994531e-1f);
+    return y > -0.5f ? -y * p : 1.f - alpha;
 }
 
 // The input scale w(alpha).
 template <int SCALE>
-__device__ __forceinline__ float scale_w(float la, float alpha) {
+__device__ __forceinline__ float scale_w(float y, float alpha) {
     if constexpr (SCALE == KDA_GLR_ONE) return 1.f;
-    const float om = one_minus_exp(la, alpha);
+    const float om = one_minus_exp2(y, alpha);
     if constexpr (SCALE == KDA_GLR_LEAKY) return om;
     return __builtin_amdgcn_sqrtf(fmaf(om, alpha, om));   // (1 - alpha)(1 + alpha)
 }
@@ -226,9 +227,11 @@ __device__ __forceinline__ void live_rows(const GlrArgs& a, int64_t row0, int ro
     hi = c1 < hi ? (int)(c1 > 0 ? c1 : 0) : hi;
 }
 
-// Byte offset of a thread's row inside a tile, kept inside the tile's rows and the row's channels.
-__device__ __forceinline__ uint32_t row_offset(uint32_t row, uint32_t rows_here, uint32_t d, uint32_t ch) {
-    return (row < rows_here ? row : rows_here - 1) * d + ch;
+// Element offset of row r of a thread whose first lies at off0, kept inside the tile (`last`: the
+// thread's channel in the tile's last row).
+__device__ __forceinline__ uint32_t row_offset(uint32_t off0, int r, uint32_t d, uint32_t last) {
+    const uint32_t off = off0 + (uint32_t)r * d;
+    return off < last ? off : last;
 }
 
 }  // namespace glr

@@ -56,17 +56,19 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
         ebits = bits_at<L>(ws.ebits, row0 + row_t);
         live_rows(a, row0, ROWS, lo, hi);
     }
+    const uint32_t off0 = (uint32_t)row_t * d + ch0, last_off = (uint32_t)(rows_here - 1) * d + ch0;
     RawRow<TIn, VEC> xr[L], dr[L], ur[L];
     const TIn* dec = (const TIn*)(has_z ? a.z : a.la) + base;
     const TIn* xp = (const TIn*)a.x + base;
     const TIn* up = (const TIn*)a.u + base;
 #pragma unroll
     for (int r = 0; r < L; ++r) {
-        const uint32_t off = row_offset(row_t + r, rows_here, d, ch0);
+        const uint32_t off = row_offset(off0, r, d, last_off);
         dr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off);
         xr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off);
         if (has_u) ur[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(up + off);
     }
+    const float gy = a.g_min * kLog2e;
     float cz[VEC];
     if (has_z) {
         load_f32<VEC>(a.A_log + (int64_t)head * a.d + ch0, cz);
@@ -82,11 +84,10 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
         if (has_u) unpack(ur[r], g);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            float la = q[v];
-            if (has_z) la = a.g_min * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(cz[v] * q[v]));
-            al[v] = exp_f(la);
+            const float y = has_z ? gy * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(cz[v] * q[v])) : q[v] * kLog2e;
+            al[v] = __builtin_amdgcn_exp2f(y);
             b[v] = has_u ? x[v] * sigmoid_f(g[v]) : x[v];
-            if (SCALE != KDA_GLR_ONE) b[v] *= scale_w<SCALE>(la, al[v]);
+            if (SCALE != KDA_GLR_ONE) b[v] *= scale_w<SCALE>(y, al[v]);
         }
         if (edge && (row_t + r < lo || row_t + r >= hi)) {   // a row in no sequence passes the state on
 #pragma unroll
@@ -156,7 +157,6 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
         for (int v = 0; v < VEC; ++v) e[v] = h[v];
     }
     // the recurrence again, from there
-    const uint32_t off0 = (uint32_t)row_t * d + ch0;
     bf16_t* yh = (bf16_t*)a.y + base;
     float* yf = (float*)a.y + base;
 #pragma unroll
