@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_abi.cpp", "kda_plan.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_intra.hip", "kda_inter.hip", "kda_fused.hip", "kda_scan.hip", "kda_varlen.hip", "kda_bwd.hip", "kda_noalloc.hip",
-           "kda_glr_abi.cpp", "kda_glr.hip", "kda_glr_fwd_bf16.hip", "kda_glr_fwd_f32.hip",
+           "kda_glr_abi.cpp", "kda_glr.hip", "kda_glr_rows.hip", "kda_glr_fwd_bf16.hip", "kda_glr_fwd_f32.hip",
            "kda_glr_bwd_bf16.hip", "kda_glr_bwd_f32.hip", "kda_norm_abi.cpp", "kda_norm.hip", "kda_norm_bf16.hip", "kda_norm_f32.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,42 +1,18 @@
-// Gated linear recurrence for gfx950: workspaces, plans and the single-token step.
+// Gated linear recurrence for gfx950: workspaces, plans and dispatch.
 #include "kda_glr_device.h"
 #include "kda_internal.h"
 
 namespace kda {
 namespace glr {
 
-// One token of every sequence: S = alpha S + w i x in place, y = S. Bound by the state's read and
-// write, and by the launch for a few sequences.
-template <int SCALE, typename TIn, typename TOut>
-__global__ __launch_bounds__(256) void glr_step_kernel(GlrArgs a) {
-    const int64_t n = a.N * a.H * a.d;
-    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < n; at += (int64_t)gridDim.x * 256) {
-        float la;
-        if (a.z) la = a.g_min * sigmoid_f(exp_f(a.A_log[at % (a.H * a.d)]) * ld_f((const TIn*)a.z + at));
-        else la = ld_f((const TIn*)a.la + at);
-        const float yl = la * kLog2e, alpha = __builtin_amdgcn_exp2f(yl);
-        float b = ld_f((const TIn*)a.x + at) * scale_w<SCALE>(yl, alpha);
-        if (a.u) b *= sigmoid_f(ld_f((const TIn*)a.u + at));
-        const float st = fmaf(alpha, a.S[at], b);
-        a.S[at] = st;
-        st_f((TOut*)a.y + at, st);
-    }
-}
-
-template <int SCALE, typename TIn, typename TOut>
-static hipError_t launch_step_t(const GlrArgs& a, hipStream_t st) {
-    const int64_t n = a.N * a.H * a.d;
-    const int64_t grid = (n + 255) / 256 < (1 << 20) ? (n + 255) / 256 : (1 << 20);
-    hipLaunchKernelGGL((glr_step_kernel<SCALE, TIn, TOut>), dim3((unsigned)grid), dim3(256), 0, st, a);
-    return hipGetLastError();
-}
-
-template <int SCALE>
-static hipError_t launch_step_s(const GlrArgs& a, hipStream_t st) {
-    if (a.in_bf16 && a.out_bf16) return launch_step_t<SCALE, bf16_t, bf16_t>(a, st);
-    if (a.in_bf16) return launch_step_t<SCALE, bf16_t, float>(a, st);
-    if (a.out_bf16) return launch_step_t<SCALE, float, bf16_t>(a, st);
-    return launch_step_t<SCALE, float, float>(a, st);
+// Whether every row of these tensors starts on 4 elements of its type.
+bool rows_of_4(const GlrArgs& a) {
+    if (a.d % 4 != 0) return false;
+    uintptr_t in = 0, out = 0;
+    for (const void* p : {a.x, a.la, a.z, a.u, (const void*)a.dx, (const void*)a.dd, (const void*)a.du})
+        in |= reinterpret_cast<uintptr_t>(p);
+    for (const void* p : {(const void*)a.y, a.dy}) out |= reinterpret_cast<uintptr_t>(p);
+    return (in & (a.in_bf16 ? 7 : 15)) == 0 && (out & (a.out_bf16 ? 7 : 15)) == 0;
 }
 
 // The first sequence that ends behind row (N if none does).
@@ -127,27 +103,20 @@ __global__ __launch_bounds__(1024) void glr_dA_kernel(GlrArgs a, GlrWs ws) {
     }
 }
 
-// Whether every row of these tensors starts on 4 elements of its type.
-static bool rows_of_4(const GlrArgs& a) {
-    if (a.d % 4 != 0) return false;
-    uintptr_t in = 0, out = 0;
-    for (const void* p : {a.x, a.la, a.z, a.u, (const void*)a.dx, (const void*)a.dd, (const void*)a.du, (const void*)a.S})
-        in |= reinterpret_cast<uintptr_t>(p);
-    for (const void* p : {(const void*)a.y, a.dy}) out |= reinterpret_cast<uintptr_t>(p);
-    return (in & (a.in_bf16 ? 7 : 15)) == 0 && (out & (a.out_bf16 ? 7 : 15)) == 0;
-}
-
 // Workspace in order: counters, marked rows, chain words, dA_log parts.
 struct Plan {
     GlrWs ws;
     size_t bytes;
 };
 
-static Plan make_plan(const GlrArgs& a, unsigned char* base, int rows, bool with_dA) {
+static Plan make_plan(const GlrArgs& a, unsigned char* base, bool backward) {
     Plan p{};
+    p.ws.vec = rows_of_4(a) ? 4 : 1;
+    // a workspace query knows no addresses: it plans for the smaller tiles, which need more
+    const int rows = backward ? kBwdRows : p.ws.vec == 4 && base ? kFwdRows : kFwdRows1;
+    const bool with_dA = backward && a.z;
     p.ws.rows = rows;
     p.ws.nt = (a.T + rows - 1) / rows;
-    p.ws.vec = rows_of_4(a) ? 4 : 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         unsigned char* r = base ? base + at : nullptr;
@@ -195,25 +164,32 @@ static hipError_t launch_bwd_s(const GlrArgs& a, const GlrWs& ws, hipStream_t st
 }
 
 static hipError_t launch_bwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
-    hipError_t e = launch_prepare(a, ws, a.dST, a.dS0, st);
+    const hipError_t e = launch_prepare(a, ws, a.dST, a.dS0, st);
     if (e != hipSuccess) return e;
-    if (a.in_bf16) e = a.packed ? launch_bwd_s<true, bf16_t>(a, ws, st) : launch_bwd_s<false, bf16_t>(a, ws, st);
-    else e = a.packed ? launch_bwd_s<true, float>(a, ws, st) : launch_bwd_s<false, float>(a, ws, st);
-    if (e != hipSuccess || !a.z) return e;
-    hipLaunchKernelGGL(glr_dA_kernel, dim3((unsigned)((a.d + 63) / 64 * a.H)), dim3(1024), 0, st, a, ws);
-    return hipGetLastError();
+    if (a.in_bf16) return a.packed ? launch_bwd_s<true, bf16_t>(a, ws, st) : launch_bwd_s<false, bf16_t>(a, ws, st);
+    return a.packed ? launch_bwd_s<true, float>(a, ws, st) : launch_bwd_s<false, float>(a, ws, st);
+}
+
+// Whether a thread per channel walks the rows one by one (kda_glr_rows.hip) instead of tiles of 256
+// of them: short sequences, which would leave a tile's threads idle, and middling ones where there
+// are channels enough to fill the GPU. bf16 with gates, 32 heads of 128 channels, by rows / in tiles:
+// 512 x 16 rows 49 us / 560, 64 x 64 rows 31 / 75, 64 x 128 rows 70 / 82; 16 x 64 rows 29 / 23,
+// 4 x 64 rows 28 / 13.
+static bool by_rows(const GlrArgs& a) {
+    if (a.packed || a.T > KDA_GLR_CHUNK) return false;
+    return a.T <= 16 || a.blocks * a.d >= (int64_t)1 << 18;
 }
 
 }  // namespace glr
 
-size_t glr_fwd_ws_bytes(const GlrArgs& a) { return glr::make_plan(a, nullptr, glr::kFwdRows, false).bytes; }
+size_t glr_fwd_ws_bytes(const GlrArgs& a) { return glr::make_plan(a, nullptr, false).bytes; }
 
 // The backward's own workspace, or, where it runs the forward first, one that holds either's (one
 // after the other) with the entry states behind.
 size_t glr_bwd_ws_bytes(const GlrArgs& a) {
-    const size_t own = glr::make_plan(a, nullptr, glr::kBwdRows, a.z != nullptr).bytes;
+    const size_t own = glr::make_plan(a, nullptr, true).bytes;
     if (a.entry) return own;
-    const size_t fwd = glr::make_plan(a, nullptr, glr::kFwdRows, false).bytes;
+    const size_t fwd = glr::make_plan(a, nullptr, false).bytes;
     return (own > fwd ? own : fwd) + (size_t)(a.blocks * a.nch * a.d) * 4;
 }
 
@@ -222,7 +198,8 @@ hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t st) {
         if (!a.S_T || a.S_T == a.S0) return hipSuccess;
         return launch_copy_or_zero(a.S_T, a.S0, a.N * a.H * a.d, st);
     }
-    return glr::launch_fwd_tiles(a, glr::make_plan(a, a.ws, glr::kFwdRows, false).ws, st);
+    if (glr::by_rows(a)) return glr::launch_rows(a, st);
+    return glr::launch_fwd_tiles(a, glr::make_plan(a, a.ws, false).ws, st);
 }
 
 hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t st) {
@@ -233,21 +210,30 @@ hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t st) {
         }
         return a.dS0 ? launch_copy_or_zero(a.dS0, a.dST, a.N * a.H * a.d, st) : hipSuccess;
     }
-    const glr::Plan p = glr::make_plan(a, a.ws, glr::kBwdRows, a.z != nullptr);
+    const glr::Plan p = glr::make_plan(a, a.ws, true);
     GlrArgs b = a;
-    if (!b.entry) {   // the forward again, for its entry states alone
-        const glr::Plan f = glr::make_plan(a, a.ws, glr::kFwdRows, false);
-        b.entry = reinterpret_cast<float*>(a.ws + (p.bytes > f.bytes ? p.bytes : f.bytes));
-        const hipError_t e = glr::launch_fwd_tiles(b, f.ws, st);
-        if (e != hipSuccess) return e;
+    hipError_t e = hipSuccess;
+    if (!a.packed && a.T <= glr::kRowsBwd) {   // too few rows for a tile's threads
+        e = glr::launch_rows_bwd(a, p.ws.dA, st);
+    } else {
+        if (!b.entry) {   // the forward again, for its entry states alone
+            const glr::Plan f = glr::make_plan(a, a.ws, false);
+            b.entry = reinterpret_cast<float*>(a.ws + (p.bytes > f.bytes ? p.bytes : f.bytes));
+            e = glr::by_rows(b) ? glr::launch_rows(b, st) : glr::launch_fwd_tiles(b, f.ws, st);
+            if (e != hipSuccess) return e;
+        }
+        e = glr::launch_bwd_tiles(b, p.ws, st);
     }
-    return glr::launch_bwd_tiles(b, p.ws, st);
+    if (e != hipSuccess || !a.z) return e;
+    hipLaunchKernelGGL(glr::glr_dA_kernel, dim3((unsigned)((a.d + 63) / 64 * a.H)), dim3(1024), 0, st, a, p.ws);
+    return hipGetLastError();
 }
 
+// A step is a prefill of one token whose states are read and written in place.
 hipError_t launch_glr_step(const GlrArgs& a, hipStream_t st) {
-    if (a.scale == KDA_GLR_ONE) return glr::launch_step_s<KDA_GLR_ONE>(a, st);
-    if (a.scale == KDA_GLR_LEAKY) return glr::launch_step_s<KDA_GLR_LEAKY>(a, st);
-    return glr::launch_step_s<KDA_GLR_NORM>(a, st);
+    GlrArgs b = a;
+    b.S0 = a.S; b.S_T = a.S;
+    return glr::launch_rows(b, st);
 }
 
 }  // namespace kda

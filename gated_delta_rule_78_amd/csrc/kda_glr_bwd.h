@@ -18,7 +18,7 @@ namespace kda {
 namespace glr {
 
 template <int SCALE, bool PACKED, int Z, int U, typename TIn, typename TOut, int VEC, int L, int THREADS>
-__global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_bwd_kernel(GlrArgs a, GlrWs ws) {
+__global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void glr_bwd_kernel(GlrArgs a, GlrWs ws) {
     using G = Tile<VEC, L, THREADS>;
     constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
     static_assert(ROWS == KDA_GLR_CHUNK, "a tile starts at an entry state");

@@ -20,7 +20,7 @@ constexpr int kCh = KDA_GLR_CHUNK;
 
 // Z, U: whether the decay comes from z and whether there is an input gate (2: looked up).
 template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
-__global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrArgs a, GlrWs ws) {
+__global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws) {
     using G = Tile<VEC, L, THREADS>;
     constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
     static_assert(kCh % L == 0 && ROWS % kCh == 0, "a chunk starts at a thread's first row");
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 ? 4 : 2) void glr_fwd_kernel(GlrA
 
 template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
 static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
-    static_assert(Tile<VEC, L, THREADS>::ROWS == kFwdRows, "the plan's tile");
+    static_assert(Tile<VEC, L, THREADS>::ROWS == (VEC == 4 ? kFwdRows : kFwdRows1), "the plan's tile");
     const int64_t ntc = (a.d + kCW - 1) / kCW;
     hipLaunchKernelGGL((glr_fwd_kernel<SCALE, PACKED, Z, U, TIn, VEC, L, THREADS>),
                        dim3((unsigned)(a.blocks * ntc * ws.nt)), dim3(THREADS), 0, st, a, ws);
@@ -199,7 +199,9 @@ static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st
 
 // 4 channels a thread where every row of every tensor starts on 4 elements (ws.vec), else 1.
 // 512 threads of 8 rows: a tile of 256 rows halves the chain's links against 128 (64K rows x 4096
-// channels: 366 us against 397), and 8 rows a thread leave room for 4 waves a SIMD.
+// channels: 366 us against 397), and 8 rows a thread leave room for 4 waves a SIMD. One channel a
+// thread and 32 rows would not: 16 rows (64 x 4096 rows of 77 bf16 channels with gates: 106 us
+// against 161).
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
     if (ws.vec == 4) {
@@ -208,7 +210,7 @@ hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
         if (a.u) return launch_fwd_k<SCALE, PACKED, 0, 1, TIn, 4, 8, 512>(a, ws, st);
         return launch_fwd_k<SCALE, PACKED, 0, 0, TIn, 4, 8, 512>(a, ws, st);
     }
-    return launch_fwd_k<SCALE, PACKED, 2, 2, TIn, 1, 32, 512>(a, ws, st);
+    return launch_fwd_k<SCALE, PACKED, 2, 2, TIn, 1, 16, 512>(a, ws, st);
 }
 
 }  // namespace glr

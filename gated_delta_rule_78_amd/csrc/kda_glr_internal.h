@@ -47,13 +47,22 @@ struct GlrWs {
     int vec;                             // channels per thread: 4 or 1
 };
 
-constexpr int kFwdRows = 256, kBwdRows = 128;   // rows of a tile
+// Rows of a tile: forward with 4 channels and with 1 channel a thread, backward.
+constexpr int kFwdRows = 256, kFwdRows1 = 128, kBwdRows = 128;
 
 // Instantiated per input type (kda_glr_fwd_*.hip, kda_glr_bwd_*.hip).
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_bwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
+
+// Whether every row of the call's tensors starts on 4 elements of its type.
+bool rows_of_4(const GlrArgs& a);
+// The forward of blocks of at most KDA_GLR_CHUNK rows, a thread per channel (kda_glr_rows.hip).
+hipError_t launch_rows(const GlrArgs& a, hipStream_t st);
+// The backward of blocks of at most kRowsBwd rows; `parts`: [blocks][d] parts of dA_log (with z).
+constexpr int kRowsBwd = 16;
+hipError_t launch_rows_bwd(const GlrArgs& a, float* parts, hipStream_t st);
 
 }  // namespace glr
 

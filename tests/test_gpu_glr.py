@@ -117,6 +117,17 @@ CASES = [
     ((0, 1, 0, 72, [1] * 40), BF16, F32, True, False, "one", False),
     ((0, 2, 0, 5, [255, 1, 256, 257, 2, 510]), F32, F32, False, True, "norm", False),
     ((0, 1, 0, 16, [0, 0, 0]), F32, F32, False, False, "one", True),
+    # many chains of tiles (the others have few)
+    ((2, 40, 600, 68, None), BF16, BF16, True, True, "norm", True),
+    ((0, 70, 0, 20, [300, 0, 7, 500]), F32, F32, True, False, "leaky", True),
+    # sequences short enough for a thread per channel, aligned and not; long ones with channels enough
+    ((40, 3, 16, 36, None), BF16, BF16, True, True, "norm", True),
+    ((70, 2, 9, 11, None), F32, BF16, False, True, "leaky", True),
+    ((33, 1, 5, 64, None), F32, F32, True, False, "one", False),
+    ((5, 1, 17, 20, None), BF16, F32, False, False, "norm", True),
+    ((1, 2, 18, 131072, None), BF16, BF16, True, True, "norm", True),
+    # a chain longer than any look back
+    ((1, 1, 6000, 8, None), F32, F32, False, True, "leaky", True),
 ]
 
 
