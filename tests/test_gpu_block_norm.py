@@ -179,6 +179,22 @@ def test_no_rows(D):
     assert out[0].shape == (0, D) and not bool(out[3].any()) and not bool(out[5].any())
 
 
+def test_offsets_past_32_bits():
+    """Rows whose first element lies past 2^31: the same as those rows alone."""
+    D = 8192
+    rows = (1 << 31) // D + 100
+    g = torch.Generator(device=DEV).manual_seed(4)
+    base = torch.randn(1024, D, generator=g, device=DEV).to(BF16)
+    f = base.repeat(-(-rows // 1024), 1)[:rows].contiguous()
+    k = dict(scale=0.5, norm_weight=1.0 + 0.1 * torch.randn(D, generator=g, device=DEV), pre_norm=False)
+    x_out, _ = kda.block_norm_fwd(f, f, **k)
+    tail = f[-100:].contiguous()
+    want, _ = kda.block_norm_fwd(tail, tail, **k)
+    assert torch.equal(x_out[-100:], want)
+    df = kda.block_norm_bwd(f, f, x_out, None, **k)[0]
+    assert torch.equal(df[-100:], kda.block_norm_bwd(tail, tail, want, None, **k)[0])
+
+
 def test_same_bits_and_captured_replay():
     c = make(2000, 1536, BF16, BF16, seed=5)
     run = lambda: kda.block_norm_fwd(c["f"], c["x"], **kw(c)) + kda.block_norm_bwd(c["f"], c["x"], c["dxo"], c["dn"], **kw(c))

@@ -322,6 +322,80 @@ def test_split_and_resume():
     check("S_T", S, ref["S_T"], F32)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_no_rows(packed):
+    """T = 0: the states pass through, every gradient sum is zero."""
+    N, H, d = 3, 2, 10
+    lead = (H, 0) if packed else (N, H, 0)
+    x = torch.empty(*lead, d, device=DEV)
+    cu = torch.zeros(N + 1, dtype=torch.int32, device=DEV) if packed else None
+    S0, A = torch.randn(N, H, d, device=DEV), torch.zeros(H, d, device=DEV)
+    y, S_T, entry = kda.glr_fwd(x, None, S0, z=x, A_log=A, in_gate=x, cu_seqlens=cu, store_entry_states=True)
+    assert y.shape == x.shape and torch.equal(S_T, S0) and entry.numel() == 0
+    assert not bool(kda.glr_fwd(x, x, None, cu_seqlens=cu)[1].any())
+    S = S0.clone()
+    assert kda.glr_fwd(x, x, S, S_T=S, cu_seqlens=cu)[1] is S and torch.equal(S, S0)
+    out = kda.glr_bwd(x, None, S0, y, S0, z=x, A_log=A, in_gate=x, cu_seqlens=cu)
+    assert torch.equal(out[3], S0) and not bool(out[4].any())
+    assert not bool(kda.glr_bwd(x, x, S0, y, None, cu_seqlens=cu)[3].any())
+
+
+def test_bad_gradients_stay_in_their_sequence():
+    lens = [300, 5, 256, 0, 190, 1]
+    c = make(0, 2, 0, 64, F32, lens=lens, u=True, s0=True, seed=14)
+    dy = c["dy"].clone()
+    dy[:, 400] = float("nan")                        # sequence 2, rows 305..560
+    dx, dd, du, dS0, _ = kda.glr_bwd(c["x"], c["la"], c["S0"], dy, c["dS_T"], **kw(c, "leaky"))
+    ref = reference(c, "leaky", c["dy"], c["dS_T"])
+    cu = c["cu"].tolist()
+    for n in (0, 1, 4, 5):
+        at = (slice(None), slice(cu[n], cu[n + 1]))
+        for k, g in (("dx", dx), ("dd", dd), ("du", du)):
+            check("%s of sequence %d" % (k, n), g[at], (ref[k][0][at], ref[k][1][at]), F32)
+        check("dS0 of sequence %d" % n, dS0[n], (ref["dS0"][0][n], ref["dS0"][1][n]), F32)
+    after = (slice(None), slice(401, cu[3]))         # behind the bad row of its own sequence: untouched
+    check("dx behind it", dx[after], (ref["dx"][0][after], ref["dx"][1][after]), F32)
+    assert not bool(torch.isfinite(dx[:, cu[2]:401]).any()) and not bool(torch.isfinite(dS0[2]).any())
+
+
+@pytest.mark.parametrize("fill", [0, 0x5a, 0xff])
+def test_one_workspace_for_many_calls(fill):
+    """A caller's workspace, whatever it holds, serves calls of any shape one after the other."""
+    ws = torch.full((64 << 20,), fill, dtype=torch.uint8, device=DEV)
+    for i, (N, H, T, d, lens) in enumerate([(2, 3, 900, 72, None), (0, 2, 0, 130, [400, 0, 3, 700]), (1, 1, 1500, 33, None)]):
+        c = make(N, H, T, d, BF16, lens=lens, z=True, u=True, s0=True, seed=30 + i)
+        k = kw(c, "norm")
+        dy = c["dy"].to(BF16)
+        want = kda.glr_fwd(c["x"], None, c["S0"], **k)[:2] + kda.glr_bwd(c["x"], None, c["S0"], dy, c["dS_T"], **k)
+        got = (kda.glr_fwd(c["x"], None, c["S0"], workspace=ws, **k)[:2]
+               + kda.glr_bwd(c["x"], None, c["S0"], dy, c["dS_T"], workspace=ws, **k))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_offsets_past_32_bits():
+    """2.2e9 elements (T x d past 2^31): the last rows against the same rows run alone from the state
+    that the long call had there."""
+    T, d = (1 << 31) // 1024 + 70000, 1024
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(1, 1, 4096, d, generator=g, device=DEV).to(BF16).repeat(1, 1, -(-T // 4096), 1)[:, :, :T].contiguous()
+    la = (torch.rand(1, 1, 4096, d, generator=g, device=DEV) * -0.5).to(BF16).repeat(1, 1, -(-T // 4096), 1)[:, :, :T].contiguous()
+    y, S_T, entry = kda.glr_fwd(x, la, None, store_entry_states=True)
+    at = (T // kda.GLR_CHUNK - 3) * kda.GLR_CHUNK
+    cut = lambda t: t[:, :, at:].contiguous()
+    y2, S2, _ = kda.glr_fwd(cut(x), cut(la), entry[:, at // kda.GLR_CHUNK].reshape(1, 1, d).contiguous())
+    torch.cuda.synchronize()
+    # the same recurrence from the same state; tiles that start elsewhere may round differently
+    assert bool(((y[:, :, at:].float() - y2.float()).abs() <= 2.0 ** -7 * y2.float().abs() + 1e-5).all())
+    assert bool(((S_T - S2).abs() <= 2.0 ** -16 * S2.abs() + 1e-5).all())
+    # and the head of it against the token loop
+    n = 300
+    q = glr.gates(host32(x[0, 0, :n]), host32(la[0, 0, :n]))
+    hs, _, _ = glr.forward(q, np.zeros(d))
+    hb, _ = glr.forward_bound(q, np.zeros(d), "one")
+    check("head", y[0, 0, :n], (hs, hb), BF16)
+
+
 def test_same_bits_every_call():
     c = make(0, 4, 0, 128, BF16, lens=[1500, 20, 3000, 700], z=True, u=True, s0=True, seed=9)
     first = None
