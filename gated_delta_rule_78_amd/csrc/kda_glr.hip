@@ -5,16 +5,6 @@
 namespace kda {
 namespace glr {
 
-// Whether every row of these tensors starts on 4 elements of its type.
-bool rows_of_4(const GlrArgs& a) {
-    if (a.d % 4 != 0) return false;
-    uintptr_t in = 0, out = 0;
-    for (const void* p : {a.x, a.la, a.z, a.u, (const void*)a.dx, (const void*)a.dd, (const void*)a.du})
-        in |= reinterpret_cast<uintptr_t>(p);
-    for (const void* p : {(const void*)a.y, a.dy}) out |= reinterpret_cast<uintptr_t>(p);
-    return (in & (a.in_bf16 ? 7 : 15)) == 0 && (out & (a.out_bf16 ? 7 : 15)) == 0;
-}
-
 // The first sequence that ends behind row (N if none does).
 __device__ __forceinline__ int64_t sequence_behind(const GlrArgs& a, int64_t row) {
     int64_t lo = 0, hi = a.N;
@@ -111,9 +101,8 @@ struct Plan {
 
 static Plan make_plan(const GlrArgs& a, unsigned char* base, bool backward) {
     Plan p{};
-    p.ws.vec = rows_of_4(a) ? 4 : 1;
-    // a workspace query knows no addresses: it plans for the smaller tiles, which need more
-    const int rows = backward ? kBwdRows : p.ws.vec == 4 && base ? kFwdRows : kFwdRows1;
+    p.ws.vec = a.d >= 4 ? 4 : 1;
+    const int rows = backward ? kBwdRows : p.ws.vec == 4 ? kFwdRows : kFwdRows1;
     const bool with_dA = backward && a.z;
     p.ws.rows = rows;
     p.ws.nt = (a.T + rows - 1) / rows;

@@ -46,7 +46,11 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
     const int ch_tile = (int)(chain % ntc) * kCW;
     const uint32_t d = (uint32_t)a.d;
     const bool on = ch_tile + ct * VEC < (int)d;
-    const uint32_t ch0 = on ? ch_tile + ct * VEC : d - VEC;   // lanes past the channels shadow the last ones
+    const uint32_t ch0 = ch_tile + ct * VEC + VEC <= d ? ch_tile + ct * VEC : d - VEC;
+    // as a lane of one channel: the channel, and whether there is one
+    const int slot = ch_tile + lane / VEC * VEC;
+    const bool has_ch = slot < (int)d;
+    const uint32_t ch = (slot + VEC <= (int)d ? slot : (int)d - VEC) + lane % VEC;
     const int64_t row0 = (int64_t)c * ROWS;
     const int rows_here = (int)(a.T - row0 < ROWS ? a.T - row0 : ROWS);
     const int64_t base = (block * a.T + row0) * a.d;
@@ -76,10 +80,10 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
 #pragma unroll
         for (int r = 0; r < L; ++r) {
             const uint32_t off = row_offset(off0, r, d, last_off);
-            dr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off);
-            xr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off);
-            if (has_u) ur[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(up + off);
-            yr[r] = *reinterpret_cast<const RawRow<TOut, VEC>*>(yp + off);
+            dr[r] = load_row<TIn, VEC>(dec + off);
+            xr[r] = load_row<TIn, VEC>(xp + off);
+            if (has_u) ur[r] = load_row<TIn, VEC>(up + off);
+            yr[r] = load_row<TOut, VEC>(yp + off);
         }
         const float gy = a.g_min * kLog2e;
         float cz[VEC];
@@ -164,15 +168,14 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
     wb.scan(sr, turn[wave], lane);
     wtR[wave][lane] = wb.total.A;
     wtg[wave][lane] = wb.total.h;
-    const uint32_t ch = ch_tile + lane;
-    float hw = a.entry[(block * a.nch + c) * a.d + (ch < d ? ch : d - 1)];
+    float hw = a.entry[(block * a.nch + c) * a.d + ch];
     lds_barrier();
     if (wave == 0) {   // lane = channel: the tile's backward span, the chain
         Span tot{wtR[W - 1][lane], wtg[W - 1][lane]};
 #pragma unroll
         for (int i = W - 2; i >= 0; --i) tot = compose<PACKED>(tot, Span{wtR[i][lane], wtg[i][lane]});
         float g = 0.f;
-        if (ch < d) {
+        if (has_ch) {
             const bool first = (int64_t)c + 1 == ws.nt, more = c > 0;
             if (!PACKED && first && a.dST) g = a.dST[block * a.d + ch];
             if (chained) {
@@ -200,7 +203,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
     // the state before each row
     auto row_x = [&](int r, float* o) {
         if constexpr (STASH) unpack(xs[r][tid], o);
-        else unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(xp + row_offset(off0, r, d, last_off)), o);
+        else unpack(load_row<TIn, VEC>(xp + row_offset(off0, r, d, last_off)), o);
     };
     float prev[L][VEC];
 #pragma unroll
@@ -240,8 +243,8 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
             unpack(ys[r][tid], dy);
         } else {
             const uint32_t off = row_offset(off0, r, d, last_off);
-            if (has_z) unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off), q);
-            unpack(*reinterpret_cast<const RawRow<TOut, VEC>*>(yp + off), dy);
+            if (has_z) unpack(load_row<TIn, VEC>(dec + off), q);
+            unpack(load_row<TOut, VEC>(yp + off), dy);
         }
         if (PACKED && (ebits >> r & 1)) {
 #pragma unroll
@@ -297,11 +300,11 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
         for (int v = 0; v < VEC; ++v) wth[wave][ct * VEC + v] = dA[v];
     }
     lds_barrier();
-    if (wave == 0 && ch_tile + lane < (int)d) {
+    if (wave == 0 && has_ch) {
         float t = wth[0][lane];
 #pragma unroll
         for (int i = 1; i < W; ++i) t += wth[i][lane];
-        ws.dA[(block * ws.nt + c) * a.d + ch_tile + lane] = t;
+        ws.dA[(block * ws.nt + c) * a.d + ch] = t;
     }
 }
 
@@ -316,7 +319,7 @@ static hipError_t launch_bwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st
     return hipGetLastError();
 }
 
-// 4 channels a thread where every row of every tensor starts on 4 elements (ws.vec), else 1.
+// 4 channels a thread (ws.vec), 1 for heads of fewer.
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_bwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
     if (ws.vec == 4) {

@@ -53,8 +53,9 @@ __device__ __forceinline__ Span compose(Span l, Span r) {
 }
 
 // A tile is some rows of kCW channels, in the registers of THREADS threads: CT lanes lie across the
-// channels with VEC channels each (VEC = 4, or 1 where rows are not aligned for 4), and each run of
-// CT lanes owns L consecutive rows, a sub-chunk.
+// channels with VEC channels each (VEC = 4, or 1 for heads of fewer), and each run of CT lanes owns L
+// consecutive rows, a sub-chunk. Where the channels are no multiple of VEC, the last lane's are the
+// head's last VEC: those it shares with its neighbour are computed, and written, twice alike.
 constexpr int kCW = 64;
 template <int VEC, int L, int THREADS>
 struct Tile {
@@ -202,15 +203,29 @@ __device__ __forceinline__ void unpack(const RawRow<float, 4>& r, float* o) {
 __device__ __forceinline__ void unpack(const RawRow<bf16_t, 1>& r, float* o) { o[0] = bf16_bits_to_f32(r.v); }
 __device__ __forceinline__ void unpack(const RawRow<float, 1>& r, float* o) { o[0] = r.v; }
 
-template <int VEC, typename T>
-__device__ __forceinline__ void store_row(T* p, const float* x) {
-    if constexpr (VEC == 4) store4(p, x[0], x[1], x[2], x[3]);
-    else st_f(p, x[0]);
+// Rows may start on any element: one 8- or 16-byte access serves any alignment.
+template <typename T, int VEC>
+__device__ __forceinline__ RawRow<T, VEC> load_row(const T* p) {
+    RawRow<T, VEC> r;
+    __builtin_memcpy(&r, p, VEC * sizeof(T));
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ void store_row(bf16_t* p, const float* x) {
+    if constexpr (VEC == 4) {
+        const uint2 u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+        __builtin_memcpy(p, &u, 8);
+    } else {
+        st_f(p, x[0]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_row(float* p, const float* x) {
+    __builtin_memcpy(p, x, VEC * 4);
 }
 template <int VEC>
 __device__ __forceinline__ void load_f32(const float* p, float* o) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) o[v] = p[v];
+    __builtin_memcpy(o, p, VEC * 4);
 }
 
 // Which sequences start and end in the rows of a packed batch (kda_glr_prepare_kernel): a bit per

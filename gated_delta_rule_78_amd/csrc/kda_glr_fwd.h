@@ -43,7 +43,11 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
     const int ch_tile = (int)(chain % ntc) * kCW;
     const uint32_t d = (uint32_t)a.d;
     const bool on = ch_tile + ct * VEC < (int)d;
-    const uint32_t ch0 = on ? ch_tile + ct * VEC : d - VEC;   // lanes past the channels shadow the last ones
+    const uint32_t ch0 = ch_tile + ct * VEC + VEC <= d ? ch_tile + ct * VEC : d - VEC;
+    // as a lane of one channel: the channel, and whether there is one
+    const int slot = ch_tile + lane / VEC * VEC;
+    const bool has_ch = slot < (int)d;
+    const uint32_t ch = (slot + VEC <= (int)d ? slot : (int)d - VEC) + lane % VEC;
     const int64_t row0 = (int64_t)c * ROWS;
     const int rows_here = (int)(a.T - row0 < ROWS ? a.T - row0 : ROWS);
     const int64_t base = (block * a.T + row0) * a.d;
@@ -64,9 +68,9 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
 #pragma unroll
     for (int r = 0; r < L; ++r) {
         const uint32_t off = row_offset(off0, r, d, last_off);
-        dr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off);
-        xr[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off);
-        if (has_u) ur[r] = *reinterpret_cast<const RawRow<TIn, VEC>*>(up + off);
+        dr[r] = load_row<TIn, VEC>(dec + off);
+        xr[r] = load_row<TIn, VEC>(xp + off);
+        if (has_u) ur[r] = load_row<TIn, VEC>(up + off);
     }
     const float gy = a.g_min * kLog2e;
     float cz[VEC];
@@ -124,12 +128,11 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
     wth[wave][lane] = wave_spans.total.h;
     lds_barrier();
     if (wave == 0) {   // lane = channel: the tile's span, the chain
-        const uint32_t ch = ch_tile + lane;
         Span tot{wtA[0][lane], wth[0][lane]};
 #pragma unroll
         for (int w = 1; w < W; ++w) tot = compose<PACKED>(tot, Span{wtA[w][lane], wth[w][lane]});
         float h = 0.f;
-        if (ch < d) {
+        if (has_ch) {
             if (!PACKED && c == 0 && a.S0) h = a.S0[block * a.d + ch];
             if (chained) {
                 const int64_t word = (block * ws.nt + c) * a.d + ch;
@@ -197,7 +200,7 @@ static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st
     return hipGetLastError();
 }
 
-// 4 channels a thread where every row of every tensor starts on 4 elements (ws.vec), else 1.
+// 4 channels a thread (ws.vec), 1 for heads of fewer.
 // 512 threads of 8 rows: a tile of 256 rows halves the chain's links against 128 (64K rows x 4096
 // channels: 366 us against 397), and 8 rows a thread leave room for 4 waves a SIMD. One channel a
 // thread and 32 rows would not: 16 rows (64 x 4096 rows of 77 bf16 channels with gates: 106 us

@@ -56,8 +56,6 @@ hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_bwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
 
-// Whether every row of the call's tensors starts on 4 elements of its type.
-bool rows_of_4(const GlrArgs& a);
 // The forward of blocks of at most KDA_GLR_CHUNK rows, a thread per channel (kda_glr_rows.hip).
 hipError_t launch_rows(const GlrArgs& a, hipStream_t st);
 // The backward of blocks of at most kRowsBwd rows; `parts`: [blocks][d] parts of dA_log (with z).

@@ -1,6 +1,7 @@
 // Gated linear recurrence for gfx950, short sequences and the single-token step: a thread owns VEC
 // channels of a block of rows and walks its rows in order, the next ones' loads in flight. Bound by
-// HBM where the channels fill the GPU, by the launch for a few sequences. At most one chunk of rows,
+// HBM where the channels fill the GPU, by the launch for a few sequences. VEC is 4 where that divides
+// the channels (no two threads may share one: states are updated in place), else 1. At most one chunk of rows,
 // so the only entry state is S0.
 #include "kda_glr_device.h"
 
@@ -24,9 +25,9 @@ __global__ __launch_bounds__(256) void glr_rows_kernel(GlrArgs a) {
     RawRow<TIn, VEC> xr[AHEAD], dr[AHEAD], ur[AHEAD];
     auto fetch = [&](int k, int64_t t) {
         const int64_t off = (t < a.T ? t : a.T - 1) * a.d;
-        dr[k] = *reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off);
-        xr[k] = *reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off);
-        if (U) ur[k] = *reinterpret_cast<const RawRow<TIn, VEC>*>(up + off);
+        dr[k] = load_row<TIn, VEC>(dec + off);
+        xr[k] = load_row<TIn, VEC>(xp + off);
+        if (U) ur[k] = load_row<TIn, VEC>(up + off);
     };
     // a single row (a step) is fetched alone
 #pragma unroll
@@ -89,7 +90,7 @@ static hipError_t launch_rows_v(const GlrArgs& a, hipStream_t st) {
 
 template <int SCALE, typename TIn>
 static hipError_t launch_rows_t(const GlrArgs& a, hipStream_t st) {
-    return rows_of_4(a) ? launch_rows_v<SCALE, TIn, 4>(a, st) : launch_rows_v<SCALE, TIn, 1>(a, st);
+    return a.d % 4 == 0 ? launch_rows_v<SCALE, TIn, 4>(a, st) : launch_rows_v<SCALE, TIn, 1>(a, st);
 }
 
 hipError_t launch_rows(const GlrArgs& a, hipStream_t st) {
@@ -132,9 +133,9 @@ __global__ __launch_bounds__(256) void glr_rows_bwd_kernel(GlrArgs a, float* par
     auto row = [&](int t, Row& r) {
         const int64_t off = t * a.d;
         float u[VEC];
-        unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(xp + off), r.x);
-        unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(dec + off), r.q);
-        if (a.u) unpack(*reinterpret_cast<const RawRow<TIn, VEC>*>(up + off), u);
+        unpack(load_row<TIn, VEC>(xp + off), r.x);
+        unpack(load_row<TIn, VEC>(dec + off), r.q);
+        if (a.u) unpack(load_row<TIn, VEC>(up + off), u);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             float y = r.q[v] * kLog2e;
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(256) void glr_rows_bwd_kernel(GlrArgs a, float* par
         Row r;
         row(t, r);
         float dy[VEC], ox[VEC], od[VEC], ou[VEC];
-        unpack(*reinterpret_cast<const RawRow<TOut, VEC>*>(yp + t * a.d), dy);
+        unpack(load_row<TOut, VEC>(yp + t * a.d), dy);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float gr = g[v] + dy[v], alpha = r.al[v];
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(256) void glr_rows_bwd_kernel(GlrArgs a, float* par
 template <int SCALE, typename TIn, typename TOut>
 static hipError_t launch_rows_bwd_t(const GlrArgs& a, float* parts, hipStream_t st) {
     const dim3 threads(256);
-    if (rows_of_4(a))
+    if (a.d % 4 == 0)
         hipLaunchKernelGGL((glr_rows_bwd_kernel<SCALE, TIn, TOut, 4>), dim3((unsigned)((a.blocks * (a.d / 4) + 255) / 256)),
                            threads, 0, st, a, parts);
     else

@@ -21,8 +21,7 @@
  *  - Log decays must be <= 0; -inf is allowed (alpha = 0: the state restarts). Positive or NaN log
  *    decays give undefined numbers. A non-finite x, decay or state makes the later outputs of its
  *    own channel and sequence non-finite (also past alpha = 0), and no others.
- *  - Every tensor is dense, its base aligned to its element (16-byte bases and d a multiple of 8
- *    take wide accesses); workspaces are aligned to 16 bytes.
+ *  - Every tensor is dense, its base aligned to its element; workspaces are aligned to 16 bytes.
  *  - Every sum runs in a fixed order: the same inputs give the same bits on every call.
  */
 #ifndef KDA_GLR_H

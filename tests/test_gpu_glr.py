@@ -245,7 +245,7 @@ def test_rows_behind_the_last_sequence_stay():
 
 def test_packed_states_in_place():
     """S_T in place of S0, sequences that start and end inside a tile, over tiles, and empty ones."""
-    c = make(0, 2, 0, 200, F32, lens=[0, 5, 3, 1, 0, 900, 127, 1, 300, 0], z=True, u=True, s0=True, seed=13)
+    c = make(0, 2, 0, 203, F32, lens=[0, 5, 3, 1, 0, 900, 127, 1, 300, 0], z=True, u=True, s0=True, seed=13)
     ref = reference(c, "norm")
     S = c["S0"].clone()
     y, S_T, _ = kda.glr_fwd(c["x"], None, S, S_T=S, **kw(c, "norm"))
