@@ -9,8 +9,8 @@ import functools
 
 import torch
 
-from . import _DTYPES, _check, _check_device, _check_workspace, _nbytes, _workspace, library
-from ._launch import check, data_ptr, raw_stream, scope
+from . import _DTYPES, _check, _check_workspace, _nbytes, _workspace, library
+from ._launch import check, on_gpu, ptr, raw_stream, scope
 
 NORM_MAX_D = 16384   # KDA_NORM_MAX_D of include/kda_norm.h
 
@@ -47,28 +47,30 @@ def _desc(rows, D, in_dtype, res_dtype, out_dtype, post_norm, pre_norm, scale, e
                     pre_eps)
 
 
-def _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight):
+def _inputs(f, index, shape, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight):
     """Checks the inputs both directions share; returns (rows, D)."""
-    dev, shape = f.device, f.shape
     if f.dtype not in _DTYPES:
         raise ValueError("unsupported input dtype %s" % f.dtype)
-    if f.dim() < 1:
+    if not shape:
         raise ValueError("f must have at least one dimension")
     D = shape[-1]
-    check("f", f, dev, f.dtype, shape)
+    check("f", f, index, f.dtype, shape)
     if x is not None:
         if x.dtype not in _DTYPES:
             raise ValueError("unsupported residual dtype %s" % x.dtype)
-        check("x", x, dev, x.dtype, shape)
+        check("x", x, index, x.dtype, shape)
     if gate is not None:
-        check("gate", gate, dev, f.dtype, shape)
-    for name, w in (("norm_weight", norm_weight), ("scale_weight", scale_weight), ("pre_weight", pre_weight)):
-        if w is not None:
-            check(name, w, dev, torch.float32, (D,))
-    if norm_weight is not None and not post_norm:
-        raise ValueError("norm_weight goes with post_norm")
-    if pre_weight is not None and not pre_norm:
-        raise ValueError("pre_weight goes with pre_norm")
+        check("gate", gate, index, f.dtype, shape)
+    if norm_weight is not None:
+        if not post_norm:
+            raise ValueError("norm_weight goes with post_norm")
+        check("norm_weight", norm_weight, index, torch.float32, (D,))
+    if scale_weight is not None:
+        check("scale_weight", scale_weight, index, torch.float32, (D,))
+    if pre_weight is not None:
+        if not pre_norm:
+            raise ValueError("pre_weight goes with pre_norm")
+        check("pre_weight", pre_weight, index, torch.float32, (D,))
     return (f.numel() // D if D else 0), D
 
 
@@ -86,32 +88,31 @@ def block_norm_fwd(f, x=None, *, gate=None, norm_weight=None, post_norm=True, ep
     ``store_x=False``; n in ``out_dtype`` (default f's type), None with ``pre_norm=False``.
     ``x_out=x`` updates the residual stream in place. Caller-supplied outputs are checked like the
     inputs; the others are allocated on ``stream``."""
-    dev = f.device
-    rows, D = _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight)
+    dev, index, shape = f.device, f.get_device(), f.shape
+    rows, D = _inputs(f, index, shape, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight)
     res_dtype = x.dtype if x is not None else (res_dtype or (x_out.dtype if x_out is not None else f.dtype))
     out_dtype = out_dtype or (n.dtype if n is not None else f.dtype)
-    for dt in (res_dtype, out_dtype):
-        if dt not in _DTYPES:
-            raise ValueError("unsupported output dtype %s" % dt)
+    if res_dtype not in _DTYPES or out_dtype not in _DTYPES:
+        raise ValueError("unsupported output dtype %s" % (out_dtype if res_dtype in _DTYPES else res_dtype))
     if x_out is not None:
-        check("x_out", x_out, dev, res_dtype, f.shape)
+        check("x_out", x_out, index, res_dtype, shape)
     if n is not None:
         if not pre_norm:
             raise ValueError("n goes with pre_norm")
-        check("n", n, dev, out_dtype, f.shape)
+        check("n", n, index, out_dtype, shape)
     if not pre_norm and x_out is None and not store_x:
         raise ValueError("nothing to compute: neither x_out nor n is wanted")
-    _check_device("block_norm_fwd", dev)
+    on_gpu("block_norm_fwd", f)
     desc = _desc(rows, D, f.dtype, res_dtype, out_dtype, bool(post_norm), bool(pre_norm), float(scale), float(eps),
                  float(pre_eps))
-    with scope(dev, stream):
+    with scope(index, stream):
         if x_out is None and store_x:
-            x_out = torch.empty(f.shape, device=dev, dtype=res_dtype)
+            x_out = torch.empty_like(f, dtype=res_dtype)
         if n is None and pre_norm:
-            n = torch.empty(f.shape, device=dev, dtype=out_dtype)
-        st = _library().kda_block_norm_fwd(desc, data_ptr(f), data_ptr(gate), data_ptr(x), data_ptr(norm_weight),
-                                           data_ptr(scale_weight), data_ptr(pre_weight), data_ptr(x_out), data_ptr(n),
-                                           raw_stream(dev, stream))
+            n = torch.empty_like(f, dtype=out_dtype)
+        st = (_lib or _library()).kda_block_norm_fwd(desc, ptr(f), ptr(gate), ptr(x), ptr(norm_weight),
+                                           ptr(scale_weight), ptr(pre_weight), ptr(x_out), ptr(n),
+                                           raw_stream(index, stream))
     _check("kda_block_norm_fwd", st)
     return x_out, n
 
@@ -126,8 +127,8 @@ def block_norm_bwd(f, x, dx_out, dn, *, gate=None, norm_weight=None, post_norm=T
     Returns (df, dx, dgate, dnorm_weight, dscale_weight, dpre_weight): tensors in their input's
     type, weight gradients [D] fp32; None for each input that was not given. ``dx=dx_out`` updates
     the residual stream's gradient in place."""
-    dev = f.device
-    rows, D = _inputs(f, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight)
+    dev, index, shape = f.device, f.get_device(), f.shape
+    rows, D = _inputs(f, index, shape, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight)
     if dx_out is None and dn is None:
         raise ValueError("one of dx_out and dn is required")
     res_dtype = x.dtype if x is not None else (dx_out.dtype if dx_out is not None else f.dtype)
@@ -136,32 +137,33 @@ def block_norm_bwd(f, x, dx_out, dn, *, gate=None, norm_weight=None, post_norm=T
         if dt not in _DTYPES:
             raise ValueError("unsupported gradient dtype %s" % dt)
     if dx_out is not None:
-        check("dx_out", dx_out, dev, res_dtype, f.shape)
+        check("dx_out", dx_out, index, res_dtype, shape)
     if dn is not None:
         if not pre_norm:
             raise ValueError("dn goes with pre_norm")
-        check("dn", dn, dev, out_dtype, f.shape)
+        check("dn", dn, index, out_dtype, shape)
     if dx is not None:
         if x is None:
             raise ValueError("dx goes with x")
-        check("dx", dx, dev, res_dtype, f.shape)
-    _check_workspace(workspace, dev)
-    _check_device("block_norm_bwd", dev)
+        check("dx", dx, index, res_dtype, shape)
+    if workspace is not None:
+        _check_workspace(workspace, dev)
+    on_gpu("block_norm_bwd", f)
     desc = _desc(rows, D, f.dtype, res_dtype, out_dtype, bool(post_norm), bool(pre_norm), float(scale), float(eps),
                  float(pre_eps))
-    lib = _library()
+    lib = _lib or _library()
     sums = norm_weight is not None or scale_weight is not None or pre_weight is not None
     need = lib.kda_block_norm_bwd_workspace_bytes(desc) if sums else 0
-    with scope(dev, stream):
+    with scope(index, stream):
         df = torch.empty_like(f)
         dgate = torch.empty_like(f) if gate is not None else None
         if dx is None and x is not None:
             dx = torch.empty_like(x)
         dws = [torch.empty_like(w) if w is not None else None for w in (norm_weight, scale_weight, pre_weight)]
         workspace = _workspace(need, workspace, dev)
-        st = lib.kda_block_norm_bwd(desc, data_ptr(f), data_ptr(gate), data_ptr(x), data_ptr(norm_weight),
-                                    data_ptr(scale_weight), data_ptr(pre_weight), data_ptr(dx_out), data_ptr(dn),
-                                    data_ptr(df), data_ptr(dgate), data_ptr(dx), *map(data_ptr, dws),
-                                    data_ptr(workspace), _nbytes(workspace), raw_stream(dev, stream))
+        st = lib.kda_block_norm_bwd(desc, ptr(f), ptr(gate), ptr(x), ptr(norm_weight),
+                                    ptr(scale_weight), ptr(pre_weight), ptr(dx_out), ptr(dn),
+                                    ptr(df), ptr(dgate), ptr(dx), *map(ptr, dws),
+                                    ptr(workspace), _nbytes(workspace), raw_stream(index, stream))
     _check("kda_block_norm_bwd", st)
     return (df, dx, dgate, *dws)

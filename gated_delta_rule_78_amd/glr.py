@@ -11,8 +11,8 @@ import functools
 
 import torch
 
-from . import _DTYPES, _check, _check_device, _check_workspace, _nbytes, _workspace, library
-from ._launch import check, data_ptr, raw_stream, scope
+from . import _DTYPES, _check, _check_workspace, _nbytes, _workspace, library
+from ._launch import check, on_gpu, ptr, raw_stream, scope
 
 GLR_CHUNK = 128   # KDA_GLR_CHUNK of include/kda_glr.h
 _SCALES = {"one": 0, "leaky": 1, "norm": 2}
@@ -59,21 +59,28 @@ def _scale(input_scale):
         raise ValueError("input_scale must be one of %s (got %r)" % (sorted(_SCALES), input_scale)) from None
 
 
-def _gates(x, log_alpha, z, A_log, in_gate, H, d):
+def _gates(x, index, shape, log_alpha, z, A_log, in_gate, H, d):
     """Checked gates of a call: exactly one of log_alpha and z, A_log [H,d] fp32 with z."""
-    dev, dt, shape = x.device, x.dtype, x.shape
-    if (log_alpha is None) == (z is None):
-        raise ValueError("give exactly one of log_alpha and z")
-    if (z is None) != (A_log is None):
-        raise ValueError("A_log goes with z")
+    dt = x.dtype
     if z is None:
-        check("log_alpha", log_alpha, dev, dt, shape)
+        if log_alpha is None:
+            raise ValueError("give exactly one of log_alpha and z")
+        if A_log is not None:
+            raise ValueError("A_log goes with z")
+        check("log_alpha", log_alpha, index, dt, shape)
+        decay = (log_alpha.data_ptr(), None, None)
     else:
-        check("z", z, dev, dt, shape)
-        check("A_log", A_log, dev, torch.float32, (H, d))
-    if in_gate is not None:
-        check("in_gate", in_gate, dev, dt, shape)
-    return GlrGates(data_ptr(log_alpha), data_ptr(z), data_ptr(A_log), data_ptr(in_gate))
+        if log_alpha is not None:
+            raise ValueError("give exactly one of log_alpha and z")
+        if A_log is None:
+            raise ValueError("A_log goes with z")
+        check("z", z, index, dt, shape)
+        check("A_log", A_log, index, torch.float32, (H, d))
+        decay = (None, z.data_ptr(), A_log.data_ptr())
+    if in_gate is None:
+        return GlrGates(*decay, None)
+    check("in_gate", in_gate, index, dt, shape)
+    return GlrGates(*decay, in_gate.data_ptr())
 
 
 def _dtype(x, out_dtype):
@@ -99,7 +106,7 @@ def _batch(x, cu_seqlens):
         return tuple(x.shape)
     if x.dim() != 3:
         raise ValueError("x must be [H,T,d] with cu_seqlens (got %s)" % (tuple(x.shape),))
-    check("cu_seqlens", cu_seqlens, x.device, torch.int32, (cu_seqlens.numel(),))
+    check("cu_seqlens", cu_seqlens, x.get_device(), torch.int32, (cu_seqlens.numel(),))
     N = cu_seqlens.numel() - 1
     if N < 1:
         raise ValueError("cu_seqlens must have at least 2 entries")
@@ -128,34 +135,35 @@ def glr_fwd(x, log_alpha=None, S0=None, *, z=None, A_log=None, g_min=-5.0, in_ga
     allocated on ``stream`` (default: the current stream of x's device).
     """
     out_dtype = _dtype(x, out_dtype)
-    dev = x.device
+    dev, index, shape = x.device, x.get_device(), x.shape
     N, H, T, d = _batch(x, cu_seqlens)
     packed = cu_seqlens is not None
-    check("x", x, dev, x.dtype, x.shape)
-    gates = _gates(x, log_alpha, z, A_log, in_gate, H, d)
+    check("x", x, index, x.dtype, shape)
+    gates = _gates(x, index, shape, log_alpha, z, A_log, in_gate, H, d)
     for name, t in (("S0", S0), ("S_T", S_T)):
         if t is not None:
-            check(name, t, dev, torch.float32, (N, H, d))
+            check(name, t, index, torch.float32, (N, H, d))
     if y is not None:
-        check("y", y, dev, out_dtype, x.shape)
+        check("y", y, index, out_dtype, shape)
     eshape = _entry_shape(N, H, T, d, packed)
     if entry_states is not None:
-        check("entry_states", entry_states, dev, torch.float32, eshape)
-    _check_workspace(workspace, dev)
-    _check_device("glr_fwd", dev)
+        check("entry_states", entry_states, index, torch.float32, eshape)
+    if workspace is not None:
+        _check_workspace(workspace, dev)
+    on_gpu("glr_fwd", x)
     desc = _desc(N, H, T, d, x.dtype, out_dtype, packed, input_scale, float(g_min))
-    lib = _library()
+    lib = _lib or _library()
     need = lib.kda_glr_fwd_workspace_bytes(desc)
-    with scope(dev, stream):
+    with scope(index, stream):
         if y is None:
-            y = torch.empty(x.shape, device=dev, dtype=out_dtype)
+            y = torch.empty_like(x, dtype=out_dtype)
         if S_T is None and store_state:
             S_T = torch.empty(N, H, d, device=dev, dtype=torch.float32)
         if entry_states is None and store_entry_states:
             entry_states = torch.empty(eshape, device=dev, dtype=torch.float32)
         workspace = _workspace(need, workspace, dev)
-        st = lib.kda_glr_fwd(desc, data_ptr(x), gates, data_ptr(cu_seqlens), data_ptr(S0), data_ptr(y), data_ptr(S_T),
-                             data_ptr(entry_states), data_ptr(workspace), _nbytes(workspace), raw_stream(dev, stream))
+        st = lib.kda_glr_fwd(desc, ptr(x), gates, ptr(cu_seqlens), ptr(S0), ptr(y), ptr(S_T),
+                             ptr(entry_states), ptr(workspace), _nbytes(workspace), raw_stream(index, stream))
     _check("kda_glr_fwd", st)
     return y, S_T, entry_states
 
@@ -171,31 +179,32 @@ def glr_bwd(x, log_alpha, S0, dy, dS_T=None, *, z=None, A_log=None, g_min=-5.0, 
     dA_log [H,d] fp32 (None without z). Packed rows in no sequence are left unwritten in the
     gradients."""
     _dtype(x, dy.dtype)
-    dev = x.device
+    dev, index, shape = x.device, x.get_device(), x.shape
     N, H, T, d = _batch(x, cu_seqlens)
     packed = cu_seqlens is not None
-    check("x", x, dev, x.dtype, x.shape)
-    gates = _gates(x, log_alpha, z, A_log, in_gate, H, d)
-    check("dy", dy, dev, dy.dtype, x.shape)
+    check("x", x, index, x.dtype, shape)
+    gates = _gates(x, index, shape, log_alpha, z, A_log, in_gate, H, d)
+    check("dy", dy, index, dy.dtype, shape)
     for name, t in (("S0", S0), ("dS_T", dS_T)):
         if t is not None:
-            check(name, t, dev, torch.float32, (N, H, d))
+            check(name, t, index, torch.float32, (N, H, d))
     if entry_states is not None:
-        check("entry_states", entry_states, dev, torch.float32, _entry_shape(N, H, T, d, packed))
-    _check_workspace(workspace, dev)
-    _check_device("glr_bwd", dev)
+        check("entry_states", entry_states, index, torch.float32, _entry_shape(N, H, T, d, packed))
+    if workspace is not None:
+        _check_workspace(workspace, dev)
+    on_gpu("glr_bwd", x)
     desc = _desc(N, H, T, d, x.dtype, dy.dtype, packed, input_scale, float(g_min))
-    lib = _library()
+    lib = _lib or _library()
     need = lib.kda_glr_bwd_workspace_bytes(desc, entry_states is not None, z is not None)
-    with scope(dev, stream):
+    with scope(index, stream):
         dx, dd = torch.empty_like(x), torch.empty_like(x)
         du = torch.empty_like(x) if in_gate is not None else None
         dA = torch.empty(H, d, device=dev, dtype=torch.float32) if z is not None else None
         dS0 = torch.empty(N, H, d, device=dev, dtype=torch.float32)
         workspace = _workspace(need, workspace, dev)
-        st = lib.kda_glr_bwd(desc, data_ptr(x), gates, data_ptr(cu_seqlens), data_ptr(S0), data_ptr(entry_states),
-                             data_ptr(dy), data_ptr(dS_T), data_ptr(dx), data_ptr(dd), data_ptr(du), data_ptr(dA),
-                             data_ptr(dS0), data_ptr(workspace), _nbytes(workspace), raw_stream(dev, stream))
+        st = lib.kda_glr_bwd(desc, ptr(x), gates, ptr(cu_seqlens), ptr(S0), ptr(entry_states),
+                             ptr(dy), ptr(dS_T), ptr(dx), ptr(dd), ptr(du), ptr(dA),
+                             ptr(dS0), ptr(workspace), _nbytes(workspace), raw_stream(index, stream))
     _check("kda_glr_bwd", st)
     return dx, dd, du, dS0, dA
 
@@ -205,20 +214,21 @@ def glr_step(x, log_alpha, S, *, z=None, A_log=None, g_min=-5.0, in_gate=None, i
     """One token of the gated linear recurrence through ``kda_glr_step``; S ([N,H,d] fp32) is
     updated in place. x and the gates: [N,H,d] as a token of ``glr_fwd``. Returns y [N,H,d]."""
     out_dtype = _dtype(x, out_dtype)
-    dev = x.device
-    if x.dim() != 3:
-        raise ValueError("x must be [N,H,d] (got %s)" % (tuple(x.shape),))
-    N, H, d = x.shape
-    check("x", x, dev, x.dtype, x.shape)
-    gates = _gates(x, log_alpha, z, A_log, in_gate, H, d)
-    check("S", S, dev, torch.float32, x.shape)
+    index, shape = x.get_device(), x.shape
+    if len(shape) != 3:
+        raise ValueError("x must be [N,H,d] (got %s)" % (tuple(shape),))
+    N, H, d = shape
+    check("x", x, index, x.dtype, shape)
+    gates = _gates(x, index, shape, log_alpha, z, A_log, in_gate, H, d)
+    check("S", S, index, torch.float32, shape)
     if y is not None:
-        check("y", y, dev, out_dtype, x.shape)
-    _check_device("glr_step", dev)
+        check("y", y, index, out_dtype, shape)
+    on_gpu("glr_step", x)
     desc = _desc(N, H, 1, d, x.dtype, out_dtype, False, input_scale, float(g_min))
-    with scope(dev, stream):
+    with scope(index, stream):
         if y is None:
-            y = torch.empty(x.shape, device=dev, dtype=out_dtype)
-        st = _library().kda_glr_step(desc, data_ptr(x), gates, data_ptr(S), data_ptr(y), raw_stream(dev, stream))
+            y = torch.empty_like(x, dtype=out_dtype)
+        st = (_lib or _library()).kda_glr_step(desc, x.data_ptr(), gates, S.data_ptr(), y.data_ptr(),
+                                               raw_stream(index, stream))
     _check("kda_glr_step", st)
     return y
