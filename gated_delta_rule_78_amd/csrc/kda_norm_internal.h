@@ -23,10 +23,15 @@ struct NormArgs {
 
 namespace norm {
 
-// Workgroups at most: what 256 CUs hold at a time (16 waves a CU in the backward, whose column sums
-// cost traffic per workgroup; 24 in the forward).
+// Workgroups at most: 24 waves a CU in the forward. In the backward 8 (one workgroup of 512 threads)
+// for rows on 8 elements, whose eight streams then stay nearer to each other in HBM (32M bf16
+// elements: 104-110 us, against 114-125 with 16), 16 where a row's edges are masked, which costs
+// issue slots (rows of 1001: 135 us against 204 with 8), and one workgroup of 1024 threads.
 inline int fwd_groups(int threads) { return 256 * 24 * 64 / threads; }
-inline int bwd_groups(int threads) { return 256 * 16 * 64 / threads; }
+inline int bwd_groups(int threads, bool aligned) {
+    const int waves = threads / 64, most = aligned && waves < 16 ? 8 : 16;
+    return 256 * (most / waves);
+}
 
 // Instantiated per type of f (kda_norm_*.hip).
 template <typename TI>

@@ -279,10 +279,11 @@ __global__ __launch_bounds__(Geo<TPR>::threads) void norm_fwd_kernel(NormArgs a)
 }
 
 // Two rows of all five tensors, the weights and the column sums: 128 registers hold them for wide
-// bf16 rows (4 waves a SIMD), 256 for the others.
+// bf16 rows (4 waves a SIMD), 256 for the others. Rows of 512 threads on 8 elements spill at 128 and
+// run one workgroup a CU anyhow.
 template <typename TI, typename TR, typename TO, int VEC, int NV, int TPR, bool ODD>
 constexpr int bwd_waves() {
-    return TPR == 1024 || (VEC == 8 && 2 * sizeof(TI) + 2 * sizeof(TR) + sizeof(TO) <= 10) ? 4 : 2;
+    return TPR == 1024 || (VEC == 8 && (TPR != 512 || ODD) && 2 * sizeof(TI) + 2 * sizeof(TR) + sizeof(TO) <= 10) ? 4 : 2;
 }
 
 template <typename TI, typename TR, typename TO, int VEC, int NV, int TPR, bool ODD>
@@ -455,7 +456,7 @@ template <typename TI, typename TR, typename TO, int VEC, int NV, int TPR, bool 
 static hipError_t launch_g(const NormArgs& a, bool bwd, hipStream_t st) {
     constexpr int RPB = Geo<TPR>::rows, threads = Geo<TPR>::threads;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
-    const int most = bwd ? bwd_groups(threads) : fwd_groups(threads);
+    const int most = bwd ? bwd_groups(threads, VEC == 8 && !ODD) : fwd_groups(threads);
     const int groups = blocks < most ? (int)blocks : most;
     if (!bwd) {
         hipLaunchKernelGGL((norm_fwd_kernel<TI, TR, TO, VEC, NV, TPR, ODD>), dim3(groups), dim3(threads), 0, st, a);
