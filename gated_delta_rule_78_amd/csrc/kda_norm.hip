@@ -39,7 +39,7 @@ hipError_t launch_colsum(const NormArgs& a, int groups, hipStream_t st) {
 }  // namespace norm
 
 size_t norm_bwd_ws_bytes(int64_t rows, int64_t D) {
-    const int most = norm::bwd_groups(256, false);   // no launch has more workgroups, nor more than rows
+    const int most = norm::bwd_groups(256, 0);   // no launch has more workgroups, nor more than rows
     return (size_t)((rows < most ? rows : most) * 2 * D) * 4;
 }
 

@@ -23,14 +23,15 @@ struct NormArgs {
 
 namespace norm {
 
-// Workgroups at most: 24 waves a CU in the forward. In the backward 8 (one workgroup of 512 threads)
-// for rows on 8 elements, whose eight streams then stay nearer to each other in HBM (32M bf16
-// elements: 104-110 us, against 114-125 with 16), 16 where a row's edges are masked, which costs
-// issue slots (rows of 1001: 135 us against 204 with 8), and one workgroup of 1024 threads.
+// Workgroups at most: 24 waves a CU in the forward. In the backward 8 for rows on 8 elements that
+// read 4 or 5 tensors, whose streams then stay nearer to each other in HBM (5 of 32M bf16 elements:
+// 104-110 us, against 114-118 with 16); 16 for fewer tensors, which need more rows in flight (2 of
+// them: 51-65 us against 59-83), and where rows start off 8 elements (reads = 0), whose masks cost
+// issue slots (rows of 1001: 135 us against 204). One workgroup of 512 or 1024 threads a CU.
 inline int fwd_groups(int threads) { return 256 * 24 * 64 / threads; }
-inline int bwd_groups(int threads, bool aligned) {
-    const int waves = threads / 64, most = aligned && waves < 16 ? 8 : 16;
-    return 256 * (most / waves);
+inline int bwd_groups(int threads, int reads) {
+    const int waves = threads / 64, most = reads >= 4 || (reads && waves == 8) ? 8 : 16;
+    return 256 * (waves > most ? 1 : most / waves);
 }
 
 // Instantiated per type of f (kda_norm_*.hip).

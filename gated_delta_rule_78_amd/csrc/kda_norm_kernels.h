@@ -456,7 +456,8 @@ template <typename TI, typename TR, typename TO, int VEC, int NV, int TPR, bool 
 static hipError_t launch_g(const NormArgs& a, bool bwd, hipStream_t st) {
     constexpr int RPB = Geo<TPR>::rows, threads = Geo<TPR>::threads;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
-    const int most = bwd ? bwd_groups(threads, VEC == 8 && !ODD) : fwd_groups(threads);
+    const int reads = 1 + !!a.gate + (a.x && a.dn) + !!a.dx_out + !!a.dn;
+    const int most = bwd ? bwd_groups(threads, VEC == 8 && !ODD ? reads : 0) : fwd_groups(threads);
     const int groups = blocks < most ? (int)blocks : most;
     if (!bwd) {
         hipLaunchKernelGGL((norm_fwd_kernel<TI, TR, TO, VEC, NV, TPR, ODD>), dim3(groups), dim3(threads), 0, st, a);
