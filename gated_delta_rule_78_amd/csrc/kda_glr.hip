@@ -68,29 +68,47 @@ static hipError_t launch_prepare(const GlrArgs& a, const GlrWs& ws, const float*
     return hipGetLastError();
 }
 
-// dA_log [H,d] from the tiles' parts [blocks][nt][d], in order: 16 groups of tiles a channel, each
-// summed by a thread, joined in LDS.
-__global__ __launch_bounds__(1024) void glr_dA_kernel(GlrArgs a, GlrWs ws) {
+// dA_log [H,d] from the n parts of a head (one per tile of each of its blocks of rows, [blocks][nt][d]),
+// in order: 16 runs of parts a channel, each summed by a thread, joined in LDS. Many parts (N large
+// and H small leaves few workgroups) take two launches: workgroup y sums parts [y chunk, (y + 1) chunk)
+// into the first of them, then one sums every chunk'th (`last`).
+__global__ __launch_bounds__(1024) void glr_dA_kernel(GlrArgs a, GlrWs ws, int64_t n, int64_t chunk, bool last) {
     __shared__ float part[16][64];
-    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
     const int64_t ntc = (a.d + 63) / 64, head = blockIdx.x / ntc, ch = (int64_t)(blockIdx.x % ntc) * 64 + lane;
-    const int64_t per = a.packed ? 1 : a.N, n = per * ws.nt, each = (n + 15) / 16;
+    const int64_t k0 = last ? 0 : blockIdx.y * chunk, step = last ? chunk : 1;
+    const int64_t left = last ? (n + chunk - 1) / chunk : n - k0, count = last || left < chunk ? left : chunk;
+    const int64_t each = (count + 15) / 16;
+    auto at = [&](int64_t k) { return ws.dA + ((k / ws.nt * a.H + head) * ws.nt + k % ws.nt) * a.d + ch; };
     float s = 0.f;
     if (ch < a.d) {
-        const int64_t k1 = (grp + 1) * each < n ? (grp + 1) * each : n;
+        const int64_t i1 = (run + 1) * each < count ? (run + 1) * each : count;
 #pragma unroll 8
-        for (int64_t k = grp * each; k < k1; ++k) {
-            const int64_t block = (k / ws.nt) * a.H + head, c = k % ws.nt;
-            s += ws.dA[(block * ws.nt + c) * a.d + ch];
-        }
+        for (int64_t i = run * each; i < i1; ++i) s += *at(k0 + i * step);
     }
-    part[grp][lane] = s;
+    part[run][lane] = s;
     __syncthreads();
-    if (grp == 0 && ch < a.d) {
+    if (run == 0 && ch < a.d) {
 #pragma unroll
         for (int i = 1; i < 16; ++i) s += part[i][lane];
-        a.dA[head * a.d + ch] = s;
+        if (last) a.dA[head * a.d + ch] = s;
+        else *at(k0) = s;
     }
+}
+
+static hipError_t launch_dA(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    const int64_t n = (a.packed ? 1 : a.N) * ws.nt;
+    const unsigned gx = (unsigned)((a.d + 63) / 64 * a.H);
+    int64_t chunk = 1;
+    if (n > 512) {
+        chunk = 256;
+        while (chunk * chunk < n) chunk *= 2;
+        hipLaunchKernelGGL(glr_dA_kernel, dim3(gx, (unsigned)((n + chunk - 1) / chunk)), dim3(1024), 0, st, a, ws, n, chunk, false);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(glr_dA_kernel, dim3(gx), dim3(1024), 0, st, a, ws, n, chunk, true);
+    return hipGetLastError();
 }
 
 // Workspace in order: counters, marked rows, chain words, dA_log parts.
@@ -106,6 +124,11 @@ static Plan make_plan(const GlrArgs& a, unsigned char* base, bool backward) {
     const bool with_dA = backward && a.z;
     p.ws.rows = rows;
     p.ws.nt = (a.T + rows - 1) / rows;
+    // Narrow heads share tiles where one each would fill the GPU (1024 x 4096 rows of 8 channels: 70 us
+    // against 180); fewer stay apart, each tile's work being a wave's latency (8 x 4096 rows: 15.8 us
+    // against 16.3, 4 x 20000 rows of 16 channels: 26.5 against 30.3). 32-bit offsets inside a tile.
+    const int64_t per = heads_a_tile(a.d);
+    p.ws.narrow = per > 1 && a.blocks * p.ws.nt >= 1024 && per * a.T * a.d < (int64_t)1 << 31;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         unsigned char* r = base ? base + at : nullptr;
@@ -113,7 +136,7 @@ static Plan make_plan(const GlrArgs& a, unsigned char* base, bool backward) {
         return r;
     };
     const size_t words = (size_t)(a.blocks * p.ws.nt * a.d);
-    const int64_t chains = a.blocks * ((a.d + kCW - 1) / kCW);
+    const int64_t chains = chain_count(a.blocks, a.d, p.ws.narrow);
     p.ws.counters = chains < (int64_t)kCounters ? chains : (int64_t)kCounters;
     if (p.ws.nt > 1) p.ws.ticket = reinterpret_cast<uint32_t*>(take((size_t)p.ws.counters * kCounterStride * 4));
     if (a.packed) {
@@ -214,8 +237,7 @@ hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t st) {
         e = glr::launch_bwd_tiles(b, p.ws, st);
     }
     if (e != hipSuccess || !a.z) return e;
-    hipLaunchKernelGGL(glr::glr_dA_kernel, dim3((unsigned)((a.d + 63) / 64 * a.H)), dim3(1024), 0, st, a, p.ws);
-    return hipGetLastError();
+    return glr::launch_dA(a, p.ws, st);
 }
 
 // A step is a prefill of one token whose states are read and written in place.

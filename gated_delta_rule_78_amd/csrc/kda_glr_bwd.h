@@ -17,7 +17,7 @@
 namespace kda {
 namespace glr {
 
-template <int SCALE, bool PACKED, int Z, int U, typename TIn, typename TOut, int VEC, int L, int THREADS>
+template <int SCALE, bool PACKED, bool NARROW, int Z, int U, typename TIn, typename TOut, int VEC, int L, int THREADS>
 __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void glr_bwd_kernel(GlrArgs a, GlrWs ws) {
     using G = Tile<VEC, L, THREADS>;
     constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
@@ -33,7 +33,8 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int ct = tid % CT, sub = tid / CT, row_t = sub * L;
-    const uint32_t ntc = (uint32_t)((a.d + kCW - 1) / kCW), chains = (uint32_t)a.blocks * ntc;
+    const uint32_t ntc = NARROW ? 1 : (uint32_t)((a.d + kCW - 1) / kCW), per = NARROW ? heads_a_tile(a.d) : 1;
+    const uint32_t chains = (uint32_t)chain_count(a.blocks, a.d, NARROW);
     const bool chained = ws.nt > 1;
     uint32_t c = blockIdx.x / chains, chain = blockIdx.x % chains;
     if (chained) {
@@ -42,18 +43,21 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
         next_tile(__builtin_amdgcn_readfirstlane(ticket), chains, c, chain);
     }
     c = (uint32_t)ws.nt - 1 - c;   // the last tile first
-    const int64_t block = chain / ntc;
+    const int64_t block0 = (int64_t)(chain / ntc) * per;   // the tile's first block of rows
     const int ch_tile = (int)(chain % ntc) * kCW;
     const uint32_t d = (uint32_t)a.d;
-    const bool on = ch_tile + ct * VEC < (int)d;
-    const uint32_t ch0 = ch_tile + ct * VEC + VEC <= d ? ch_tile + ct * VEC : d - VEC;
-    // as a lane of one channel: the channel, and whether there is one
-    const int slot = ch_tile + lane / VEC * VEC;
-    const bool has_ch = slot < (int)d;
-    const uint32_t ch = (slot + VEC <= (int)d ? slot : (int)d - VEC) + lane % VEC;
+    const Place<NARROW, VEC> at(ct * VEC, ch_tile, d, a.blocks - block0);
+    const bool on = at.on;
+    const uint32_t ch0 = at.ch;
+    const int64_t block = block0 + at.local;
+    // as a lane of one channel: the block, the channel, and whether there is one
+    const Place<NARROW, VEC> own(lane / VEC * VEC, ch_tile, d, a.blocks - block0);
+    const bool has_ch = own.on;
+    const int64_t block_l = block0 + own.local;
+    const uint32_t ch = own.ch + lane % VEC;
     const int64_t row0 = (int64_t)c * ROWS;
     const int rows_here = (int)(a.T - row0 < ROWS ? a.T - row0 : ROWS);
-    const int64_t base = (block * a.T + row0) * a.d;
+    const int64_t base = (block0 * a.T + row0) * a.d;
     const int head = (int)(PACKED ? block : block % a.H);
 
     int lo = 0, hi = rows_here;     // rows of the tile that are in a sequence
@@ -63,7 +67,9 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
         ebits = bits_at<L>(ws.ebits, row0 + row_t);
         live_rows(a, row0, ROWS, lo, hi);
     }
-    const uint32_t off0 = (uint32_t)row_t * d + ch0, last_off = (uint32_t)(rows_here - 1) * d + ch0;
+    // (narrow heads: a tile's blocks lie within 2^31 elements)
+    const uint32_t in_tile = (NARROW ? at.local * (uint32_t)(a.T * a.d) : 0) + ch0;
+    const uint32_t off0 = (uint32_t)row_t * d + in_tile, last_off = (uint32_t)(rows_here - 1) * d + in_tile;
     const TIn* dec = (const TIn*)(has_z ? a.z : a.la) + base;
     const TIn* xp = (const TIn*)a.x + base;
     const TIn* up = (const TIn*)a.u + base;
@@ -168,7 +174,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
     wb.scan(sr, turn[wave], lane);
     wtR[wave][lane] = wb.total.A;
     wtg[wave][lane] = wb.total.h;
-    float hw = a.entry[(block * a.nch + c) * a.d + ch];
+    float hw = a.entry[(block_l * a.nch + c) * a.d + ch];
     lds_barrier();
     if (wave == 0) {   // lane = channel: the tile's backward span, the chain
         Span tot{wtR[W - 1][lane], wtg[W - 1][lane]};
@@ -177,9 +183,9 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
         float g = 0.f;
         if (has_ch) {
             const bool first = (int64_t)c + 1 == ws.nt, more = c > 0;
-            if (!PACKED && first && a.dST) g = a.dST[block * a.d + ch];
+            if (!PACKED && first && a.dST) g = a.dST[block_l * a.d + ch];
             if (chained) {
-                const int64_t word = (block * ws.nt + c) * a.d + ch;
+                const int64_t word = (block_l * ws.nt + c) * a.d + ch;
                 const bool cut = PACKED && __float_as_int(tot.A) < 0;
                 if (cut && more) publish(ws.state + word, 0, tot.h);
                 if (!first) {
@@ -188,7 +194,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
                 }
                 if (!cut && more) publish(ws.state + word, 0, apply<PACKED>(tot, g));
             }
-            if (!PACKED && c == 0 && a.dS0) a.dS0[block * a.d + ch] = apply<PACKED>(tot, g);
+            if (!PACKED && c == 0 && a.dS0) a.dS0[block_l * a.d + ch] = apply<PACKED>(tot, g);
         }
         gin[lane] = g;
     }
@@ -304,31 +310,32 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
         float t = wth[0][lane];
 #pragma unroll
         for (int i = 1; i < W; ++i) t += wth[i][lane];
-        ws.dA[(block * ws.nt + c) * a.d + ch] = t;
+        ws.dA[(block_l * ws.nt + c) * a.d + ch] = t;
     }
 }
 
-template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
+template <int SCALE, bool PACKED, bool NARROW, int Z, int U, typename TIn, int VEC, int L, int THREADS>
 static hipError_t launch_bwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
     static_assert(Tile<VEC, L, THREADS>::ROWS == kBwdRows, "the plan's tile");
-    const dim3 grid((unsigned)(a.blocks * ((a.d + kCW - 1) / kCW) * ws.nt));
+    const dim3 grid((unsigned)(chain_count(a.blocks, a.d, NARROW) * ws.nt));
     if (a.out_bf16)
-        hipLaunchKernelGGL((glr_bwd_kernel<SCALE, PACKED, Z, U, TIn, bf16_t, VEC, L, THREADS>), grid, dim3(THREADS), 0, st, a, ws);
+        hipLaunchKernelGGL((glr_bwd_kernel<SCALE, PACKED, NARROW, Z, U, TIn, bf16_t, VEC, L, THREADS>), grid, dim3(THREADS), 0, st, a, ws);
     else
-        hipLaunchKernelGGL((glr_bwd_kernel<SCALE, PACKED, Z, U, TIn, float, VEC, L, THREADS>), grid, dim3(THREADS), 0, st, a, ws);
+        hipLaunchKernelGGL((glr_bwd_kernel<SCALE, PACKED, NARROW, Z, U, TIn, float, VEC, L, THREADS>), grid, dim3(THREADS), 0, st, a, ws);
     return hipGetLastError();
 }
 
 // 4 channels a thread (ws.vec), 1 for heads of fewer.
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_bwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    if (ws.narrow) return launch_bwd_k<SCALE, PACKED, true, 2, 2, TIn, 4, 4, 512>(a, ws, st);
     if (ws.vec == 4) {
-        if (a.z && a.u) return launch_bwd_k<SCALE, PACKED, 1, 1, TIn, 4, 4, 512>(a, ws, st);
-        if (a.z) return launch_bwd_k<SCALE, PACKED, 1, 0, TIn, 4, 4, 512>(a, ws, st);
-        if (a.u) return launch_bwd_k<SCALE, PACKED, 0, 1, TIn, 4, 4, 512>(a, ws, st);
-        return launch_bwd_k<SCALE, PACKED, 0, 0, TIn, 4, 4, 512>(a, ws, st);
+        if (a.z && a.u) return launch_bwd_k<SCALE, PACKED, false, 1, 1, TIn, 4, 4, 512>(a, ws, st);
+        if (a.z) return launch_bwd_k<SCALE, PACKED, false, 1, 0, TIn, 4, 4, 512>(a, ws, st);
+        if (a.u) return launch_bwd_k<SCALE, PACKED, false, 0, 1, TIn, 4, 4, 512>(a, ws, st);
+        return launch_bwd_k<SCALE, PACKED, false, 0, 0, TIn, 4, 4, 512>(a, ws, st);
     }
-    return launch_bwd_k<SCALE, PACKED, 2, 2, TIn, 1, 16, 512>(a, ws, st);
+    return launch_bwd_k<SCALE, PACKED, false, 2, 2, TIn, 1, 16, 512>(a, ws, st);
 }
 
 }  // namespace glr

@@ -65,6 +65,37 @@ struct Tile {
     static constexpr int ROWS = THREADS / CT * L;
 };
 
+// Narrow heads (d <= kCW / 2) lie side by side in a tile: 4-channel slots of ceil(d / 4) a head.
+__host__ __device__ inline uint32_t heads_a_tile(int64_t d) {
+    return d > kCW / 2 || d < 4 ? 1 : kCW / (((uint32_t)d + 3) & ~3u);
+}
+// Tiles across the channels, all blocks together: the chains.
+__host__ __device__ inline int64_t chain_count(int64_t blocks, int64_t d, bool narrow) {
+    const int64_t n = narrow ? heads_a_tile(d) : 1;
+    return n > 1 ? (blocks + n - 1) / n : blocks * ((d + kCW - 1) / kCW);
+}
+// Where a thread's VEC channels lie that has the tile's slot'th channel: the block counted from the
+// tile's first (`left` of them are there), the first channel, and whether there are any.
+template <bool NARROW, int VEC>
+struct Place {
+    uint32_t local, ch;
+    bool on;
+    __device__ __forceinline__ Place(int slot, int ch_tile, uint32_t d, int64_t left) {
+        local = 0;
+        if constexpr (NARROW) {
+            const uint32_t width = (d + 3) & ~3u;
+            local = (uint32_t)slot / width;
+            slot -= (int)(local * width);
+            on = local < kCW / width && local < left;
+            if (!on) local = 0;
+        } else {
+            slot += ch_tile;
+            on = slot < (int)d;
+        }
+        ch = slot + VEC <= (int)d ? slot : d - VEC;
+    }
+};
+
 // ---- the chain -------------------------------------------------------------------------------
 // Tiles of one block of rows and channel tile form a chain. A tile publishes its span as one
 // 64-bit word per channel as soon as it has read its rows, and the state behind it as another once

@@ -19,7 +19,7 @@ namespace glr {
 constexpr int kCh = KDA_GLR_CHUNK;
 
 // Z, U: whether the decay comes from z and whether there is an input gate (2: looked up).
-template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
+template <int SCALE, bool PACKED, bool NARROW, int Z, int U, typename TIn, int VEC, int L, int THREADS>
 __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws) {
     using G = Tile<VEC, L, THREADS>;
     constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
@@ -31,7 +31,8 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int ct = tid % CT, sub = tid / CT, row_t = sub * L;
-    const uint32_t ntc = (uint32_t)((a.d + kCW - 1) / kCW), chains = (uint32_t)a.blocks * ntc;
+    const uint32_t ntc = NARROW ? 1 : (uint32_t)((a.d + kCW - 1) / kCW), per = NARROW ? heads_a_tile(a.d) : 1;
+    const uint32_t chains = (uint32_t)chain_count(a.blocks, a.d, NARROW);
     const bool chained = ws.nt > 1;
     uint32_t c = blockIdx.x / chains, chain = blockIdx.x % chains;
     if (chained) {
@@ -39,18 +40,21 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
         lds_barrier();
         next_tile(__builtin_amdgcn_readfirstlane(ticket), chains, c, chain);
     }
-    const int64_t block = chain / ntc;
+    const int64_t block0 = (int64_t)(chain / ntc) * per;   // the tile's first block of rows
     const int ch_tile = (int)(chain % ntc) * kCW;
     const uint32_t d = (uint32_t)a.d;
-    const bool on = ch_tile + ct * VEC < (int)d;
-    const uint32_t ch0 = ch_tile + ct * VEC + VEC <= d ? ch_tile + ct * VEC : d - VEC;
-    // as a lane of one channel: the channel, and whether there is one
-    const int slot = ch_tile + lane / VEC * VEC;
-    const bool has_ch = slot < (int)d;
-    const uint32_t ch = (slot + VEC <= (int)d ? slot : (int)d - VEC) + lane % VEC;
+    const Place<NARROW, VEC> at(ct * VEC, ch_tile, d, a.blocks - block0);
+    const bool on = at.on;
+    const uint32_t ch0 = at.ch;
+    const int64_t block = block0 + at.local;
+    // as a lane of one channel: the block, the channel, and whether there is one
+    const Place<NARROW, VEC> own(lane / VEC * VEC, ch_tile, d, a.blocks - block0);
+    const bool has_ch = own.on;
+    const int64_t block_l = block0 + own.local;
+    const uint32_t ch = own.ch + lane % VEC;
     const int64_t row0 = (int64_t)c * ROWS;
     const int rows_here = (int)(a.T - row0 < ROWS ? a.T - row0 : ROWS);
-    const int64_t base = (block * a.T + row0) * a.d;
+    const int64_t base = (block0 * a.T + row0) * a.d;
     const int head = (int)(PACKED ? block : block % a.H);
 
     int lo = 0, hi = rows_here;     // rows of the tile that are in a sequence
@@ -60,7 +64,9 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
         ebits = bits_at<L>(ws.ebits, row0 + row_t);
         live_rows(a, row0, ROWS, lo, hi);
     }
-    const uint32_t off0 = (uint32_t)row_t * d + ch0, last_off = (uint32_t)(rows_here - 1) * d + ch0;
+    // (narrow heads: a tile's blocks lie within 2^31 elements)
+    const uint32_t in_tile = (NARROW ? at.local * (uint32_t)(a.T * a.d) : 0) + ch0;
+    const uint32_t off0 = (uint32_t)row_t * d + in_tile, last_off = (uint32_t)(rows_here - 1) * d + in_tile;
     RawRow<TIn, VEC> xr[L], dr[L], ur[L];
     const TIn* dec = (const TIn*)(has_z ? a.z : a.la) + base;
     const TIn* xp = (const TIn*)a.x + base;
@@ -133,9 +139,9 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
         for (int w = 1; w < W; ++w) tot = compose<PACKED>(tot, Span{wtA[w][lane], wth[w][lane]});
         float h = 0.f;
         if (has_ch) {
-            if (!PACKED && c == 0 && a.S0) h = a.S0[block * a.d + ch];
+            if (!PACKED && c == 0 && a.S0) h = a.S0[block_l * a.d + ch];
             if (chained) {
-                const int64_t word = (block * ws.nt + c) * a.d + ch;
+                const int64_t word = (block_l * ws.nt + c) * a.d + ch;
                 const bool more = (int64_t)c + 1 < ws.nt;
                 const bool cut = PACKED && __float_as_int(tot.A) < 0;
                 if (cut && more) publish(ws.state + word, 0, tot.h);
@@ -191,12 +197,11 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
     }
 }
 
-template <int SCALE, bool PACKED, int Z, int U, typename TIn, int VEC, int L, int THREADS>
+template <int SCALE, bool PACKED, bool NARROW, int Z, int U, typename TIn, int VEC, int L, int THREADS>
 static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
     static_assert(Tile<VEC, L, THREADS>::ROWS == (VEC == 4 ? kFwdRows : kFwdRows1), "the plan's tile");
-    const int64_t ntc = (a.d + kCW - 1) / kCW;
-    hipLaunchKernelGGL((glr_fwd_kernel<SCALE, PACKED, Z, U, TIn, VEC, L, THREADS>),
-                       dim3((unsigned)(a.blocks * ntc * ws.nt)), dim3(THREADS), 0, st, a, ws);
+    hipLaunchKernelGGL((glr_fwd_kernel<SCALE, PACKED, NARROW, Z, U, TIn, VEC, L, THREADS>),
+                       dim3((unsigned)(chain_count(a.blocks, a.d, NARROW) * ws.nt)), dim3(THREADS), 0, st, a, ws);
     return hipGetLastError();
 }
 
@@ -207,13 +212,14 @@ static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st
 // against 161).
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
+    if (ws.narrow) return launch_fwd_k<SCALE, PACKED, true, 2, 2, TIn, 4, 8, 512>(a, ws, st);
     if (ws.vec == 4) {
-        if (a.z && a.u) return launch_fwd_k<SCALE, PACKED, 1, 1, TIn, 4, 8, 512>(a, ws, st);
-        if (a.z) return launch_fwd_k<SCALE, PACKED, 1, 0, TIn, 4, 8, 512>(a, ws, st);
-        if (a.u) return launch_fwd_k<SCALE, PACKED, 0, 1, TIn, 4, 8, 512>(a, ws, st);
-        return launch_fwd_k<SCALE, PACKED, 0, 0, TIn, 4, 8, 512>(a, ws, st);
+        if (a.z && a.u) return launch_fwd_k<SCALE, PACKED, false, 1, 1, TIn, 4, 8, 512>(a, ws, st);
+        if (a.z) return launch_fwd_k<SCALE, PACKED, false, 1, 0, TIn, 4, 8, 512>(a, ws, st);
+        if (a.u) return launch_fwd_k<SCALE, PACKED, false, 0, 1, TIn, 4, 8, 512>(a, ws, st);
+        return launch_fwd_k<SCALE, PACKED, false, 0, 0, TIn, 4, 8, 512>(a, ws, st);
     }
-    return launch_fwd_k<SCALE, PACKED, 2, 2, TIn, 1, 16, 512>(a, ws, st);
+    return launch_fwd_k<SCALE, PACKED, false, 2, 2, TIn, 1, 16, 512>(a, ws, st);
 }
 
 }  // namespace glr

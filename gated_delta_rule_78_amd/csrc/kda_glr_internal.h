@@ -45,6 +45,7 @@ struct GlrWs {
     float* dA;                           // [blocks][nt][d]
     int64_t nt, rows;                    // tiles per block, rows per tile
     int vec;                             // channels per thread: 4 or 1
+    bool narrow;                         // several heads side by side in a tile
 };
 
 // Rows of a tile: forward with 4 channels and with 1 channel a thread, backward.

@@ -126,6 +126,17 @@ CASES = [
     ((33, 1, 5, 64, None), F32, F32, True, False, "one", False),
     ((5, 1, 17, 20, None), BF16, F32, False, False, "norm", True),
     ((1, 2, 18, 131072, None), BF16, BF16, True, True, "norm", True),
+    # narrow heads, several in a tile (1024 tiles and more): the last tile's places not all taken,
+    # channels off 4; dA_log from many parts
+    ((49, 7, 300, 8, None), BF16, BF16, True, True, "norm", True),
+    ((180, 3, 260, 20, None), F32, F32, False, True, "leaky", True),
+    ((1030, 1, 17, 31, None), BF16, F32, True, False, "one", False),
+    ((55, 19, 20, 4, None), BF16, BF16, False, True, "norm", True),
+    ((0, 513, 0, 9, [55, 0, 200, 1, 100]), F32, BF16, True, True, "leaky", True),
+    ((0, 515, 0, 7, [3, 400]), BF16, BF16, False, False, "norm", False),
+    ((0, 3, 0, 32, [130, 1, 126]), F32, F32, True, True, "norm", True),
+    ((1, 1, 300, 12, None), BF16, BF16, True, False, "norm", True),
+    ((700, 2, 3, 5, None), F32, F32, True, True, "norm", True),
     # a chain longer than any look back
     ((1, 1, 6000, 8, None), F32, F32, False, True, "leaky", True),
 ]
