@@ -9,7 +9,12 @@
 // from the entry state that the forward stored, so that every tensor is read once here too. Between
 // the passes over the rows the gates stay in registers (computing them twice costs more issue slots
 // than the memory leaves free) and x, z and dy wait in LDS as they were read: 128 registers a
-// thread hold no more, and 168 would leave one workgroup a CU.
+// thread hold no more, and 168 would leave one workgroup a CU (no LDS: 270 us for both directions of
+// the shape below, against 200; 256 threads of 8 rows: 211 against 202).
+//
+// Measured, bf16 with both gates and w = sqrt(1 - alpha^2): 2 x 4096 rows of 4096 channels 121 us for
+// 470 MB read and written, 3.9 TB/s; its issue slots and the latency of a tile's start, with two
+// workgroups a CU, share the bound.
 #pragma once
 
 #include "kda_glr_device.h"

@@ -18,6 +18,12 @@
 // so a row's first vector may begin up to 7 elements before the row. Workgroups step by a multiple
 // of 8 rows, which keeps that offset, and so every thread's channels, the same for all its rows.
 // Only a row's first and last vector are masked.
+//
+// Measured, bf16 (kernel alone): 8192 rows of 4096 with gate and residual, forward 61.3 us, 5.5 TB/s,
+// backward 102 us, 5.3 TB/s; 262144 rows of 128 with a gate, forward 39.6 us, 5.1 TB/s, backward 58.5
+// us, 5.7 TB/s. Without the next rows in flight both directions of the first take 299 us instead of
+// 169; with 1024 threads a row, 232. Rows off 8 elements: 1001 channels 72 and 135 us for the bytes of
+// the first; past 8192 channels 16384 takes 75 % (forward) and 59 % of the copy rate.
 #pragma once
 
 #include "kda_math.h"
