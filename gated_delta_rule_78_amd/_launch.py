@@ -5,8 +5,8 @@ import contextlib
 import torch
 
 _NOTHING = contextlib.nullcontext()
-_current_device = torch._C._cuda_getDevice            # torch.cuda.current_device without its wrappers
-_current_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream without the Stream object
+_current_device = getattr(torch._C, "_cuda_getDevice", None)            # torch.cuda.current_device without its wrappers
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # torch.cuda.current_stream without the Stream object
 
 
 def check(name, t, index, dtype, shape):

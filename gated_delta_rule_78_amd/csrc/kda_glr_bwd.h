@@ -6,11 +6,11 @@
 //
 // The tiles, their chain and their bound are the forward's (kda_glr_fwd.h), the chain run from the
 // last tile to the first with spans g -> A g + b; the states h_{t-1} are run again inside the tile
-// from the entry state that the forward stored, so that every tensor is read once here too. Between
-// the passes over the rows the gates stay in registers (computing them twice costs more issue slots
-// than the memory leaves free) and x, z and dy wait in LDS as they were read: 128 registers a
-// thread hold no more, and 168 would leave one workgroup a CU (no LDS: 270 us for both directions of
-// the shape below, against 200; 256 threads of 8 rows: 211 against 202).
+// from the entry state that the forward stored, so that every tensor is read once here too (fp32
+// rows without z: dy twice). Between the passes over the rows the gates stay in registers (computing
+// them twice costs more issue slots than the memory leaves free) and x, z and dy wait in LDS as they
+// were read: 128 registers a thread hold no more, and 168 would leave one workgroup a CU (no LDS:
+// 270 us for both directions of the shape below, against 200; 256 threads of 8 rows: 211 against 202).
 //
 // Measured, bf16 with both gates and w = sqrt(1 - alpha^2): 2 x 4096 rows of 4096 channels 121 us for
 // 470 MB read and written, 3.9 TB/s; its issue slots and the latency of a tile's start, with two
@@ -22,17 +22,27 @@
 namespace kda {
 namespace glr {
 
+// Workgroups a CU: two with 48 KiB of rows in LDS, which hold all of a bf16 tile and x of an fp32
+// one (dy and z are read again); or one, with the registers and the LDS for everything, where fp32
+// rows come with z (2 x 4096 rows of 4096 fp32 channels, both gates: 225 us against 257, and 294
+// with two and nothing in LDS; without z two win, 145 against 154).
+template <int Z, typename TIn, int VEC>
+constexpr int groups_a_cu() {
+    return sizeof(TIn) == 4 && (Z != 0 || VEC == 1) ? 1 : 2;
+}
+
 template <int SCALE, bool PACKED, bool NARROW, int Z, int U, typename TIn, typename TOut, int VEC, int L, int THREADS>
-__global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void glr_bwd_kernel(GlrArgs a, GlrWs ws) {
+__global__ __launch_bounds__(THREADS, (2 * groups_a_cu<Z, TIn, VEC>())) void glr_bwd_kernel(GlrArgs a, GlrWs ws) {
     using G = Tile<VEC, L, THREADS>;
     constexpr int CT = G::CT, SPW = G::SPW, W = G::W, ROWS = G::ROWS;
     static_assert(ROWS == KDA_GLR_CHUNK, "a tile starts at an entry state");
     __shared__ float wtA[W][kCW], wth[W][kCW], wtg[W][kCW], wtR[W][kCW], gin[kCW];
     __shared__ __align__(16) float turn[W][SPW > 1 ? 2 * SPW * kCW : 1];
-    // fp32 rows are read from memory again instead: they would take all of LDS for one workgroup
-    constexpr bool STASH = sizeof(TIn) == 2 && sizeof(TOut) == 2;
-    __shared__ RawRow<TIn, VEC> xs[STASH ? L : 1][THREADS], zs[STASH && Z != 0 ? L : 1][THREADS];
-    __shared__ RawRow<TOut, VEC> ys[STASH ? L : 1][THREADS];
+    // the rows in LDS: x, then dy, then z, as far as they fit
+    constexpr int kStash = (groups_a_cu<Z, TIn, VEC>() == 1 ? 96 : 48) << 10, XB = THREADS * L * VEC * (int)sizeof(TIn), YB = THREADS * L * VEC * (int)sizeof(TOut);
+    constexpr bool SX = XB <= kStash, SY = XB + YB <= kStash, SZ = Z != 0 && 2 * XB + (SY ? YB : 0) <= kStash;
+    __shared__ RawRow<TIn, VEC> xs[SX ? L : 1][THREADS], zs[SZ ? L : 1][THREADS];
+    __shared__ RawRow<TOut, VEC> ys[SY ? L : 1][THREADS];
     __shared__ uint32_t ticket;
     const bool has_z = Z == 2 ? a.z != nullptr : Z == 1, has_u = U == 2 ? a.u != nullptr : U == 1;
 
@@ -112,11 +122,9 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
             unpack(dr[r], q);
             unpack(yr[r], dy);
             if (has_u) unpack(ur[r], u);
-            if constexpr (STASH) {
-                xs[r][tid] = xr[r];
-                if (has_z) zs[r][tid] = dr[r];
-                ys[r][tid] = yr[r];
-            }
+            if constexpr (SX) xs[r][tid] = xr[r];
+            if constexpr (SZ) zs[r][tid] = dr[r];
+            if constexpr (SY) ys[r][tid] = yr[r];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 float y;
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
     wb.spread(gw, turn[wave], lane, g);
     // the state before each row
     auto row_x = [&](int r, float* o) {
-        if constexpr (STASH) unpack(xs[r][tid], o);
+        if constexpr (SX) unpack(xs[r][tid], o);
         else unpack(load_row<TIn, VEC>(xp + row_offset(off0, r, d, last_off)), o);
     };
     float prev[L][VEC];
@@ -249,14 +257,11 @@ __global__ __launch_bounds__(THREADS, VEC == 4 || sizeof(TIn) == 2 ? 4 : 2) void
         float x[VEC], q[VEC], dy[VEC], ox[VEC], od[VEC], ou[VEC];
         const bool live = row_t + r >= lo && row_t + r < hi;
         row_x(r, x);
-        if constexpr (STASH) {
-            if (has_z) unpack(zs[r][tid], q);
-            unpack(ys[r][tid], dy);
-        } else {
-            const uint32_t off = row_offset(off0, r, d, last_off);
-            if (has_z) unpack(load_row<TIn, VEC>(dec + off), q);
-            unpack(load_row<TOut, VEC>(yp + off), dy);
-        }
+        const uint32_t off = row_offset(off0, r, d, last_off);
+        if constexpr (SZ) unpack(zs[r][tid], q);
+        else if (has_z) unpack(load_row<TIn, VEC>(dec + off), q);
+        if constexpr (SY) unpack(ys[r][tid], dy);
+        else unpack(load_row<TOut, VEC>(yp + off), dy);
         if (PACKED && (ebits >> r & 1)) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
