@@ -38,7 +38,7 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
     const uint32_t ntc = NARROW ? 1 : (uint32_t)((a.d + kCW - 1) / kCW), per = NARROW ? heads_a_tile(a.d) : 1;
     const uint32_t chains = (uint32_t)chain_count(a.blocks, a.d, NARROW);
     const bool chained = ws.nt > 1;
-    uint32_t c = blockIdx.x / chains, chain = blockIdx.x % chains;
+    uint32_t c = blockIdx.x / chains, chain = chain_of(blockIdx.x % chains, chains);
     if (chained) {
         if (tid == 0) ticket = atomicAdd(ws.ticket + chain % kCounters * kCounterStride, 1u);
         lds_barrier();
