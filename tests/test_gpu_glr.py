@@ -137,6 +137,8 @@ CASES = [
     ((0, 3, 0, 32, [130, 1, 126]), F32, F32, True, True, "norm", True),
     ((1, 1, 300, 12, None), BF16, BF16, True, False, "norm", True),
     ((700, 2, 3, 5, None), F32, F32, True, True, "norm", True),
+    # more chains than tile counters, no multiple of the XCDs
+    ((1, 1, 260, 66010, None), BF16, BF16, True, True, "norm", True),
     # a chain longer than any look back
     ((1, 1, 6000, 8, None), F32, F32, False, True, "leaky", True),
 ]
