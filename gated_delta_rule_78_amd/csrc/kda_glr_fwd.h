@@ -214,7 +214,7 @@ static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st
 // channels: 366 us against 404 with 256 threads, before the last steps), and 8 rows a thread leave
 // room for 4 waves a SIMD. 512 rows on 1024 threads wait longer at their barriers (369 us, packed
 // batches 81 us against 71). One channel a thread (16 rows) needs four times the accesses: 64 x 4096
-// rows of 77 bf16 channels with gates take 106 us that way and 67 with 4, which any head of 4 has.
+// rows of 77 bf16 channels with gates take 106 us that way and 60 with 4, which any head of 4 has.
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
     if (ws.narrow) return launch_fwd_k<SCALE, PACKED, true, 2, 2, TIn, 4, 8, 512>(a, ws, st);

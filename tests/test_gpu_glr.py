@@ -353,6 +353,32 @@ def test_no_rows(packed):
     assert not bool(kda.glr_bwd(x, x, S0, y, None, cu_seqlens=cu)[3].any())
 
 
+def test_narrow_heads_share_tiles_and_nothing_else():
+    """Heads side by side in a tile: bad numbers in one change no bit of the others, and rows behind
+    the last sequence stay as they were."""
+    c = make(60, 20, 300, 12, BF16, z=True, u=True, s0=True, seed=15)
+    run = lambda x, dy: run_fwd(dict(c, x=x), "norm", F32)[:2] + kda.glr_bwd(
+        x, None, c["S0"], dy, c["dS_T"], **kw(c, "norm"))[:4]
+    clean = run(c["x"], c["dy"])
+    x, dy = c["x"].clone(), c["dy"].clone()
+    x[5, 7, 100], dy[31, 0, 200] = float("inf"), float("nan")
+    bad = run(x, dy)
+    keep = torch.ones(60, 20, dtype=torch.bool, device=DEV)
+    keep[5, 7] = keep[31, 0] = False
+    for want, got in zip(clean, bad):
+        assert torch.equal(want[keep], got[keep])
+    assert not bool(torch.isfinite(bad[0][5, 7, 100:]).any()) and not bool(torch.isfinite(bad[2][31, 0, :201]).any())
+
+    p = make(0, 700, 0, 7, F32, lens=[70, 200], z=True, u=True, s0=True, tail=40, seed=16)
+    y, S_T, entry = run_fwd(p, "leaky", F32)
+    for k in ("x", "z", "u", "dy"):
+        p[k][:, 270:] = float("nan")
+    y2, S2, _ = run_fwd(p, "leaky", F32)
+    assert bool((y2[:, 270:] == GUARD).all()) and torch.equal(y2, y) and torch.equal(S2, S_T)
+    for g in kda.glr_bwd(p["x"], None, p["S0"], p["dy"], p["dS_T"], entry_states=entry, **kw(p, "leaky")):
+        assert bool(torch.isfinite(g[:, :270] if g.dim() == 3 and g.shape[1] == 310 else g).all())
+
+
 def test_bad_gradients_stay_in_their_sequence():
     lens = [300, 5, 256, 0, 190, 1]
     c = make(0, 2, 0, 64, F32, lens=lens, u=True, s0=True, seed=14)
