@@ -23,7 +23,7 @@
 // backward 102 us, 5.3 TB/s; 262144 rows of 128 with a gate, forward 39.6 us, 5.1 TB/s, backward 58.5
 // us, 5.7 TB/s. Without the next rows in flight both directions of the first take 299 us instead of
 // 169; with 1024 threads a row, 232. Rows off 8 elements: 1001 channels 72 and 135 us for the bytes of
-// the first; past 8192 channels 16384 takes 75 % (forward) and 59 % of the copy rate.
+// the first; 16384 channels take 75 % (forward) and 57 % of the copy rate, 10001 40 % and 19 %.
 #pragma once
 
 #include "kda_math.h"
@@ -110,8 +110,12 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* red) {
 }
 
 // A thread's channels of every row it works on: VEC from col on per vector, those inside [0, D).
-// ODD: rows may start off 8 elements.
-template <int VEC, int NV, int TPR, bool ODD>
+// ODD: rows may start off 8 elements. FRESH: which elements of a vector lie in the row is worked out
+// anew at every use. Kept over the rows, as the compiler would, the conditions take more scalar
+// registers than there are, which 1024 threads feel in the forward (rows of 10001 bf16 channels: 167
+// us against 227, 6001: 117 against 127); fewer threads and the backward rather have the issue slots
+// (1001, backward: 140 us against 174).
+template <int VEC, int NV, int TPR, bool ODD, bool FRESH>
 struct Cols {
     int col[NV];
     bool full[NV], any[NV];
@@ -125,16 +129,24 @@ struct Cols {
             full[j] = ODD ? col[j] >= 0 && col[j] + VEC <= a.D : any[j];
         }
     }
-    __device__ __forceinline__ bool in(const NormArgs& a, int j, int i) const {
-        return ODD ? col[j] + i >= 0 && col[j] + i < a.D : any[j];
+    struct In {   // whether element i of a vector lies in the row
+        int col, D;
+        bool any;
+        __device__ __forceinline__ bool operator()(int i) const {
+            return ODD ? col + i >= 0 && col + i < D : any;
+        }
+    };
+    __device__ __forceinline__ In in(const NormArgs& a, int j) const {
+        int c = col[j];
+        if (FRESH) asm volatile("" : "+v"(c));
+        return In{c, (int)a.D, any[j]};
     }
 };
 
 // The weights of a thread's channels: lp = scale lam w_post and r = w_pre, which is all either
 // direction needs. Kept in registers while there are at most 8 channels, else read at every use.
-template <int VEC, int NV, int TPR, bool ODD>
+template <int VEC, int NV, typename C>
 struct Weights {
-    using C = Cols<VEC, NV, TPR, ODD>;
     static constexpr bool KEEP = VEC * NV <= 8;
     float lp[KEEP ? NV : 1][VEC], r[KEEP ? NV : 1][VEC];
 
@@ -150,9 +162,10 @@ struct Weights {
             get(a.lam, l);
             get(a.w_pre, r[slot]);
         } else {
+            const auto in = c.in(a, j);
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (c.in(a, j, i)) {
+                if (in(i)) {
                     if (a.w_post) p[i] = a.w_post[c.col[j] + i];
                     if (a.lam) l[i] = a.lam[c.col[j] + i];
                     if (a.w_pre) r[slot][i] = a.w_pre[c.col[j] + i];
@@ -193,19 +206,21 @@ __device__ __forceinline__ void fetch(Raw<T, VEC>& r, const void* p, int64_t at,
 // Zeros for a partial vector's elements outside the row (the neighbouring rows').
 template <typename T, int VEC, typename C>
 __device__ __forceinline__ void mask(Raw<T, VEC>& r, const NormArgs& a, const C& c, int j) {
+    const auto in = c.in(a, j);
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-        if (!c.in(a, j, i)) clear(r, i);
+        if (!in(i)) clear(r, i);
 }
-template <typename T, int VEC, int NV, int TPR, bool ODD>
+template <typename T, int VEC, int NV, int TPR, bool ODD, bool FRESH>
 __device__ __forceinline__ void put(void* p, int64_t at, const float* x, const NormArgs& a,
-                                    const Cols<VEC, NV, TPR, ODD>& c, int j) {
+                                    const Cols<VEC, NV, TPR, ODD, FRESH>& c, int j) {
     if (c.full[j]) {
         store_vec<T, VEC>((T*)p + at, x);
     } else if (ODD && c.any[j]) {
+        const auto in = c.in(a, j);
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            if (c.in(a, j, i)) st_f((T*)p + at + i, x[i]);
+            if (in(i)) st_f((T*)p + at + i, x[i]);
     }
 }
 
@@ -218,9 +233,10 @@ __global__ __launch_bounds__(Geo<TPR>::threads) void norm_fwd_kernel(NormArgs a)
     const float inv = 1.f / (float)a.D;
     const int64_t step = (int64_t)gridDim.x * RPB, total = a.rows * a.D;
     int64_t row = (int64_t)blockIdx.x * RPB + grp;
-    Cols<VEC, NV, TPR, ODD> co;
+    using C = Cols<VEC, NV, TPR, ODD, ODD && TPR == 1024>;
+    C co;
     co.init(a, row);
-    Weights<VEC, NV, TPR, ODD> wt;
+    Weights<VEC, NV, C> wt;
     Raw<TI, VEC> f[NV], g[NV], fn[NV], gn[NV];
     Raw<TR, VEC> x[NV], xn[NV];
     auto next = [&](int64_t at_row) {
@@ -304,9 +320,10 @@ __global__ __launch_bounds__(Geo<TPR>::threads, (bwd_waves<TI, TR, TO, VEC, NV, 
     const float inv = 1.f / (float)a.D;
     const int64_t step = (int64_t)gridDim.x * RPB, total = a.rows * a.D;
     int64_t row = (int64_t)blockIdx.x * RPB + grp;
-    Cols<VEC, NV, TPR, ODD> co;
+    using Co = Cols<VEC, NV, TPR, ODD, false>;
+    Co co;
     co.init(a, row);
-    Weights<VEC, NV, TPR, ODD> wt;
+    Weights<VEC, NV, Co> wt;
     float acc[2][LEAN ? 1 : NV][VEC];      // this thread's columns of Q and dw_pre
     auto slot = [&](int k, int j, int i) -> float& {
         if constexpr (LEAN) return colsum[k * C + (j * VEC + i) * TPR + lane];
@@ -441,7 +458,7 @@ __global__ __launch_bounds__(Geo<TPR>::threads, (bwd_waves<TI, TR, TO, VEC, NV, 
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    if (co.in(a, j, i)) colsum[grp * C + co.col[j] + i] = slot(k, j, i);
+                    if (co.in(a, j)(i)) colsum[grp * C + co.col[j] + i] = slot(k, j, i);
             lds_barrier();
             for (int c = threadIdx.x; c < a.D; c += Geo<TPR>::threads) {
                 float s = 0.f;
@@ -453,7 +470,7 @@ __global__ __launch_bounds__(Geo<TPR>::threads, (bwd_waves<TI, TR, TO, VEC, NV, 
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    if (co.in(a, j, i)) ws[co.col[j] + i] = slot(k, j, i);
+                    if (co.in(a, j)(i)) ws[co.col[j] + i] = slot(k, j, i);
         }
     }
 }
