@@ -65,6 +65,7 @@ CASES = [
     (7, 5000, F32, F32, dict(pre=False)),
     (2, 8192, BF16, BF16, {}),
     (3, 11111, BF16, BF16, {}),
+    (3, 10001, F32, F32, {}),
     (2, 16384, F32, F32, {}),
     (3, 12000, BF16, F32, dict(gate=False)),
     # more rows than workgroups, rows off 8 elements
