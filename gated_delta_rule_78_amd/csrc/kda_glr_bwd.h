@@ -59,14 +59,14 @@ __global__ __launch_bounds__(THREADS, (2 * groups_a_cu<Z, TIn, VEC>())) void glr
     }
     c = (uint32_t)ws.nt - 1 - c;   // the last tile first
     const int64_t block0 = (int64_t)(chain / ntc) * per;   // the tile's first block of rows
-    const int ch_tile = (int)(chain % ntc) * kCW;
+    const uint32_t tile = chain % ntc;                      // across the head's channels
     const uint32_t d = (uint32_t)a.d;
-    const Place<NARROW, VEC> at(ct * VEC, ch_tile, d, a.blocks - block0);
+    const Place<NARROW, VEC> at(ct * VEC, tile, d, a.blocks - block0);
     const bool on = at.on;
     const uint32_t ch0 = at.ch;
     const int64_t block = block0 + at.local;
     // as a lane of one channel: the block, the channel, and whether there is one
-    const Place<NARROW, VEC> own(lane / VEC * VEC, ch_tile, d, a.blocks - block0);
+    const Place<NARROW, VEC> own(lane / VEC * VEC, tile, d, a.blocks - block0);
     const bool has_ch = own.on;
     const int64_t block_l = block0 + own.local;
     const uint32_t ch = own.ch + lane % VEC;

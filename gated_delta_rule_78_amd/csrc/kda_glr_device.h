@@ -1,9 +1,11 @@
 // Device code shared by the gated linear recurrence's kernels: the gates and their derivatives, the
-// composition of row spans, the tile geometry and the chain that carries states between tiles.
+// composition of row spans and the chain that carries states between tiles (their geometry:
+// kda_glr_tiles.h).
 #pragma once
 
 #include "kda_glr.h"
 #include "kda_glr_internal.h"
+#include "kda_glr_tiles.h"
 #include "kda_math.h"
 
 namespace kda {
@@ -52,50 +54,6 @@ __device__ __forceinline__ Span compose(Span l, Span r) {
     return o;
 }
 
-// A tile is some rows of kCW channels, in the registers of THREADS threads: CT lanes lie across the
-// channels with VEC channels each (VEC = 4, or 1 for heads of fewer), and each run of CT lanes owns L
-// consecutive rows, a sub-chunk. Where the channels are no multiple of VEC, the last lane's are the
-// head's last VEC: those it shares with its neighbour are computed, and written, twice alike.
-constexpr int kCW = 64;
-template <int VEC, int L, int THREADS>
-struct Tile {
-    static constexpr int CT = kCW / VEC;            // threads across the channels
-    static constexpr int SPW = 64 / CT;             // sub-chunks per wave
-    static constexpr int W = THREADS / 64;          // waves
-    static constexpr int ROWS = THREADS / CT * L;
-};
-
-// Narrow heads (d <= kCW / 2) lie side by side in a tile: 4-channel slots of ceil(d / 4) a head.
-__host__ __device__ inline uint32_t heads_a_tile(int64_t d) {
-    return d > kCW / 2 || d < 4 ? 1 : kCW / (((uint32_t)d + 3) & ~3u);
-}
-// Tiles across the channels, all blocks together: the chains.
-__host__ __device__ inline int64_t chain_count(int64_t blocks, int64_t d, bool narrow) {
-    const int64_t n = narrow ? heads_a_tile(d) : 1;
-    return n > 1 ? (blocks + n - 1) / n : blocks * ((d + kCW - 1) / kCW);
-}
-// Where a thread's VEC channels lie that has the tile's slot'th channel: the block counted from the
-// tile's first (`left` of them are there), the first channel, and whether there are any.
-template <bool NARROW, int VEC>
-struct Place {
-    uint32_t local, ch;
-    bool on;
-    __device__ __forceinline__ Place(int slot, int ch_tile, uint32_t d, int64_t left) {
-        local = 0;
-        if constexpr (NARROW) {
-            const uint32_t width = (d + 3) & ~3u;
-            local = (uint32_t)slot / width;
-            slot -= (int)(local * width);
-            on = local < kCW / width && local < left;
-            if (!on) local = 0;
-        } else {
-            slot += ch_tile;
-            on = slot < (int)d;
-        }
-        ch = slot + VEC <= (int)d ? slot : d - VEC;
-    }
-};
-
 // ---- the chain -------------------------------------------------------------------------------
 // Tiles of one block of rows and channel tile form a chain. A tile publishes its span as one
 // 64-bit word per channel as soon as it has read its rows, and the state behind it as another once
@@ -105,23 +63,6 @@ struct Place {
 // workgroup that started earlier and itself only waits for earlier ones: every wait ends. One
 // counter for all chains holds the launch back: a word takes an atomic every 14 ns (64K rows x 4096
 // channels: 445 us with one counter).
-constexpr uint32_t kCounters = 1024, kCounterStride = 32;   // a counter per cache line
-
-// The chain of the p'th workgroup of a round over all of them. Workgroups go to the 8 XCDs in turn, so
-// neighbouring chains get places 8 apart: where rows do not start on cache lines, chains of the same
-// rows share lines, which one L2 then holds and writes whole (8 x 4096 rows of 1001 bf16 channels: 43 us
-// against 63; 64 x 4096 rows of 100: 38 against 54).
-__device__ __forceinline__ uint32_t chain_of(uint32_t p, uint32_t chains) {
-    const uint32_t x = p % 8, each = chains / 8, more = chains % 8;
-    return x * each + (x < more ? x : more) + p / 8;
-}
-
-// The tile of ticket k: a counter serves every kCounters-th chain, first tiles first.
-__device__ __forceinline__ void next_tile(uint32_t k, uint32_t chains, uint32_t& c, uint32_t& chain) {
-    const uint32_t g = chain % kCounters, n = (chains - g + kCounters - 1) / kCounters;
-    c = k / n;
-    chain = g + kCounters * (k % n);
-}
 
 typedef unsigned long long u64;
 constexpr u64 kNone = ~0ull;
@@ -268,7 +209,7 @@ __device__ __forceinline__ void load_f32(const float* p, float* o) {
     __builtin_memcpy(o, p, VEC * 4);
 }
 
-// Which sequences start and end in the rows of a packed batch (kda_glr_prepare_kernel): a bit per
+// Which sequences start and end in the rows of a packed batch (glr_prepare_kernel): a bit per
 // row, and the sequence where the bit is set. bits_at: those of the L rows from row on (L divides
 // 32, row a multiple of L).
 template <int L>
