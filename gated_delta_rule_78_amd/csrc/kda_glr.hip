@@ -1,5 +1,6 @@
 // Gated linear recurrence for gfx950: workspaces, plans and dispatch.
 #include "kda_glr_device.h"
+#include "kda_glr_plan.h"
 #include "kda_internal.h"
 
 namespace kda {
@@ -98,16 +99,16 @@ __global__ __launch_bounds__(1024) void glr_dA_kernel(GlrArgs a, GlrWs ws, int64
 
 static hipError_t launch_dA(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
     const int64_t n = (a.packed ? 1 : a.N) * ws.nt;
-    const unsigned gx = (unsigned)((a.d + 63) / 64 * a.H);
+    const unsigned gx = (unsigned)dA_groups(a);
     int64_t chunk = 1;
     if (n > 512) {
         chunk = 256;
         while (chunk * chunk < n) chunk *= 2;
-        hipLaunchKernelGGL(glr_dA_kernel, dim3(gx, (unsigned)((n + chunk - 1) / chunk)), dim3(1024), 0, st, a, ws, n, chunk, false);
+        hipLaunchKernelGGL(glr_dA_kernel, dim3(gx, (unsigned)((n + chunk - 1) / chunk)), dim3(kDAThreads), 0, st, a, ws, n, chunk, false);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(glr_dA_kernel, dim3(gx), dim3(1024), 0, st, a, ws, n, chunk, true);
+    hipLaunchKernelGGL(glr_dA_kernel, dim3(gx), dim3(kDAThreads), 0, st, a, ws, n, chunk, true);
     return hipGetLastError();
 }
 
@@ -119,16 +120,13 @@ struct Plan {
 
 static Plan make_plan(const GlrArgs& a, unsigned char* base, bool backward) {
     Plan p{};
-    p.ws.vec = a.d >= 4 ? 4 : 1;
-    const int rows = backward ? kBwdRows : p.ws.vec == 4 ? kFwdRows : kFwdRows1;
+    const Tiling t = tiling(a, backward);
+    const int64_t rows = t.rows;
     const bool with_dA = backward && a.z;
+    p.ws.vec = t.vec;
     p.ws.rows = rows;
-    p.ws.nt = (a.T + rows - 1) / rows;
-    // Narrow heads share tiles where one each would fill the GPU (1024 x 4096 rows of 8 channels: 70 us
-    // against 180); fewer stay apart, each tile's work being a wave's latency (8 x 4096 rows: 15.8 us
-    // against 16.3, 4 x 20000 rows of 16 channels: 26.5 against 30.3). 32-bit offsets inside a tile.
-    const int64_t per = heads_a_tile(a.d);
-    p.ws.narrow = per > 1 && a.blocks * p.ws.nt >= 1024 && per * a.T * a.d < (int64_t)1 << 31;
+    p.ws.nt = t.nt;
+    p.ws.narrow = t.narrow;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         unsigned char* r = base ? base + at : nullptr;
@@ -182,16 +180,6 @@ static hipError_t launch_bwd_tiles(const GlrArgs& a, const GlrWs& ws, hipStream_
     return a.packed ? launch_bwd_s<true, float>(a, ws, st) : launch_bwd_s<false, float>(a, ws, st);
 }
 
-// Whether a thread per channel walks the rows one by one (kda_glr_rows.hip) instead of tiles of 256
-// of them: short sequences, which would leave a tile's threads idle, and middling ones where there
-// are channels enough to fill the GPU. bf16 with gates, 32 heads of 128 channels, by rows / in tiles:
-// 512 x 16 rows 49 us / 560, 64 x 64 rows 31 / 75, 64 x 128 rows 70 / 82; 16 x 64 rows 29 / 23,
-// 4 x 64 rows 28 / 13.
-static bool by_rows(const GlrArgs& a) {
-    if (a.packed || a.T > KDA_GLR_CHUNK) return false;
-    return a.T <= 16 || a.blocks * a.d >= (int64_t)1 << 18;
-}
-
 }  // namespace glr
 
 size_t glr_fwd_ws_bytes(const GlrArgs& a) { return glr::make_plan(a, nullptr, false).bytes; }
@@ -225,7 +213,7 @@ hipError_t launch_glr_bwd(const GlrArgs& a, hipStream_t st) {
     const glr::Plan p = glr::make_plan(a, a.ws, true);
     GlrArgs b = a;
     hipError_t e = hipSuccess;
-    if (!a.packed && a.T <= glr::kRowsBwd) {   // too few rows for a tile's threads
+    if (glr::bwd_by_rows(a)) {
         e = glr::launch_rows_bwd(a, p.ws.dA, st);
     } else {
         if (!b.entry) {   // the forward again, for its entry states alone

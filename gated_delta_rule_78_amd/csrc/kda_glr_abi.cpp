@@ -6,6 +6,7 @@
 
 #include "kda_check.h"
 #include "kda_glr_internal.h"
+#include "kda_glr_plan.h"
 
 namespace {
 
@@ -58,7 +59,8 @@ extern "C" {
 
 size_t kda_glr_fwd_workspace_bytes(const kda_glr_desc* d) {
     if (check_desc(d, false) != KDA_OK || d->T == 0) return 0;
-    return kda::glr_fwd_ws_bytes(to_args(d, nullptr));
+    const GlrArgs a = to_args(d, nullptr);
+    return kda::glr::fwd_launchable(a) ? kda::glr_fwd_ws_bytes(a) : 0;
 }
 
 kda_status kda_glr_fwd(const kda_glr_desc* d, const void* x, const kda_glr_gates* gates, const int32_t* cu_seqlens,
@@ -75,6 +77,7 @@ kda_status kda_glr_fwd(const kda_glr_desc* d, const void* x, const kda_glr_gates
         if (gs != KDA_OK) return gs;
     }
     GlrArgs a = to_args(d, rows ? gates : nullptr);
+    if (!kda::glr::fwd_launchable(a)) return KDA_ERR_UNSUPPORTED;
     const int64_t n = a.blocks * d->T * d->d, ein = elem_bytes(d->in_dtype), eout = elem_bytes(d->out_dtype);
     const int64_t states = d->N * d->H * d->d * 4;
     const size_t need = rows ? kda::glr_fwd_ws_bytes(a) : 0;
@@ -101,7 +104,7 @@ size_t kda_glr_bwd_workspace_bytes(const kda_glr_desc* d, int32_t has_entry_stat
     static float some;
     a.entry = has_entry_states ? &some : nullptr;   // only whether they are there is looked at
     a.z = has_z ? &some : nullptr;
-    return kda::glr_bwd_ws_bytes(a);
+    return kda::glr::bwd_launchable(a) ? kda::glr_bwd_ws_bytes(a) : 0;
 }
 
 kda_status kda_glr_bwd(const kda_glr_desc* d, const void* x, const kda_glr_gates* gates, const int32_t* cu_seqlens,
@@ -125,6 +128,7 @@ kda_status kda_glr_bwd(const kda_glr_desc* d, const void* x, const kda_glr_gates
     const int64_t ein = elem_bytes(d->in_dtype), eout = elem_bytes(d->out_dtype);
     const int64_t states = d->N * d->H * d->d * 4;
     a.entry = rows ? const_cast<float*>(entry_states) : nullptr;
+    if (!kda::glr::bwd_launchable(a)) return KDA_ERR_UNSUPPORTED;
     const size_t need = rows ? kda::glr_bwd_ws_bytes(a) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (cu_seqlens && !kda::aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
@@ -152,6 +156,7 @@ kda_status kda_glr_step(const kda_glr_desc* d, const void* x, const kda_glr_gate
     kda_glr_desc one = *d;
     one.T = 1; one.packed = 0;
     GlrArgs a = to_args(&one, gates);
+    if (!kda::glr::step_launchable(a)) return KDA_ERR_UNSUPPORTED;
     const int64_t n = d->N * d->H * d->d, ein = elem_bytes(d->in_dtype), eout = elem_bytes(d->out_dtype);
     const Operand in[] = {{x, n * ein, ein}, {a.la, n * ein, ein}, {a.z, n * ein, ein}, {a.u, n * ein, ein},
                           {a.A_log, d->H * d->d * 4, 4}};

@@ -18,6 +18,7 @@
 #pragma once
 
 #include "kda_glr_device.h"
+#include "kda_glr_plan.h"
 
 namespace kda {
 namespace glr {
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(THREADS, (2 * groups_a_cu<Z, TIn, VEC>())) void glr
 
 template <int SCALE, bool PACKED, bool NARROW, int Z, int U, typename TIn, int VEC, int L, int THREADS>
 static hipError_t launch_bwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
-    static_assert(Tile<VEC, L, THREADS>::ROWS == kBwdRows, "the plan's tile");
+    static_assert(THREADS == kTileThreads && Tile<VEC, L, THREADS>::ROWS == kBwdRows, "the plan's tile");
     const dim3 grid((unsigned)(chain_count(a.blocks, a.d, NARROW) * ws.nt));
     if (a.out_bf16)
         hipLaunchKernelGGL((glr_bwd_kernel<SCALE, PACKED, NARROW, Z, U, TIn, bf16_t, VEC, L, THREADS>), grid, dim3(THREADS), 0, st, a, ws);

@@ -16,6 +16,7 @@
 #pragma once
 
 #include "kda_glr_device.h"
+#include "kda_glr_plan.h"
 
 namespace kda {
 namespace glr {
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(THREADS, 4) void glr_fwd_kernel(GlrArgs a, GlrWs ws
 
 template <int SCALE, bool PACKED, bool NARROW, int Z, int U, typename TIn, int VEC, int L, int THREADS>
 static hipError_t launch_fwd_k(const GlrArgs& a, const GlrWs& ws, hipStream_t st) {
-    static_assert(Tile<VEC, L, THREADS>::ROWS == (VEC == 4 ? kFwdRows : kFwdRows1), "the plan's tile");
+    static_assert(THREADS == kTileThreads && Tile<VEC, L, THREADS>::ROWS == (VEC == 4 ? kFwdRows : kFwdRows1), "the plan's tile");
     hipLaunchKernelGGL((glr_fwd_kernel<SCALE, PACKED, NARROW, Z, U, TIn, VEC, L, THREADS>),
                        dim3((unsigned)(chain_count(a.blocks, a.d, NARROW) * ws.nt)), dim3(THREADS), 0, st, a, ws);
     return hipGetLastError();

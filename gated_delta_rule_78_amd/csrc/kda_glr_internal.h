@@ -57,7 +57,8 @@ hipError_t launch_fwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
 template <int SCALE, bool PACKED, typename TIn>
 hipError_t launch_bwd_t(const GlrArgs& a, const GlrWs& ws, hipStream_t st);
 
-// The forward of blocks of at most KDA_GLR_CHUNK rows, a thread per channel (kda_glr_rows.hip).
+// The forward of blocks of at most KDA_GLR_CHUNK rows, a thread per 4 channels, or per channel where 4
+// do not divide them (kda_glr_rows.hip).
 hipError_t launch_rows(const GlrArgs& a, hipStream_t st);
 // The backward of blocks of at most kRowsBwd rows; `parts`: [blocks][d] parts of dA_log (with z).
 constexpr int kRowsBwd = 16;

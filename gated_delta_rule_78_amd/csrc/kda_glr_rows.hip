@@ -5,16 +5,17 @@
 // divides the channels (no two threads may share one: states are updated in place), else 1. At most
 // one chunk of rows, so the only entry state is S0.
 #include "kda_glr_device.h"
+#include "kda_glr_plan.h"
 
 namespace kda {
 namespace glr {
 
 // Z, U: whether the decay comes from z and whether there is an input gate.
 template <int SCALE, int Z, int U, typename TIn, int VEC>
-__global__ __launch_bounds__(256) void glr_rows_kernel(GlrArgs a) {
+__global__ __launch_bounds__(kRowsThreads) void glr_rows_kernel(GlrArgs a) {
     constexpr int AHEAD = 4;        // rows in flight
     const uint32_t per = (uint32_t)(a.d / VEC);
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = a.blocks * per;
+    const int64_t i = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x, all = a.blocks * per;
     if (i >= all) return;
     const int64_t block = all >> 32 ? i / per : (uint32_t)i / per;
     const int64_t ch0 = (i - block * per) * VEC;
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(256) void glr_rows_kernel(GlrArgs a) {
 
 template <int SCALE, typename TIn, int VEC>
 static hipError_t launch_rows_v(const GlrArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.blocks * (a.d / VEC) + 255) / 256)), threads(256);
+    const dim3 grid((unsigned)rows_groups(a)), threads(kRowsThreads);
     if (a.z && a.u) hipLaunchKernelGGL((glr_rows_kernel<SCALE, 1, 1, TIn, VEC>), grid, threads, 0, st, a);
     else if (a.z) hipLaunchKernelGGL((glr_rows_kernel<SCALE, 1, 0, TIn, VEC>), grid, threads, 0, st, a);
     else if (a.u) hipLaunchKernelGGL((glr_rows_kernel<SCALE, 0, 1, TIn, VEC>), grid, threads, 0, st, a);
@@ -104,9 +105,9 @@ hipError_t launch_rows(const GlrArgs& a, hipStream_t st) {
 // The backward of blocks of at most kRowsBwd rows (formulas: kda_glr_bwd.h): the states before each
 // row in registers, then the rows from the last to the first, read again from the caches.
 template <int SCALE, typename TIn, typename TOut, int VEC>
-__global__ __launch_bounds__(256) void glr_rows_bwd_kernel(GlrArgs a, float* parts) {
+__global__ __launch_bounds__(kRowsThreads) void glr_rows_bwd_kernel(GlrArgs a, float* parts) {
     const uint32_t per = (uint32_t)(a.d / VEC);
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, all = a.blocks * per;
+    const int64_t i = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x, all = a.blocks * per;
     if (i >= all) return;
     const int64_t block = all >> 32 ? i / per : (uint32_t)i / per;
     const int64_t ch0 = (i - block * per) * VEC;
@@ -203,13 +204,9 @@ __global__ __launch_bounds__(256) void glr_rows_bwd_kernel(GlrArgs a, float* par
 
 template <int SCALE, typename TIn, typename TOut>
 static hipError_t launch_rows_bwd_t(const GlrArgs& a, float* parts, hipStream_t st) {
-    const dim3 threads(256);
-    if (a.d % 4 == 0)
-        hipLaunchKernelGGL((glr_rows_bwd_kernel<SCALE, TIn, TOut, 4>), dim3((unsigned)((a.blocks * (a.d / 4) + 255) / 256)),
-                           threads, 0, st, a, parts);
-    else
-        hipLaunchKernelGGL((glr_rows_bwd_kernel<SCALE, TIn, TOut, 1>), dim3((unsigned)((a.blocks * a.d + 255) / 256)),
-                           threads, 0, st, a, parts);
+    const dim3 grid((unsigned)rows_groups(a)), threads(kRowsThreads);
+    if (a.d % 4 == 0) hipLaunchKernelGGL((glr_rows_bwd_kernel<SCALE, TIn, TOut, 4>), grid, threads, 0, st, a, parts);
+    else hipLaunchKernelGGL((glr_rows_bwd_kernel<SCALE, TIn, TOut, 1>), grid, threads, 0, st, a, parts);
     return hipGetLastError();
 }
 

@@ -23,6 +23,10 @@
  *    own channel and sequence non-finite (also past alpha = 0), and no others.
  *  - Every tensor is dense, its base aligned to its element; workspaces are aligned to 16 bytes.
  *  - Every sum runs in a fixed order: the same inputs give the same bits on every call.
+ *  - A launch has fewer than 2^32 threads. A call that would need more is refused with
+ *    KDA_ERR_UNSUPPORTED, and its workspace query answers 0: from 2^23 tiles on (at most 64 channels
+ *    by 256 rows of a block, 128 rows in the backward and for d < 4), 2^22 heads with z in the
+ *    backward (d <= 64), or 2^34 channels of all sequences in a step or in 16 rows and fewer.
  */
 #ifndef KDA_GLR_H
 #define KDA_GLR_H
