@@ -109,6 +109,13 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* red) {
     }
 }
 
+// 1 / sqrt(v), v > 0. The hardware's root takes subnormal numbers for zero (a row of zeros with an eps
+// that small has one); they are scaled by an even power of two.
+__device__ __forceinline__ float inv_root(float v) {
+    const bool small = v < 0x1p-126f;
+    return __builtin_amdgcn_rsqf(small ? v * 0x1p100f : v) * (small ? 0x1p50f : 1.f);
+}
+
 // A thread's channels of every row it works on: VEC from col on per vector, those inside [0, D).
 // ODD: rows may start off 8 elements. FRESH: which elements of a vector lie in the row is worked out
 // anew at every use. Kept over the rows, as the compiler would, the conditions take more scalar
@@ -270,7 +277,7 @@ __global__ __launch_bounds__(Geo<TPR>::threads) void norm_fwd_kernel(NormArgs a)
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) s[0] = fmaf(at(f[j], i), at(f[j], i), s[0]);
             row_sum<TPR>(s, red[phase][0][grp]);
-            r1 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps));
+            r1 = inv_root(fmaf(s[0], inv, a.eps));
         }
         float xo[NV][VEC];
         float s2[1] = {0.f};
@@ -288,7 +295,7 @@ __global__ __launch_bounds__(Geo<TPR>::threads) void norm_fwd_kernel(NormArgs a)
         }
         if (!a.pre) continue;
         row_sum<TPR>(s2, red[phase][1][grp]);
-        const float r2 = __builtin_amdgcn_rsqf(fmaf(s2[0], inv, a.pre_eps));
+        const float r2 = inv_root(fmaf(s2[0], inv, a.pre_eps));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int k = wt.at(a, co, j);
@@ -374,7 +381,7 @@ __global__ __launch_bounds__(Geo<TPR>::threads, (bwd_waves<TI, TR, TO, VEC, NV, 
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) s[0] = fmaf(at(f[j], i), at(f[j], i), s[0]);
             row_sum<TPR>(s, red[phase][grp][0]);
-            r1 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps));
+            r1 = inv_root(fmaf(s[0], inv, a.eps));
         }
         // the gate; x' again, and the pre-norm's part of its gradient
         float r2 = 0.f, m2 = 0.f;
@@ -402,7 +409,7 @@ __global__ __launch_bounds__(Geo<TPR>::threads, (bwd_waves<TI, TR, TO, VEC, NV, 
             }
             if (a.dn) {
                 row_sum<TPR>(s, red[phase][grp][1]);
-                r2 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.pre_eps));
+                r2 = inv_root(fmaf(s[0], inv, a.pre_eps));
                 m2 = s[1] * inv * r2;   // mean(t xh)
             }
         }
