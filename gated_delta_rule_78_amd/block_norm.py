@@ -86,8 +86,9 @@ def block_norm_fwd(f, x=None, *, gate=None, norm_weight=None, post_norm=True, ep
         n = pre_weight * x_out / sqrt(mean(x_out^2) + pre_eps)
     Returns (x_out, n): x_out in x's type (``res_dtype``, default f's type, without x), None with
     ``store_x=False``; n in ``out_dtype`` (default f's type), None with ``pre_norm=False``.
-    ``x_out=x`` updates the residual stream in place. Caller-supplied outputs are checked like the
-    inputs; the others are allocated on ``stream``."""
+    ``x_out=x`` updates the residual stream in place. The sums of a row's squares must be finite in
+    fp32. Caller-supplied outputs are checked like the inputs; the others are allocated on
+    ``stream``."""
     dev, index, shape = f.device, f.get_device(), f.shape
     rows, D = _inputs(f, index, shape, x, gate, norm_weight, post_norm, scale_weight, pre_norm, pre_weight)
     res_dtype = x.dtype if x is not None else (res_dtype or (x_out.dtype if x_out is not None else f.dtype))

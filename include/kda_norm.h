@@ -14,8 +14,10 @@
  *
  *  - Weights are fp32 and NULL means ones. Everything in between is fp32: n is computed from
  *    x_out before x_out is rounded; every output is rounded once.
- *  - 1 <= D <= KDA_NORM_MAX_D. The mean squares must be finite in fp32; a row that holds a
- *    non-finite value gives non-finite outputs in its own row (and weight gradients), no others.
+ *  - 1 <= D <= KDA_NORM_MAX_D. The sums of a row's squares, of f and of x_out, must be finite in
+ *    fp32, not their means alone: past that (values of 2^57 in all of 16384 channels) the norm is
+ *    0. A row that holds a non-finite value gives non-finite outputs in its own row (and weight
+ *    gradients), no others.
  *  - Every tensor is dense, its base aligned to its element (16-byte bases take wide accesses);
  *    workspaces are aligned to 16 bytes. Sums over rows run in a fixed order:
  *    the same inputs give the same bits on every call.

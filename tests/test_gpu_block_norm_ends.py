@@ -1,5 +1,5 @@
-"""The block norms where fp32 ends: an eps below its normal numbers, with rows of zeros, whose root is then
-taken of eps alone."""
+"""The block norms where fp32 ends: an eps below its normal numbers with rows of zeros, whose root is then
+taken of eps alone, and rows whose sum of squares is near the largest number."""
 import numpy as np
 import pytest
 import torch
@@ -33,3 +33,22 @@ def test_subnormal_eps(D, dt, eps, pre_eps):
     for key, t in got.items():
         check("ends", t, ref, key, F32 if key in ("dw_post", "dlam", "dw_pre") else dt)
     assert not bool(got["x_out"][0].any()) and not bool(got["n"][0].any())
+
+
+@pytest.mark.parametrize("D,dt", [(64, F32), (1001, BF16), (4096, BF16), (16384, F32)])
+def test_largest_values(D, dt):
+    """Rows whose sum of squares is just finite: 3/4 of the largest number in fp32, in f and in x_out."""
+    say("largest values, %d channels" % D)
+    c = make(3, D, dt, F32, gate=False, seed=12)
+    big = (0.75 * 2.0 ** 128 / D) ** 0.5
+    c["f"][0] = (torch.where(c["f"][0] < 0, -big, big) * (1 - 2.0 ** -8)).to(dt)      # rounds to at most big
+    c["x"][1] = torch.where(c["x"][1] < 0, -big, big)
+    kw = dict(norm_weight=c["w_post"], eps=1e-6, scale=0.7, scale_weight=c["lam"], pre_weight=c["w_pre"], pre_eps=1e-6)
+    got = dict(zip(("x_out", "n"), kda.block_norm_fwd(c["f"], c["x"], **kw)))
+    got.update(zip(("df", "dx"), kda.block_norm_bwd(c["f"], c["x"], c["dxo"], c["dn"], **kw)[:2]))
+    r32 = lambda v: float(np.float32(v))
+    ref = block_norm.evaluate(*[host32(c[k]) if c[k] is not None else None for k in ("f", "x", "gate", "w_post", "lam", "w_pre")],
+                              post=True, pre=True, scale=r32(0.7), eps=r32(1e-6), pre_eps=r32(1e-6), dxo=host32(c["dxo"]),
+                              dn=host32(c["dn"]))
+    for key, t in got.items():
+        check("ends", t, ref, key, dt if key in ("n", "df") else F32)
