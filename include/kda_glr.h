@@ -47,7 +47,8 @@ typedef enum kda_glr_scale {
     KDA_GLR_ONE = 0,    /* w = 1                                                                */
     KDA_GLR_LEAKY = 1,  /* w = 1 - alpha                                                        */
     KDA_GLR_NORM = 2    /* w = sqrt(1 - alpha^2); the backward takes dw/dlog_alpha = 0 at
-                           alpha = 1, where w = 0 and the derivative has no value              */
+                           alpha = 1, where w = 0 and the derivative has no value. Log decays
+                           within 2^-126 of 0 (subnormal ones) may count as 0                  */
 } kda_glr_scale;
 
 /* Shape and types of one call over a batch of sequences. */
