@@ -62,7 +62,8 @@ __device__ __forceinline__ Span compose(Span l, Span r) {
 // takes its tile from its chain's counter, in chain order, so every tile it waits for is held by a
 // workgroup that started earlier and itself only waits for earlier ones: every wait ends. One
 // counter for all chains holds the launch back: a word takes an atomic every 14 ns (64K rows x 4096
-// channels: 445 us with one counter).
+// channels: 445 us with one counter). The method is the published single-pass scan with decoupled
+// look-back (Merrill and Garland, 2016).
 
 typedef unsigned long long u64;
 constexpr u64 kNone = ~0ull;
@@ -119,7 +120,7 @@ __device__ __forceinline__ float look_back(const u64* span, const u64* state, in
         }
         __builtin_amdgcn_s_sleep(2);
     }
-    return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(0x7fc00000u);   // gave up, which the order of the tiles rules out: NaN from here on
 }
 
 // Spans of a wave's threads (SPW sub-chunks of CT threads, VEC channels each), turned through LDS so

@@ -22,6 +22,10 @@
  *    decays give undefined numbers. A non-finite x, decay or state makes the later outputs of its
  *    own channel and sequence non-finite (also past alpha = 0), and no others.
  *  - Every tensor is dense, its base aligned to its element; workspaces are aligned to 16 bytes.
+ *  - Long sequences pass their states between workgroups of one launch, which wait for each other.
+ *    The order in which they start lets every wait end. Each is bounded all the same (2^26 looks,
+ *    over half a minute): one that gave up would hand on NaN, which makes the outputs behind it NaN
+ *    while the call has long returned KDA_OK.
  *  - Every sum runs in a fixed order: the same inputs give the same bits on every call.
  *  - A launch has fewer than 2^32 threads. A call that would need more is refused with
  *    KDA_ERR_UNSUPPORTED, and its workspace query answers 0: from 2^23 tiles on (at most 64 channels
