@@ -29,7 +29,10 @@ def ptr(t):
 def scope(index, stream):
     """Context of a launch and of its allocations: ``index`` is the current device (a launch on a
     device's default stream goes to the device that is current), and with ``stream`` the current
-    stream, so that the caching allocator ties the blocks to the stream the kernels run on."""
+    stream, so that the caching allocator ties the blocks to the stream the kernels run on. A stream of
+    another device is refused: its kernels would run there, on memory of this one."""
+    if stream is not None and stream.device.index != index:
+        raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, index))
     here = index == _current_device()
     if stream is None and here:
         return _NOTHING
