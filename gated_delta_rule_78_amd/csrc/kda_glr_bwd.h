@@ -12,9 +12,10 @@
 // were read: 128 registers a thread hold no more, and 168 would leave one workgroup a CU (no LDS:
 // 270 us for both directions of the shape below, against 200; 256 threads of 8 rows: 211 against 202).
 //
-// Measured, bf16 with both gates and w = sqrt(1 - alpha^2): 2 x 4096 rows of 4096 channels 121 us for
-// 470 MB read and written, 3.9 TB/s; its issue slots and the latency of a tile's start, with two
-// workgroups a CU, share the bound.
+// Measured, bf16 with both gates and w = sqrt(1 - alpha^2): 2 x 4096 rows of 4096 channels 122 us for
+// 470 MB read and written, 3.8 TB/s; its issue slots (85 an element, 60 % of the SIMDs' by counters) and
+// the latency of a tile's start, with two workgroups a CU, share the bound. Packed batches spill there
+// (24 registers a thread): 12 sequences, 32 x 8192 rows of 128 channels, take 191 us.
 #pragma once
 
 #include "kda_glr_device.h"

@@ -2,8 +2,8 @@
 //     h_t = alpha_t h_{t-1} + w(alpha_t) i_t x_t,   y_t = h_t.
 //
 // The operator moves one word in per tensor and one out per element, so HBM bounds it and every
-// input should be read once; the gates' exponentials and roots come close behind (about 50 issue
-// slots an element with every gate). The rows of a block are split into tiles: a workgroup holds
+// input should be read once; the gates' exponentials and roots come close behind (46 issue
+// slots an element with every gate, 28 with log decays, by counters). The rows of a block are split into tiles: a workgroup holds
 // its tile's decays and inputs in registers, reduces them to the tile's span h -> A h + b (a scan
 // over threads, waves and LDS), gets the state before the tile from the chain of the tiles before
 // it (kda_glr_device.h), and runs the recurrence again from there with the rows still in registers.
@@ -11,8 +11,8 @@
 // nothing, are usually there.
 //
 // Measured, bf16 (kernel alone): 32 x 64K rows of 128 channels with log decays 343 us, 4.7 TB/s; 32 x
-// 8K rows 42.4 us; 2 x 4096 rows of 4096 channels with both gates and w = sqrt(1 - alpha^2) 66.8 us,
-// 4.0 TB/s, where half of the issue slots go to the gates.
+// 8K rows 41.8 us; 2 x 4096 rows of 4096 channels with both gates and w = sqrt(1 - alpha^2) 67.6 us,
+// 4.0 TB/s.
 #pragma once
 
 #include "kda_glr_device.h"

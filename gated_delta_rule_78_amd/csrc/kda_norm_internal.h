@@ -25,9 +25,9 @@ namespace norm {
 
 // Workgroups at most: 24 waves a CU in the forward. In the backward 8 for rows on 8 elements that
 // read 4 or 5 tensors, whose streams then stay nearer to each other in HBM (5 of 32M bf16 elements:
-// 104-110 us, against 114-118 with 16); 16 for fewer tensors, which need more rows in flight (2 of
-// them: 51-65 us against 59-83), and where rows start off 8 elements (reads = 0), whose masks cost
-// issue slots (rows of 1001: 135 us against 204). One workgroup of 512 or 1024 threads a CU.
+// 104-111 us, against 111-120 with 16); 16 for fewer tensors, which need more rows in flight (2 of
+// them: 51-65 us against 60-84), and where rows start off 8 elements (reads = 0), whose masks cost
+// issue slots (rows of 1001: 132 us against 204). One workgroup of 512 or 1024 threads a CU.
 inline int fwd_groups(int threads) { return 256 * 24 * 64 / threads; }
 inline int bwd_groups(int threads, int reads) {
     const int waves = threads / 64, most = reads >= 4 || (reads && waves == 8) ? 8 : 16;

@@ -19,11 +19,12 @@
 // of 8 rows, which keeps that offset, and so every thread's channels, the same for all its rows.
 // Only a row's first and last vector are masked.
 //
-// Measured, bf16 (kernel alone): 8192 rows of 4096 with gate and residual, forward 61.3 us, 5.5 TB/s,
-// backward 102 us, 5.3 TB/s; 262144 rows of 128 with a gate, forward 39.6 us, 5.1 TB/s, backward 58.5
-// us, 5.7 TB/s. Without the next rows in flight both directions of the first take 299 us instead of
-// 169; with 1024 threads a row, 232. Rows off 8 elements: 1001 channels 72 and 135 us for the bytes of
-// the first; 16384 channels take 75 % (forward) and 57 % of the copy rate, 10001 40 % and 19 %.
+// Measured, bf16 (kernel alone): 8192 rows of 4096 with gate and residual, forward 61 us, 5.5 TB/s,
+// backward 104 us, 5.2 TB/s (fp32 122 and 197 us); 262144 rows of 128 with a gate, forward 38.9 us, 5.2
+// TB/s, backward 58.2 us, 5.8 TB/s. Without the next rows in flight both directions of the first take
+// 205 us instead of 183, one call after the other; with 1024 threads a row, 235. Rows off 8 elements:
+// 1001 channels 72 and 132 us for the bytes of the first. 16384 channels reach 71 % (forward) and 55 %
+// of the 5.3 TB/s of a copy, 10001 38 % and 17 %.
 #pragma once
 
 #include "kda_math.h"
