@@ -73,7 +73,8 @@ typedef struct kda_glr_desc {
 typedef struct kda_glr_gates {
     const void* log_alpha;   /* log decay, shape of x, in_dtype                                */
     const void* z;           /* decay pre-activation, shape of x, in_dtype                     */
-    const float* A_log;      /* [H,d] fp32 log scale of z                                      */
+    const float* A_log;      /* [H,d] fp32 log scale of z; g_min * exp(A_log) and g_min *      */
+                             /* log2(e) must be finite in fp32                                 */
     const void* in_gate;     /* input gate pre-activation, shape of x, in_dtype, or NULL       */
 } kda_glr_gates;
 
