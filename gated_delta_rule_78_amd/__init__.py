@@ -17,6 +17,11 @@ The elementwise operators around the core (``include/kda_glr.h``, ``include/kda_
 
     glr_fwd, glr_bwd, glr_step          gated linear recurrence: prefill, backward, one token
     block_norm_fwd, block_norm_bwd      post-norm, gate, residual and pre-norm; their backward
+
+The attention layers between KDA layers (``include/kda_attn.h``):
+
+    head_rope_fwd, head_rope_bwd        per-head norm of q and k with the position rotation
+    kv_append                           new tokens' keys and values into a paged cache
 """
 import contextlib
 import ctypes
@@ -26,7 +31,7 @@ import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "SCRATCH_BYTES", "chunk_fwd_varlen", "chunk_bwd", "chunk_bwd_workspace_bytes", "decode_step", "chunk_workspace_bytes", "varlen_workspace_bytes",
            "library", "KDAError", "LIB_PATH", "glr_fwd", "glr_bwd", "glr_step", "GLR_CHUNK", "block_norm_fwd", "block_norm_bwd",
-           "NORM_MAX_D"]
+           "NORM_MAX_D", "head_rope_fwd", "head_rope_bwd", "kv_append", "ROPE_MAX_D"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -465,6 +470,7 @@ def decode_step(q, k, v, log_alpha, beta, S, *, out_dtype=None, o=None, z=None, 
     return o
 
 
-# The elementwise operators build on the helpers above.
+# The operators around the core build on the helpers above.
+from .attn import ROPE_MAX_D, head_rope_bwd, head_rope_fwd, kv_append  # noqa: E402
 from .block_norm import NORM_MAX_D, block_norm_bwd, block_norm_fwd  # noqa: E402
 from .glr import GLR_CHUNK, glr_bwd, glr_fwd, glr_step  # noqa: E402

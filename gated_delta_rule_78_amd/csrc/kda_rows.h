@@ -1,0 +1,105 @@
+// Argument checks of strided rows [n0, n1, n2, d] (last dimension contiguous): their extent, whether
+// rows share elements, and whether two of them interleave without sharing any.
+#pragma once
+
+#include "kda_check.h"
+
+namespace kda {
+
+struct Rows {
+    const void* p;          // NULL: absent
+    int64_t n[3], s[3];     // sizes and strides (elements) of the three outer dimensions
+    int64_t d;              // contiguous elements
+    int64_t e;              // bytes of an element
+
+    bool empty() const { return !p || n[0] == 0 || n[1] == 0 || n[2] == 0; }
+
+    // Elements from the first to behind the last; false where that passes 2^61 or a stride is negative.
+    bool extent(int64_t* out) const {
+        int64_t m = d;
+        for (int i = 0; i < 3; ++i) {
+            if (n[i] <= 1) continue;
+            int64_t t;
+            if (s[i] < 0 || __builtin_mul_overflow(n[i] - 1, s[i], &t) || __builtin_add_overflow(m, t, &m)) return false;
+        }
+        *out = m;
+        return m <= (int64_t)1 << 61;
+    }
+    Range range() const {
+        int64_t m = 0;
+        if (empty() || !extent(&m)) return Range{0, 0};
+        return range_of(p, m * e);
+    }
+    // Dimensions of more than one row, by falling stride.
+    int order(int* o) const {
+        int k = 0;
+        for (int i = 0; i < 3; ++i)
+            if (n[i] > 1) o[k++] = i;
+        for (int i = 0; i < k; ++i)
+            for (int j = i + 1; j < k; ++j)
+                if (s[o[j]] > s[o[i]]) {
+                    const int t = o[i];
+                    o[i] = o[j];
+                    o[j] = t;
+                }
+        return k;
+    }
+    // No two rows share elements: every stride steps over all that the smaller ones reach.
+    bool distinct() const {
+        if (empty()) return true;
+        int o[3];
+        int64_t reach = d;
+        for (int i = order(o) - 1; i >= 0; --i) {
+            if (s[o[i]] < reach) return false;
+            int64_t t;
+            if (__builtin_mul_overflow(n[o[i]] - 1, s[o[i]], &t) || __builtin_add_overflow(reach, t, &reach)) return false;
+        }
+        return true;
+    }
+};
+
+inline bool rows_ok(const Rows& r) {
+    int64_t m;
+    return r.empty() || (aligned(r.p, (uintptr_t)r.e) && r.extent(&m));
+}
+
+// a and b, both distinct and of one element type, share no element though their ranges may overlap:
+// with the same sizes and strides, some stride has b's rows in the gaps that a's leave (or the
+// other way round), as the two halves of one buffer.
+inline bool interleaved(const Rows& a, const Rows& b) {
+    for (int i = 0; i < 3; ++i)
+        if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.s[i] != b.s[i])) return false;
+    int o[3];
+    const int k = a.order(o);
+    const intptr_t pa = reinterpret_cast<intptr_t>(a.p), pb = reinterpret_cast<intptr_t>(b.p);
+    const Rows &lo = pa <= pb ? a : b, &hi = pa <= pb ? b : a;
+    const int64_t bytes = pa <= pb ? pb - pa : pa - pb;
+    if (bytes % a.e) return false;
+    int64_t gap = bytes / a.e;
+    for (int i = 0; i < k; ++i) {
+        // what the dimensions of smaller strides reach
+        int64_t rl = lo.d, rh = hi.d;
+        for (int j = i + 1; j < k; ++j) {
+            rl += (lo.n[o[j]] - 1) * lo.s[o[j]];
+            rh += (hi.n[o[j]] - 1) * hi.s[o[j]];
+        }
+        const int64_t step = a.s[o[i]];
+        if (i > 0 && a.s[o[i - 1]] % step) return false;    // rows of different outer indices at different places
+        gap %= step;
+        if (gap >= rl && gap + rh <= step) return true;
+    }
+    return gap >= lo.d && k == 0;
+}
+
+template <int NI, int NO>
+bool rows_apart(const Range (&in)[NI], const Range (&out)[NO]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlaps(out[i], in[j])) return false;
+        for (int j = i + 1; j < NO; ++j)
+            if (overlaps(out[i], out[j])) return false;
+    }
+    return true;
+}
+
+}  // namespace kda
