@@ -22,6 +22,7 @@ The attention layers between KDA layers (``include/kda_attn.h``):
 
     head_rope_fwd, head_rope_bwd        per-head norm of q and k with the position rotation
     kv_append                           new tokens' keys and values into a paged cache
+    paged_attn                          attention of new tokens over a paged cache
 """
 import contextlib
 import ctypes
@@ -31,7 +32,7 @@ import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "SCRATCH_BYTES", "chunk_fwd_varlen", "chunk_bwd", "chunk_bwd_workspace_bytes", "decode_step", "chunk_workspace_bytes", "varlen_workspace_bytes",
            "library", "KDAError", "LIB_PATH", "glr_fwd", "glr_bwd", "glr_step", "GLR_CHUNK", "block_norm_fwd", "block_norm_bwd",
-           "NORM_MAX_D", "head_rope_fwd", "head_rope_bwd", "kv_append", "ROPE_MAX_D"]
+           "NORM_MAX_D", "head_rope_fwd", "head_rope_bwd", "kv_append", "paged_attn", "ROPE_MAX_D"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -471,6 +472,6 @@ def decode_step(q, k, v, log_alpha, beta, S, *, out_dtype=None, o=None, z=None, 
 
 
 # The operators around the core build on the helpers above.
-from .attn import ROPE_MAX_D, head_rope_bwd, head_rope_fwd, kv_append  # noqa: E402
+from .attn import ROPE_MAX_D, head_rope_bwd, head_rope_fwd, kv_append, paged_attn  # noqa: E402
 from .block_norm import NORM_MAX_D, block_norm_bwd, block_norm_fwd  # noqa: E402
 from .glr import GLR_CHUNK, glr_bwd, glr_fwd, glr_step  # noqa: E402

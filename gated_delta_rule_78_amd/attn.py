@@ -5,6 +5,7 @@
         -> (dq, dk, dq_weight, dk_weight)
     kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, inv_freq) -> q_out
                                                                  new tokens into a paged cache
+    paged_attn(q, k_cache, v_cache, block_table, kv_lens) -> o   attention of new tokens over it
 """
 import ctypes
 import functools
@@ -43,6 +44,14 @@ class KvAppendDesc(ctypes.Structure):
                 ("rope_scale", ctypes.c_float)]
 
 
+class PagedAttnDesc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64), ("T", ctypes.c_int64),
+                ("dk", ctypes.c_int64), ("dv", ctypes.c_int64), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("q", RowStrides), ("o", RowStrides), ("k_cache", PageStrides), ("v_cache", PageStrides),
+                ("packed", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -60,6 +69,11 @@ def _library():
         lib.kda_head_rope_bwd.restype = I
         lib.kda_kv_append.argtypes = [K] + [P] * 13
         lib.kda_kv_append.restype = I
+        A = ctypes.POINTER(PagedAttnDesc)
+        lib.kda_paged_attn_workspace_bytes.argtypes = [A]
+        lib.kda_paged_attn_workspace_bytes.restype = Z
+        lib.kda_paged_attn.argtypes = [A] + [P] * 9 + [Z, P]
+        lib.kda_paged_attn.restype = I
         _lib = lib
     return _lib
 
@@ -255,3 +269,63 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, inv_freq=None, *,
                                                 ptr(v_cache), raw_stream(index, stream))
     _check("kda_kv_append", st)
     return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_desc(N, Hq, Hk, T, dk, dv, pages, page_size, max_pages, table_stride, window, rows, caches, packed, scale):
+    """The call's descriptor and the workspace it needs."""
+    desc = PagedAttnDesc(N, Hq, Hk, T, dk, dv, pages, page_size, max_pages, table_stride, window,
+                         *(RowStrides(*s) for s in rows), *(PageStrides(*s) for s in caches), packed, scale)
+    return desc, _library().kda_paged_attn_workspace_bytes(desc)
+
+
+def paged_attn(q, k_cache, v_cache, block_table, kv_lens, *, cu_seqlens=None, scale=None, window=0, o=None, lse=None,
+               return_lse=False, workspace=None, stream=None):
+    """Attention of new tokens over their sequences' positions in a paged cache, through ``kda_paged_attn``.
+
+    q: [N,Hq,T,dk], T new tokens of each of N sequences, or packed [Hq,T,dk] with cu_seqlens (int32
+    [N+1]); bf16, any strides in multiples of 8 with contiguous channels. k_cache [pages,Hk,page_size,dk],
+    v_cache [pages,Hk,page_size,dv], block_table [N,max_pages], kv_lens [N] as ``kv_append`` left them:
+    the new tokens are each sequence's last, token i of n at position kv_lens - n + i. It sees the positions
+    up to its own, with ``window`` > 0 the last ``window`` of them.
+        o = softmax(scale * q k^T) v,   lse = log sum exp(scale * q k^T)     (scale: default 1 / sqrt(dk))
+    Query head h reads key head h // (Hq / Hk). Returns o [N,Hq,T,dv] (packed [Hq,T,dv]) bf16, its
+    dimensions in memory in q's order; with ``return_lse`` (o, lse), lse fp32 [N,Hq,T] (packed [Hq,T]).
+    A token that sees nothing has o = 0 and lse = -inf."""
+    BF16 = torch.bfloat16
+    index = q.get_device()
+    N, packed = _cache_inputs(index, q, cu_seqlens, kv_lens, block_table)
+    *b, Hq, T, dk = q.shape
+    _check_rows("q", q, index, BF16, q.shape)
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [pages,Hk,page_size,d] (got shapes %s, %s)"
+                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
+    pages, Hk, page_size, dv = v_cache.shape
+    _check_rows("k_cache", k_cache, index, BF16, (pages, Hk, page_size, dk))
+    _check_rows("v_cache", v_cache, index, BF16, v_cache.shape)
+    if o is not None:
+        _check_rows("o", o, index, BF16, (*b, Hq, T, dv))
+    if lse is not None:
+        check("lse", lse, index, torch.float32, (*b, Hq, T))
+    if workspace is not None:
+        _check_workspace(workspace, q.device)
+    on_gpu("paged_attn", q)
+    with scope(index, stream):
+        if o is None:
+            if dv == dk:
+                o = torch.empty_like(q)
+            else:      # q's order of dimensions: token-major rows stay so
+                s = q.stride()
+                o = (torch.empty(*b, T, Hq, dv, dtype=BF16, device=q.device).transpose(-3, -2) if s[-3] < s[-2]
+                     else torch.empty(*b, Hq, T, dv, dtype=BF16, device=q.device))
+        if lse is None and return_lse:
+            lse = torch.empty(*b, Hq, T, dtype=torch.float32, device=q.device)
+        desc, need = _attn_desc(N, Hq, Hk, T, dk, dv, pages, page_size, block_table.shape[1], block_table.stride(0),
+                                int(window), (_outer(q), _outer(o)), (k_cache.stride()[:3], v_cache.stride()[:3]), packed,
+                                float(dk ** -0.5 if scale is None else scale))
+        workspace = _workspace(need, workspace, q.device)
+        st = (_lib or _library()).kda_paged_attn(desc, ptr(q), ptr(k_cache), ptr(v_cache), ptr(cu_seqlens), ptr(kv_lens),
+                                                 ptr(block_table), ptr(o), ptr(lse), ptr(workspace), _nbytes(workspace),
+                                                 raw_stream(index, stream))
+    _check("kda_paged_attn", st)
+    return (o, lse) if return_lse else o

@@ -15,7 +15,8 @@ LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_abi.cpp", "kda_plan.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_intra.hip", "kda_inter.hip", "kda_fused.hip", "kda_scan.hip", "kda_varlen.hip", "kda_bwd.hip", "kda_noalloc.hip",
            "kda_glr_abi.cpp", "kda_glr.hip", "kda_glr_rows.hip", "kda_glr_fwd_bf16.hip", "kda_glr_fwd_f32.hip",
            "kda_glr_bwd_bf16.hip", "kda_glr_bwd_f32.hip", "kda_norm_abi.cpp", "kda_norm.hip", "kda_norm_bf16.hip", "kda_norm_f32.hip",
-           "kda_rope_abi.cpp", "kda_rope.hip", "kda_rope_bf16.hip", "kda_rope_f32.hip"]
+           "kda_rope_abi.cpp", "kda_rope.hip", "kda_rope_bf16.hip", "kda_rope_f32.hip", "kda_attn_abi.cpp", "kda_attn.hip",
+           "kda_attn_d128_128.hip", "kda_attn_d128_64.hip", "kda_attn_d64_128.hip", "kda_attn_d64_64.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -1,0 +1,722 @@
+// Attention of new tokens over a paged cache for gfx950 (include/kda_attn.h), bf16, head sizes as
+// template parameters (instantiated in kda_attn_d*.hip).
+//
+//     x_j = c q . k_j  (c = scale log2 e),  o = sum_j 2^(x_j - m) v_j / l,  l = sum_j 2^(x_j - m)
+//
+// in one pass over the keys with a running reference m and sum l, both fp32. Products are transposed:
+// S^T = K Q^T puts a query in a lane (column n = lane % 32 of the 32x32 product) and the block's keys
+// in its registers, so row sums and the rescaling of O^T = V^T P^T need one exchange (the two halves
+// of the wave), and the registers of P^T are the second product's operand as they stand: operand slot
+// e of half h at k step kk is key 16 kk + 8 (e / 4) + 4 h + e % 4, and V is read with that order by
+// transposed LDS reads.
+//
+// P is rounded to bf16 (half a step, 2^-8, of each probability) to enter the matrix product, l is the
+// sum of the unrounded ones.
+#pragma once
+
+#include "kda_attn_plan.h"
+#include "kda_mfma.h"
+
+namespace kda {
+namespace attn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Maximum and sum over the two lanes of a query, one in each half of the wave.
+__device__ __forceinline__ float both_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// 16 bytes a lane from a raw buffer straight into LDS, to lds + 16 lane. Offsets at or past the
+// descriptor's size store zeros. The compiler does not count these loads: whoever reads the LDS waits
+// with wait_vm first.
+__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(off), "s"(rsrc));
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// One tile's place: which sequence, rows and keys.
+struct Tile {
+    int64_t seq, first;     // sequence, first token of it in the rows' T (packed) or 0
+    int n, kv;              // its new tokens, its keys
+    int row0, rows;         // first row, rows of the sequence in all
+    int head;               // key head
+    int lo, hi;             // keys that any row sees: [lo, hi)
+    int chunk, chunks;
+    int64_t slot;           // partial result, when chunks > 1
+};
+
+__device__ __forceinline__ int find_entry(const PlanEntry* p, int64_t N, int idx, int PlanEntry::*key) {
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, n = N + 1;      // p[0] is 0: some entry is always at or below idx
+    for (;;) {
+        const int64_t step = (n + 63) / 64, i = lo + lane * step;
+        const bool le = lane * step < n && p[i < N ? i : N].*key <= idx;
+        const int cnt = __popcll(__ballot(le));
+        const int64_t at = (int64_t)(cnt > 0 ? cnt - 1 : 0) * step;
+        lo += at;
+        n = n - at < step ? n - at : step;
+        if (step == 1) return (int)lo;
+    }
+}
+
+// New tokens and keys of a sequence; false where it has no rows of this kind.
+__device__ __forceinline__ bool sequence(const AttnArgs& a, int64_t s, int64_t& first, int& n, int& kv) {
+    first = 0;
+    n = (int)a.T;
+    if (a.packed) {
+        const int64_t c0 = a.cu[s], c1 = a.cu[s + 1];
+        const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.T;
+        first = ok ? c0 : 0;
+        n = ok ? (int)(c1 - c0) : 0;
+    }
+    const int most = a.max_pages * a.page_size;
+    kv = a.kv_lens[s];
+    kv = kv < 0 ? 0 : kv > most ? most : kv;
+    return n > 0;
+}
+
+// Keys that the longest tile of a sequence reads, in units.
+__device__ __forceinline__ int64_t tile_units(const AttnArgs& a, int kv, int rows) {
+    int64_t k = kv;
+    if (a.window > 0) {
+        const int64_t w = a.window + (rows + a.G - 1) / a.G + kUnit;
+        k = k < w ? k : w;
+    }
+    return k > 0 ? (k + kUnit - 1) / kUnit : 1;
+}
+
+__device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, int n, bool narrow) {
+    const int64_t rows = (int64_t)n * a.G;
+    if (rows <= kNarrowRows) return narrow ? 1 : 0;
+    return narrow ? 0 : (rows + kWideRows - 1) / kWideRows;
+}
+
+// ---- a page table walked by one wave ------------------------------------------------------------
+
+// Position of a group of 16 keys in the pages: everything uniform. 64 entries of the table are held in
+// a register, one a lane.
+struct Pages {
+    const int32_t* table;
+    int max_pages, page_size, pages;
+    int pg, row;            // page index and row of the current key
+    int base, held;         // held: this lane's entry of page base + lane
+
+    __device__ __forceinline__ void seek(int key) {
+        pg = uniform(key / page_size);
+        row = key - pg * page_size;
+    }
+    __device__ __forceinline__ void advance(int keys) {
+        row += keys;
+        while (row >= page_size) {
+            row -= page_size;
+            ++pg;
+        }
+    }
+    __device__ __forceinline__ void fetch() {
+        base = pg;
+        const int i = pg + (int)(threadIdx.x & 63);
+        held = i < max_pages ? table[i] : -1;
+    }
+    // the current page's number, or -1
+    __device__ __forceinline__ int page() {
+        if (pg - base >= 64) fetch();
+        const int p = __builtin_amdgcn_readlane(held, pg - base);
+        return p >= 0 && p < pages ? p : -1;
+    }
+};
+
+// Descriptor of one head's rows of a page, as far as `valid` rows.
+__device__ __forceinline__ i32x4 page_rsrc(const void* cache, int page, int64_t sp, int64_t head_off, int64_t st, int valid, int d) {
+    const uint64_t base = reinterpret_cast<uint64_t>(cache) + 2 * ((uint64_t)(page < 0 ? 0 : page) * sp + head_off);
+    i32x4 r;
+    r[0] = uniform((int)(uint32_t)base);
+    r[1] = uniform((int)(uint32_t)(base >> 32) & 0xffff);
+    r[2] = uniform(page < 0 || valid <= 0 ? 0 : (int)(2 * ((valid - 1) * st + d)));
+    r[3] = kBufFlags;
+    return r;
+}
+
+// LDS tiles: rows of D channels, 16-byte pieces permuted within a row (piece c of row r at place
+// c ^ f(r)) so that a wave's reads meet every bank once.
+template <int D>
+struct TileK {       // read row-wise: lanes 0..31 one row each
+    static constexpr int kRowBytes = 2 * D, kPieces = D / 8, kRowsPerLoad = 1024 / kRowBytes;
+    __device__ static __forceinline__ int f(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
+};
+template <int D>
+struct TileV {       // read transposed: 4 rows x 32 bytes a group of 16 lanes
+    static constexpr int kRowBytes = 2 * D, kPieces = D / 8, kRowsPerLoad = 1024 / kRowBytes;
+    __device__ static __forceinline__ int f(int row) { return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3); }
+};
+
+// Rows row .. row + kRowsPerLoad - 1 of a tile, from page row `prow`.
+template <typename L>
+__device__ __forceinline__ void load_rows(i32x4 rsrc, uint32_t lds, int row, int prow, uint32_t stride_bytes) {
+    const int lane = threadIdx.x & 63;
+    const int lr = lane / L::kPieces, c = (lane % L::kPieces) ^ L::f(row + lr);
+    load_to_lds(rsrc, (uint32_t)(prow + lr) * stride_bytes + c * 16, lds + row * L::kRowBytes);
+}
+
+// ---- one wave's rows against a block of keys ------------------------------------------------------
+
+template <int DK, int DV, int KB>
+struct Wave {
+    static constexpr int kKS = DK / 16, kDT = DV / 32, kMT = KB / 32;
+    bf16x8 Q[kKS];
+    f32x16 O[kDT];
+    float m, l;             // reference of this lane's query and this half's sum
+    int pos;                // this lane's query's position; negative: sees nothing
+    int first, last;        // least and largest position of the wave's live rows
+    bool live;              // any row at all
+
+    __device__ __forceinline__ void start(const AttnArgs& a, const Tile& t, int row_base) {
+        const int lane = threadIdx.x & 63, h = lane >> 5;
+        const int r = t.row0 + row_base + (lane & 31);
+        const bool in = r < t.rows;
+        const int tok = in ? r / a.G : 0, hd = in ? r - tok * a.G : 0;
+        pos = in ? t.kv - t.n + tok : -1;
+        const int r0 = t.row0 + row_base, r1 = r0 + 31 < t.rows ? r0 + 31 : t.rows - 1;
+        live = r0 < t.rows;
+        first = live ? t.kv - t.n + r0 / a.G : 0;
+        last = live ? t.kv - t.n + r1 / a.G : -1;
+        const bf16_t* p = static_cast<const bf16_t*>(a.q) + (a.packed ? 0 : t.seq * a.sq.b) + (t.first + tok) * a.sq.t +
+                          ((int64_t)t.head * a.G + hd) * a.sq.h + 8 * h;
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (in) u = *reinterpret_cast<const uint4*>(p + 16 * ks);
+            u.x ^= a.flip; u.y ^= a.flip; u.z ^= a.flip; u.w ^= a.flip;
+            Q[ks] = __builtin_bit_cast(bf16x8, u);
+        }
+#pragma unroll
+        for (int i = 0; i < kDT; ++i)
+#pragma unroll
+            for (int r2 = 0; r2 < 16; ++r2) O[i][r2] = 0.f;
+        m = -INFINITY;
+        l = 0.f;
+    }
+
+    // Whether any of the wave's rows sees a key of [kb, kb + KB).
+    __device__ __forceinline__ bool sees(const AttnArgs& a, int kb) const {
+        if (!live || kb > last) return false;
+        return a.window <= 0 || (int64_t)kb + KB - 1 > (int64_t)first - a.window;
+    }
+
+    __device__ __forceinline__ void block(const AttnArgs& a, const char* ks_, const char* vs_, int kb) {
+        const int lane = threadIdx.x & 63, h = lane >> 5, n = lane & 31, l16 = lane & 15;
+        f32x16 S[kMT];
+        // S^T = K Q^T
+        {
+            const char* kp = ks_ + n * TileK<DK>::kRowBytes;
+            const int sw = 16 * (h ^ TileK<DK>::f(n));
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) S[mt][r] = 0.f;
+            }
+#pragma unroll
+            for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+                    S[mt] = mfma32(read16(kp + (sw ^ (32 * ks)) + mt * 32 * TileK<DK>::kRowBytes), Q[ks], S[mt]);
+        }
+        const bool masked = kb + KB - 1 > first || (a.window > 0 && (int64_t)kb <= (int64_t)last - a.window);
+        if (masked) {
+            const int64_t from = a.window > 0 ? (int64_t)pos - a.window : -1;
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = kb + 32 * mt + (r & 3) + 8 * (r >> 2) + 4 * h;
+                    if (j > pos || j <= from) S[mt][r] = -INFINITY;
+                }
+        }
+        // the running reference: raised (and O, l scaled down) only when a score passes it by 2^8, which
+        // keeps every 2^(x - m) below 2^8
+        float mx = S[0][0];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, S[mt][r]);
+        mx = both_max(mx) * a.c;
+        if (__any(mx > m + 8.f)) {
+            const float mn = mx > m + 8.f ? mx : m;
+            const float f = mn == m ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < kDT; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) O[i][r] *= f;
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+        bf16x8 P[2 * kMT];
+        float sum = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = __builtin_amdgcn_exp2f(fmaf(S[mt][8 * kk + e], a.c, -sub));
+                    sum += p[e];
+                }
+                uint4 u;
+                u.x = pack_bf16x2(p[0], p[1]); u.y = pack_bf16x2(p[2], p[3]);
+                u.z = pack_bf16x2(p[4], p[5]); u.w = pack_bf16x2(p[6], p[7]);
+                P[2 * mt + kk] = __builtin_bit_cast(bf16x8, u);
+            }
+        l += sum;
+        // O^T += V^T P^T
+        const int vrow = 4 * h + (l16 >> 2);
+        const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
+        const int q2 = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1), fv = TileV<DV>::f(vrow);
+        bool bad = false;
+        if (masked && (last != first || a.window > 0)) bad = any_bad(vs_);
+        if (bad) {
+            block_bad(a, vp, q2 ^ fv, P, kb);
+            return;
+        }
+#pragma unroll
+        for (int s = 0; s < 2 * kMT; ++s)
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, q2 ^ fv, s, dt), P[s], O[dt]);
+    }
+
+    __device__ static __forceinline__ bf16x8 read_v(const char* vp, int piece, int s, int dt) {
+        const bf16_t* p = reinterpret_cast<const bf16_t*>(vp + 16 * (piece ^ (4 * dt)) + 16 * s * TileV<DV>::kRowBytes);
+        return cat(tr_read(p), tr_read(p + 8 * DV));
+    }
+
+    // Whether the V block holds an infinity or a NaN. Only then can a key that some rows do not see
+    // reach them: a probability of 0 times it.
+    __device__ __forceinline__ bool any_bad(const char* vs_) const {
+        const int lane = threadIdx.x & 63;
+        uint32_t hit = 0;
+#pragma unroll
+        for (int i = 0; i < KB * DV * 2 / 1024; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vs_ + i * 1024 + lane * 16);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                hit |= (uint32_t)((w[k] & 0x7f80u) == 0x7f80u) | (uint32_t)((w[k] & 0x7f800000u) == 0x7f800000u);
+        }
+        return __any(hit);
+    }
+
+    // The same product with such values: they are taken out of V, and a second product of ones, where V
+    // held them and where the row sees the key, says which outputs they belong to; those become NaN.
+    __device__ __forceinline__ void block_bad(const AttnArgs& a, const char* vp, int piece, const bf16x8* P, int kb) {
+        const int h = (threadIdx.x >> 5) & 1;
+        const int64_t from = a.window > 0 ? (int64_t)pos - a.window : -1;
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt) {
+            f32x16 C;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) C[r] = 0.f;
+#pragma unroll
+            for (int s = 0; s < 2 * kMT; ++s) {
+                uint4 v = __builtin_bit_cast(uint4, read_v(vp, piece, s, dt)), ones, seen;
+                uint32_t* vw = &v.x;
+                uint32_t* ow = &ones.x;
+                uint32_t* sw = &seen.x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool lo = (vw[k] & 0x7f80u) == 0x7f80u, hi = (vw[k] & 0x7f800000u) == 0x7f800000u;
+                    ow[k] = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
+                    vw[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+                    uint32_t b = 0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int el = 2 * k + e, j = kb + 16 * s + (el & 3) + 8 * (el >> 2) + 4 * h;
+                        if (j <= pos && j > from) b |= 0x3f80u << (16 * e);
+                    }
+                    sw[k] = b;
+                }
+                O[dt] = mfma32(__builtin_bit_cast(bf16x8, v), P[s], O[dt]);
+                C = mfma32(__builtin_bit_cast(bf16x8, ones), __builtin_bit_cast(bf16x8, seen), C);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (C[r] > 0.f) O[dt][r] = NAN;
+        }
+    }
+
+    // dv of register quad g of tile dt
+    __device__ static __forceinline__ int dv_of(int dt, int g) { return 32 * dt + 8 * g + 4 * ((threadIdx.x >> 5) & 1); }
+
+    // Results of a tile whose keys were all here, or a partial one.
+    __device__ __forceinline__ void finish(const AttnArgs& a, const Tile& t, int row_base, float* part, int part_rows) {
+        const int n = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+        const int r = t.row0 + row_base + n;
+        l = both_sum(l);
+        if (r >= t.rows) return;
+        if (t.chunks > 1) {
+            float* p = part + (t.slot * part_rows + row_base + n) * (DV + 2);
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float2* q = reinterpret_cast<float2*>(p + dv_of(dt, g));
+                    q[0] = make_float2(O[dt][4 * g], O[dt][4 * g + 1]);
+                    q[1] = make_float2(O[dt][4 * g + 2], O[dt][4 * g + 3]);
+                }
+            if (h == 0) *reinterpret_cast<float2*>(p + DV) = make_float2(m, l);
+            return;
+        }
+        const int tok = r / a.G, hd = r - tok * a.G;
+        const int64_t head = (int64_t)t.head * a.G + hd;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : t.seq * a.so.b) + (t.first + tok) * a.so.t + head * a.so.h;
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                store4(o + dv_of(dt, g), O[dt][4 * g] * inv, O[dt][4 * g + 1] * inv, O[dt][4 * g + 2] * inv, O[dt][4 * g + 3] * inv);
+        if (a.lse && h == 0)
+            a.lse[(a.packed ? 0 : t.seq * a.Hq * a.T) + head * a.T + t.first + tok] =
+                l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+};
+
+// The tile and chunk of this workgroup; false behind the last.
+template <bool NARROW>
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, Tile& t) {
+    const PlanEntry* plan = static_cast<const PlanEntry*>(a.ws) + (NARROW ? 0 : a.N + 1);
+    const int idx = blockIdx.x;
+    if (idx >= plan[a.N].item) return false;
+    const int64_t s = uniform(find_entry(plan, a.N, idx, &PlanEntry::item));
+    const PlanEntry e = plan[s];
+    t.seq = s;
+    int n, kv;
+    sequence(a, s, t.first, n, kv);
+    t.first = uniform((int)t.first);
+    t.n = uniform(n);
+    t.kv = uniform(kv);
+    t.rows = t.n * a.G;
+    const int tiles = (int)tiles_of(a, t.n, NARROW);
+    const int j = idx - uniform(e.item);
+    t.head = uniform(j % a.Hk);
+    const int rest = uniform(j / a.Hk);
+    t.chunks = uniform(e.chunks);
+    t.chunk = uniform(rest % t.chunks);
+    const int tile = uniform(tiles - 1 - rest / t.chunks);        // the tiles with the most keys first
+    constexpr int R = NARROW ? kNarrowRows : kWideRows;
+    t.row0 = tile * R;
+    t.slot = uniform(e.slot) + ((int64_t)tile * a.Hk + t.head) * t.chunks + t.chunk;
+    const int r1 = t.row0 + R < t.rows ? t.row0 + R : t.rows;
+    const int p0 = t.kv - t.n + t.row0 / a.G, p1 = t.kv - t.n + (r1 - 1) / a.G;
+    t.hi = uniform(p1 + 1 > 0 ? p1 + 1 : 0);
+    const int64_t w0 = a.window > 0 ? (int64_t)p0 - a.window + 1 : 0;
+    t.lo = uniform(w0 > 0 ? (int)w0 : 0);
+    return true;
+}
+
+// Keys [from, to) of this chunk: whole units from the unit of t.lo on.
+__device__ __forceinline__ void chunk_keys(const Tile& t, int& from, int& to) {
+    const int u0 = t.lo / kUnit, u1 = (t.hi + kUnit - 1) / kUnit;
+    const int per = u1 > u0 ? (u1 - u0 + t.chunks - 1) / t.chunks : 0;
+    from = (u0 + t.chunk * per) * kUnit;
+    to = from + per * kUnit;
+    to = to < t.hi ? to : t.hi;
+}
+
+__device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
+    char* p = static_cast<char*>(a.ws) + plan_bytes(a.N);
+    if (!narrow && has_narrow(a)) p += slots_most() * partial_bytes(kNarrowRows, a.dv);
+    return reinterpret_cast<float*>(p);
+}
+
+// ---- wide tiles: four waves of 32 rows share blocks of 64 keys in LDS ----------------------------
+
+template <int DK, int DV>
+__global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnArgs a) {
+    constexpr int KB = 64, KBYTES = KB * DK * 2, VBYTES = KB * DV * 2;
+    __shared__ __align__(1024) char smem[2][KBYTES + VBYTES];
+    Tile t;
+    if (!find_tile<false>(a, t)) return;
+    const int w = uniform(threadIdx.x >> 6);
+    int from, to;
+    chunk_keys(t, from, to);
+    Wave<DK, DV, KB> wave;
+    wave.start(a, t, 32 * w);
+    Pages pg;
+    pg.table = a.table + t.seq * a.table_stride;
+    pg.max_pages = a.max_pages;
+    pg.page_size = a.page_size;
+    pg.pages = a.pages;
+    pg.seek(from);
+    pg.fetch();
+    const uint32_t lds0 = lds_address(smem[0]), lds1 = lds_address(smem[1]);
+    const uint32_t kst = (uint32_t)a.skc.t * 2, vst = (uint32_t)a.svc.t * 2;
+    const int64_t kho = t.head * a.skc.h, vho = t.head * a.svc.h;
+    // 16 keys at a time; each wave its share of a group's rows
+    auto issue = [&](uint32_t lds, int kb) {
+#pragma unroll
+        for (int g = 0; g < KB / 16; ++g) {
+            const int page = pg.page();
+            const int valid = t.hi - (kb + 16 * g - pg.row);       // rows of this page that any row sees
+            const int vr = valid < pg.page_size ? valid : pg.page_size;
+            typedef TileK<DK> LK;
+            typedef TileV<DV> LV;
+            constexpr int NK = 16 / LK::kRowsPerLoad, NV = 16 / LV::kRowsPerLoad;    // loads a group
+            if (NK == 4 || (w >> 1) == (g & 1)) {
+                const int i = NK == 4 ? w : (w & 1);
+                load_rows<LK>(page_rsrc(a.k_cache, page, a.skc.p, kho, a.skc.t, vr, DK), lds, 16 * g + i * LK::kRowsPerLoad,
+                              pg.row + i * LK::kRowsPerLoad, kst);
+            }
+            if (NV == 4 || (w >> 1) == (g & 1)) {
+                const int i = NV == 4 ? w : (w & 1);
+                load_rows<LV>(page_rsrc(a.v_cache, page, a.svc.p, vho, a.svc.t, vr, DV), lds + KBYTES, 16 * g + i * LV::kRowsPerLoad,
+                              pg.row + i * LV::kRowsPerLoad, vst);
+            }
+            pg.advance(16);
+        }
+    };
+    if (from < to) issue(lds0, from);
+    int buf = 0;
+    for (int kb = from; kb < to; kb += KB) {
+        wait_vm<0>();          // this wave's loads of the block
+        lds_barrier();         // everyone's; the other buffer is free again
+        if (kb + KB < to) issue(buf ? lds0 : lds1, kb + KB);
+        const char* s = smem[buf];
+        if (wave.sees(a, kb)) wave.block(a, s, s + KBYTES, kb);
+        buf ^= 1;
+    }
+    wave.finish(a, t, 32 * w, partials(a, false), kWideRows);
+}
+
+// ---- narrow tiles: four waves with the same 32 rows, each its own blocks of 32 keys ----------------
+
+template <int DK, int DV>
+__global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
+    constexpr int KB = 32, KBYTES = KB * DK * 2, VBYTES = KB * DV * 2;
+    constexpr int kJoin = 32 * (DV + 2) * 4;            // a wave's result, for the join at the end
+    constexpr int kWaveBytes = KBYTES + VBYTES > kJoin ? KBYTES + VBYTES : (kJoin + 1023) / 1024 * 1024;
+    __shared__ __align__(1024) char smem[kWaves][kWaveBytes];
+    Tile t;
+    if (!find_tile<true>(a, t)) return;
+    const int w = uniform(threadIdx.x >> 6);
+    int from, to;
+    chunk_keys(t, from, to);
+    Wave<DK, DV, KB> wave;
+    wave.start(a, t, 0);
+    Pages pg;
+    pg.table = a.table + t.seq * a.table_stride;
+    pg.max_pages = a.max_pages;
+    pg.page_size = a.page_size;
+    pg.pages = a.pages;
+    const int mine = from + KB * w;
+    pg.seek(mine);
+    pg.fetch();
+    const uint32_t lds = lds_address(smem[w]);
+    const uint32_t kst = (uint32_t)a.skc.t * 2, vst = (uint32_t)a.svc.t * 2;
+    const int64_t kho = t.head * a.skc.h, vho = t.head * a.svc.h;
+    typedef TileK<DK> LK;
+    typedef TileV<DV> LV;
+    int page[2], prow[2], vr[2];
+    auto locate = [&](int kb) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            page[g] = pg.page();
+            prow[g] = pg.row;
+            const int valid = t.hi - (kb + 16 * g - pg.row);
+            vr[g] = valid < pg.page_size ? valid : pg.page_size;
+            pg.advance(16);
+        }
+        pg.advance(KB * (kWaves - 1));
+    };
+    auto issue_k = [&]() {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const i32x4 r = page_rsrc(a.k_cache, page[g], a.skc.p, kho, a.skc.t, vr[g], DK);
+#pragma unroll
+            for (int i = 0; i < 16 / LK::kRowsPerLoad; ++i)
+                load_rows<LK>(r, lds, 16 * g + i * LK::kRowsPerLoad, prow[g] + i * LK::kRowsPerLoad, kst);
+        }
+    };
+    auto issue_v = [&]() {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const i32x4 r = page_rsrc(a.v_cache, page[g], a.svc.p, vho, a.svc.t, vr[g], DV);
+#pragma unroll
+            for (int i = 0; i < 16 / LV::kRowsPerLoad; ++i)
+                load_rows<LV>(r, lds + KBYTES, 16 * g + i * LV::kRowsPerLoad, prow[g] + i * LV::kRowsPerLoad, vst);
+        }
+    };
+    for (int kb = mine; kb < to; kb += KB * kWaves) {
+        locate(kb);
+        issue_k();
+        issue_v();
+        wait_vm<0>();
+        wave_lds_sync();
+        if (wave.sees(a, kb)) wave.block(a, smem[w], smem[w] + KBYTES, kb);
+        wave_lds_sync();        // this block's reads are through before the next loads land
+    }
+    // join the waves: every wave leaves m, l, O in LDS; wave w takes the rows' channels in turn
+    lds_barrier();
+    constexpr int DT = DV / 32;
+    const int n = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+    wave.l = both_sum(wave.l);
+    float* js = reinterpret_cast<float*>(smem[w]);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) js[n * (DV + 2) + Wave<DK, DV, KB>::dv_of(dt, g) + e] = wave.O[dt][4 * g + e];
+    if (h == 0) {
+        js[n * (DV + 2) + DV] = wave.m;
+        js[n * (DV + 2) + DV + 1] = wave.l;
+    }
+    lds_barrier();
+    float* part = partials(a, true);
+    const int rows = t.rows < kNarrowRows ? t.rows : kNarrowRows;
+    for (int r = w; r < rows; r += kWaves) {
+        const int lane = threadIdx.x & 63;
+        float mw[kWaves], mm = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            mw[i] = reinterpret_cast<const float*>(smem[i])[r * (DV + 2) + DV];
+            mm = fmaxf(mm, mw[i]);
+        }
+        float acc[DV / 64], ll = 0.f;
+#pragma unroll
+        for (int k = 0; k < DV / 64; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const float* src = reinterpret_cast<const float*>(smem[i]) + r * (DV + 2);
+            const float f = mw[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw[i] - mm);
+            if (mw[i] == -INFINITY) continue;      // saw nothing: its O is 0
+            ll = fmaf(f, src[DV + 1], ll);
+#pragma unroll
+            for (int k = 0; k < DV / 64; ++k) acc[k] = fmaf(f, src[lane + 64 * k], acc[k]);
+        }
+        if (t.chunks > 1) {
+            float* p = part + (t.slot * kNarrowRows + r) * (DV + 2);
+#pragma unroll
+            for (int k = 0; k < DV / 64; ++k) p[lane + 64 * k] = acc[k];
+            if (lane == 0) {
+                p[DV] = mm;
+                p[DV + 1] = ll;
+            }
+            continue;
+        }
+        const int tok = r / a.G, hd = r - tok * a.G;
+        const int64_t head = (int64_t)t.head * a.G + hd;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : t.seq * a.so.b) + (t.first + tok) * a.so.t + head * a.so.h;
+#pragma unroll
+        for (int k = 0; k < DV / 64; ++k) st_f(o + lane + 64 * k, acc[k] * inv);
+        if (a.lse && lane == 0)
+            a.lse[(a.packed ? 0 : t.seq * a.Hq * a.T) + head * a.T + t.first + tok] =
+                ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+    }
+}
+
+// ---- the chunks of cut tiles joined ---------------------------------------------------------------
+
+// Workgroup x: the x-th (tile, head) that is cut; y: a run of its rows.
+template <int DV, bool NARROW>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int rows_each) {
+    constexpr int R = NARROW ? kNarrowRows : kWideRows;
+    constexpr int LPR = DV / 4, NG = kThreads / LPR;     // 4 channels a thread, NG chunks at a time
+    __shared__ float4 sum[NG][LPR];
+    __shared__ float ml[2][kThreads / 64];
+    __shared__ float wgt[kThreads];
+    const PlanEntry* plan = static_cast<const PlanEntry*>(a.ws) + (NARROW ? 0 : a.N + 1);
+    const int idx = blockIdx.x;
+    if (idx >= plan[a.N].cut) return;
+    const int64_t s = uniform(find_entry(plan, a.N, idx, &PlanEntry::cut));
+    const PlanEntry e = plan[s];
+    int64_t first;
+    int n, kv;
+    sequence(a, s, first, n, kv);
+    const int rows = n * a.G, j = idx - e.cut, C = e.chunks;
+    const int head_k = j % a.Hk, tile = j / a.Hk;
+    const int64_t slot = e.slot + ((int64_t)tile * a.Hk + head_k) * C;
+    const float* part = partials(a, NARROW);
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = tid / LPR, ch = tid % LPR;
+    const int y0 = blockIdx.y * rows_each, y1 = y0 + rows_each < R ? y0 + rows_each : R;
+    for (int rr = y0; rr < y1 && tile * R + rr < rows; ++rr) {
+        const float* base = part + (slot * R + rr) * (DV + 2);
+        const int64_t step = (int64_t)R * (DV + 2);
+        // the chunks' largest reference
+        float mm = -INFINITY;
+        for (int c = tid; c < C; c += kThreads) mm = fmaxf(mm, base[c * step + DV]);
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) mm = fmaxf(mm, __shfl_xor(mm, k));
+        lds_barrier();
+        if (lane == 0) ml[0][wv] = mm;
+        lds_barrier();
+        mm = fmaxf(fmaxf(ml[0][0], ml[0][1]), fmaxf(ml[0][2], ml[0][3]));
+        float ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < C; c0 += kThreads) {
+            float f = 0.f;
+            if (c0 + tid < C) {
+                const float m = base[(c0 + tid) * step + DV];
+                f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mm);
+                if (f != 0.f) ll = fmaf(f, base[(c0 + tid) * step + DV + 1], ll);
+            }
+            lds_barrier();
+            wgt[tid] = f;
+            lds_barrier();
+            const int left = C - c0 < kThreads ? C - c0 : kThreads;
+            for (int c = g; c < left; c += NG) {
+                const float wf = wgt[c];
+                const float2* p = reinterpret_cast<const float2*>(base + (c0 + c) * step + 4 * ch);
+                if (wf != 0.f) {
+                    const float2 u = p[0], v = p[1];
+                    acc.x = fmaf(wf, u.x, acc.x); acc.y = fmaf(wf, u.y, acc.y);
+                    acc.z = fmaf(wf, v.x, acc.z); acc.w = fmaf(wf, v.y, acc.w);
+                }
+            }
+        }
+        sum[g][ch] = acc;
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) ll += __shfl_xor(ll, k);
+        if (lane == 0) ml[1][wv] = ll;
+        lds_barrier();
+        ll = (ml[1][0] + ml[1][1]) + (ml[1][2] + ml[1][3]);
+        if (g == 0) {
+#pragma unroll
+            for (int k = 1; k < NG; ++k) {
+                const float4 v = sum[k][ch];
+                acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+            }
+            const int r = tile * R + rr, tok = r / a.G, hd = r - tok * a.G;
+            const int64_t head = (int64_t)head_k * a.G + hd;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : s * a.so.b) + (first + tok) * a.so.t + head * a.so.h;
+            store4(o + 4 * ch, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (a.lse && ch == 0)
+                a.lse[(a.packed ? 0 : s * a.Hq * a.T) + head * a.T + first + tok] =
+                    ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+        }
+    }
+}
+
+}  // namespace attn
+}  // namespace kda
