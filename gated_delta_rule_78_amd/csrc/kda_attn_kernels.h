@@ -113,17 +113,21 @@ __device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, int n, bool narro
 
 // ---- a page table walked by one wave ------------------------------------------------------------
 
-// Position of a group of 16 keys in the pages: everything uniform. 64 entries of the table are held in
-// a register, one a lane.
+// A place among the pages, all of it uniform. 64 entries of the table are held in a register, one a lane.
 struct Pages {
     const int32_t* table;
     int max_pages, page_size, pages;
     int pg, row;            // page index and row of the current key
     int base, held;         // held: this lane's entry of page base + lane
 
-    __device__ __forceinline__ void seek(int key) {
+    __device__ __forceinline__ Pages(const AttnArgs& a, int64_t seq, int key) {
+        table = a.table + seq * a.table_stride;
+        max_pages = a.max_pages;
+        page_size = a.page_size;
+        pages = a.pages;
         pg = uniform(key / page_size);
         row = key - pg * page_size;
+        fetch();
     }
     __device__ __forceinline__ void advance(int keys) {
         row += keys;
@@ -137,45 +141,87 @@ struct Pages {
         const int i = pg + (int)(threadIdx.x & 63);
         held = i < max_pages ? table[i] : -1;
     }
-    // the current page's number, or -1
-    __device__ __forceinline__ int page() {
-        if (pg - base >= 64) fetch();
-        const int p = __builtin_amdgcn_readlane(held, pg - base);
+    // number of the page `ahead` (< 48) of the current one, or -1
+    __device__ __forceinline__ int page(int ahead) {
+        if (pg + ahead - base >= 64) fetch();
+        const int p = __builtin_amdgcn_readlane(held, pg + ahead - base);
         return p >= 0 && p < pages ? p : -1;
     }
 };
-
-// Descriptor of one head's rows of a page, as far as `valid` rows.
-__device__ __forceinline__ i32x4 page_rsrc(const void* cache, int page, int64_t sp, int64_t head_off, int64_t st, int valid, int d) {
-    const uint64_t base = reinterpret_cast<uint64_t>(cache) + 2 * ((uint64_t)(page < 0 ? 0 : page) * sp + head_off);
-    i32x4 r;
-    r[0] = uniform((int)(uint32_t)base);
-    r[1] = uniform((int)(uint32_t)(base >> 32) & 0xffff);
-    r[2] = uniform(page < 0 || valid <= 0 ? 0 : (int)(2 * ((valid - 1) * st + d)));
-    r[3] = kBufFlags;
-    return r;
-}
 
 // LDS tiles: rows of D channels, 16-byte pieces permuted within a row (piece c of row r at place
 // c ^ f(r)) so that a wave's reads meet every bank once.
 template <int D>
 struct TileK {       // read row-wise: lanes 0..31 one row each
-    static constexpr int kRowBytes = 2 * D, kPieces = D / 8, kRowsPerLoad = 1024 / kRowBytes;
+    static constexpr int kD = D, kRowBytes = 2 * D, kPieces = D / 8, kRows = 1024 / kRowBytes;   // kRows: of one load
     __device__ static __forceinline__ int f(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
 };
 template <int D>
 struct TileV {       // read transposed: 4 rows x 32 bytes a group of 16 lanes
-    static constexpr int kRowBytes = 2 * D, kPieces = D / 8, kRowsPerLoad = 1024 / kRowBytes;
+    static constexpr int kD = D, kRowBytes = 2 * D, kPieces = D / 8, kRows = 1024 / kRowBytes;
     __device__ static __forceinline__ int f(int row) { return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3); }
 };
 
-// Rows row .. row + kRowsPerLoad - 1 of a tile, from page row `prow`.
-template <typename L>
-__device__ __forceinline__ void load_rows(i32x4 rsrc, uint32_t lds, int row, int prow, uint32_t stride_bytes) {
-    const int lane = threadIdx.x & 63;
-    const int lr = lane / L::kPieces, c = (lane % L::kPieces) ^ L::f(row + lr);
-    load_to_lds(rsrc, (uint32_t)(prow + lr) * stride_bytes + c * 16, lds + row * L::kRowBytes);
-}
+// One cache's rows of a key head, and the loads of a tile of ROWS keys by WAVES waves: load i of wave
+// w takes rows kRows (WAVES i + w) and on, within 16 keys that one page holds.
+template <typename L, int ROWS, int WAVES>
+struct Loader {
+    static constexpr int kLoads = ROWS / (L::kRows * WAVES);
+    uint64_t base;          // of the head in page 0
+    uint32_t page_bytes, row_bytes;
+    int full;               // bytes from a page's first row of this head to behind its last
+    uint32_t lane_off;      // this lane's row and piece in the first load
+    int w;
+
+    __device__ __forceinline__ Loader(const void* cache, const kda_page_strides& st, int head, int page_size, int wave) {
+        base = reinterpret_cast<uint64_t>(cache) + 2 * (uint64_t)(head * st.h);
+        page_bytes = (uint32_t)(2 * st.p);
+        row_bytes = (uint32_t)(2 * st.t);
+        full = (page_size - 1) * (int)row_bytes + L::kRowBytes;
+        w = wave;
+        const int lane = threadIdx.x & 63, lr = lane / L::kPieces;
+        lane_off = (uint32_t)(w * L::kRows + lr) * row_bytes + 16 * ((lane % L::kPieces) ^ L::f(w * L::kRows) ^ L::f(lr));
+    }
+    // `valid` rows of the page exist; the others read as zeros
+    __device__ __forceinline__ i32x4 rsrc(int page, int page_size, int valid) const {
+        const uint64_t at = base + (uint64_t)page_bytes * (uint32_t)(page < 0 ? 0 : page);
+        int size = valid >= page_size ? full : valid > 0 ? (valid - 1) * (int)row_bytes + L::kRowBytes : 0;
+        i32x4 r;
+        r[0] = uniform((int)(uint32_t)at);
+        r[1] = uniform((int)(uint32_t)(at >> 32) & 0xffff);
+        r[2] = uniform(page < 0 ? 0 : size);
+        r[3] = kBufFlags;
+        return r;
+    }
+    // The piece permutation of load i differs from the first one's by a constant.
+    __device__ __forceinline__ uint32_t lane_offset(int i) const {
+        constexpr int step = L::kRows * WAVES;
+        return lane_off ^ (uint32_t)(16 * L::f(i * step));
+    }
+    // The tile at the walk's place; keys from `hi` on read as zeros, kb is the tile's first key.
+    __device__ __forceinline__ void issue(Pages& pg, int kb, int hi, uint32_t lds) const {
+        constexpr int step = L::kRows * WAVES;
+        lds += w * 1024;
+        if (pg.row + ROWS <= pg.page_size) {
+            const i32x4 r = rsrc(pg.page(0), pg.page_size, hi - kb + pg.row);
+            uint32_t s = pg.row * row_bytes;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) load_to_lds(r, lane_offset(i) + s + i * step * row_bytes, lds + i * WAVES * 1024);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = (i * step + w * L::kRows) & ~15;      // the 16 keys of the load
+            int row = pg.row + at, ahead = 0;
+            while (row >= pg.page_size) {
+                row -= pg.page_size;
+                ++ahead;
+            }
+            const i32x4 r = rsrc(pg.page(ahead), pg.page_size, hi - kb - at + row);
+            load_to_lds(r, lane_offset(i) + (uint32_t)(row + i * step - at) * row_bytes, lds + i * WAVES * 1024);
+        }
+    }
+};
 
 // ---- one wave's rows against a block of keys ------------------------------------------------------
 
@@ -185,7 +231,7 @@ struct Wave {
     bf16x8 Q[kKS];
     f32x16 O[kDT];
     float m, l;             // reference of this lane's query and this half's sum
-    int pos;                // this lane's query's position; negative: sees nothing
+    int pos, from;          // this lane's query sees keys from + 1 .. pos
     int first, last;        // least and largest position of the wave's live rows
     bool live;              // any row at all
 
@@ -195,9 +241,11 @@ struct Wave {
         const bool in = r < t.rows;
         const int tok = in ? r / a.G : 0, hd = in ? r - tok * a.G : 0;
         pos = in ? t.kv - t.n + tok : -1;
+        pos = pos < -1 ? -1 : pos;
+        from = a.window > 0 && pos - a.window > -1 ? (int)(pos - a.window) : -1;
         const int r0 = t.row0 + row_base, r1 = r0 + 31 < t.rows ? r0 + 31 : t.rows - 1;
         live = r0 < t.rows;
-        first = live ? t.kv - t.n + r0 / a.G : 0;
+        first = live ? t.kv - t.n + r0 / a.G : -1;
         last = live ? t.kv - t.n + r1 / a.G : -1;
         const bf16_t* p = static_cast<const bf16_t*>(a.q) + (a.packed ? 0 : t.seq * a.sq.b) + (t.first + tok) * a.sq.t +
                           ((int64_t)t.head * a.G + hd) * a.sq.h + 8 * h;
@@ -222,34 +270,34 @@ struct Wave {
         return a.window <= 0 || (int64_t)kb + KB - 1 > (int64_t)first - a.window;
     }
 
+    // Whether some row does not see some key of [kb, kb + KB).
+    __device__ __forceinline__ bool masks(const AttnArgs& a, int kb) const {
+        return kb + KB - 1 > first || (a.window > 0 && (int64_t)kb <= (int64_t)last - a.window);
+    }
+
+    template <bool MASKED>
     __device__ __forceinline__ void block(const AttnArgs& a, const char* ks_, const char* vs_, int kb) {
-        const int lane = threadIdx.x & 63, h = lane >> 5, n = lane & 31, l16 = lane & 15;
+        const int lane = fresh_lane(), h = lane >> 5, n = lane & 31;
         f32x16 S[kMT];
         // S^T = K Q^T
         {
             const char* kp = ks_ + n * TileK<DK>::kRowBytes;
             const int sw = 16 * (h ^ TileK<DK>::f(n));
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) S[mt][r] = 0.f;
-            }
+            constexpr f32x16 zero = {};
 #pragma unroll
             for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt)
-                    S[mt] = mfma32(read16(kp + (sw ^ (32 * ks)) + mt * 32 * TileK<DK>::kRowBytes), Q[ks], S[mt]);
+                    S[mt] = mfma32(read16(kp + (sw ^ (32 * ks)) + mt * 32 * TileK<DK>::kRowBytes), Q[ks], ks ? S[mt] : zero);
         }
-        const bool masked = kb + KB - 1 > first || (a.window > 0 && (int64_t)kb <= (int64_t)last - a.window);
-        if (masked) {
-            const int64_t from = a.window > 0 ? (int64_t)pos - a.window : -1;
+        if constexpr (MASKED) {
+            const uint32_t span = (uint32_t)(pos - from);      // keys from + 1 .. pos are seen
+            const uint32_t j0 = (uint32_t)(kb + 4 * h - from - 1);
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int j = kb + 32 * mt + (r & 3) + 8 * (r >> 2) + 4 * h;
-                    if (j > pos || j <= from) S[mt][r] = -INFINITY;
-                }
+                for (int r = 0; r < 16; ++r)
+                    if (j0 + (uint32_t)(32 * mt + (r & 3) + 8 * (r >> 2)) >= span) S[mt][r] = -INFINITY;
         }
         // the running reference: raised (and O, l scaled down) only when a score passes it by 2^8, which
         // keeps every 2^(x - m) below 2^8
@@ -289,14 +337,15 @@ struct Wave {
             }
         l += sum;
         // O^T += V^T P^T
-        const int vrow = 4 * h + (l16 >> 2);
+        const int lane2 = fresh_lane(), l16 = lane2 & 15;
+        const int vrow = 4 * (lane2 >> 5) + (l16 >> 2);
         const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
-        const int q2 = 2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1), fv = TileV<DV>::f(vrow);
-        bool bad = false;
-        if (masked && (last != first || a.window > 0)) bad = any_bad(vs_);
-        if (bad) {
-            block_bad(a, vp, q2 ^ fv, P, kb);
-            return;
+        const int q2 = 2 * ((lane2 >> 4) & 1) + ((l16 & 3) >> 1), fv = TileV<DV>::f(vrow);
+        if constexpr (MASKED) {
+            if ((last != first || a.window > 0) && any_bad(vs_)) {
+                block_bad(vp, q2 ^ fv, P, kb);
+                return;
+            }
         }
 #pragma unroll
         for (int s = 0; s < 2 * kMT; ++s)
@@ -312,7 +361,7 @@ struct Wave {
     // Whether the V block holds an infinity or a NaN. Only then can a key that some rows do not see
     // reach them: a probability of 0 times it.
     __device__ __forceinline__ bool any_bad(const char* vs_) const {
-        const int lane = threadIdx.x & 63;
+        const int lane = fresh_lane();
         uint32_t hit = 0;
 #pragma unroll
         for (int i = 0; i < KB * DV * 2 / 1024; ++i) {
@@ -327,9 +376,8 @@ struct Wave {
 
     // The same product with such values: they are taken out of V, and a second product of ones, where V
     // held them and where the row sees the key, says which outputs they belong to; those become NaN.
-    __device__ __forceinline__ void block_bad(const AttnArgs& a, const char* vp, int piece, const bf16x8* P, int kb) {
-        const int h = (threadIdx.x >> 5) & 1;
-        const int64_t from = a.window > 0 ? (int64_t)pos - a.window : -1;
+    __device__ __forceinline__ void block_bad(const char* vp, int piece, const bf16x8* P, int kb) {
+        const int h = fresh_lane() >> 5;
 #pragma unroll
         for (int dt = 0; dt < kDT; ++dt) {
             f32x16 C;
@@ -337,6 +385,7 @@ struct Wave {
             for (int r = 0; r < 16; ++r) C[r] = 0.f;
 #pragma unroll
             for (int s = 0; s < 2 * kMT; ++s) {
+                __builtin_amdgcn_sched_barrier(0);      // a rare path: few registers rather than overlap
                 uint4 v = __builtin_bit_cast(uint4, read_v(vp, piece, s, dt)), ones, seen;
                 uint32_t* vw = &v.x;
                 uint32_t* ow = &ones.x;
@@ -461,48 +510,33 @@ __global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnArgs a) {
     chunk_keys(t, from, to);
     Wave<DK, DV, KB> wave;
     wave.start(a, t, 32 * w);
-    Pages pg;
-    pg.table = a.table + t.seq * a.table_stride;
-    pg.max_pages = a.max_pages;
-    pg.page_size = a.page_size;
-    pg.pages = a.pages;
-    pg.seek(from);
-    pg.fetch();
+    Pages pg(a, t.seq, from);
+    const Loader<TileK<DK>, KB, kWaves> lk(a.k_cache, a.skc, t.head, a.page_size, w);
+    const Loader<TileV<DV>, KB, kWaves> lv(a.v_cache, a.svc, t.head, a.page_size, w);
     const uint32_t lds0 = lds_address(smem[0]), lds1 = lds_address(smem[1]);
-    const uint32_t kst = (uint32_t)a.skc.t * 2, vst = (uint32_t)a.svc.t * 2;
-    const int64_t kho = t.head * a.skc.h, vho = t.head * a.svc.h;
-    // 16 keys at a time; each wave its share of a group's rows
     auto issue = [&](uint32_t lds, int kb) {
-#pragma unroll
-        for (int g = 0; g < KB / 16; ++g) {
-            const int page = pg.page();
-            const int valid = t.hi - (kb + 16 * g - pg.row);       // rows of this page that any row sees
-            const int vr = valid < pg.page_size ? valid : pg.page_size;
-            typedef TileK<DK> LK;
-            typedef TileV<DV> LV;
-            constexpr int NK = 16 / LK::kRowsPerLoad, NV = 16 / LV::kRowsPerLoad;    // loads a group
-            if (NK == 4 || (w >> 1) == (g & 1)) {
-                const int i = NK == 4 ? w : (w & 1);
-                load_rows<LK>(page_rsrc(a.k_cache, page, a.skc.p, kho, a.skc.t, vr, DK), lds, 16 * g + i * LK::kRowsPerLoad,
-                              pg.row + i * LK::kRowsPerLoad, kst);
-            }
-            if (NV == 4 || (w >> 1) == (g & 1)) {
-                const int i = NV == 4 ? w : (w & 1);
-                load_rows<LV>(page_rsrc(a.v_cache, page, a.svc.p, vho, a.svc.t, vr, DV), lds + KBYTES, 16 * g + i * LV::kRowsPerLoad,
-                              pg.row + i * LV::kRowsPerLoad, vst);
-            }
-            pg.advance(16);
-        }
+        lk.issue(pg, kb, t.hi, lds);
+        lv.issue(pg, kb, t.hi, lds + KBYTES);
+        pg.advance(KB);
     };
     if (from < to) issue(lds0, from);
-    int buf = 0;
-    for (int kb = from; kb < to; kb += KB) {
+    int buf = 0, kb = from;
+    auto arrive = [&]() {
         wait_vm<0>();          // this wave's loads of the block
         lds_barrier();         // everyone's; the other buffer is free again
         if (kb + KB < to) issue(buf ? lds0 : lds1, kb + KB);
-        const char* s = smem[buf];
-        if (wave.sees(a, kb)) wave.block(a, s, s + KBYTES, kb);
-        buf ^= 1;
+    };
+    // blocks that every row sees whole, and the others, in loops of their own (the waves change over at
+    // different blocks, but pass the same barriers): O stays in one place through either
+    while (kb < to) {
+        for (; kb < to && !wave.masks(a, kb); kb += KB, buf ^= 1) {
+            arrive();
+            wave.template block<false>(a, smem[buf], smem[buf] + KBYTES, kb);
+        }
+        for (; kb < to && wave.masks(a, kb); kb += KB, buf ^= 1) {
+            arrive();
+            if (wave.sees(a, kb)) wave.template block<true>(a, smem[buf], smem[buf] + KBYTES, kb);
+        }
     }
     wave.finish(a, t, 32 * w, partials(a, false), kWideRows);
 }
@@ -522,57 +556,29 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
     chunk_keys(t, from, to);
     Wave<DK, DV, KB> wave;
     wave.start(a, t, 0);
-    Pages pg;
-    pg.table = a.table + t.seq * a.table_stride;
-    pg.max_pages = a.max_pages;
-    pg.page_size = a.page_size;
-    pg.pages = a.pages;
     const int mine = from + KB * w;
-    pg.seek(mine);
-    pg.fetch();
+    Pages pg(a, t.seq, mine);
+    const Loader<TileK<DK>, KB, 1> lk(a.k_cache, a.skc, t.head, a.page_size, 0);
+    const Loader<TileV<DV>, KB, 1> lv(a.v_cache, a.svc, t.head, a.page_size, 0);
     const uint32_t lds = lds_address(smem[w]);
-    const uint32_t kst = (uint32_t)a.skc.t * 2, vst = (uint32_t)a.svc.t * 2;
-    const int64_t kho = t.head * a.skc.h, vho = t.head * a.svc.h;
-    typedef TileK<DK> LK;
-    typedef TileV<DV> LV;
-    int page[2], prow[2], vr[2];
-    auto locate = [&](int kb) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            page[g] = pg.page();
-            prow[g] = pg.row;
-            const int valid = t.hi - (kb + 16 * g - pg.row);
-            vr[g] = valid < pg.page_size ? valid : pg.page_size;
-            pg.advance(16);
-        }
-        pg.advance(KB * (kWaves - 1));
-    };
-    auto issue_k = [&]() {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const i32x4 r = page_rsrc(a.k_cache, page[g], a.skc.p, kho, a.skc.t, vr[g], DK);
-#pragma unroll
-            for (int i = 0; i < 16 / LK::kRowsPerLoad; ++i)
-                load_rows<LK>(r, lds, 16 * g + i * LK::kRowsPerLoad, prow[g] + i * LK::kRowsPerLoad, kst);
-        }
-    };
-    auto issue_v = [&]() {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const i32x4 r = page_rsrc(a.v_cache, page[g], a.svc.p, vho, a.svc.t, vr[g], DV);
-#pragma unroll
-            for (int i = 0; i < 16 / LV::kRowsPerLoad; ++i)
-                load_rows<LV>(r, lds + KBYTES, 16 * g + i * LV::kRowsPerLoad, prow[g] + i * LV::kRowsPerLoad, vst);
-        }
-    };
-    for (int kb = mine; kb < to; kb += KB * kWaves) {
-        locate(kb);
-        issue_k();
-        issue_v();
+    int kb = mine;
+    auto arrive = [&]() {
+        wave_lds_sync();        // the last block's reads are through before the next loads land
+        lk.issue(pg, kb, t.hi, lds);
+        lv.issue(pg, kb, t.hi, lds + KBYTES);
+        pg.advance(KB * kWaves);
         wait_vm<0>();
         wave_lds_sync();
-        if (wave.sees(a, kb)) wave.block(a, smem[w], smem[w] + KBYTES, kb);
-        wave_lds_sync();        // this block's reads are through before the next loads land
+    };
+    while (kb < to) {
+        for (; kb < to && !wave.masks(a, kb); kb += KB * kWaves) {
+            arrive();
+            wave.template block<false>(a, smem[w], smem[w] + KBYTES, kb);
+        }
+        for (; kb < to && wave.masks(a, kb); kb += KB * kWaves) {
+            arrive();
+            if (wave.sees(a, kb)) wave.template block<true>(a, smem[w], smem[w] + KBYTES, kb);
+        }
     }
     // join the waves: every wave leaves m, l, O in LDS; wave w takes the rows' channels in turn
     lds_barrier();
