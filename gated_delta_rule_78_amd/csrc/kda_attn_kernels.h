@@ -341,16 +341,26 @@ struct Wave {
         const int vrow = 4 * (lane2 >> 5) + (l16 >> 2);
         const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
         const int q2 = 2 * ((lane2 >> 4) & 1) + ((l16 & 3) >> 1), fv = TileV<DV>::f(vrow);
+        const int piece = q2 ^ fv;
         if constexpr (MASKED) {
-            if ((last != first || a.window > 0) && any_bad(vs_)) {
-                block_bad(vp, q2 ^ fv, P, kb);
-                return;
-            }
+            // a key that some rows do not see reaches them as a probability of 0 times its value: where V holds
+            // an infinity or a NaN it is left out, and the outputs it belongs to become NaN
+            const bool bad = (last != first || a.window > 0) && any_bad(vs_);
+#pragma unroll
+            for (int s = 0; s < 2 * kMT; ++s)
+#pragma unroll
+                for (int dt = 0; dt < kDT; ++dt) {
+                    bf16x8 v = read_v(vp, piece, s, dt);
+                    if (bad) v = split_bad(v, false);
+                    O[dt] = mfma32(v, P[s], O[dt]);
+                }
+            if (bad) mark_bad(vp, piece, kb);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2 * kMT; ++s)
+#pragma unroll
+                for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, piece, s, dt), P[s], O[dt]);
         }
-#pragma unroll
-        for (int s = 0; s < 2 * kMT; ++s)
-#pragma unroll
-            for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, q2 ^ fv, s, dt), P[s], O[dt]);
     }
 
     __device__ static __forceinline__ bf16x8 read_v(const char* vp, int piece, int s, int dt) {
@@ -363,7 +373,7 @@ struct Wave {
     __device__ __forceinline__ bool any_bad(const char* vs_) const {
         const int lane = fresh_lane();
         uint32_t hit = 0;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < KB * DV * 2 / 1024; ++i) {
             const uint4 u = *reinterpret_cast<const uint4*>(vs_ + i * 1024 + lane * 16);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -374,41 +384,44 @@ struct Wave {
         return __any(hit);
     }
 
-    // The same product with such values: they are taken out of V, and a second product of ones, where V
-    // held them and where the row sees the key, says which outputs they belong to; those become NaN.
-    __device__ __forceinline__ void block_bad(const char* vp, int piece, const bf16x8* P, int kb) {
+    // V without its infinities and NaN (zeros there), or ones where it holds them and zeros elsewhere.
+    __device__ static __forceinline__ bf16x8 split_bad(bf16x8 x, bool ones) {
+        const uint4 u = __builtin_bit_cast(uint4, x);
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
+            if (ones)
+                w[k] = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
+            else
+                w[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+        }
+        return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+
+    // Counts, for every output, the infinities and NaN among the values that its row sees, and makes those
+    // outputs NaN.
+    __device__ __forceinline__ void mark_bad(const char* vp, int piece, int kb) {
         const int h = fresh_lane() >> 5;
+        const uint32_t span = (uint32_t)(pos - from), j0 = (uint32_t)(kb + 4 * h - from - 1);
 #pragma unroll
         for (int dt = 0; dt < kDT; ++dt) {
-            f32x16 C;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) C[r] = 0.f;
+            f32x16 C = {};
 #pragma unroll
             for (int s = 0; s < 2 * kMT; ++s) {
-                __builtin_amdgcn_sched_barrier(0);      // a rare path: few registers rather than overlap
-                uint4 v = __builtin_bit_cast(uint4, read_v(vp, piece, s, dt)), ones, seen;
-                uint32_t* vw = &v.x;
-                uint32_t* ow = &ones.x;
-                uint32_t* sw = &seen.x;
+                uint32_t seen[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const bool lo = (vw[k] & 0x7f80u) == 0x7f80u, hi = (vw[k] & 0x7f800000u) == 0x7f800000u;
-                    ow[k] = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
-                    vw[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
-                    uint32_t b = 0;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int el = 2 * k + e, j = kb + 16 * s + (el & 3) + 8 * (el >> 2) + 4 * h;
-                        if (j <= pos && j > from) b |= 0x3f80u << (16 * e);
-                    }
-                    sw[k] = b;
+                    uint32_t j = j0 + (uint32_t)(16 * s + 2 * (k & 1) + 8 * (k >> 1));
+                    asm volatile("" : "+v"(j));      // formed anew for each product: a rare path, few registers
+                    seen[k] = (j < span ? 0x3f80u : 0u) | (j + 1 < span ? 0x3f800000u : 0u);
                 }
-                O[dt] = mfma32(__builtin_bit_cast(bf16x8, v), P[s], O[dt]);
-                C = mfma32(__builtin_bit_cast(bf16x8, ones), __builtin_bit_cast(bf16x8, seen), C);
+                C = mfma32(split_bad(read_v(vp, piece, s, dt), true),
+                           __builtin_bit_cast(bf16x8, make_uint4(seen[0], seen[1], seen[2], seen[3])), C);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (C[r] > 0.f) O[dt][r] = NAN;
+            for (int r = 0; r < 16; ++r) O[dt][r] = C[r] > 0.f ? NAN : O[dt][r];
         }
     }
 

@@ -108,3 +108,42 @@ def test_parity(c):
     o, lse = call(c, x)
     torch.cuda.synchronize()
     check(c, x, o, lse)
+
+
+BAD = [
+    ([40], [30], 2, 1, 64, 64, 16, 0, False),
+    ([1, 50, 9], [10, 100, 3], 4, 2, 128, 128, 64, 0, True),
+    ([4, 4], [60, 200], 4, 1, 128, 64, 16, 20, False),
+    ([90], [100], 8, 2, 64, 128, 32, 33, False),
+]
+
+
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("c", BAD, ids=ids)
+def test_bad_values_reach_only_rows_that_see_them(c, value, where):
+    """A non-finite key or value of one position: rows that do not see it keep their bits, rows that do see
+    a non-finite value get one."""
+    x = make(c)
+    clean, clean_l = call(c, x)
+    s = len(c[0]) - 1 if c[8] else 0
+    n, kv = c[0][s], c[0][s] + c[1][s]
+    for j in (kv - 1, kv - n // 2 - 1, max(0, kv - n - 5)):
+        t = (x["kc"] if where == "k" else x["vc"]).clone()
+        page = int(x["table"][s, j // c[6]])
+        t[page, 0, j % c[6], 3] = value
+        y = dict(x, **{"kc" if where == "k" else "vc": t})
+        o, lse = call(c, y)
+        a, b, la, lb = (torch.from_numpy(tokens(u, c[8])) for u in (clean, o, clean_l, lse))
+        T, Hq = a.shape[:2]
+        sees = torch.zeros(T, Hq, dtype=torch.bool)
+        for i in range(n):
+            pos = kv - n + i
+            if j <= pos and (c[7] == 0 or j > pos - c[7]):
+                sees[x["cu_host"][s] + i, :Hq // c[3]] = True
+        assert torch.equal(a[~sees], b[~sees]) and torch.equal(la[~sees], lb[~sees]), j
+        if where == "v":
+            assert not torch.isfinite(b[sees][:, 3]).any() and torch.equal(lb, la), j
+            assert torch.isfinite(b[..., 4:]).all(), j
+        elif value != value:
+            assert torch.isnan(b[sees]).all() and torch.isnan(lb[sees]).all(), j
