@@ -29,7 +29,7 @@ __global__ __launch_bounds__(1024) void attn_plan_kernel(AttnArgs a) {
     int64_t len[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        len[k] = (int64_t)((units[k] + kTarget - 1) / kTarget);
+        len[k] = (int64_t)((units[k] + target(k == 0) - 1) / target(k == 0));
         if (len[k] < kMinUnits) len[k] = kMinUnits;
     }
     PlanEntry* plan = static_cast<PlanEntry*>(a.ws);
@@ -86,7 +86,7 @@ namespace {
 // Workgroups at most: every tile once, and the chunks beyond the first of each.
 int64_t groups_most(const AttnArgs& a, bool narrow) {
     const int64_t tiles = tiles_most(a, narrow ? kNarrowRows : kWideRows, narrow) * a.Hk;
-    return tiles + (may_cut(a) ? kTarget : 0);
+    return tiles + (may_cut(a) ? target(narrow) : 0);
 }
 
 template <int DK, int DV>
@@ -99,7 +99,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
         e = launch_main<DK, DV>(a, narrow, groups_most(a, narrow), st);
         if (e != hipSuccess || !may_cut(a)) continue;
         const int rows = narrow ? kNarrowRows : kWideRows, each = 4;
-        const dim3 grid((unsigned)kTarget, (unsigned)(rows / each));
+        const dim3 grid((unsigned)target(narrow), (unsigned)(rows / each));
         if (narrow)
             hipLaunchKernelGGL((attn_join_kernel<DV, true>), grid, dim3(kThreads), 0, st, a, each);
         else
@@ -115,15 +115,15 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
 size_t attn_ws_bytes(const AttnArgs& a) {
     using namespace attn;
     int64_t b = plan_bytes(a.N);
-    if (has_narrow(a)) b += slots_most() * partial_bytes(kNarrowRows, a.dv);
-    if (has_wide(a)) b += slots_most() * partial_bytes(kWideRows, a.dv);
+    if (has_narrow(a)) b += slots_most(true) * partial_bytes(kNarrowRows, a.dv);
+    if (has_wide(a)) b += slots_most(false) * partial_bytes(kWideRows, a.dv);
     return (size_t)b;
 }
 
 hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t st) {
     using namespace attn;
     for (int k = 0; k < 2; ++k)     // a launch has fewer than 2^32 threads
-        if (groups_most(a, k == 0) >= (int64_t)1 << 24) return hipErrorInvalidConfiguration;
+        if (groups_most(a, k == 0) >= (int64_t)1 << 23) return hipErrorInvalidConfiguration;
     if (a.dk == 128) return a.dv == 128 ? launch<128, 128>(a, st) : launch<128, 64>(a, st);
     return a.dv == 128 ? launch<64, 128>(a, st) : launch<64, 64>(a, st);
 }

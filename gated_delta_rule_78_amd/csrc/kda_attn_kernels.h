@@ -113,15 +113,23 @@ __device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, int n, bool narro
 
 // ---- a page table walked by one wave ------------------------------------------------------------
 
-// A place among the pages, all of it uniform. 64 entries of the table are held in a register, one a lane.
+// A place among a sequence's pages, all of it uniform but for what is held: lane i holds the addresses
+// of one key head's rows in page base + i of either cache (their upper half -1 for a page number
+// outside the cache), so that going to a page costs a wave four lane reads.
 struct Pages {
     const int32_t* table;
+    const void *kc, *vc;
+    int64_t kp, vp, kh, vh;         // page strides and head offsets, elements
     int max_pages, page_size, pages;
-    int pg, row;            // page index and row of the current key
-    int base, held;         // held: this lane's entry of page base + lane
+    int pg, row;                    // page index and row of the current key
+    int base;
+    uint32_t klo, khi, vlo, vhi;    // held
 
-    __device__ __forceinline__ Pages(const AttnArgs& a, int64_t seq, int key) {
+    __device__ __forceinline__ Pages(const AttnArgs& a, int64_t seq, int head, int key) {
         table = a.table + seq * a.table_stride;
+        kc = a.k_cache; vc = a.v_cache;
+        kp = a.skc.p; vp = a.svc.p;
+        kh = head * a.skc.h; vh = head * a.svc.h;
         max_pages = a.max_pages;
         page_size = a.page_size;
         pages = a.pages;
@@ -138,14 +146,30 @@ struct Pages {
     }
     __device__ __forceinline__ void fetch() {
         base = pg;
-        const int i = pg + (int)(threadIdx.x & 63);
-        held = i < max_pages ? table[i] : -1;
+        const int i = pg + fresh_lane(), p = i < max_pages ? table[i] : -1;
+        const bool ok = p >= 0 && p < pages;
+        const uint64_t k = reinterpret_cast<uint64_t>(kc) + 2 * (uint64_t)((ok ? p : 0) * kp + kh);
+        const uint64_t v = reinterpret_cast<uint64_t>(vc) + 2 * (uint64_t)((ok ? p : 0) * vp + vh);
+        klo = (uint32_t)k; khi = ok ? (uint32_t)(k >> 32) & 0xffff : 0xffffffffu;
+        vlo = (uint32_t)v; vhi = ok ? (uint32_t)(v >> 32) & 0xffff : 0xffffffffu;
     }
-    // number of the page `ahead` (< 48) of the current one, or -1
-    __device__ __forceinline__ int page(int ahead) {
+    // Descriptors of the page `ahead` (< 48) of the current one, of which `valid` rows exist; the others
+    // read as zeros.
+    template <typename LK, typename LV>
+    __device__ __forceinline__ void descriptors(int ahead, int valid, const LK& lk, const LV& lv, i32x4& k, i32x4& v) {
         if (pg + ahead - base >= 64) fetch();
-        const int p = __builtin_amdgcn_readlane(held, pg + ahead - base);
-        return p >= 0 && p < pages ? p : -1;
+        const int i = pg + ahead - base;
+        const bool all = valid >= page_size, none = valid <= 0;
+        k[0] = __builtin_amdgcn_readlane(klo, i);
+        k[1] = __builtin_amdgcn_readlane(khi, i);
+        v[0] = __builtin_amdgcn_readlane(vlo, i);
+        v[1] = __builtin_amdgcn_readlane(vhi, i);
+        const bool bad = k[1] < 0 || none;
+        k[2] = bad ? 0 : all ? lk.full : (valid - 1) * (int)lk.row_bytes + LK::kRowBytes;
+        v[2] = bad ? 0 : all ? lv.full : (valid - 1) * (int)lv.row_bytes + LV::kRowBytes;
+        k[1] &= 0xffff;
+        v[1] &= 0xffff;
+        k[3] = v[3] = kBufFlags;
     }
 };
 
@@ -157,71 +181,74 @@ struct TileK {       // read row-wise: lanes 0..31 one row each
     __device__ static __forceinline__ int f(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
 };
 template <int D>
-struct TileV {       // read transposed: 4 rows x 32 bytes a group of 16 lanes
+struct TileV {       // read transposed: 4 rows x 64 bytes a half wave
     static constexpr int kD = D, kRowBytes = 2 * D, kPieces = D / 8, kRows = 1024 / kRowBytes;
-    __device__ static __forceinline__ int f(int row) { return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3); }
+    __device__ static __forceinline__ int f(int row) { return D == 128 ? 4 * (row & 3) : 4 * ((row >> 1) & 1); }
 };
 
-// One cache's rows of a key head, and the loads of a tile of ROWS keys by WAVES waves: load i of wave
-// w takes rows kRows (WAVES i + w) and on, within 16 keys that one page holds.
+// The loads of a tile of ROWS keys of one cache by WAVES waves: load i of wave w takes the kRows rows
+// from kRows (WAVES i + w) on, all within 16 keys that one page holds.
 template <typename L, int ROWS, int WAVES>
 struct Loader {
-    static constexpr int kLoads = ROWS / (L::kRows * WAVES);
-    uint64_t base;          // of the head in page 0
-    uint32_t page_bytes, row_bytes;
-    int full;               // bytes from a page's first row of this head to behind its last
-    uint32_t lane_off;      // this lane's row and piece in the first load
+    static constexpr int kLoads = ROWS / (L::kRows * WAVES), kStep = L::kRows * WAVES, kRowBytes = L::kRowBytes;
+    uint32_t row_bytes;
+    int full;               // bytes from a page's first row of the head to behind its last
+    uint32_t lane_row, lane_piece;      // offsets of this lane's row and piece in the first load
     int w;
 
-    __device__ __forceinline__ Loader(const void* cache, const kda_page_strides& st, int head, int page_size, int wave) {
-        base = reinterpret_cast<uint64_t>(cache) + 2 * (uint64_t)(head * st.h);
-        page_bytes = (uint32_t)(2 * st.p);
+    __device__ __forceinline__ Loader(const kda_page_strides& st, int page_size, int wave) {
         row_bytes = (uint32_t)(2 * st.t);
-        full = (page_size - 1) * (int)row_bytes + L::kRowBytes;
+        full = (page_size - 1) * (int)row_bytes + kRowBytes;
         w = wave;
         const int lane = threadIdx.x & 63, lr = lane / L::kPieces;
-        lane_off = (uint32_t)(w * L::kRows + lr) * row_bytes + 16 * ((lane % L::kPieces) ^ L::f(w * L::kRows) ^ L::f(lr));
+        lane_row = (uint32_t)(w * L::kRows + lr) * row_bytes;
+        lane_piece = 16 * ((lane % L::kPieces) ^ L::f(w * L::kRows) ^ L::f(lr));
     }
-    // `valid` rows of the page exist; the others read as zeros
-    __device__ __forceinline__ i32x4 rsrc(int page, int page_size, int valid) const {
-        const uint64_t at = base + (uint64_t)page_bytes * (uint32_t)(page < 0 ? 0 : page);
-        int size = valid >= page_size ? full : valid > 0 ? (valid - 1) * (int)row_bytes + L::kRowBytes : 0;
-        i32x4 r;
-        r[0] = uniform((int)(uint32_t)at);
-        r[1] = uniform((int)(uint32_t)(at >> 32) & 0xffff);
-        r[2] = uniform(page < 0 ? 0 : size);
-        r[3] = kBufFlags;
-        return r;
+    // Load i from the page of descriptor r whose row `row` is the tile's row 0. The piece permutation
+    // differs from the first load's by a constant.
+    __device__ __forceinline__ void load(i32x4 r, int i, int row, uint32_t lds) const {
+        load_to_lds(r, (lane_piece ^ (uint32_t)(16 * L::f(i * kStep))) + lane_row + (uint32_t)(row + i * kStep) * row_bytes,
+                    lds + (i * WAVES + w) * 1024);
     }
-    // The piece permutation of load i differs from the first one's by a constant.
-    __device__ __forceinline__ uint32_t lane_offset(int i) const {
-        constexpr int step = L::kRows * WAVES;
-        return lane_off ^ (uint32_t)(16 * L::f(i * step));
-    }
-    // The tile at the walk's place; keys from `hi` on read as zeros, kb is the tile's first key.
-    __device__ __forceinline__ void issue(Pages& pg, int kb, int hi, uint32_t lds) const {
-        constexpr int step = L::kRows * WAVES;
-        lds += w * 1024;
-        if (pg.row + ROWS <= pg.page_size) {
-            const i32x4 r = rsrc(pg.page(0), pg.page_size, hi - kb + pg.row);
-            uint32_t s = pg.row * row_bytes;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) load_to_lds(r, lane_offset(i) + s + i * step * row_bytes, lds + i * WAVES * 1024);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int at = (i * step + w * L::kRows) & ~15;      // the 16 keys of the load
-            int row = pg.row + at, ahead = 0;
-            while (row >= pg.page_size) {
-                row -= pg.page_size;
-                ++ahead;
-            }
-            const i32x4 r = rsrc(pg.page(ahead), pg.page_size, hi - kb - at + row);
-            load_to_lds(r, lane_offset(i) + (uint32_t)(row + i * step - at) * row_bytes, lds + i * WAVES * 1024);
-        }
-    }
+    __device__ __forceinline__ int first_row(int i) const { return i * kStep + w * L::kRows; }
 };
+
+// The keys' and the values' tile at the walk's place; keys from `hi` on read as zeros, kb is the first.
+template <int ROWS, typename LK, typename LV>
+__device__ __forceinline__ void load_block(Pages& pg, const LK& lk, const LV& lv, int kb, int hi, uint32_t klds, uint32_t vlds) {
+    i32x4 rk, rv;
+    if (pg.row + ROWS <= pg.page_size) {
+        pg.descriptors(0, hi - kb + pg.row, lk, lv, rk, rv);
+#pragma unroll
+        for (int i = 0; i < LK::kLoads; ++i) lk.load(rk, i, pg.row, klds);
+#pragma unroll
+        for (int i = 0; i < LV::kLoads; ++i) lv.load(rv, i, pg.row, vlds);
+        return;
+    }
+    // the tile spans pages: each load finds its own
+    auto place = [&](int at, int& row) {
+        int ahead = 0;
+        row = pg.row + at;
+        while (row >= pg.page_size) {
+            row -= pg.page_size;
+            ++ahead;
+        }
+        pg.descriptors(ahead, hi - kb - at + row, lk, lv, rk, rv);
+    };
+    int row;
+#pragma unroll
+    for (int i = 0; i < LK::kLoads; ++i) {
+        const int at = lk.first_row(i) & ~15;
+        place(at, row);
+        lk.load(rk, i, row - at, klds);
+    }
+#pragma unroll
+    for (int i = 0; i < LV::kLoads; ++i) {
+        const int at = lv.first_row(i) & ~15;
+        place(at, row);
+        lv.load(rv, i, row - at, vlds);
+    }
+}
 
 // ---- one wave's rows against a block of keys ------------------------------------------------------
 
@@ -275,37 +302,44 @@ struct Wave {
         return kb + KB - 1 > first || (a.window > 0 && (int64_t)kb <= (int64_t)last - a.window);
     }
 
+    // S^T = K Q^T of a block, and the registers of P^T that the second product takes.
+    struct Scores {
+        f32x16 s[kMT];
+    };
+    struct Probs {
+        bf16x8 p[2 * kMT];
+    };
+
+    __device__ __forceinline__ void scores(const char* ks_, Scores& S) const {
+        const int lane = fresh_lane(), n = lane & 31;
+        const char* kp = ks_ + n * TileK<DK>::kRowBytes;
+        const int sw = 16 * ((lane >> 5) ^ TileK<DK>::f(n));
+        constexpr f32x16 zero = {};
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+                S.s[mt] = mfma32(read16(kp + (sw ^ (32 * ks)) + mt * 32 * TileK<DK>::kRowBytes), Q[ks], ks ? S.s[mt] : zero);
+    }
+
     template <bool MASKED>
-    __device__ __forceinline__ void block(const AttnArgs& a, const char* ks_, const char* vs_, int kb) {
-        const int lane = fresh_lane(), h = lane >> 5, n = lane & 31;
-        f32x16 S[kMT];
-        // S^T = K Q^T
-        {
-            const char* kp = ks_ + n * TileK<DK>::kRowBytes;
-            const int sw = 16 * (h ^ TileK<DK>::f(n));
-            constexpr f32x16 zero = {};
-#pragma unroll
-            for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-                    S[mt] = mfma32(read16(kp + (sw ^ (32 * ks)) + mt * 32 * TileK<DK>::kRowBytes), Q[ks], ks ? S[mt] : zero);
-        }
+    __device__ __forceinline__ void softmax(const AttnArgs& a, Scores& S, Probs& P, int kb) {
         if constexpr (MASKED) {
             const uint32_t span = (uint32_t)(pos - from);      // keys from + 1 .. pos are seen
-            const uint32_t j0 = (uint32_t)(kb + 4 * h - from - 1);
+            const uint32_t j0 = (uint32_t)(kb + 4 * (fresh_lane() >> 5) - from - 1);
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (j0 + (uint32_t)(32 * mt + (r & 3) + 8 * (r >> 2)) >= span) S[mt][r] = -INFINITY;
+                    if (j0 + (uint32_t)(32 * mt + (r & 3) + 8 * (r >> 2)) >= span) S.s[mt][r] = -INFINITY;
         }
         // the running reference: raised (and O, l scaled down) only when a score passes it by 2^8, which
         // keeps every 2^(x - m) below 2^8
-        float mx = S[0][0];
+        float mx = S.s[0][0];
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, S[mt][r]);
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, S.s[mt][r]);
         mx = both_max(mx) * a.c;
         if (__any(mx > m + 8.f)) {
             const float mn = mx > m + 8.f ? mx : m;
@@ -318,7 +352,6 @@ struct Wave {
                 for (int r = 0; r < 16; ++r) O[i][r] *= f;
         }
         const float sub = m == -INFINITY ? 0.f : m;
-        bf16x8 P[2 * kMT];
         float sum = 0.f;
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
@@ -327,21 +360,24 @@ struct Wave {
                 float p[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    p[e] = __builtin_amdgcn_exp2f(fmaf(S[mt][8 * kk + e], a.c, -sub));
+                    p[e] = __builtin_amdgcn_exp2f(fmaf(S.s[mt][8 * kk + e], a.c, -sub));
                     sum += p[e];
                 }
                 uint4 u;
                 u.x = pack_bf16x2(p[0], p[1]); u.y = pack_bf16x2(p[2], p[3]);
                 u.z = pack_bf16x2(p[4], p[5]); u.w = pack_bf16x2(p[6], p[7]);
-                P[2 * mt + kk] = __builtin_bit_cast(bf16x8, u);
+                P.p[2 * mt + kk] = __builtin_bit_cast(bf16x8, u);
             }
         l += sum;
-        // O^T += V^T P^T
-        const int lane2 = fresh_lane(), l16 = lane2 & 15;
-        const int vrow = 4 * (lane2 >> 5) + (l16 >> 2);
+    }
+
+    // O^T += V^T P^T
+    template <bool MASKED>
+    __device__ __forceinline__ void values(const AttnArgs& a, const char* vs_, const Probs& P, int kb) {
+        const int lane = fresh_lane(), l16 = lane & 15;
+        const int vrow = 4 * (lane >> 5) + (l16 >> 2);
         const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
-        const int q2 = 2 * ((lane2 >> 4) & 1) + ((l16 & 3) >> 1), fv = TileV<DV>::f(vrow);
-        const int piece = q2 ^ fv;
+        const int piece = (2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ TileV<DV>::f(vrow);
         if constexpr (MASKED) {
             // a key that some rows do not see reaches them as a probability of 0 times its value: where V holds
             // an infinity or a NaN it is left out, and the outputs it belongs to become NaN
@@ -352,15 +388,54 @@ struct Wave {
                 for (int dt = 0; dt < kDT; ++dt) {
                     bf16x8 v = read_v(vp, piece, s, dt);
                     if (bad) v = split_bad(v, false);
-                    O[dt] = mfma32(v, P[s], O[dt]);
+                    O[dt] = mfma32(v, P.p[s], O[dt]);
                 }
             if (bad) mark_bad(vp, piece, kb);
         } else {
 #pragma unroll
             for (int s = 0; s < 2 * kMT; ++s)
 #pragma unroll
-                for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, piece, s, dt), P[s], O[dt]);
+                for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, piece, s, dt), P.p[s], O[dt]);
         }
+    }
+
+    // scores of one block and values of the one before as one stream of products, each operand read from LDS
+    // AHEAD products before its own. The order is pinned: left to itself the compiler waits for every
+    // operand right after asking for it.
+    __device__ __forceinline__ void scores_values(const char* ks_, Scores& S, const char* vs_, const Probs& P) {
+        constexpr int NQ = kKS * kMT, N = NQ + 2 * kMT * kDT, AHEAD = 8;
+        const int lane = fresh_lane(), n = lane & 31, l16 = lane & 15;
+        const char* kp = ks_ + n * TileK<DK>::kRowBytes;
+        const int sw = 16 * ((lane >> 5) ^ TileK<DK>::f(n));
+        const int vrow = 4 * (lane >> 5) + (l16 >> 2);
+        const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
+        const int piece = (2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ TileV<DV>::f(vrow);
+        constexpr f32x16 zero = {};
+        bf16x8 F[N];
+#pragma unroll
+        for (int x = 0; x < N + AHEAD; ++x) {
+            if (x < NQ)
+                F[x] = read16(kp + (sw ^ (32 * (x / kMT))) + (x % kMT) * 32 * TileK<DK>::kRowBytes);
+            else if (x < N)
+                F[x] = read_v(vp, piece, (x - NQ) / kDT, (x - NQ) % kDT);
+            const int y = x - AHEAD;
+            if (y >= 0) {
+                if (y < NQ)
+                    S.s[y % kMT] = mfma32(F[y], Q[y / kMT], y < kMT ? zero : S.s[y % kMT]);
+                else
+                    O[(y - NQ) % kDT] = mfma32(F[y], P.p[(y - NQ) / kDT], O[(y - NQ) % kDT]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    template <bool MASKED>
+    __device__ __forceinline__ void block(const AttnArgs& a, const char* ks_, const char* vs_, int kb) {
+        Scores S;
+        Probs P;
+        scores(ks_, S);
+        softmax<MASKED>(a, S, P, kb);
+        values<MASKED>(a, vs_, P, kb);
     }
 
     __device__ static __forceinline__ bf16x8 read_v(const char* vp, int piece, int s, int dt) {
@@ -506,50 +581,101 @@ __device__ __forceinline__ void chunk_keys(const Tile& t, int& from, int& to) {
 
 __device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
     char* p = static_cast<char*>(a.ws) + plan_bytes(a.N);
-    if (!narrow && has_narrow(a)) p += slots_most() * partial_bytes(kNarrowRows, a.dv);
+    if (!narrow && has_narrow(a)) p += slots_most(true) * partial_bytes(kNarrowRows, a.dv);
     return reinterpret_cast<float*>(p);
 }
 
-// ---- wide tiles: four waves of 32 rows share blocks of 64 keys in LDS ----------------------------
+// ---- wide tiles: eight waves of 32 rows share blocks of 64 keys in LDS -----------------------------
+//
+// The waves form two groups of four, one of each on every SIMD, half a step apart: while one group
+// multiplies (the scores of block i and the values of block i - 1) the other does the softmax of its
+// scores, so that the SIMD's matrix and vector units work at once. Phase 2i is the first group's
+// products of step i and the second's softmax of step i - 1, phase 2i + 1 the other way round; a barrier
+// ends each. LDS holds four blocks of keys and values. In its softmax of block i a wave asks for its
+// share of block i + 2 (first group) or i + 3 (second): a block's place is free by then, and what is
+// asked for is awaited at the barrier before phase 2j, three or four phases later.
 
 template <int DK, int DV>
-__global__ __launch_bounds__(kThreads, 2) void attn_wide_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) {
     constexpr int KB = 64, KBYTES = KB * DK * 2, VBYTES = KB * DV * 2;
-    __shared__ __align__(1024) char smem[2][KBYTES + VBYTES];
+    typedef Wave<DK, DV, KB> W;
+    typedef Loader<TileK<DK>, KB, kWideWaves> LK;
+    typedef Loader<TileV<DV>, KB, kWideWaves> LV;
+    __shared__ __align__(1024) char smem[4][KBYTES + VBYTES];
     Tile t;
     if (!find_tile<false>(a, t)) return;
     const int w = uniform(threadIdx.x >> 6);
     int from, to;
     chunk_keys(t, from, to);
-    Wave<DK, DV, KB> wave;
+    const int nb = to > from ? (to - from + KB - 1) / KB : 0;
+    W wave;
     wave.start(a, t, 32 * w);
-    Pages pg(a, t.seq, from);
-    const Loader<TileK<DK>, KB, kWaves> lk(a.k_cache, a.skc, t.head, a.page_size, w);
-    const Loader<TileV<DV>, KB, kWaves> lv(a.v_cache, a.svc, t.head, a.page_size, w);
-    const uint32_t lds0 = lds_address(smem[0]), lds1 = lds_address(smem[1]);
-    auto issue = [&](uint32_t lds, int kb) {
-        lk.issue(pg, kb, t.hi, lds);
-        lv.issue(pg, kb, t.hi, lds + KBYTES);
-        pg.advance(KB);
-    };
-    if (from < to) issue(lds0, from);
-    int buf = 0, kb = from;
-    auto arrive = [&]() {
-        wait_vm<0>();          // this wave's loads of the block
-        lds_barrier();         // everyone's; the other buffer is free again
-        if (kb + KB < to) issue(buf ? lds0 : lds1, kb + KB);
-    };
-    // blocks that every row sees whole, and the others, in loops of their own (the waves change over at
-    // different blocks, but pass the same barriers): O stays in one place through either
-    while (kb < to) {
-        for (; kb < to && !wave.masks(a, kb); kb += KB, buf ^= 1) {
-            arrive();
-            wave.template block<false>(a, smem[buf], smem[buf] + KBYTES, kb);
+    if (nb > 0) {
+        Pages pg(a, t.seq, t.head, from);
+        const LK lk(a.skc, a.page_size, w);
+        const LV lv(a.svc, a.page_size, w);
+        const uint32_t lds = lds_address(smem);
+        int asked = 0;
+        auto ask = [&]() {
+            if (asked >= nb) return;
+            const uint32_t at = lds + (asked & 3) * (KBYTES + VBYTES);
+            load_block<KB>(pg, lk, lv, from + asked * KB, t.hi, at, at + KBYTES);
+            pg.advance(KB);
+            ++asked;
+        };
+        // before phase 2i: this wave's share of block i has landed (block i + 1 may be on its way), then everyone's
+        auto even = [&](int i) {
+            if (i + 1 < nb)
+                wait_vm<LK::kLoads + LV::kLoads>();
+            else
+                wait_vm<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            lds_barrier();
+        };
+        auto odd = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            lds_barrier();
+        };
+        const bool second = w >= 4;
+        ask();
+        ask();
+        if (second) ask();
+        typename W::Scores S;
+        typename W::Probs P;
+        even(0);
+        if (second) odd();
+        bool seen = wave.sees(a, from);
+        if (seen) wave.scores(smem[0], S);
+        if (second) even(1); else odd();
+        ask();
+        if (seen) wave.template softmax<true>(a, S, P, from);
+        // blocks that all rows see whole, the one before too, and the others, in loops of their own (the waves
+        // change over at different blocks, but pass the same barriers): O stays in one place through either
+        int i = 1;
+        while (i < nb) {
+            for (; i < nb && !wave.masks(a, from + i * KB) && !wave.masks(a, from + (i - 1) * KB); ++i) {
+                if (second) odd(); else even(i);
+                wave.scores_values(smem[i & 3], S, smem[(i - 1) & 3] + KBYTES, P);
+                if (second) even(i + 1); else odd();
+                ask();
+                wave.template softmax<false>(a, S, P, 0);
+                seen = true;
+            }
+            for (; i < nb && (wave.masks(a, from + i * KB) || wave.masks(a, from + (i - 1) * KB)); ++i) {
+                if (second) odd(); else even(i);
+                const int kb = from + i * KB;
+                const bool sees = wave.sees(a, kb);
+                if (sees) wave.scores(smem[i & 3], S);
+                if (seen) wave.template values<true>(a, smem[(i - 1) & 3] + KBYTES, P, kb - KB);
+                if (second) even(i + 1); else odd();
+                ask();
+                if (sees) wave.template softmax<true>(a, S, P, kb);
+                seen = sees;
+            }
         }
-        for (; kb < to && wave.masks(a, kb); kb += KB, buf ^= 1) {
-            arrive();
-            if (wave.sees(a, kb)) wave.template block<true>(a, smem[buf], smem[buf] + KBYTES, kb);
-        }
+        if (second) odd(); else even(nb);
+        if (seen) wave.template values<true>(a, smem[(nb - 1) & 3] + KBYTES, P, from + (nb - 1) * KB);
+        if (!second) odd();
     }
     wave.finish(a, t, 32 * w, partials(a, false), kWideRows);
 }
@@ -570,15 +696,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
     Wave<DK, DV, KB> wave;
     wave.start(a, t, 0);
     const int mine = from + KB * w;
-    Pages pg(a, t.seq, mine);
-    const Loader<TileK<DK>, KB, 1> lk(a.k_cache, a.skc, t.head, a.page_size, 0);
-    const Loader<TileV<DV>, KB, 1> lv(a.v_cache, a.svc, t.head, a.page_size, 0);
+    Pages pg(a, t.seq, t.head, mine);
+    const Loader<TileK<DK>, KB, 1> lk(a.skc, a.page_size, 0);
+    const Loader<TileV<DV>, KB, 1> lv(a.svc, a.page_size, 0);
     const uint32_t lds = lds_address(smem[w]);
     int kb = mine;
     auto arrive = [&]() {
         wave_lds_sync();        // the last block's reads are through before the next loads land
-        lk.issue(pg, kb, t.hi, lds);
-        lv.issue(pg, kb, t.hi, lds + KBYTES);
+        load_block<KB>(pg, lk, lv, kb, t.hi, lds, lds + KBYTES);
         pg.advance(KB * kWaves);
         wait_vm<0>();
         wave_lds_sync();

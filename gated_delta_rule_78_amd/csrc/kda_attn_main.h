@@ -8,7 +8,7 @@ namespace attn {
 
 template <int DK, int DV>
 hipError_t launch_main(const AttnArgs& a, bool narrow, int64_t groups, hipStream_t st) {
-    const dim3 grid((unsigned)groups), block(kThreads);
+    const dim3 grid((unsigned)groups), block(narrow ? kThreads : kWideThreads);
     if (narrow)
         hipLaunchKernelGGL((attn_narrow_kernel<DK, DV>), grid, block, 0, st, a);
     else

@@ -4,7 +4,7 @@
 // r % G of the group, so that all of them read each key once. A sequence's rows make tiles, narrow
 // ones where it has at most kNarrowRows rows (the waves of a workgroup then share out the keys), wide
 // ones else (the waves share out the rows). A tile's keys are cut into C chunks, C the same for every
-// tile of a sequence: ceil(keys / L), L such that all calls' keys make about kTarget chunks. Chunks
+// tile of a sequence: ceil(keys / L), L such that all calls' keys make about target() chunks. Chunks
 // of a cut tile leave their sums in the workspace and a second launch joins them.
 #pragma once
 
@@ -15,11 +15,13 @@
 namespace kda {
 namespace attn {
 
-constexpr int kThreads = 256, kWaves = 4;
-constexpr int kNarrowRows = 32, kWideRows = 128;
+constexpr int kThreads = 256, kWaves = 4;          // narrow tiles
+constexpr int kWideThreads = 512, kWideWaves = 8;  // wide tiles
+constexpr int kNarrowRows = 32, kWideRows = 256;
 constexpr int kUnit = 128;             // keys: what L counts in
 constexpr int kMinUnits = 4;           // of a chunk
-constexpr int64_t kTarget = 512;       // chunks
+// Chunks: as many workgroups of a kind as the GPU's 256 CUs hold.
+__host__ __device__ constexpr int64_t target(bool narrow) { return narrow ? 512 : 256; }
 
 // Per sequence and kind, with a last entry that holds the totals.
 struct PlanEntry {
@@ -29,14 +31,14 @@ struct PlanEntry {
     int32_t chunks;    // C
 };
 
-// Workspace: PlanEntry[2][N + 1], then the partial results: per kind kSlots of rows x (DV + 2) floats.
+// Workspace: PlanEntry[2][N + 1], then the partial results: per kind slots_most() of rows x (DV + 2) floats.
 __host__ __device__ inline int64_t plan_bytes(int64_t N) { return ((N + 1) * 2 * (int64_t)sizeof(PlanEntry) + 255) / 256 * 256; }
 __host__ __device__ inline int64_t tiles_most(const AttnArgs& a, int rows, bool narrow) {
     const int64_t all = (a.packed ? a.T : a.N * a.T) * a.G, seqs = a.packed && a.T < a.N ? a.T : a.N;
     return narrow ? seqs : all / rows + seqs;
 }
 // cut chunks: ceil(k / L) <= 2 k / L of each tile with k > L
-__host__ __device__ inline int64_t slots_most() { return 2 * kTarget; }
+__host__ __device__ inline int64_t slots_most(bool narrow) { return 2 * target(narrow); }
 __host__ __device__ inline int64_t partial_bytes(int rows, int dv) { return (int64_t)rows * (dv + 2) * 4; }
 
 // Which kinds a call can hold, from what the host knows.
