@@ -42,9 +42,10 @@ __device__ __forceinline__ float both_sum(float x) {
 // 16 bytes a lane from a raw buffer straight into LDS, to lds + 16 lane. Offsets at or past the
 // descriptor's size store zeros. The compiler does not count these loads: whoever reads the LDS waits
 // with wait_vm first.
-__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t off, uint32_t lds) {
+__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t off, uint32_t lds) {
+    const i32x4 rsrc = {uniform(r[0]), uniform(r[1]), uniform(r[2]), uniform(r[3])};
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(off), "s"(rsrc));
+                 :: "s"(uniform((int)lds)), "v"(off), "s"(rsrc));
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -64,20 +65,6 @@ struct Tile {
     int chunk, chunks;
     int64_t slot;           // partial result, when chunks > 1
 };
-
-__device__ __forceinline__ int find_entry(const PlanEntry* p, int64_t N, int idx, int PlanEntry::*key) {
-    const int lane = threadIdx.x & 63;
-    int64_t lo = 0, n = N + 1;      // p[0] is 0: some entry is always at or below idx
-    for (;;) {
-        const int64_t step = (n + 63) / 64, i = lo + lane * step;
-        const bool le = lane * step < n && p[i < N ? i : N].*key <= idx;
-        const int cnt = __popcll(__ballot(le));
-        const int64_t at = (int64_t)(cnt > 0 ? cnt - 1 : 0) * step;
-        lo += at;
-        n = n - at < step ? n - at : step;
-        if (step == 1) return (int)lo;
-    }
-}
 
 // New tokens and keys of a sequence; false where it has no rows of this kind.
 __device__ __forceinline__ bool sequence(const AttnArgs& a, int64_t s, int64_t& first, int& n, int& kv) {
@@ -111,6 +98,87 @@ __device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, int n, bool narro
     return narrow ? 0 : (rows + kWideRows - 1) / kWideRows;
 }
 
+// ---- which sequence, tile and chunk a workgroup has ------------------------------------------------
+
+// Running sums over the sequences.
+struct Counts {
+    int items, slots, cuts;     // workgroups, partial results, (tile, head)s that are cut
+};
+
+__device__ __forceinline__ int lane_read(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+
+__device__ __forceinline__ int wave_scan(int x) {      // inclusive
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const int y = __shfl_up(x, m);
+        if (lane >= m) x += y;
+    }
+    return x;
+}
+
+struct Place {
+    int64_t seq, first;
+    int n, kv;
+    int index;                  // of the workgroup (or cut) within the sequence
+    int chunks, slot;           // C; the sequence's first partial result
+};
+
+// Where workgroup idx is (CUT: where the idx-th cut (tile, head) is); false behind the last. Uniform.
+template <bool NARROW, bool CUT>
+__device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& out) {
+    const int lane = threadIdx.x & 63;
+    constexpr int R = NARROW ? kNarrowRows : kWideRows;
+    int64_t first = 0;
+    int n = 0, kv = 0, k = (int)((a.N + 63) / 64);
+    unsigned long long units = 0;
+    for (int64_t s = (int64_t)lane * k; s < a.N && s < (int64_t)(lane + 1) * k; ++s)
+        if (sequence(a, s, first, n, kv)) units += (unsigned long long)(tiles_of(a, n, NARROW) * tile_units(a, kv, R)) * a.Hk;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) units += __shfl_xor(units, m);
+    int64_t len = (int64_t)((units + target(NARROW) - 1) / target(NARROW));
+    len = len < kMinUnits ? kMinUnits : len;
+    Counts base = {0, 0, 0};
+    int64_t lo = 0, left = a.N;
+    for (bool again = false;; again = true) {
+        k = (int)((left + 63) / 64);
+        Counts c = {0, 0, 0};
+        int chunks = 1;
+        const int64_t s0 = lo + (int64_t)lane * k, s1 = s0 + k < lo + left ? s0 + k : lo + left;
+        for (int64_t s = s0; s < s1; ++s) {
+            if (k > 1 || again) sequence(a, s, first, n, kv);       // else still held from above
+            if (n <= 0) continue;
+            const int64_t tiles = tiles_of(a, n, NARROW) * a.Hk;
+            chunks = (int)((tile_units(a, kv, R) + len - 1) / len);
+            c.items += (int)(tiles * chunks);
+            if (chunks > 1) {
+                c.slots += (int)(tiles * chunks);
+                c.cuts += (int)tiles;
+            }
+        }
+        if (s0 >= s1) n = 0;
+        const int items = wave_scan(c.items) + base.items - c.items, slots = wave_scan(c.slots) + base.slots - c.slots,
+                  cuts = wave_scan(c.cuts) + base.cuts - c.cuts;
+        const int at = CUT ? cuts : items, count = CUT ? c.cuts : c.items;
+        const uint64_t mine = __ballot(at <= idx && idx < at + count);
+        if (mine == 0) return false;
+        const int w = __builtin_ctzll(mine);
+        base = Counts{lane_read(items, w), lane_read(slots, w), lane_read(cuts, w)};
+        lo = lo + (int64_t)w * k;
+        if (k == 1) {
+            out.seq = uniform((int)lo);
+            out.first = uniform(lane_read((int)first, w));
+            out.n = uniform(lane_read(n, w));
+            out.kv = uniform(lane_read(kv, w));
+            out.chunks = uniform(lane_read(chunks, w));
+            out.slot = uniform(base.slots);
+            out.index = uniform(idx - (CUT ? base.cuts : base.items));
+            return true;
+        }
+        left = left - (int64_t)w * k < k ? left - (int64_t)w * k : k;
+    }
+}
+
 // ---- a page table walked by one wave ------------------------------------------------------------
 
 // A place among a sequence's pages, all of it uniform but for what is held: lane i holds the addresses
@@ -134,7 +202,7 @@ struct Pages {
         page_size = a.page_size;
         pages = a.pages;
         pg = uniform(key / page_size);
-        row = key - pg * page_size;
+        row = uniform(key - pg * page_size);
         fetch();
     }
     __device__ __forceinline__ void advance(int keys) {
@@ -272,8 +340,8 @@ struct Wave {
         from = a.window > 0 && pos - a.window > -1 ? (int)(pos - a.window) : -1;
         const int r0 = t.row0 + row_base, r1 = r0 + 31 < t.rows ? r0 + 31 : t.rows - 1;
         live = r0 < t.rows;
-        first = live ? t.kv - t.n + r0 / a.G : -1;
-        last = live ? t.kv - t.n + r1 / a.G : -1;
+        first = uniform(live ? t.kv - t.n + r0 / a.G : -1);
+        last = uniform(live ? t.kv - t.n + r1 / a.G : -1);
         const bf16_t* p = static_cast<const bf16_t*>(a.q) + (a.packed ? 0 : t.seq * a.sq.b) + (t.first + tok) * a.sq.t +
                           ((int64_t)t.head * a.G + hd) * a.sq.h + 8 * h;
 #pragma unroll
@@ -371,32 +439,28 @@ struct Wave {
         l += sum;
     }
 
-    // O^T += V^T P^T
-    template <bool MASKED>
+    // A key that some rows do not see reaches them as a probability of 0 times its value: whether the block
+    // at kb has such keys and V holds an infinity or a NaN.
+    __device__ __forceinline__ bool bad_values(const AttnArgs& a, const char* vs_, int kb) const {
+        return (last != first || a.window > 0) && masks(a, kb) && any_bad(vs_);
+    }
+
+    // O^T += V^T P^T. Bad values are left out, and the outputs that they belong to become NaN.
     __device__ __forceinline__ void values(const AttnArgs& a, const char* vs_, const Probs& P, int kb) {
         const int lane = fresh_lane(), l16 = lane & 15;
         const int vrow = 4 * (lane >> 5) + (l16 >> 2);
         const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
         const int piece = (2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ TileV<DV>::f(vrow);
-        if constexpr (MASKED) {
-            // a key that some rows do not see reaches them as a probability of 0 times its value: where V holds
-            // an infinity or a NaN it is left out, and the outputs it belongs to become NaN
-            const bool bad = (last != first || a.window > 0) && any_bad(vs_);
+        const bool bad = bad_values(a, vs_, kb);
 #pragma unroll
-            for (int s = 0; s < 2 * kMT; ++s)
+        for (int s = 0; s < 2 * kMT; ++s)
 #pragma unroll
-                for (int dt = 0; dt < kDT; ++dt) {
-                    bf16x8 v = read_v(vp, piece, s, dt);
-                    if (bad) v = split_bad(v, false);
-                    O[dt] = mfma32(v, P.p[s], O[dt]);
-                }
-            if (bad) mark_bad(vp, piece, kb);
-        } else {
-#pragma unroll
-            for (int s = 0; s < 2 * kMT; ++s)
-#pragma unroll
-                for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, piece, s, dt), P.p[s], O[dt]);
-        }
+            for (int dt = 0; dt < kDT; ++dt) {
+                bf16x8 v = read_v(vp, piece, s, dt);
+                if (bad) v = split_bad(v, false);
+                O[dt] = mfma32(v, P.p[s], O[dt]);
+            }
+        if (bad) mark_bad(vp, piece, kb);
     }
 
     // scores of one block and values of the one before as one stream of products, each operand read from LDS
@@ -429,13 +493,28 @@ struct Wave {
         }
     }
 
+    // The values alone, where nothing is masked.
+    __device__ __forceinline__ void plain_values(const char* vs_, const Probs& P) {
+        const int lane = fresh_lane(), l16 = lane & 15;
+        const int vrow = 4 * (lane >> 5) + (l16 >> 2);
+        const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
+        const int piece = (2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ TileV<DV>::f(vrow);
+#pragma unroll
+        for (int s = 0; s < 2 * kMT; ++s)
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, piece, s, dt), P.p[s], O[dt]);
+    }
+
     template <bool MASKED>
     __device__ __forceinline__ void block(const AttnArgs& a, const char* ks_, const char* vs_, int kb) {
         Scores S;
         Probs P;
         scores(ks_, S);
         softmax<MASKED>(a, S, P, kb);
-        values<MASKED>(a, vs_, P, kb);
+        if constexpr (MASKED)
+            values(a, vs_, P, kb);
+        else
+            plain_values(vs_, P);
     }
 
     __device__ static __forceinline__ bf16x8 read_v(const char* vp, int piece, int s, int dt) {
@@ -540,28 +619,22 @@ struct Wave {
 // The tile and chunk of this workgroup; false behind the last.
 template <bool NARROW>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, Tile& t) {
-    const PlanEntry* plan = static_cast<const PlanEntry*>(a.ws) + (NARROW ? 0 : a.N + 1);
-    const int idx = blockIdx.x;
-    if (idx >= plan[a.N].item) return false;
-    const int64_t s = uniform(find_entry(plan, a.N, idx, &PlanEntry::item));
-    const PlanEntry e = plan[s];
-    t.seq = s;
-    int n, kv;
-    sequence(a, s, t.first, n, kv);
-    t.first = uniform((int)t.first);
-    t.n = uniform(n);
-    t.kv = uniform(kv);
+    Place p;
+    if (!find_place<NARROW, false>(a, blockIdx.x, p)) return false;
+    t.seq = uniform((int)p.seq);
+    t.first = uniform((int)p.first);
+    t.n = uniform(p.n);
+    t.kv = uniform(p.kv);
     t.rows = t.n * a.G;
     const int tiles = (int)tiles_of(a, t.n, NARROW);
-    const int j = idx - uniform(e.item);
-    t.head = uniform(j % a.Hk);
-    const int rest = uniform(j / a.Hk);
-    t.chunks = uniform(e.chunks);
+    t.head = uniform(p.index % a.Hk);
+    const int rest = uniform(p.index / a.Hk);
+    t.chunks = uniform(p.chunks);
     t.chunk = uniform(rest % t.chunks);
     const int tile = uniform(tiles - 1 - rest / t.chunks);        // the tiles with the most keys first
     constexpr int R = NARROW ? kNarrowRows : kWideRows;
     t.row0 = tile * R;
-    t.slot = uniform(e.slot) + ((int64_t)tile * a.Hk + t.head) * t.chunks + t.chunk;
+    t.slot = p.slot + ((int64_t)tile * a.Hk + t.head) * t.chunks + t.chunk;
     const int r1 = t.row0 + R < t.rows ? t.row0 + R : t.rows;
     const int p0 = t.kv - t.n + t.row0 / a.G, p1 = t.kv - t.n + (r1 - 1) / a.G;
     t.hi = uniform(p1 + 1 > 0 ? p1 + 1 : 0);
@@ -573,14 +646,14 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, Tile& t) {
 // Keys [from, to) of this chunk: whole units from the unit of t.lo on.
 __device__ __forceinline__ void chunk_keys(const Tile& t, int& from, int& to) {
     const int u0 = t.lo / kUnit, u1 = (t.hi + kUnit - 1) / kUnit;
-    const int per = u1 > u0 ? (u1 - u0 + t.chunks - 1) / t.chunks : 0;
+    const int per = uniform(u1 > u0 ? (u1 - u0 + t.chunks - 1) / t.chunks : 0);
     from = (u0 + t.chunk * per) * kUnit;
     to = from + per * kUnit;
-    to = to < t.hi ? to : t.hi;
+    to = uniform(to < t.hi ? to : t.hi);
 }
 
 __device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
-    char* p = static_cast<char*>(a.ws) + plan_bytes(a.N);
+    char* p = static_cast<char*>(a.ws);
     if (!narrow && has_narrow(a)) p += slots_most(true) * partial_bytes(kNarrowRows, a.dv);
     return reinterpret_cast<float*>(p);
 }
@@ -665,8 +738,9 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
                 if (second) odd(); else even(i);
                 const int kb = from + i * KB;
                 const bool sees = wave.sees(a, kb);
+                const char* vs = smem[(i - 1) & 3] + KBYTES;
                 if (sees) wave.scores(smem[i & 3], S);
-                if (seen) wave.template values<true>(a, smem[(i - 1) & 3] + KBYTES, P, kb - KB);
+                if (seen) wave.values(a, vs, P, kb - KB);
                 if (second) even(i + 1); else odd();
                 ask();
                 if (sees) wave.template softmax<true>(a, S, P, kb);
@@ -674,7 +748,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
             }
         }
         if (second) odd(); else even(nb);
-        if (seen) wave.template values<true>(a, smem[(nb - 1) & 3] + KBYTES, P, from + (nb - 1) * KB);
+        if (seen) wave.values(a, smem[(nb - 1) & 3] + KBYTES, P, from + (nb - 1) * KB);
         if (!second) odd();
     }
     wave.finish(a, t, 32 * w, partials(a, false), kWideRows);
@@ -781,82 +855,69 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
 
 // ---- the chunks of cut tiles joined ---------------------------------------------------------------
 
-// Workgroup x: the x-th (tile, head) that is cut; y: a run of its rows.
+// Workgroup x: the x-th (tile, head) that is cut; y: a run of its rows, a wave a row. A lane holds 4
+// channels, so that a wave reads several chunks at a time.
 template <int DV, bool NARROW>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int rows_each) {
     constexpr int R = NARROW ? kNarrowRows : kWideRows;
-    constexpr int LPR = DV / 4, NG = kThreads / LPR;     // 4 channels a thread, NG chunks at a time
-    __shared__ float4 sum[NG][LPR];
-    __shared__ float ml[2][kThreads / 64];
-    __shared__ float wgt[kThreads];
-    const PlanEntry* plan = static_cast<const PlanEntry*>(a.ws) + (NARROW ? 0 : a.N + 1);
-    const int idx = blockIdx.x;
-    if (idx >= plan[a.N].cut) return;
-    const int64_t s = uniform(find_entry(plan, a.N, idx, &PlanEntry::cut));
-    const PlanEntry e = plan[s];
-    int64_t first;
-    int n, kv;
-    sequence(a, s, first, n, kv);
-    const int rows = n * a.G, j = idx - e.cut, C = e.chunks;
-    const int head_k = j % a.Hk, tile = j / a.Hk;
-    const int64_t slot = e.slot + ((int64_t)tile * a.Hk + head_k) * C;
-    const float* part = partials(a, NARROW);
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = tid / LPR, ch = tid % LPR;
+    constexpr int LPR = DV / 4, NG = 64 / LPR;
+    Place p;
+    if (!find_place<NARROW, true>(a, blockIdx.x, p)) return;
+    const int rows = p.n * a.G, C = p.chunks;
+    const int head_k = p.index % a.Hk, tile = p.index / a.Hk;
+    const int64_t slot = p.slot + ((int64_t)tile * a.Hk + head_k) * C;
+    const int lane = threadIdx.x & 63, g = lane / LPR, ch = lane % LPR;
+    const int64_t step = (int64_t)R * (DV + 2);
     const int y0 = blockIdx.y * rows_each, y1 = y0 + rows_each < R ? y0 + rows_each : R;
-    for (int rr = y0; rr < y1 && tile * R + rr < rows; ++rr) {
-        const float* base = part + (slot * R + rr) * (DV + 2);
-        const int64_t step = (int64_t)R * (DV + 2);
-        // the chunks' largest reference
-        float mm = -INFINITY;
-        for (int c = tid; c < C; c += kThreads) mm = fmaxf(mm, base[c * step + DV]);
+    for (int rr = y0 + uniform(threadIdx.x >> 6); rr < y1 && tile * R + rr < rows; rr += kWaves) {
+        const float* base = partials(a, NARROW) + (slot * R + rr) * (DV + 2);
+        float mm = -INFINITY, ll = 0.f;
+        for (int c = lane; c < C; c += 64) mm = fmaxf(mm, base[c * step + DV]);
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) mm = fmaxf(mm, __shfl_xor(mm, k));
-        lds_barrier();
-        if (lane == 0) ml[0][wv] = mm;
-        lds_barrier();
-        mm = fmaxf(fmaxf(ml[0][0], ml[0][1]), fmaxf(ml[0][2], ml[0][3]));
-        float ll = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = 0; c0 < C; c0 += kThreads) {
+        for (int c0 = 0; c0 < C; c0 += 64) {
             float f = 0.f;
-            if (c0 + tid < C) {
-                const float m = base[(c0 + tid) * step + DV];
-                f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mm);
-                if (f != 0.f) ll = fmaf(f, base[(c0 + tid) * step + DV + 1], ll);
+            if (c0 + lane < C) {
+                const float2 ml = *reinterpret_cast<const float2*>(base + (c0 + lane) * step + DV);
+                f = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - mm);
+                if (ml.x != -INFINITY) ll = fmaf(f, ml.y, ll);
             }
-            lds_barrier();
-            wgt[tid] = f;
-            lds_barrier();
-            const int left = C - c0 < kThreads ? C - c0 : kThreads;
-            for (int c = g; c < left; c += NG) {
-                const float wf = wgt[c];
-                const float2* p = reinterpret_cast<const float2*>(base + (c0 + c) * step + 4 * ch);
-                if (wf != 0.f) {
-                    const float2 u = p[0], v = p[1];
-                    acc.x = fmaf(wf, u.x, acc.x); acc.y = fmaf(wf, u.y, acc.y);
-                    acc.z = fmaf(wf, v.x, acc.z); acc.w = fmaf(wf, v.y, acc.w);
+            const int left = C - c0 < 64 ? C - c0 : 64;
+            for (int b = 0; b < left; b += 8 * NG) {      // 8 loads in flight; past the last chunk weights of 0
+                float wf[8];
+                float2 u[8], v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int c = b + k * NG + g;
+                    wf[k] = __shfl(f, c & 63);
+                    wf[k] = c < left ? wf[k] : 0.f;
+                    const float2* q = reinterpret_cast<const float2*>(base + (c0 + (c < left ? c : left - 1)) * step + 4 * ch);
+                    u[k] = q[0];
+                    v[k] = q[1];
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    acc.x = fmaf(wf[k], u[k].x, acc.x); acc.y = fmaf(wf[k], u[k].y, acc.y);
+                    acc.z = fmaf(wf[k], v[k].x, acc.z); acc.w = fmaf(wf[k], v[k].y, acc.w);
                 }
             }
         }
-        sum[g][ch] = acc;
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) ll += __shfl_xor(ll, k);
-        if (lane == 0) ml[1][wv] = ll;
-        lds_barrier();
-        ll = (ml[1][0] + ml[1][1]) + (ml[1][2] + ml[1][3]);
-        if (g == 0) {
 #pragma unroll
-            for (int k = 1; k < NG; ++k) {
-                const float4 v = sum[k][ch];
-                acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
-            }
+        for (int k = LPR; k < 64; k <<= 1) {
+            acc.x += __shfl_xor(acc.x, k); acc.y += __shfl_xor(acc.y, k);
+            acc.z += __shfl_xor(acc.z, k); acc.w += __shfl_xor(acc.w, k);
+        }
+        if (g == 0) {
             const int r = tile * R + rr, tok = r / a.G, hd = r - tok * a.G;
             const int64_t head = (int64_t)head_k * a.G + hd;
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : s * a.so.b) + (first + tok) * a.so.t + head * a.so.h;
+            bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : p.seq * a.so.b) + (p.first + tok) * a.so.t + head * a.so.h;
             store4(o + 4 * ch, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
             if (a.lse && ch == 0)
-                a.lse[(a.packed ? 0 : s * a.Hq * a.T) + head * a.T + first + tok] =
+                a.lse[(a.packed ? 0 : p.seq * a.Hq * a.T) + head * a.T + p.first + tok] =
                     ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
         }
     }

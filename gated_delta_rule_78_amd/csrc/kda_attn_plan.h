@@ -4,8 +4,10 @@
 // r % G of the group, so that all of them read each key once. A sequence's rows make tiles, narrow
 // ones where it has at most kNarrowRows rows (the waves of a workgroup then share out the keys), wide
 // ones else (the waves share out the rows). A tile's keys are cut into C chunks, C the same for every
-// tile of a sequence: ceil(keys / L), L such that all calls' keys make about target() chunks. Chunks
-// of a cut tile leave their sums in the workspace and a second launch joins them.
+// tile of a sequence: ceil(keys / L), L such that the keys of all tiles make about target() chunks.
+// Chunks of a cut tile leave their sums in the workspace and a second launch joins them. Every wave
+// works out from the lengths which sequence and chunk its workgroup has: 64 sequences take one round
+// of loads and a scan over the lanes, as long as it would take to read a list made by another launch.
 #pragma once
 
 #include <stdint.h>
@@ -19,20 +21,11 @@ constexpr int kThreads = 256, kWaves = 4;          // narrow tiles
 constexpr int kWideThreads = 512, kWideWaves = 8;  // wide tiles
 constexpr int kNarrowRows = 32, kWideRows = 256;
 constexpr int kUnit = 128;             // keys: what L counts in
-constexpr int kMinUnits = 4;           // of a chunk
+constexpr int kMinUnits = 1;           // of a chunk
 // Chunks: as many workgroups of a kind as the GPU's 256 CUs hold.
 __host__ __device__ constexpr int64_t target(bool narrow) { return narrow ? 512 : 256; }
 
-// Per sequence and kind, with a last entry that holds the totals.
-struct PlanEntry {
-    int32_t item;      // first workgroup
-    int32_t slot;      // first partial result
-    int32_t cut;       // first (tile, head) that is cut
-    int32_t chunks;    // C
-};
-
-// Workspace: PlanEntry[2][N + 1], then the partial results: per kind slots_most() of rows x (DV + 2) floats.
-__host__ __device__ inline int64_t plan_bytes(int64_t N) { return ((N + 1) * 2 * (int64_t)sizeof(PlanEntry) + 255) / 256 * 256; }
+// Workspace: the partial results, per kind slots_most() of rows x (DV + 2) floats.
 __host__ __device__ inline int64_t tiles_most(const AttnArgs& a, int rows, bool narrow) {
     const int64_t all = (a.packed ? a.T : a.N * a.T) * a.G, seqs = a.packed && a.T < a.N ? a.T : a.N;
     return narrow ? seqs : all / rows + seqs;
