@@ -37,7 +37,7 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
 
 size_t attn_ws_bytes(const AttnArgs& a) {
     using namespace attn;
-    int64_t b = 0;
+    int64_t b = kHeadBytes;
     if (has_narrow(a)) b += slots_most(true) * partial_bytes(kNarrowRows, a.dv);
     if (has_wide(a)) b += slots_most(false) * partial_bytes(kWideRows, a.dv);
     return (size_t)b;

@@ -107,13 +107,17 @@ struct Counts {
 
 __device__ __forceinline__ int lane_read(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
 
-__device__ __forceinline__ int wave_scan(int x) {      // inclusive
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const int y = __shfl_up(x, m);
-        if (lane >= m) x += y;
-    }
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int dpp_i32(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROW_MASK, 0xf, true);
+}
+__device__ __forceinline__ int wave_scan(int x) {      // inclusive; the steps of wave_prefix_sum
+    x += dpp_i32<0x111, 0xf>(x);
+    x += dpp_i32<0x112, 0xf>(x);
+    x += dpp_i32<0x114, 0xf>(x);
+    x += dpp_i32<0x118, 0xf>(x);
+    x += dpp_i32<0x142, 0xa>(x);
+    x += dpp_i32<0x143, 0xc>(x);
     return x;
 }
 
@@ -125,19 +129,19 @@ struct Place {
 };
 
 // Where workgroup idx is (CUT: where the idx-th cut (tile, head) is); false behind the last. Uniform.
+// all_cuts: how many (tile, head)s are cut in all.
 template <bool NARROW, bool CUT>
-__device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& out) {
+__device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& out, int& all_cuts) {
     const int lane = threadIdx.x & 63;
     constexpr int R = NARROW ? kNarrowRows : kWideRows;
     int64_t first = 0;
     int n = 0, kv = 0, k = (int)((a.N + 63) / 64);
-    unsigned long long units = 0;
+    float units = 0.f;
     for (int64_t s = (int64_t)lane * k; s < a.N && s < (int64_t)(lane + 1) * k; ++s)
-        if (sequence(a, s, first, n, kv)) units += (unsigned long long)(tiles_of(a, n, NARROW) * tile_units(a, kv, R)) * a.Hk;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) units += __shfl_xor(units, m);
-    int64_t len = (int64_t)((units + target(NARROW) - 1) / target(NARROW));
-    len = len < kMinUnits ? kMinUnits : len;
+        if (sequence(a, s, first, n, kv)) units += (float)(tiles_of(a, n, NARROW) * a.Hk) * (float)tile_units(a, kv, R);
+    // the sum's rounding may not make len too small: chunks would pass the workspace's slots
+    units = lane_value(wave_prefix_sum(units), 63) * 1.01f;
+    const int len = (int)fminf(fmaxf(ceilf(units / (float)target(NARROW)), (float)kMinUnits), 16777216.f);
     Counts base = {0, 0, 0};
     int64_t lo = 0, left = a.N;
     for (bool again = false;; again = true) {
@@ -148,17 +152,18 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
         for (int64_t s = s0; s < s1; ++s) {
             if (k > 1 || again) sequence(a, s, first, n, kv);       // else still held from above
             if (n <= 0) continue;
-            const int64_t tiles = tiles_of(a, n, NARROW) * a.Hk;
-            chunks = (int)((tile_units(a, kv, R) + len - 1) / len);
-            c.items += (int)(tiles * chunks);
+            const int tiles = (int)tiles_of(a, n, NARROW) * a.Hk;
+            chunks = ((int)tile_units(a, kv, R) + len - 1) / len;
+            c.items += tiles * chunks;
             if (chunks > 1) {
-                c.slots += (int)(tiles * chunks);
-                c.cuts += (int)tiles;
+                c.slots += tiles * chunks;
+                c.cuts += tiles;
             }
         }
         if (s0 >= s1) n = 0;
         const int items = wave_scan(c.items) + base.items - c.items, slots = wave_scan(c.slots) + base.slots - c.slots,
                   cuts = wave_scan(c.cuts) + base.cuts - c.cuts;
+        if (!again) all_cuts = lane_read(cuts + c.cuts, 63);
         const int at = CUT ? cuts : items, count = CUT ? c.cuts : c.items;
         const uint64_t mine = __ballot(at <= idx && idx < at + count);
         if (mine == 0) return false;
@@ -293,28 +298,27 @@ __device__ __forceinline__ void load_block(Pages& pg, const LK& lk, const LV& lv
         for (int i = 0; i < LV::kLoads; ++i) lv.load(rv, i, pg.row, vlds);
         return;
     }
-    // the tile spans pages: each load finds its own
-    auto place = [&](int at, int& row) {
-        int ahead = 0;
-        row = pg.row + at;
+    // the tile spans pages: 16 keys at a time, for the loads that lie in them
+#pragma unroll
+    for (int at = 0; at < ROWS; at += 16) {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < LK::kLoads; ++i) any |= (lk.first_row(i) & ~15) == at;
+#pragma unroll
+        for (int i = 0; i < LV::kLoads; ++i) any |= (lv.first_row(i) & ~15) == at;
+        if (!any) continue;
+        int ahead = 0, row = pg.row + at;
         while (row >= pg.page_size) {
             row -= pg.page_size;
             ++ahead;
         }
         pg.descriptors(ahead, hi - kb - at + row, lk, lv, rk, rv);
-    };
-    int row;
 #pragma unroll
-    for (int i = 0; i < LK::kLoads; ++i) {
-        const int at = lk.first_row(i) & ~15;
-        place(at, row);
-        lk.load(rk, i, row - at, klds);
-    }
+        for (int i = 0; i < LK::kLoads; ++i)
+            if ((lk.first_row(i) & ~15) == at) lk.load(rk, i, row - at, klds);
 #pragma unroll
-    for (int i = 0; i < LV::kLoads; ++i) {
-        const int at = lv.first_row(i) & ~15;
-        place(at, row);
-        lv.load(rv, i, row - at, vlds);
+        for (int i = 0; i < LV::kLoads; ++i)
+            if ((lv.first_row(i) & ~15) == at) lv.load(rv, i, row - at, vlds);
     }
 }
 
@@ -620,7 +624,10 @@ struct Wave {
 template <bool NARROW>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, Tile& t) {
     Place p;
-    if (!find_place<NARROW, false>(a, blockIdx.x, p)) return false;
+    int all_cuts = 0;
+    const bool found = find_place<NARROW, false>(a, blockIdx.x, p, all_cuts);
+    if (blockIdx.x == 0 && threadIdx.x == 0) static_cast<int*>(a.ws)[NARROW ? 0 : 1] = all_cuts;
+    if (!found) return false;
     t.seq = uniform((int)p.seq);
     t.first = uniform((int)p.first);
     t.n = uniform(p.n);
@@ -653,7 +660,7 @@ __device__ __forceinline__ void chunk_keys(const Tile& t, int& from, int& to) {
 }
 
 __device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
-    char* p = static_cast<char*>(a.ws);
+    char* p = static_cast<char*>(a.ws) + kHeadBytes;
     if (!narrow && has_narrow(a)) p += slots_most(true) * partial_bytes(kNarrowRows, a.dv);
     return reinterpret_cast<float*>(p);
 }
@@ -861,8 +868,10 @@ template <int DV, bool NARROW>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int rows_each) {
     constexpr int R = NARROW ? kNarrowRows : kWideRows;
     constexpr int LPR = DV / 4, NG = 64 / LPR;
+    if ((int)blockIdx.x >= static_cast<const int*>(a.ws)[NARROW ? 0 : 1]) return;
     Place p;
-    if (!find_place<NARROW, true>(a, blockIdx.x, p)) return;
+    int all_cuts;
+    if (!find_place<NARROW, true>(a, blockIdx.x, p, all_cuts)) return;
     const int rows = p.n * a.G, C = p.chunks;
     const int head_k = p.index % a.Hk, tile = p.index / a.Hk;
     const int64_t slot = p.slot + ((int64_t)tile * a.Hk + head_k) * C;

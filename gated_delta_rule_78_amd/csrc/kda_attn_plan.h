@@ -25,7 +25,9 @@ constexpr int kMinUnits = 1;           // of a chunk
 // Chunks: as many workgroups of a kind as the GPU's 256 CUs hold.
 __host__ __device__ constexpr int64_t target(bool narrow) { return narrow ? 512 : 256; }
 
-// Workspace: the partial results, per kind slots_most() of rows x (DV + 2) floats.
+// Workspace: two counts, how many (tile, head)s of either kind are cut (the first workgroup of a kind
+// writes its one), then the partial results, per kind slots_most() of rows x (DV + 2) floats.
+constexpr int64_t kHeadBytes = 256;
 __host__ __device__ inline int64_t tiles_most(const AttnArgs& a, int rows, bool narrow) {
     const int64_t all = (a.packed ? a.T : a.N * a.T) * a.G, seqs = a.packed && a.T < a.N ? a.T : a.N;
     return narrow ? seqs : all / rows + seqs;
