@@ -1,9 +1,11 @@
 // Device code shared by the head norms with rotation and the cache append (include/kda_attn.h).
 //
-// A workgroup of 256 threads takes the rows (token, head) of a few tokens. The tokens' cosines and
-// sines are formed once, in LDS, and serve every head. A row is held by `lpr` lanes, 8 pairs a lane
-// (both members of a pair in one lane, so a rotation needs no exchange), 64 / lpr rows a wave at a
-// time and kUnroll of those in flight.
+// A workgroup of 256 threads takes the rows (token, head) of a few tokens of one tensor, q or k. It asks
+// for its first rows, then forms the tokens' cosines and sines in LDS, once for all heads. A row is held
+// by `lpr` lanes, 8 pairs a lane (both members of a pair in one lane, so a rotation needs no exchange),
+// 64 / lpr rows a wave at a time, the next ones on their way meanwhile. The code is kept short and its
+// loops rolled: a cold kernel runs at some 0.2 us per 64 bytes of it, which small calls wait for (four
+// rows a lane at once: 11.5 KB and 9 us for one token).
 #pragma once
 
 #include "kda_device.h"
@@ -19,14 +21,70 @@ constexpr int kMaxTokens = 16;     // of a workgroup
 // element: single channels, pair c + lpr * j of lane c.
 enum Layout { kHalfWide = 0, kInterWide = 1, kHalfElem = 2, kInterElem = 3 };
 
-// Per token of a workgroup: element offsets of its rows in every tensor.
-struct Token {
-    int64_t q, k, v, qo, ko, vo;
-    int64_t sdq, sdk;
-    int32_t pos;
-    int32_t live;     // in a sequence: q is read and written
-    int32_t stored;   // append: k and v have a place in the cache
+template <int LAY>
+constexpr bool kLaysWide = LAY == kHalfWide || LAY == kInterWide;
+
+// What a workgroup is about: one tensor's rows (kValues: the append's copy of v).
+enum Kind { kQueries = 0, kKeys = 1, kValues = 2 };
+
+// How the rows are shared out: workgroups group0[kind] .. group0[kind + 1] - 1 take `tokens` tokens each
+// of a kind.
+struct Shape {
+    int lpr;                // lanes a row
+    int v_wide;             // append: v in 16-byte accesses
+    int tokens[3];
+    int64_t group0[4];
+    uint32_t magic[3];      // ceil(2^32 / heads), 0 for one head
 };
+
+// A token of a workgroup, in LDS.
+struct Token {
+    int64_t dst;            // append: where its k (or v) goes in the cache
+    int32_t pos;
+    int32_t on;             // its row is to be written
+};
+
+// Quotient of a row index by the heads: exact for n < 2^16 with magic = ceil(2^32 / h) (h > 1).
+__device__ __forceinline__ int div_heads(int n, uint32_t magic) {
+    return magic ? (int)__umulhi((uint32_t)n, magic) : n;
+}
+
+// A row: its block, token of the block and head, and its token in the workgroup.
+struct Row {
+    uint32_t b, u, h;
+    int t;
+    // element offset; h and t strides have 32 bits
+    __device__ __forceinline__ int64_t at(const kda_row_strides& s) const {
+        return (int64_t)((uint64_t)b * (uint64_t)s.b + (uint64_t)u * (uint32_t)s.t + (uint64_t)h * (uint32_t)s.h);
+    }
+};
+
+// The rows of a workgroup: row r is token u0 + r / H, head r % H.
+struct Rows3 {
+    uint32_t u0, T;
+    int H, count;
+    uint32_t magic;
+    bool one;               // one block of rows: no division by T
+    __device__ __forceinline__ Row row(int r) const {
+        Row x;
+        x.t = div_heads(r, magic);
+        x.h = (uint32_t)(r - x.t * H);
+        x.u = u0 + x.t;
+        x.b = 0;
+        if (!one) {
+            x.b = x.u / T;
+            x.u -= x.b * T;
+        }
+        return x;
+    }
+};
+
+// 1 / sqrt(v) for v > 0, subnormal ones too: off by at most one unit in the last place.
+__device__ __forceinline__ float inv_root(float v) {
+    const bool small = v < 0x1p-96f;
+    const float r = __builtin_amdgcn_rsqf(small ? v * 0x1p96f : v);
+    return small ? r * 0x1p48f : r;
+}
 
 // cos and sin of 2 pi t: t less its nearest quarter in fp64 (exact), then the series of both on
 // [-pi/4, pi/4] up to x^9 and x^10, whose next terms are below 2e-9 and 2e-10 there.
@@ -55,7 +113,7 @@ __device__ __forceinline__ void sincos_turns(double t, float& s, float& c) {
 __device__ __forceinline__ void fill_angles(const RopeArgs& a, const Token* tok, int ntok, float2* cs) {
     const int P = a.d / 2, R = a.rot / 2;
     for (int e = threadIdx.x; e < ntok * P; e += kThreads) {
-        const int t = e / P, i = e - t * P;
+        const int t = ntok == 1 ? 0 : e / P, i = e - t * P;
         float2 v = make_float2(1.f, 0.f);
         if (i < R) {
             // one turn is 2 pi; the product of a 32-bit position and a 24-bit frequency is off by 2^-53
@@ -90,17 +148,6 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int64_t N, int64
 
 // ---- a lane's 8 pairs of a row ------------------------------------------------------------------
 
-template <typename T>
-struct Raw;
-template <>
-struct Raw<bf16_t> {
-    uint4 a, b;
-};
-template <>
-struct Raw<float> {
-    uint4 a0, a1, b0, b1;
-};
-
 struct Lane {
     int c, g;           // place in the row, row of the wave
     int lpr;            // lanes a row, a power of two
@@ -130,11 +177,13 @@ __device__ __forceinline__ Lane make_lane(const RopeArgs& a, int lpr) {
         l.oa = 16 * l.c;
         l.ob = l.oa + 8;
         l.live = l.oa < a.d;
+        if (!l.live) l.oa = 0, l.ob = 0;
     } else if (LAY == kHalfWide) {
         const int p = 8 * l.c;
         l.live = p < l.P;
         l.oa = p < l.R ? p : l.R + p;                     // rot + (p - rot/2)
         l.ob = p < l.R ? p + l.R : l.R + l.H2 + p;
+        if (!l.live) l.oa = 0, l.ob = 0;
     } else {
         l.live = true;
         l.oa = l.ob = 0;
@@ -142,36 +191,62 @@ __device__ __forceinline__ Lane make_lane(const RopeArgs& a, int lpr) {
     return l;
 }
 
+// The 16 channels as they come from memory, turned into floats only where a row is worked on: several
+// rows are in flight, and packed bf16 is half the registers. Interleaved wide rows hold channels in order.
 template <typename T, int LAY>
-__device__ __forceinline__ void load_row(const Lane& l, const T* row, bool on, float* x);
+struct Raw {
+    static constexpr bool kWide = LAY == kHalfWide || LAY == kInterWide;
+    static constexpr int kWords = kWide ? 4 * sizeof(T) / 4 * 4 : 16;      // 8 for bf16, 16 for fp32; elements one each
+    uint32_t w[kWords];
 
-__device__ __forceinline__ void unpack8(const bf16_t* p, float* x) { unpack16(*reinterpret_cast<const uint4*>(p), p, x); }
-__device__ __forceinline__ void unpack8(const float* p, float* x) {
-    unpack16(*reinterpret_cast<const uint4*>(p), p, x);
-    unpack16(*reinterpret_cast<const uint4*>(p + 4), p, x + 4);
-}
-
-// x[0..7] the first members of the lane's pairs, x[8..15] the second.
-template <typename T, int LAY>
-__device__ __forceinline__ void load_row(const Lane& l, const T* row, bool on, float* x) {
-    if constexpr (LAY == kHalfWide || LAY == kInterWide) {
-        if (on && l.live) {
-            unpack8(row + l.oa, x);
-            unpack8(row + l.ob, x + 8);
+    // The row exists: lanes past it read its first channels, so that no load waits for a branch.
+    __device__ __forceinline__ void load(const Lane& l, const T* row) {
+        if constexpr (kWide) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < kWords / 8; ++k) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(row + (h ? l.ob : l.oa) + k * (16 / (int)sizeof(T)));
+                    uint32_t* d = w + h * (kWords / 2) + 4 * k;
+                    d[0] = u.x; d[1] = u.y; d[2] = u.z; d[3] = u.w;
+                }
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int p = l.c + l.lpr * j;
-            const bool in = on && p < l.P;
-            x[j] = in ? ld_f(row + l.ia<LAY>(p)) : 0.f;
-            x[8 + j] = in ? ld_f(row + l.ib<LAY>(p)) : 0.f;
+            for (int j = 0; j < 8; ++j) {
+                const int p = l.c + l.lpr * j, q = p < l.P ? p : 0;
+                w[j] = bits(row[l.template ia<LAY>(q)]);
+                w[8 + j] = bits(row[l.template ib<LAY>(q)]);
+            }
         }
     }
-}
+    // x[0..7] the first members of the lane's pairs, x[8..15] the second; zeros past the row's end.
+    __device__ __forceinline__ void get(const Lane& l, float* x) const {
+        if constexpr (kWide && sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xffff0000u);
+                if (LAY == kInterWide) {
+                    x[j] = lo;
+                    x[8 + j] = hi;
+                } else {
+                    x[2 * j] = lo;
+                    x[2 * j + 1] = hi;
+                }
+            }
+        } else if constexpr (kWide) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[LAY == kInterWide ? (j & 1) * 8 + (j >> 1) : j] = __uint_as_float(w[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = sizeof(T) == 2 ? __uint_as_float(w[j] << 16) : __uint_as_float(w[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (kWide ? !l.live : l.c + l.lpr * j >= l.P) x[j] = x[8 + j] = 0.f;
+    }
+    __device__ static __forceinline__ uint32_t bits(bf16_t v) { return v; }
+    __device__ static __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+};
 
 template <typename T, int LAY>
 __device__ __forceinline__ void store_row(const Lane& l, T* row, const float* x) {
@@ -192,20 +267,7 @@ __device__ __forceinline__ void store_row(const Lane& l, T* row, const float* x)
     }
 }
 
-// Interleaved wide loads hold channels in order: into first and second members, and back.
-template <int LAY>
-__device__ __forceinline__ void to_pairs(float* x) {
-    if constexpr (LAY == kInterWide) {
-        float y[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            y[j] = x[2 * j];
-            y[8 + j] = x[2 * j + 1];
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = y[j];
-    }
-}
+// Pairs to channels in order, for interleaved wide stores.
 template <int LAY>
 __device__ __forceinline__ void from_pairs(float* x) {
     if constexpr (LAY == kInterWide) {
@@ -230,13 +292,14 @@ __device__ __forceinline__ void load_weight(const Lane& l, const float* w, float
     if constexpr (LAY == kHalfWide || LAY == kInterWide) {
         // weights have no alignment beyond their element
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = l.live ? w[l.oa + j] : 0.f;
-            x[8 + j] = l.live ? w[l.ob + j] : 0.f;
+        for (int j = 0; j < 16; ++j) {
+            const int c = j < 8 ? l.oa + j : l.ob + j - 8;
+            x[LAY == kInterWide ? (j & 1) * 8 + (j >> 1) : j] = w[c];
         }
-        to_pairs<LAY>(x);
     } else {
-        load_row<float, LAY>(l, w, true, x);
+        Raw<float, LAY> r;
+        r.load(l, w);
+        r.get(l, x);
     }
 }
 
@@ -262,21 +325,17 @@ __device__ __forceinline__ void load_angles(const Lane& l, const float2* cs, flo
     }
 }
 
+// Sum over the lpr lanes of a row, in every one of them: the lane one further, two further, then the
+// mirror images in 8 and 16 lanes (whose 4 and 8 lanes hold the same by then), then across.
 __device__ __forceinline__ float row_sum(float s, int lpr) {
-    for (int m = 1; m < lpr; m <<= 1) s += __shfl_xor(s, m);
+    if (lpr > 1) s += dpp_f32<0xB1, 0xf>(s);
+    if (lpr > 2) s += dpp_f32<0x4E, 0xf>(s);
+    if (lpr > 4) s += dpp_f32<0x141, 0xf>(s);
+    if (lpr > 8) s += dpp_f32<0x140, 0xf>(s);
+    if (lpr > 16) s += __shfl_xor(s, 16);
+    if (lpr > 32) s += __shfl_xor(s, 32);
     return s;
 }
-
-// Quotient of a row index by the heads: exact for n < 2^16 with magic = ceil(2^32 / h) (h > 1).
-__device__ __forceinline__ int div_heads(int n, uint32_t magic) {
-    return magic ? (int)__umulhi((uint32_t)n, magic) : n;
-}
-
-struct Shape {
-    int lpr;            // lanes a row
-    int tokens;         // a workgroup
-    uint32_t mq, mk;    // ceil(2^32 / heads), 0 for one head
-};
 
 }  // namespace rope
 }  // namespace kda

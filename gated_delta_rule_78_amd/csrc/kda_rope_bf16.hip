@@ -3,8 +3,8 @@
 
 namespace kda {
 namespace rope {
-template hipError_t launch_rows<bf16_t, bf16_t, false>(const RopeArgs&, const Shape&, int, bool, hipStream_t);
-template hipError_t launch_rows<bf16_t, bf16_t, true>(const RopeArgs&, const Shape&, int, bool, hipStream_t);
-template hipError_t launch_grads<bf16_t>(const RopeArgs&, const Shape&, int, int, bool, hipStream_t);
+template hipError_t launch_rows<bf16_t, bf16_t, false>(const RopeArgs&, const Shape&, int, hipStream_t);
+template hipError_t launch_rows<bf16_t, bf16_t, true>(const RopeArgs&, const Shape&, int, hipStream_t);
+template hipError_t launch_grads<bf16_t>(const RopeArgs&, const Shape&, int, bool, hipStream_t);
 }  // namespace rope
 }  // namespace kda

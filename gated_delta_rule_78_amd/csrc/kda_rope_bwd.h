@@ -3,8 +3,8 @@
 //   dy = R^T dz,  xh = x / sqrt(mean x^2 + eps),  dweight = sum dy xh,
 //   dx = (t - xh mean(t xh)) / sqrt(mean x^2 + eps),  t = dy weight        (dx = dy without norm)
 //
-// Workgroups walk blocks of tokens with the weights' sums in registers; each writes its sums once,
-// and a second launch adds them in order (rope_colsum_kernel).
+// Workgroups walk blocks of tokens of one tensor with the weight's sums in registers; each writes its
+// sums once, and a second launch adds them in order (rope_colsum_kernel).
 #pragma once
 
 #include "kda_rope_fwd.h"
@@ -12,124 +12,110 @@
 namespace kda {
 namespace rope {
 
-template <typename T, int LAY, bool KEYS>
-__device__ __forceinline__ void grad_rows(const RopeArgs& a, const Lane& l, const Token* tok, const float2* cs, int ntok,
-                                          uint32_t magic, float* dw) {
-    constexpr int U = sizeof(T) == 2 ? 2 : 1;
-    const int H = KEYS ? a.Hk : a.Hq, rg = 64 / l.lpr, rows = ntok * H, P = a.d / 2;
-    const T* src = static_cast<const T*>(KEYS ? a.k : a.q);
-    const T* grd = static_cast<const T*>(KEYS ? a.dko : a.dqo);
-    T* dst = static_cast<T*>(KEYS ? a.dk : a.dq);
-    const int64_t sh = KEYS ? a.sk.h : a.sq.h, gh = KEYS ? a.sko.h : a.sqo.h, dh = KEYS ? a.sdk.h : a.sdq.h;
-    const float inv_d = 1.f / (float)a.d;
-    float w[16];
-    if (a.norm) load_weight<LAY>(l, KEYS ? a.wk : a.wq, w);
-    for (int base = (threadIdx.x >> 6) * rg * U; base < rows; base += kWaves * rg * U) {
-        float z[U][16], x[U][16];
-        int tk[U];
-        int64_t out[U];
-        bool on[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = base + u * rg + l.g;
-            on[u] = r < rows;
-            const int rr = on[u] ? r : 0;
-            const int t = div_heads(rr, magic), h = rr - t * H;
-            tk[u] = t;
-            out[u] = (KEYS ? tok[t].sdk : tok[t].sdq) + h * dh;
-            load_row<T, LAY>(l, grd + ((KEYS ? tok[t].ko : tok[t].qo) + h * gh), on[u], z[u]);
-            if (a.norm) load_row<T, LAY>(l, src + ((KEYS ? tok[t].k : tok[t].q) + h * sh), on[u], x[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            to_pairs<LAY>(z[u]);
-            if (a.rot) {
-                float co[8], si[8];
-                load_angles<LAY>(l, cs + tk[u] * P, co, si);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float va = z[u][j], vb = z[u][8 + j];
-                    z[u][j] = fmaf(va, co[j], vb * si[j]);
-                    z[u][8 + j] = fmaf(vb, co[j], -va * si[j]);
-                }
-            }
-            if (a.norm) {
-                to_pairs<LAY>(x[u]);
-                float s = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s = fmaf(x[u][j], x[u][j], s);
-                s = row_sum(s, l.lpr);
-                const float r = 1.f / sqrtf(fmaf(s, inv_d, a.eps));
-                float m = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    x[u][j] *= r;
-                    dw[j] = fmaf(z[u][j], x[u][j], dw[j]);
-                    z[u][j] *= w[j];
-                    m = fmaf(z[u][j], x[u][j], m);
-                }
-                m = row_sum(m, l.lpr) * inv_d;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) z[u][j] = r * fmaf(-m, x[u][j], z[u][j]);
-            }
-            from_pairs<LAY>(z[u]);
-            if (on[u]) store_row<T, LAY>(l, dst + out[u], z[u]);
-        }
-    }
-}
-
-// Sums of the workgroup's waves and row groups into ws[group][KEYS][d].
-template <int LAY>
-__device__ __forceinline__ void put_sums(const RopeArgs& a, const Lane& l, float* dw, float* part, int kind) {
-    const int wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        for (int m = l.lpr; m < 64; m <<= 1) dw[j] += __shfl_xor(dw[j], m);
-    from_pairs<LAY>(dw);
-    if (l.g == 0) store_row<float, LAY>(l, part + (size_t)wave * a.d, dw);
-    lds_barrier();
-    for (int c = threadIdx.x; c < a.d; c += kThreads) {
-        float s = part[c];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) s += part[w * a.d + c];
-        a.ws[((int64_t)blockIdx.x * 2 + kind) * a.d + c] = s;
-    }
-    lds_barrier();
-}
-
 template <typename T, int LAY>
-__global__ __launch_bounds__(kThreads) void rope_bwd_kernel(RopeArgs a, Shape s, int sums) {
+__global__ __launch_bounds__(kThreads, kLaysWide<LAY> ? 3 : 2) void rope_bwd_kernel(RopeArgs a, Shape s, int sums) {
     extern __shared__ __align__(16) float2 cs[];     // the tokens' angles, or the waves' weight sums
     __shared__ Token tok[kMaxTokens];
-    const int64_t all = a.B * a.T;
+    const int64_t wg = blockIdx.x;
+    const bool keys = wg >= s.group0[1];
+    const int kind = keys ? kKeys : kQueries;
+    const int64_t all = a.B * a.T, groups = s.group0[kind + 1] - s.group0[kind];
     const Lane l = make_lane<LAY>(a, s.lpr);
-    float dwq[16], dwk[16];
+    const int rg = 64 / l.lpr, P = a.d / 2;
+    const T *src = static_cast<const T*>(keys ? a.k : a.q), *grd = static_cast<const T*>(keys ? a.dko : a.dqo);
+    T* dst = static_cast<T*>(keys ? a.dk : a.dq);
+    const kda_row_strides &si = keys ? a.sk : a.sq, &sg = keys ? a.sko : a.sqo, &so = keys ? a.sdk : a.sdq;
+    const float inv_d = 1.f / (float)a.d;
+    float w[16], dw[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) dwq[j] = dwk[j] = 0.f;
-    for (int64_t u0 = (int64_t)blockIdx.x * s.tokens; u0 < all; u0 += (int64_t)gridDim.x * s.tokens) {
-        const int ntok = (int)(all - u0 < s.tokens ? all - u0 : s.tokens);
+    for (int j = 0; j < 16; ++j) dw[j] = 0.f;
+    if (a.norm) load_weight<LAY>(l, keys ? a.wk : a.wq, w);
+    for (int64_t g = wg - s.group0[kind]; g * s.tokens[kind] < all; g += groups) {
+        int ntok;
+        const Rows3 rows = rows_of(a, s, kind, g, ntok);
+        int r = (threadIdx.x >> 6) * rg + l.g;
+        Row row = rows.row(r < rows.count ? r : 0);
+        Raw<T, LAY> rz, rx;
+        auto load = [&]() {
+            rz.load(l, grd + row.at(sg));
+            if (a.norm) rx.load(l, src + row.at(si));
+        };
+        load();
         lds_barrier();                               // the block before is through with LDS
-        fill_tokens<false>(a, tok, u0, ntok);
+        fill_tokens<false>(a, tok, rows.u0, ntok, kind);
         lds_barrier();
         if (a.rot) {
             fill_angles(a, tok, ntok, cs);
             lds_barrier();
         }
-        if (a.Hq) grad_rows<T, LAY, false>(a, l, tok, cs, ntok, s.mq, dwq);
-        if (a.Hk) grad_rows<T, LAY, true>(a, l, tok, cs, ntok, s.mk, dwk);
+#pragma unroll 1
+        for (int first = (threadIdx.x >> 6) * rg; first < rows.count; first += kWaves * rg) {
+            const bool on = r < rows.count;
+            const Row now = row;
+            float z[16], x[16];
+            rz.get(l, z);
+            if (a.norm) rx.get(l, x);
+            r += kWaves * rg;
+            if (first + kWaves * rg < rows.count) {
+                row = rows.row(r < rows.count ? r : 0);
+                load();
+            }
+            if (a.rot) {
+                float co[8], sn[8];
+                load_angles<LAY>(l, cs + now.t * P, co, sn);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float va = z[j], vb = z[8 + j];
+                    z[j] = fmaf(va, co[j], vb * sn[j]);
+                    z[8 + j] = fmaf(vb, co[j], -va * sn[j]);
+                }
+            }
+            if (a.norm) {
+                float q = 0.f, m = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) q = fmaf(x[j], x[j], q);
+                const float n = inv_root(fmaf(row_sum(q, l.lpr), inv_d, a.eps));
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    x[j] *= n;
+                    if (on) dw[j] = fmaf(z[j], x[j], dw[j]);
+                    z[j] *= w[j];
+                    m = fmaf(z[j], x[j], m);
+                }
+                m = row_sum(m, l.lpr) * inv_d;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = n * fmaf(-m, x[j], z[j]);
+            }
+            from_pairs<LAY>(z);
+            if (on) store_row<T, LAY>(l, dst + now.at(so), z);
+        }
     }
     if (sums) {
+        // the sums of the wave's row groups, then of the waves, into ws[workgroup][d]
         float* part = reinterpret_cast<float*>(cs);
         lds_barrier();
-        put_sums<LAY>(a, l, dwq, part, 0);
-        put_sums<LAY>(a, l, dwk, part, 1);
+#pragma unroll 1
+        for (int m = l.lpr; m < 64; m <<= 1) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) dw[j] += __shfl_xor(dw[j], m);
+        }
+        from_pairs<LAY>(dw);
+        if (l.g == 0) store_row<float, LAY>(l, part + (size_t)(threadIdx.x >> 6) * a.d, dw);
+        lds_barrier();
+        for (int c = threadIdx.x; c < a.d; c += kThreads) {
+            float v = part[c];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) v += part[i * a.d + c];
+            a.ws[wg * a.d + c] = v;
+        }
     }
 }
 
 template <typename T>
-hipError_t launch_grads(const RopeArgs& a, const Shape& s, int lay, int groups, bool sums, hipStream_t st) {
-    const dim3 grid((unsigned)groups), block(kThreads);
-    size_t lds = a.rot ? (size_t)s.tokens * (a.d / 2) * sizeof(float2) : 0;
+hipError_t launch_grads(const RopeArgs& a, const Shape& s, int lay, bool sums, hipStream_t st) {
+    const dim3 grid((unsigned)s.group0[2]), block(kThreads);
+    const int most = s.tokens[0] > s.tokens[1] ? s.tokens[0] : s.tokens[1];
+    size_t lds = a.rot ? (size_t)most * (a.d / 2) * sizeof(float2) : 0;
     const size_t part = (size_t)kWaves * a.d * sizeof(float);
     if (sums && part > lds) lds = part;
     const int sm = sums;

@@ -7,40 +7,36 @@
 namespace kda {
 namespace rope {
 
+// Positions of a workgroup's tokens, and for the append their places in the cache; a wave a token.
 template <bool APPEND>
-__device__ __forceinline__ void fill_tokens(const RopeArgs& a, Token* tok, int64_t u0, int ntok) {
+__device__ __forceinline__ void fill_tokens(const RopeArgs& a, Token* tok, int64_t u0, int ntok, int kind) {
     const int lane = threadIdx.x & 63;
-    for (int i = threadIdx.x >> 6; i < ntok; i += kWaves) {      // a wave per token
-        const int64_t u = u0 + i, b = u / a.T, t = u - b * a.T;
+    for (int i = threadIdx.x >> 6; i < ntok; i += kWaves) {
+        const int64_t u = u0 + i, b = a.B == 1 ? 0 : u / a.T, t = u - b * a.T;
         Token x;
-        x.live = 1;
-        x.stored = 0;
-        x.q = b * a.sq.b + t * a.sq.t;
-        x.k = b * a.sk.b + t * a.sk.t;
-        x.qo = b * a.sqo.b + t * a.sqo.t;
-        x.ko = b * a.sko.b + t * a.sko.t;
-        x.v = x.vo = 0;
-        x.sdq = b * a.sdq.b + t * a.sdq.t;
-        x.sdk = b * a.sdk.b + t * a.sdk.t;
+        x.on = 1;
+        x.dst = 0;
         int64_t pos;
         if constexpr (APPEND) {
-            x.v = b * a.sv.b + t * a.sv.t;
             int64_t s = b, first = 0, n = a.T;
+            bool live = true;
             if (a.packed) {
                 s = find_sequence(a.cu, a.N, t);
-                x.live = s >= 0 && s < a.N;
-                s = x.live ? s : 0;
+                live = s >= 0 && s < a.N;
+                s = live ? s : 0;
                 first = a.cu[s];
                 n = (int64_t)a.cu[s + 1] - first;
             }
             pos = (int64_t)a.kv_lens[s] - n + (t - first);
-            if (x.live && pos >= 0 && pos < (int64_t)a.max_pages * a.page_size) {
-                const int32_t pg = (int32_t)pos / a.page_size, row = (int32_t)pos - pg * a.page_size;
-                const int32_t page = a.table[s * a.table_stride + pg];
-                if (page >= 0 && page < a.pages) {
-                    x.stored = 1;
-                    x.ko = page * a.skc.p + row * a.skc.t;
-                    x.vo = page * a.svc.p + row * a.svc.t;
+            x.on = live;
+            if (kind != kQueries) {
+                x.on = 0;
+                if (live && pos >= 0 && pos < (int64_t)a.max_pages * a.page_size) {
+                    const int32_t pg = (int32_t)pos / a.page_size, row = (int32_t)pos - pg * a.page_size;
+                    const int32_t page = a.table[s * a.table_stride + pg];
+                    const kda_page_strides& st = kind == kKeys ? a.skc : a.svc;
+                    x.on = page >= 0 && page < a.pages;
+                    x.dst = page * st.p + row * st.t;
                 }
             }
         } else {
@@ -51,80 +47,25 @@ __device__ __forceinline__ void fill_tokens(const RopeArgs& a, Token* tok, int64
     }
 }
 
-// Rows of one kind (queries or keys) of the workgroup's tokens. KEYS: offsets k, ko and `stored`.
-template <typename TI, typename TO, int LAY, bool KEYS, bool APPEND>
-__device__ __forceinline__ void norm_rows(const RopeArgs& a, const Lane& l, const Token* tok, const float2* cs, int ntok,
-                                          uint32_t magic) {
-    constexpr int U = sizeof(TI) == 2 ? 4 : 2;
-    const int H = KEYS ? a.Hk : a.Hq, rg = 64 / l.lpr, rows = ntok * H, P = a.d / 2;
-    const TI* src = static_cast<const TI*>(KEYS ? a.k : a.q);
-    TO* dst = static_cast<TO*>(KEYS ? a.k_out : a.q_out);
-    const int64_t sh = KEYS ? a.sk.h : a.sq.h;
-    const int64_t dh = KEYS ? (APPEND ? a.skc.h : a.sko.h) : a.sqo.h;
-    const float inv_d = 1.f / (float)a.d;
-    float w[16];
-    if (a.norm) load_weight<LAY>(l, KEYS ? a.wk : a.wq, w);
-    for (int base = (threadIdx.x >> 6) * rg * U; base < rows; base += kWaves * rg * U) {
-        float x[U][16];
-        int tk[U];
-        int64_t out[U];
-        bool on[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = base + u * rg + l.g;
-            on[u] = r < rows;
-            const int rr = on[u] ? r : 0;
-            const int t = div_heads(rr, magic), h = rr - t * H;
-            tk[u] = t;
-            on[u] = on[u] && (KEYS && APPEND ? tok[t].stored : tok[t].live);
-            out[u] = (KEYS ? tok[t].ko : tok[t].qo) + h * dh;
-            load_row<TI, LAY>(l, src + ((KEYS ? tok[t].k : tok[t].q) + h * sh), on[u], x[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            to_pairs<LAY>(x[u]);
-            if (a.norm) {
-                float s = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s = fmaf(x[u][j], x[u][j], s);
-                s = row_sum(s, l.lpr);
-                const float r = 1.f / sqrtf(fmaf(s, inv_d, a.eps));
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[u][j] = x[u][j] * r * w[j];
-            }
-            if (a.rot) {
-                float co[8], si[8];
-                load_angles<LAY>(l, cs + tk[u] * P, co, si);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float va = x[u][j], vb = x[u][8 + j];
-                    x[u][j] = fmaf(va, co[j], -vb * si[j]);
-                    x[u][8 + j] = fmaf(vb, co[j], va * si[j]);
-                }
-            }
-            from_pairs<LAY>(x[u]);
-            if (on[u]) store_row<TO, LAY>(l, dst + out[u], x[u]);
-        }
-    }
-}
-
 // The new tokens' values into the cache: 8 channels an access where rows lie on 16 bytes.
 template <typename TI, bool WIDE>
-__device__ __forceinline__ void copy_values(const RopeArgs& a, const Token* tok, int ntok) {
+__device__ __forceinline__ void copy_values(const RopeArgs& a, const Rows3& rows, const Token* tok) {
     constexpr int V = WIDE ? 8 : 1;
-    const int per = a.dv / V, total = ntok * a.Hk * per;
+    const int per = a.dv / V, total = rows.count * per;
     for (int e = threadIdx.x; e < total; e += kThreads) {
-        const int row = e / per, c = (e - row * per) * V, t = row / a.Hk, h = row - t * a.Hk;
-        if (!tok[t].stored) continue;
-        const TI* p = static_cast<const TI*>(a.v) + (tok[t].v + h * a.sv.h + c);
-        bf16_t* o = static_cast<bf16_t*>(a.v_out) + (tok[t].vo + h * a.svc.h + c);
+        const int r = e / per, c = (e - r * per) * V;
+        const Row x = rows.row(r);
+        if (!tok[x.t].on) continue;
+        const TI* p = static_cast<const TI*>(a.v) + (x.at(a.sv) + c);
+        bf16_t* o = static_cast<bf16_t*>(a.v_out) + (tok[x.t].dst + x.h * a.svc.h + c);
         if constexpr (WIDE) {
             if constexpr (sizeof(TI) == 2) {
                 *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(p);
             } else {
-                float x[8];
-                unpack8(p, x);
-                store8(o, x);
+                float f[8];
+                unpack16(*reinterpret_cast<const uint4*>(p), p, f);
+                unpack16(*reinterpret_cast<const uint4*>(p + 4), p, f + 4);
+                store8(o, f);
             }
         } else {
             st_f(o, ld_f(p));
@@ -132,39 +73,102 @@ __device__ __forceinline__ void copy_values(const RopeArgs& a, const Token* tok,
     }
 }
 
+// The rows of workgroup `group` of a kind.
+__device__ __forceinline__ Rows3 rows_of(const RopeArgs& a, const Shape& s, int kind, int64_t group, int& ntok) {
+    Rows3 r;
+    const int64_t u0 = group * s.tokens[kind], all = a.B * a.T;
+    ntok = (int)(all - u0 < s.tokens[kind] ? all - u0 : s.tokens[kind]);
+    r.u0 = (uint32_t)u0;
+    r.T = (uint32_t)a.T;
+    r.H = kind == kQueries ? a.Hq : a.Hk;
+    r.count = ntok * r.H;
+    r.magic = s.magic[kind];
+    r.one = a.B == 1;
+    return r;
+}
+
 template <typename TI, typename TO, int LAY, bool APPEND>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, Shape s, int v_wide) {
+__global__ __launch_bounds__(kThreads, kLaysWide<LAY> ? 5 : 3) void rope_kernel(RopeArgs a, Shape s) {
     extern __shared__ __align__(16) float2 cs[];
     __shared__ Token tok[kMaxTokens];
-    const int64_t u0 = (int64_t)blockIdx.x * s.tokens, all = a.B * a.T;
-    const int ntok = (int)(all - u0 < s.tokens ? all - u0 : s.tokens);
+    const int64_t wg = blockIdx.x;
+    const int kind = wg < s.group0[1] ? kQueries : wg < s.group0[2] ? kKeys : kValues;
+    int ntok;
+    const Rows3 rows = rows_of(a, s, kind, wg - s.group0[kind], ntok);
+    if constexpr (APPEND) {
+        if (kind == kValues) {
+            fill_tokens<true>(a, tok, rows.u0, ntok, kind);
+            lds_barrier();
+            if (s.v_wide)
+                copy_values<TI, true>(a, rows, tok);
+            else
+                copy_values<TI, false>(a, rows, tok);
+            return;
+        }
+    }
+    const bool keys = kind == kKeys, to_cache = APPEND && keys;
     const Lane l = make_lane<LAY>(a, s.lpr);
-    fill_tokens<APPEND>(a, tok, u0, ntok);
+    const int rg = 64 / l.lpr, P = a.d / 2;
+    const TI* src = static_cast<const TI*>(keys ? a.k : a.q);
+    TO* dst = static_cast<TO*>(keys ? a.k_out : a.q_out);
+    const kda_row_strides &si = keys ? a.sk : a.sq, &so = keys ? a.sko : a.sqo;
+    const float inv_d = 1.f / (float)a.d;
+    int r = (threadIdx.x >> 6) * rg + l.g;
+    Row row = rows.row(r < rows.count ? r : 0);
+    Raw<TI, LAY> raw;
+    raw.load(l, src + row.at(si));
+    float w[16];
+    if (a.norm) load_weight<LAY>(l, keys ? a.wk : a.wq, w);
+    fill_tokens<APPEND>(a, tok, rows.u0, ntok, kind);
     lds_barrier();
     if (a.rot) {
         fill_angles(a, tok, ntok, cs);
         lds_barrier();
     }
-    if (a.Hq) norm_rows<TI, TO, LAY, false, APPEND>(a, l, tok, cs, ntok, s.mq);
-    if (a.Hk) norm_rows<TI, TO, LAY, true, APPEND>(a, l, tok, cs, ntok, s.mk);
-    if constexpr (APPEND) {
-        if (v_wide)
-            copy_values<TI, true>(a, tok, ntok);
-        else
-            copy_values<TI, false>(a, tok, ntok);
+#pragma unroll 1
+    for (int first = (threadIdx.x >> 6) * rg; first < rows.count; first += kWaves * rg) {
+        const bool on = r < rows.count && tok[row.t].on;
+        const Row now = row;
+        float x[16];
+        raw.get(l, x);
+        r += kWaves * rg;
+        if (first + kWaves * rg < rows.count) {
+            row = rows.row(r < rows.count ? r : 0);
+            raw.load(l, src + row.at(si));
+        }
+        if (a.norm) {
+            float q = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) q = fmaf(x[j], x[j], q);
+            const float n = inv_root(fmaf(row_sum(q, l.lpr), inv_d, a.eps));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = x[j] * n * w[j];
+        }
+        if (a.rot) {
+            float co[8], sn[8];
+            load_angles<LAY>(l, cs + now.t * P, co, sn);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float va = x[j], vb = x[8 + j];
+                x[j] = fmaf(va, co[j], -vb * sn[j]);
+                x[8 + j] = fmaf(vb, co[j], va * sn[j]);
+            }
+        }
+        from_pairs<LAY>(x);
+        if (on) store_row<TO, LAY>(l, dst + (to_cache ? tok[now.t].dst + now.h * a.skc.h : now.at(so)), x);
     }
 }
 
 template <typename TI, typename TO, bool APPEND>
-hipError_t launch_rows(const RopeArgs& a, const Shape& s, int lay, bool v_wide, hipStream_t st) {
-    const dim3 grid((unsigned)((a.B * a.T + s.tokens - 1) / s.tokens)), block(kThreads);
-    const size_t lds = a.rot ? (size_t)s.tokens * (a.d / 2) * sizeof(float2) : 0;
-    const int vw = v_wide;
+hipError_t launch_rows(const RopeArgs& a, const Shape& s, int lay, hipStream_t st) {
+    const dim3 grid((unsigned)s.group0[3]), block(kThreads);
+    const int most = s.tokens[0] > s.tokens[1] ? s.tokens[0] : s.tokens[1];
+    const size_t lds = a.rot ? (size_t)most * (a.d / 2) * sizeof(float2) : 0;
     switch (lay) {
-        case kHalfWide: hipLaunchKernelGGL((rope_kernel<TI, TO, kHalfWide, APPEND>), grid, block, lds, st, a, s, vw); break;
-        case kInterWide: hipLaunchKernelGGL((rope_kernel<TI, TO, kInterWide, APPEND>), grid, block, lds, st, a, s, vw); break;
-        case kHalfElem: hipLaunchKernelGGL((rope_kernel<TI, TO, kHalfElem, APPEND>), grid, block, lds, st, a, s, vw); break;
-        default: hipLaunchKernelGGL((rope_kernel<TI, TO, kInterElem, APPEND>), grid, block, lds, st, a, s, vw); break;
+        case kHalfWide: hipLaunchKernelGGL((rope_kernel<TI, TO, kHalfWide, APPEND>), grid, block, lds, st, a, s); break;
+        case kInterWide: hipLaunchKernelGGL((rope_kernel<TI, TO, kInterWide, APPEND>), grid, block, lds, st, a, s); break;
+        case kHalfElem: hipLaunchKernelGGL((rope_kernel<TI, TO, kHalfElem, APPEND>), grid, block, lds, st, a, s); break;
+        default: hipLaunchKernelGGL((rope_kernel<TI, TO, kInterElem, APPEND>), grid, block, lds, st, a, s); break;
     }
     return hipGetLastError();
 }
