@@ -94,41 +94,85 @@ def _outer(t):
     return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
+def _strides(stride):
+    return RowStrides(*(stride[:3] if len(stride) == 4 else (0, *stride[:2]) if stride else (0, 0, 0)))
+
+
+# The entry points look their arguments over in one condition each, since a decode step's kernels take a
+# few microseconds; only where it fails does _explain go through them one by one and raise.
+
+def _explain(checks):
+    for f, *args in checks:
+        f(*args)
+    raise ValueError("arguments do not go together")
+
+
 @functools.lru_cache(maxsize=1024)
-def _rope_desc(B, Hq, Hk, T, d, rot, strides, dtype, interleaved, norm, eps, rope_scale):
+def _rope_desc(q, k, q_strides, k_strides, qo, ko, dq, dk, rot, dtype, interleaved, norm, eps, rope_scale):
     """The call's descriptor: nothing but its arguments, so calls of one shape share it."""
-    return HeadRopeDesc(B, Hq, Hk, T, d, rot, *(RowStrides(*s) for s in strides), _DTYPES[dtype], interleaved, norm, eps,
-                        rope_scale)
+    x = q if q is not None else k
+    B, T, d = (x[0] if len(x) == 4 else 1), x[-2], x[-1]
+    return HeadRopeDesc(B, q[-3] if q is not None else 0, k[-3] if k is not None else 0, T, d, rot,
+                        *(_strides(s) for s in (q_strides, k_strides, qo, ko, dq, dk)), _DTYPES[dtype], interleaved, norm,
+                        eps, rope_scale)
 
 
 def _rope_inputs(fn, q, k, inv_freq, positions, q_weight, k_weight, norm):
-    """Checks the inputs that both directions share; returns (a row tensor, its GPU, B, Hq, Hk, T, d, rot)."""
+    """Checks the inputs that both directions share; returns (shapes and strides of q and k, GPU, rot)."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("one of q and k is required")
-    if x.dtype not in _DTYPES:
-        raise ValueError("unsupported dtype %s" % x.dtype)
-    if x.dim() not in (3, 4):
-        raise ValueError("rows must be [B,H,T,d] or [H,T,d] (got shape %s)" % (tuple(x.shape),))
-    index, shape = x.get_device(), x.shape
-    *b, _, T, d = shape
-    Hq, Hk = (0 if t is None or t.dim() < 3 else t.shape[-3] for t in (q, k))
-    for name, t, H in (("q", q, Hq), ("k", k, Hk)):
-        if t is not None:
-            _check_rows(name, t, index, x.dtype, (*b, H, T, d))
+    index, dt, shape = x.get_device(), x.dtype, x.shape
+    rows, d = shape[:-3] + shape[-2:-1], shape[-1:]
+    qs = ks = None
+    qst = kst = ()
+    ok = dt in _DTYPES and 3 <= len(shape) <= 4
+    if q is not None:
+        qs, qst = q.shape, q.stride()
+        ok = ok and qst[-1] == 1
+    if k is not None:
+        ks, kst = k.shape, k.stride()
+        ok = (ok and kst[-1] == 1 and k.dtype is dt and len(ks) == len(shape) and ks[:-3] == shape[:-3] and ks[-2:] == shape[-2:]
+              and k.get_device() == index)
+    if positions is not None:
+        ok = (ok and positions.shape == rows and positions.dtype is torch.int32 and positions.get_device() == index
+              and positions.is_contiguous())
     rot = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        check("inv_freq", inv_freq, index, torch.float32, (rot // 2,))
-    if positions is not None:
-        check("positions", positions, index, torch.int32, (*b, T))
+        rot = 2 * inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+        ok = (ok and rot >= 0 and inv_freq.dtype is torch.float32 and inv_freq.get_device() == index
+              and inv_freq.is_contiguous())
+    if q_weight is not None:
+        ok = (ok and norm and q_weight.shape == d and q_weight.dtype is torch.float32 and q_weight.get_device() == index
+              and q_weight.is_contiguous())
+    if k_weight is not None:
+        ok = (ok and norm and k_weight.shape == d and k_weight.dtype is torch.float32 and k_weight.get_device() == index
+              and k_weight.is_contiguous())
+    if not ok:
+        if dt not in _DTYPES:
+            raise ValueError("unsupported dtype %s" % dt)
+        if not 3 <= len(shape) <= 4:
+            raise ValueError("rows must be [B,H,T,d] or [H,T,d] (got shape %s)" % (tuple(shape),))
+        like = lambda t: shape[:-3] + t.shape[-3:-2] + shape[-2:] if t.dim() >= 3 else shape
+        _explain([(_check_rows, n, t, index, dt, like(t)) for n, t in (("q", q), ("k", k)) if t is not None]
+                 + ([(check, "positions", positions, index, torch.int32, rows)] if positions is not None else [])
+                 + ([(check, "inv_freq", inv_freq, index, torch.float32, (inv_freq.numel(),))] if inv_freq is not None else [])
+                 + _weights(q_weight, k_weight, norm, index, d))
+    if not x.is_cuda:
+        on_gpu(fn, x)
+    return qs, ks, qst, kst, index, rot
+
+
+def _weights(q_weight, k_weight, norm, index, d):
+    out = []
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            if not norm:
-                raise ValueError("%s goes with norm" % name)
-            check(name, w, index, torch.float32, (d,))
-    on_gpu(fn, x)
-    return x, index, b[0] if b else 1, Hq, Hk, T, d, rot
+            out += [(check, name, w, index, torch.float32, d)] if norm else [(_refuse, "%s goes with norm" % name)]
+    return out
+
+
+def _refuse(text):
+    raise ValueError(text)
 
 
 def head_rope_fwd(q, k, inv_freq, positions=None, *, interleaved=False, rope_scale=1.0, q_weight=None, k_weight=None,
@@ -143,22 +187,26 @@ def head_rope_fwd(q, k, inv_freq, positions=None, *, interleaved=False, rope_sca
         y = weight * x / sqrt(mean(x^2) + eps)      (norm False: x itself; weights [d] fp32 or None)
     Returns (q_out, k_out) in the inputs' type, their dimensions in memory in the inputs' order;
     None for an input that was not given. Caller-supplied outputs are checked like the inputs."""
-    x, index, B, Hq, Hk, T, d, rot = _rope_inputs("head_rope_fwd", q, k, inv_freq, positions, q_weight, k_weight, norm)
-    for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)):
+    qs, ks, qst, kst, index, rot = _rope_inputs("head_rope_fwd", q, k, inv_freq, positions, q_weight, k_weight, norm)
+    for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)) if q_out is not None or k_out is not None else ():
         if o is not None:
             if t is None:
                 raise ValueError("%s goes with %s" % (name, name[0]))
             _check_rows(name, o, index, t.dtype, t.shape)
     with scope(index, stream):
-        if q_out is None and q is not None:
+        if q_out is None and qs is not None:
             q_out = torch.empty_like(q)
-        if k_out is None and k is not None:
+        if k_out is None and ks is not None:
             k_out = torch.empty_like(k)
-        desc = _rope_desc(B, Hq, Hk, T, d, rot, (_outer(q), _outer(k), _outer(q_out), _outer(k_out), (0, 0, 0), (0, 0, 0)),
-                          x.dtype, bool(interleaved), bool(norm), float(eps), float(rope_scale))
-        st = (_lib or _library()).kda_head_rope_fwd(desc, ptr(q), ptr(k), ptr(q_weight), ptr(k_weight), ptr(inv_freq),
-                                                    ptr(positions), ptr(q_out), ptr(k_out), raw_stream(index, stream))
-    _check("kda_head_rope_fwd", st)
+        desc = _rope_desc(qs, ks, qst, kst, q_out.stride() if qs is not None else (), k_out.stride() if ks is not None else (),
+                          (), (), rot, (q if qs is not None else k).dtype, bool(interleaved), bool(norm), float(eps),
+                          float(rope_scale))
+        st = (_lib or _library()).kda_head_rope_fwd(
+            desc, None if q is None else q.data_ptr(), None if k is None else k.data_ptr(), ptr(q_weight), ptr(k_weight),
+            ptr(inv_freq), ptr(positions), None if q is None else q_out.data_ptr(), None if k is None else k_out.data_ptr(),
+            raw_stream(index, stream))
+    if st:
+        _check("kda_head_rope_fwd", st)
     return q_out, k_out
 
 
@@ -169,12 +217,13 @@ def head_rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, *, interleaved
     Inputs as the forward's; dq_out, dk_out: gradients of its outputs, in their shape and type, any
     strides. Returns (dq, dk, dq_weight, dk_weight): rows in their input's type, weight gradients [d]
     fp32; None for each input that was not given."""
-    x, index, B, Hq, Hk, T, d, rot = _rope_inputs("head_rope_bwd", q, k, inv_freq, positions, q_weight, k_weight, norm)
+    qs, ks, qst, kst, index, rot = _rope_inputs("head_rope_bwd", q, k, inv_freq, positions, q_weight, k_weight, norm)
     for name, g, t in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
         if (g is None) != (t is None):
             raise ValueError("%s goes with %s" % (name, name[1]))
         if g is not None:
             _check_rows(name, g, index, t.dtype, t.shape)
+    x = q if q is not None else k
     if workspace is not None:
         _check_workspace(workspace, x.device)
     sums = q_weight is not None or k_weight is not None
@@ -184,8 +233,9 @@ def head_rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, *, interleaved
         dk = torch.empty_like(k) if k is not None else None
         dwq = torch.empty_like(q_weight) if q_weight is not None and q is not None else None
         dwk = torch.empty_like(k_weight) if k_weight is not None and k is not None else None
-        desc = _rope_desc(B, Hq, Hk, T, d, rot, (_outer(q), _outer(k), _outer(dq_out), _outer(dk_out), _outer(dq), _outer(dk)),
-                          x.dtype, bool(interleaved), bool(norm), float(eps), float(rope_scale))
+        st = lambda t: t.stride() if t is not None else ()
+        desc = _rope_desc(qs, ks, qst, kst, st(dq_out), st(dk_out), st(dq), st(dk), rot, x.dtype, bool(interleaved), bool(norm),
+                          float(eps), float(rope_scale))
         workspace = _workspace(lib.kda_head_rope_bwd_workspace_bytes(desc) if sums else 0, workspace, x.device)
         st = lib.kda_head_rope_bwd(desc, ptr(q), ptr(k), ptr(q_weight), ptr(k_weight), ptr(inv_freq), ptr(positions),
                                    ptr(dq_out), ptr(dk_out), ptr(dq), ptr(dk), ptr(dwq), ptr(dwk), ptr(workspace),
@@ -194,25 +244,35 @@ def head_rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, *, interleaved
     return dq, dk, dwq, dwk
 
 
-def _cache_inputs(index, first, cu_seqlens, kv_lens, block_table):
-    """Checks what tells sequences and pages apart; returns (N, packed)."""
-    packed = cu_seqlens is not None
-    if first.dim() != (3 if packed else 4):
-        raise ValueError("rows must be [H,T,d] with cu_seqlens, [N,H,T,d] without (got shape %s)" % (tuple(first.shape),))
-    N = cu_seqlens.numel() - 1 if packed else first.shape[0]
-    if packed:
-        check("cu_seqlens", cu_seqlens, index, torch.int32, (N + 1,))
-    check("kv_lens", kv_lens, index, torch.int32, (N,))
-    _check_rows("block_table", block_table, index, torch.int32, (N, block_table.shape[-1]))
-    return N, packed
+def _sequences_ok(index, N, cu_seqlens, kv_lens, block_table):
+    """What tells sequences and pages apart: N sequences' lengths and table."""
+    return (kv_lens.shape == (N,) and kv_lens.dtype is torch.int32 and kv_lens.get_device() == index
+            and kv_lens.is_contiguous() and block_table.dim() == 2 and block_table.shape[0] == N
+            and block_table.dtype is torch.int32 and block_table.get_device() == index
+            and (block_table.stride(1) == 1 or block_table.shape[1] == 1)
+            and (cu_seqlens is None or cu_seqlens.dtype is torch.int32 and cu_seqlens.get_device() == index
+                 and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()))
+
+
+def _sequence_checks(index, N, cu_seqlens, kv_lens, block_table):
+    return ([(check, "cu_seqlens", cu_seqlens, index, torch.int32, (N + 1,))] if cu_seqlens is not None else []) + [
+        (check, "kv_lens", kv_lens, index, torch.int32, (N,)),
+        (_check_rows, "block_table", block_table, index, torch.int32, (N, block_table.shape[-1] if block_table.dim() else 0))]
+
+
+def _rows_dims(t, cu_seqlens):
+    """Sequences of [N,H,T,d] rows, or of packed [H,T,d] ones."""
+    if t.dim() != (4 if cu_seqlens is None else 3):
+        raise ValueError("rows must be [H,T,d] with cu_seqlens, [N,H,T,d] without (got shape %s)" % (tuple(t.shape),))
+    return t.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
 
 
 @functools.lru_cache(maxsize=1024)
-def _append_desc(N, Hq, Hk, T, dk, dv, rot, pages, page_size, max_pages, table_stride, rows, caches, dtype, packed,
+def _append_desc(q, k, v, q_strides, k_strides, v_strides, qo, kc, kcs, vcs, N, max_pages, table_stride, rot, dtype, packed,
                  interleaved, norm, eps, rope_scale):
-    return KvAppendDesc(N, Hq, Hk, T, dk, dv, rot, pages, page_size, max_pages, table_stride,
-                        *(RowStrides(*s) for s in rows), *(PageStrides(*s) for s in caches), _DTYPES[dtype], packed,
-                        interleaved, norm, eps, rope_scale)
+    return KvAppendDesc(N, q[-3] if q is not None else 0, k[-3], k[-2], k[-1], v[-1], rot, kc[0], kc[2], max_pages,
+                        table_stride, *(_strides(s) for s in (q_strides, k_strides, v_strides, qo)),
+                        *(PageStrides(*s[:3]) for s in (kcs, vcs)), _DTYPES[dtype], packed, interleaved, norm, eps, rope_scale)
 
 
 def kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, inv_freq=None, *, cu_seqlens=None, interleaved=False,
@@ -226,56 +286,64 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, inv_freq=None, *,
     strides with contiguous channels. block_table: int32 [N,max_pages]; position j of sequence s is
     row j % page_size of page block_table[s, j // page_size]. kv_lens: int32 [N], positions in use
     with the new tokens, which are each sequence's last. Norm and rotation as ``head_rope_fwd``."""
-    if k.dtype not in _DTYPES:
-        raise ValueError("unsupported dtype %s" % k.dtype)
-    index, dt = k.get_device(), k.dtype
-    N, packed = _cache_inputs(index, k, cu_seqlens, kv_lens, block_table)
-    *b, Hk, T, dk = k.shape
-    dv = v.shape[-1]
-    _check_rows("k", k, index, dt, k.shape)
-    _check_rows("v", v, index, dt, (*b, Hk, T, dv))
-    Hq = 0
-    if q is not None:
-        Hq = q.shape[-3] if q.dim() >= 3 else 0
-        _check_rows("q", q, index, dt, (*b, Hq, T, dk))
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages,Hk,page_size,dk] (got shape %s)" % (tuple(k_cache.shape),))
-    pages, page_size = k_cache.shape[0], k_cache.shape[2]
-    _check_rows("k_cache", k_cache, index, torch.bfloat16, (pages, Hk, page_size, dk))
-    _check_rows("v_cache", v_cache, index, torch.bfloat16, (pages, Hk, page_size, dv))
-    rot = 0
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        check("inv_freq", inv_freq, index, torch.float32, (rot // 2,))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            if not norm:
-                raise ValueError("%s goes with norm" % name)
-            check(name, w, index, torch.float32, (dk,))
+    BF16 = torch.bfloat16
+    N = _rows_dims(k, cu_seqlens)
+    index, dt, ks, kst, vs, vst = k.get_device(), k.dtype, k.shape, k.stride(), v.shape, v.stride()
+    kc, kcs, vc, vcs = k_cache.shape, k_cache.stride(), v_cache.shape, v_cache.stride()
+    qs, qst = (q.shape, q.stride()) if q is not None else (None, ())
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    d = ks[-1:]
+    if not (dt in _DTYPES and v.dtype is dt and k_cache.dtype is BF16 and v_cache.dtype is BF16 and kst[-1] == 1
+            and (vst[-1] == 1 or vs[-1] == 1) and vs[:-1] == ks[:-1] and v.get_device() == index and len(kc) == 4 and len(vc) == 4
+            and kc[1] == ks[-3] and kc[3:] == d and kc[:3] == vc[:3] and vc[3:] == vs[-1:] and kcs[3] == 1
+            and (vcs[3] == 1 or vs[-1] == 1) and k_cache.get_device() == index and v_cache.get_device() == index
+            and (q is None or q.dtype is dt and qst[-1] == 1 and len(qs) == len(ks) and qs[:-3] == ks[:-3] and qs[-2:] == ks[-2:]
+                 and q.get_device() == index)
+            and (inv_freq is None or rot >= 0 and inv_freq.dtype is torch.float32 and inv_freq.get_device() == index
+                 and inv_freq.is_contiguous())
+            and (q_weight is None or norm and q_weight.shape == d and q_weight.dtype is torch.float32
+                 and q_weight.get_device() == index and q_weight.is_contiguous())
+            and (k_weight is None or norm and k_weight.shape == d and k_weight.dtype is torch.float32
+                 and k_weight.get_device() == index and k_weight.is_contiguous())
+            and _sequences_ok(index, N, cu_seqlens, kv_lens, block_table)):
+        if dt not in _DTYPES:
+            raise ValueError("unsupported dtype %s" % dt)
+        if len(kc) != 4:
+            raise ValueError("k_cache must be [pages,Hk,page_size,dk] (got shape %s)" % (tuple(kc),))
+        like = ks[:-3] + (qs[-3:-2] if qs is not None and len(qs) >= 3 else ks[-3:-2]) + ks[-2:]
+        _explain([(_check_rows, "k", k, index, dt, ks), (_check_rows, "v", v, index, dt, ks[:-1] + vs[-1:])]
+                 + ([(_check_rows, "q", q, index, dt, like)] if q is not None else [])
+                 + [(_check_rows, "k_cache", k_cache, index, BF16, (kc[0], ks[-3], kc[2], ks[-1])),
+                    (_check_rows, "v_cache", v_cache, index, BF16, (kc[0], ks[-3], kc[2], vs[-1]))]
+                 + ([(check, "inv_freq", inv_freq, index, torch.float32, (inv_freq.numel(),))] if inv_freq is not None else [])
+                 + _weights(q_weight, k_weight, norm, index, d) + _sequence_checks(index, N, cu_seqlens, kv_lens, block_table))
     if q_out is not None:
         if q is None:
             raise ValueError("q_out goes with q")
-        _check_rows("q_out", q_out, index, torch.bfloat16, q.shape)
-    on_gpu("kv_append", k)
+        _check_rows("q_out", q_out, index, BF16, q.shape)
+    if not k.is_cuda:
+        on_gpu("kv_append", k)
     with scope(index, stream):
         if q_out is None and q is not None:
-            q_out = torch.empty_like(q, dtype=torch.bfloat16)
-        desc = _append_desc(N, Hq, Hk, T, dk, dv, rot, pages, page_size, block_table.shape[1], block_table.stride(0),
-                            (_outer(q), _outer(k), _outer(v), _outer(q_out)),
-                            (k_cache.stride()[:3], v_cache.stride()[:3]), dt, packed, bool(interleaved), bool(norm),
-                            float(eps), float(rope_scale))
-        st = (_lib or _library()).kda_kv_append(desc, ptr(q), ptr(k), ptr(v), ptr(q_weight), ptr(k_weight), ptr(inv_freq),
-                                                ptr(cu_seqlens), ptr(kv_lens), ptr(block_table), ptr(q_out), ptr(k_cache),
-                                                ptr(v_cache), raw_stream(index, stream))
-    _check("kda_kv_append", st)
+            q_out = torch.empty_like(q, dtype=BF16)
+        desc = _append_desc(qs, ks, vs, qst, kst, vst, q_out.stride() if q is not None else (), kc, kcs, vcs, N,
+                            block_table.shape[1], block_table.stride(0), rot, dt, cu_seqlens is not None, bool(interleaved),
+                            bool(norm), float(eps), float(rope_scale))
+        st = (_lib or _library()).kda_kv_append(
+            desc, ptr(q), k.data_ptr(), v.data_ptr(), ptr(q_weight), ptr(k_weight), ptr(inv_freq), ptr(cu_seqlens),
+            kv_lens.data_ptr(), block_table.data_ptr(), ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+            raw_stream(index, stream))
+    if st:
+        _check("kda_kv_append", st)
     return q_out
 
 
 @functools.lru_cache(maxsize=1024)
-def _attn_desc(N, Hq, Hk, T, dk, dv, pages, page_size, max_pages, table_stride, window, rows, caches, packed, scale):
+def _attn_desc(q, q_strides, o_strides, kc, kcs, vc, vcs, N, max_pages, table_stride, window, packed, scale):
     """The call's descriptor and the workspace it needs."""
-    desc = PagedAttnDesc(N, Hq, Hk, T, dk, dv, pages, page_size, max_pages, table_stride, window,
-                         *(RowStrides(*s) for s in rows), *(PageStrides(*s) for s in caches), packed, scale)
+    desc = PagedAttnDesc(N, q[-3], vc[1], q[-2], q[-1], vc[3], vc[0], vc[2], max_pages, table_stride, window,
+                         _strides(q_strides), _strides(o_strides), PageStrides(*kcs[:3]), PageStrides(*vcs[:3]), packed,
+                         float(q[-1] ** -0.5 if scale is None else scale))
     return desc, _library().kda_paged_attn_workspace_bytes(desc)
 
 
@@ -293,39 +361,43 @@ def paged_attn(q, k_cache, v_cache, block_table, kv_lens, *, cu_seqlens=None, sc
     dimensions in memory in q's order; with ``return_lse`` (o, lse), lse fp32 [N,Hq,T] (packed [Hq,T]).
     A token that sees nothing has o = 0 and lse = -inf."""
     BF16 = torch.bfloat16
-    index = q.get_device()
-    N, packed = _cache_inputs(index, q, cu_seqlens, kv_lens, block_table)
-    *b, Hq, T, dk = q.shape
-    _check_rows("q", q, index, BF16, q.shape)
-    if k_cache.dim() != 4 or v_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must be [pages,Hk,page_size,d] (got shapes %s, %s)"
-                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
-    pages, Hk, page_size, dv = v_cache.shape
-    _check_rows("k_cache", k_cache, index, BF16, (pages, Hk, page_size, dk))
-    _check_rows("v_cache", v_cache, index, BF16, v_cache.shape)
+    N = _rows_dims(q, cu_seqlens)
+    index, qs, qst = q.get_device(), q.shape, q.stride()
+    kc, kcs, vc, vcs = k_cache.shape, k_cache.stride(), v_cache.shape, v_cache.stride()
+    if not (q.dtype is BF16 and k_cache.dtype is BF16 and v_cache.dtype is BF16 and qst[-1] == 1 and len(kc) == 4
+            and len(vc) == 4 and kc[:3] == vc[:3] and kc[3:] == qs[-1:] and kcs[3] == 1 and vcs[3] == 1
+            and k_cache.get_device() == index and v_cache.get_device() == index
+            and _sequences_ok(index, N, cu_seqlens, kv_lens, block_table)):
+        if len(kc) != 4 or len(vc) != 4:
+            raise ValueError("k_cache and v_cache must be [pages,Hk,page_size,d] (got shapes %s, %s)" % (tuple(kc), tuple(vc)))
+        _explain([(_check_rows, "q", q, index, BF16, qs), (_check_rows, "k_cache", k_cache, index, BF16, vc[:3] + qs[-1:]),
+                  (_check_rows, "v_cache", v_cache, index, BF16, vc)]
+                 + _sequence_checks(index, N, cu_seqlens, kv_lens, block_table))
+    out = qs[:-1] + vc[3:]
     if o is not None:
-        _check_rows("o", o, index, BF16, (*b, Hq, T, dv))
+        _check_rows("o", o, index, BF16, out)
     if lse is not None:
-        check("lse", lse, index, torch.float32, (*b, Hq, T))
+        check("lse", lse, index, torch.float32, qs[:-1])
     if workspace is not None:
         _check_workspace(workspace, q.device)
-    on_gpu("paged_attn", q)
+    if not q.is_cuda:
+        on_gpu("paged_attn", q)
     with scope(index, stream):
         if o is None:
-            if dv == dk:
+            if out == qs:
                 o = torch.empty_like(q)
             else:      # q's order of dimensions: token-major rows stay so
-                s = q.stride()
-                o = (torch.empty(*b, T, Hq, dv, dtype=BF16, device=q.device).transpose(-3, -2) if s[-3] < s[-2]
-                     else torch.empty(*b, Hq, T, dv, dtype=BF16, device=q.device))
+                turned = qst[-3] < qst[-2]
+                o = torch.empty(out[:-3] + (out[-2], out[-3], out[-1]) if turned else out, dtype=BF16, device=q.device)
+                o = o.transpose(-3, -2) if turned else o
         if lse is None and return_lse:
-            lse = torch.empty(*b, Hq, T, dtype=torch.float32, device=q.device)
-        desc, need = _attn_desc(N, Hq, Hk, T, dk, dv, pages, page_size, block_table.shape[1], block_table.stride(0),
-                                int(window), (_outer(q), _outer(o)), (k_cache.stride()[:3], v_cache.stride()[:3]), packed,
-                                float(dk ** -0.5 if scale is None else scale))
+            lse = torch.empty(qs[:-1], dtype=torch.float32, device=q.device)
+        desc, need = _attn_desc(qs, qst, o.stride(), kc, kcs, vc, vcs, N, block_table.shape[1], block_table.stride(0), int(window),
+                                cu_seqlens is not None, scale)
         workspace = _workspace(need, workspace, q.device)
-        st = (_lib or _library()).kda_paged_attn(desc, ptr(q), ptr(k_cache), ptr(v_cache), ptr(cu_seqlens), ptr(kv_lens),
-                                                 ptr(block_table), ptr(o), ptr(lse), ptr(workspace), _nbytes(workspace),
-                                                 raw_stream(index, stream))
-    _check("kda_paged_attn", st)
+        st = (_lib or _library()).kda_paged_attn(
+            desc, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ptr(cu_seqlens), kv_lens.data_ptr(),
+            block_table.data_ptr(), o.data_ptr(), ptr(lse), ptr(workspace), _nbytes(workspace), raw_stream(index, stream))
+    if st:
+        _check("kda_paged_attn", st)
     return (o, lse) if return_lse else o
