@@ -43,8 +43,10 @@ size_t attn_ws_bytes(const AttnArgs& a) {
     return (size_t)b;
 }
 
-hipError_t launch_paged_attn(const AttnArgs& a, hipStream_t st) {
+hipError_t launch_paged_attn(const AttnArgs& args, hipStream_t st) {
     using namespace attn;
+    AttnArgs a = args;
+    set_divisors(a);
     for (int k = 0; k < 2; ++k)     // a launch has fewer than 2^32 threads
         if (groups_most(a, k == 0) >= (int64_t)1 << 23) return hipErrorInvalidConfiguration;
     if (a.dk == 128) return a.dv == 128 ? launch<128, 128>(a, st) : launch<128, 64>(a, st);

@@ -24,7 +24,7 @@ kda_status check_desc(const kda_paged_attn_desc* d) {
     if (!(d->scale >= -3.4028234e38f && d->scale <= 3.4028234e38f)) return KDA_ERR_INVALID_ARG;
     if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128) || d->page_size % 16 || d->page_size > 1 << 20)
         return KDA_ERR_UNSUPPORTED;
-    if (d->Hq > 4096 || d->N >= kMaxRows || d->T >= kMaxRows || d->T * d->Hq >= kMaxRows * 64 || d->window >= kMaxRows)
+    if (d->Hq > 512 || d->N >= kMaxRows || d->T >= kMaxRows || d->T * d->Hq >= kMaxRows * 64 || d->window >= kMaxRows)
         return KDA_ERR_UNSUPPORTED;
     if (d->T * (d->Hq / d->Hk) >= kMaxRows || (!d->packed && d->N * d->T * (d->Hq / d->Hk) >= kMaxRows)) return KDA_ERR_UNSUPPORTED;
     if (d->pages >= kMaxRows || d->max_pages >= kMaxRows || d->max_pages * d->page_size >= kMaxRows ||

@@ -17,6 +17,9 @@ struct AttnArgs {
     kda_row_strides sq, so;
     kda_page_strides skc, svc;
     bool packed;
+    uint32_t mG, mHk;           // ceil(2^32 / G), ceil(2^32 / Hk); 0 for 1
+    int32_t span[2];            // keys that a wide, a narrow tile reads at most (the window and its tokens)
+    int32_t page_shift;         // log2(page_size), or -1
     float c;                    // |scale| * log2(e), at least the smallest normal number
     uint32_t flip;              // sign bits of two bf16 where scale < 0: q enters negated
     const void *q, *k_cache, *v_cache;

@@ -55,11 +55,17 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
+// n / d by the magic number of d: exact where n d < 2^32.
+__device__ __forceinline__ int div_by(int n, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)n, magic) : n; }
+
 // One tile's place: which sequence, rows and keys.
+struct Tile;
+__device__ __forceinline__ void row_of(const AttnArgs& a, const Tile& t, int r, int& tok, int& hd);
 struct Tile {
     int64_t seq, first;     // sequence, first token of it in the rows' T (packed) or 0
     int n, kv;              // its new tokens, its keys
     int row0, rows;         // first row, rows of the sequence in all
+    int tok0, rem0;         // token and head (of the group) of row0
     int head;               // key head
     int lo, hi;             // keys that any row sees: [lo, hi)
     int chunk, chunks;
@@ -82,20 +88,23 @@ __device__ __forceinline__ bool sequence(const AttnArgs& a, int64_t s, int64_t& 
     return n > 0;
 }
 
-// Keys that the longest tile of a sequence reads, in units.
-__device__ __forceinline__ int64_t tile_units(const AttnArgs& a, int kv, int rows) {
-    int64_t k = kv;
-    if (a.window > 0) {
-        const int64_t w = a.window + (rows + a.G - 1) / a.G + kUnit;
-        k = k < w ? k : w;
-    }
-    return k > 0 ? (k + kUnit - 1) / kUnit : 1;
+// Row row0 + r of a tile: its token and its head in the group.
+__device__ __forceinline__ void row_of(const AttnArgs& a, const Tile& t, int r, int& tok, int& hd) {
+    const int x = t.rem0 + r, q = div_by(x, a.mG);
+    tok = t.tok0 + q;
+    hd = x - q * a.G;
 }
 
-__device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, int n, bool narrow) {
-    const int64_t rows = (int64_t)n * a.G;
+// Keys that the longest tile of a sequence reads, in units.
+__device__ __forceinline__ int tile_units(const AttnArgs& a, int kv, bool narrow) {
+    const int k = kv < a.span[narrow] ? kv : a.span[narrow];
+    return k > 0 ? (int)(((uint32_t)k + kUnit - 1) / kUnit) : 1;
+}
+
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, bool narrow) {
+    const uint32_t rows = (uint32_t)n * (uint32_t)a.G;
     if (rows <= kNarrowRows) return narrow ? 1 : 0;
-    return narrow ? 0 : (rows + kWideRows - 1) / kWideRows;
+    return narrow ? 0 : (int)((rows + kWideRows - 1) / kWideRows);
 }
 
 // ---- which sequence, tile and chunk a workgroup has ------------------------------------------------
@@ -132,28 +141,32 @@ struct Place {
 // all_cuts: how many (tile, head)s are cut in all.
 template <bool NARROW, bool CUT>
 __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& out, int& all_cuts) {
-    const int lane = threadIdx.x & 63;
-    constexpr int R = NARROW ? kNarrowRows : kWideRows;
+    const int lane = threadIdx.x & 63, N = (int)a.N;
     int64_t first = 0;
-    int n = 0, kv = 0, k = (int)((a.N + 63) / 64);
+    int n = 0, kv = 0, k = (N + 63) / 64;
     float units = 0.f;
-    for (int64_t s = (int64_t)lane * k; s < a.N && s < (int64_t)(lane + 1) * k; ++s)
-        if (sequence(a, s, first, n, kv)) units += (float)(tiles_of(a, n, NARROW) * a.Hk) * (float)tile_units(a, kv, R);
-    // the sum's rounding may not make len too small: chunks would pass the workspace's slots
+    if (k == 1) {
+        if (lane < N && sequence(a, lane, first, n, kv))
+            units = (float)(tiles_of(a, n, NARROW) * a.Hk) * (float)tile_units(a, kv, NARROW);
+    } else {
+        for (int s = lane * k; s < N && s < (lane + 1) * k; ++s)
+            if (sequence(a, s, first, n, kv)) units += (float)(tiles_of(a, n, NARROW) * a.Hk) * (float)tile_units(a, kv, NARROW);
+    }
+    // chunk length; the sum's rounding may not make it too small: chunks would pass the workspace's slots
     units = lane_value(wave_prefix_sum(units), 63) * 1.01f;
-    const int len = (int)fminf(fmaxf(ceilf(units / (float)target(NARROW)), (float)kMinUnits), 16777216.f);
+    const float inv = 1.f / fminf(fmaxf(ceilf(units / (float)target(NARROW)), (float)kMinUnits), 16777216.f);
     Counts base = {0, 0, 0};
-    int64_t lo = 0, left = a.N;
-    for (bool again = false;; again = true) {
-        k = (int)((left + 63) / 64);
+    int lo = 0, left = N;
+    for (bool held = k == 1;; held = false) {
+        k = (left + 63) / 64;
         Counts c = {0, 0, 0};
         int chunks = 1;
-        const int64_t s0 = lo + (int64_t)lane * k, s1 = s0 + k < lo + left ? s0 + k : lo + left;
-        for (int64_t s = s0; s < s1; ++s) {
-            if (k > 1 || again) sequence(a, s, first, n, kv);       // else still held from above
+        const int s0 = lo + lane * k, s1 = s0 + k < lo + left ? s0 + k : lo + left;
+        for (int s = s0; s < s1; ++s) {
+            if (!held) sequence(a, s, first, n, kv);
             if (n <= 0) continue;
-            const int tiles = (int)tiles_of(a, n, NARROW) * a.Hk;
-            chunks = ((int)tile_units(a, kv, R) + len - 1) / len;
+            const int tiles = tiles_of(a, n, NARROW) * a.Hk;
+            chunks = (int)fmaxf(ceilf((float)tile_units(a, kv, NARROW) * inv - 0.001f), 1.f);
             c.items += tiles * chunks;
             if (chunks > 1) {
                 c.slots += tiles * chunks;
@@ -163,15 +176,15 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
         if (s0 >= s1) n = 0;
         const int items = wave_scan(c.items) + base.items - c.items, slots = wave_scan(c.slots) + base.slots - c.slots,
                   cuts = wave_scan(c.cuts) + base.cuts - c.cuts;
-        if (!again) all_cuts = lane_read(cuts + c.cuts, 63);
+        if (lo == 0 && left == N) all_cuts = lane_read(cuts + c.cuts, 63);
         const int at = CUT ? cuts : items, count = CUT ? c.cuts : c.items;
         const uint64_t mine = __ballot(at <= idx && idx < at + count);
         if (mine == 0) return false;
         const int w = __builtin_ctzll(mine);
         base = Counts{lane_read(items, w), lane_read(slots, w), lane_read(cuts, w)};
-        lo = lo + (int64_t)w * k;
+        lo = lo + w * k;
         if (k == 1) {
-            out.seq = uniform((int)lo);
+            out.seq = uniform(lo);
             out.first = uniform(lane_read((int)first, w));
             out.n = uniform(lane_read(n, w));
             out.kv = uniform(lane_read(kv, w));
@@ -180,7 +193,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
             out.index = uniform(idx - (CUT ? base.cuts : base.items));
             return true;
         }
-        left = left - (int64_t)w * k < k ? left - (int64_t)w * k : k;
+        left = left - w * k < k ? left - w * k : k;
     }
 }
 
@@ -191,8 +204,8 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
 // outside the cache), so that going to a page costs a wave four lane reads.
 struct Pages {
     const int32_t* table;
-    const void *kc, *vc;
-    int64_t kp, vp, kh, vh;         // page strides and head offsets, elements
+    uint64_t kc, vc;                // the head's rows in page 0 of either cache
+    uint32_t kp, vp;                // bytes from page to page
     int max_pages, page_size, pages;
     int pg, row;                    // page index and row of the current key
     int base;
@@ -200,13 +213,13 @@ struct Pages {
 
     __device__ __forceinline__ Pages(const AttnArgs& a, int64_t seq, int head, int key) {
         table = a.table + seq * a.table_stride;
-        kc = a.k_cache; vc = a.v_cache;
-        kp = a.skc.p; vp = a.svc.p;
-        kh = head * a.skc.h; vh = head * a.svc.h;
+        kc = reinterpret_cast<uint64_t>(a.k_cache) + 2 * (uint64_t)(head * a.skc.h);
+        vc = reinterpret_cast<uint64_t>(a.v_cache) + 2 * (uint64_t)(head * a.svc.h);
+        kp = (uint32_t)(2 * a.skc.p); vp = (uint32_t)(2 * a.svc.p);
         max_pages = a.max_pages;
         page_size = a.page_size;
         pages = a.pages;
-        pg = uniform(key / page_size);
+        pg = uniform(a.page_shift >= 0 ? key >> a.page_shift : key / page_size);
         row = uniform(key - pg * page_size);
         fetch();
     }
@@ -221,8 +234,7 @@ struct Pages {
         base = pg;
         const int i = pg + fresh_lane(), p = i < max_pages ? table[i] : -1;
         const bool ok = p >= 0 && p < pages;
-        const uint64_t k = reinterpret_cast<uint64_t>(kc) + 2 * (uint64_t)((ok ? p : 0) * kp + kh);
-        const uint64_t v = reinterpret_cast<uint64_t>(vc) + 2 * (uint64_t)((ok ? p : 0) * vp + vh);
+        const uint64_t k = kc + (uint64_t)(uint32_t)(ok ? p : 0) * kp, v = vc + (uint64_t)(uint32_t)(ok ? p : 0) * vp;
         klo = (uint32_t)k; khi = ok ? (uint32_t)(k >> 32) & 0xffff : 0xffffffffu;
         vlo = (uint32_t)v; vhi = ok ? (uint32_t)(v >> 32) & 0xffff : 0xffffffffu;
     }
@@ -233,16 +245,12 @@ struct Pages {
         if (pg + ahead - base >= 64) fetch();
         const int i = pg + ahead - base;
         const bool all = valid >= page_size, none = valid <= 0;
-        k[0] = __builtin_amdgcn_readlane(klo, i);
-        k[1] = __builtin_amdgcn_readlane(khi, i);
-        v[0] = __builtin_amdgcn_readlane(vlo, i);
-        v[1] = __builtin_amdgcn_readlane(vhi, i);
-        const bool bad = k[1] < 0 || none;
-        k[2] = bad ? 0 : all ? lk.full : (valid - 1) * (int)lk.row_bytes + LK::kRowBytes;
-        v[2] = bad ? 0 : all ? lv.full : (valid - 1) * (int)lv.row_bytes + LV::kRowBytes;
-        k[1] &= 0xffff;
-        v[1] &= 0xffff;
-        k[3] = v[3] = kBufFlags;
+        const int khi_ = __builtin_amdgcn_readlane(khi, i), vhi_ = __builtin_amdgcn_readlane(vhi, i);
+        const bool bad = khi_ < 0 || none;
+        const int ks = bad ? 0 : all ? lk.full : (valid - 1) * (int)lk.row_bytes + LK::kRowBytes;
+        const int vs = bad ? 0 : all ? lv.full : (valid - 1) * (int)lv.row_bytes + LV::kRowBytes;
+        k = i32x4{(int)__builtin_amdgcn_readlane(klo, i), khi_ & 0xffff, ks, kBufFlags};
+        v = i32x4{(int)__builtin_amdgcn_readlane(vlo, i), vhi_ & 0xffff, vs, kBufFlags};
     }
 };
 
@@ -286,41 +294,48 @@ struct Loader {
     __device__ __forceinline__ int first_row(int i) const { return i * kStep + w * L::kRows; }
 };
 
-// The keys' and the values' tile at the walk's place; keys from `hi` on read as zeros, kb is the first.
-template <int ROWS, typename LK, typename LV>
-__device__ __forceinline__ void load_block(Pages& pg, const LK& lk, const LV& lv, int kb, int hi, uint32_t klds, uint32_t vlds) {
-    i32x4 rk, rv;
-    if (pg.row + ROWS <= pg.page_size) {
-        pg.descriptors(0, hi - kb + pg.row, lk, lv, rk, rv);
-#pragma unroll
-        for (int i = 0; i < LK::kLoads; ++i) lk.load(rk, i, pg.row, klds);
-#pragma unroll
-        for (int i = 0; i < LV::kLoads; ++i) lv.load(rv, i, pg.row, vlds);
-        return;
-    }
-    // the tile spans pages: 16 keys at a time, for the loads that lie in them
-#pragma unroll
-    for (int at = 0; at < ROWS; at += 16) {
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < LK::kLoads; ++i) any |= (lk.first_row(i) & ~15) == at;
-#pragma unroll
-        for (int i = 0; i < LV::kLoads; ++i) any |= (lv.first_row(i) & ~15) == at;
-        if (!any) continue;
-        int ahead = 0, row = pg.row + at;
-        while (row >= pg.page_size) {
-            row -= pg.page_size;
-            ++ahead;
+// Descriptors of the ROWS keys at a walk's place, 16 at a time (all in the first one where one page holds
+// them), and the page row of each 16's first key.
+template <int ROWS>
+struct Block {
+    i32x4 k[ROWS / 16], v[ROWS / 16];
+    int row[ROWS / 16];
+    bool one;
+
+    // keys from `hi` on read as zeros, kb is the first
+    template <typename LK, typename LV>
+    __device__ __forceinline__ void find(Pages& pg, const LK& lk, const LV& lv, int kb, int hi) {
+        one = pg.row + ROWS <= pg.page_size;
+        row[0] = pg.row;
+        if (one) {
+            pg.descriptors(0, hi - kb + pg.row, lk, lv, k[0], v[0]);
+            return;
         }
-        pg.descriptors(ahead, hi - kb - at + row, lk, lv, rk, rv);
 #pragma unroll
-        for (int i = 0; i < LK::kLoads; ++i)
-            if ((lk.first_row(i) & ~15) == at) lk.load(rk, i, row - at, klds);
-#pragma unroll
-        for (int i = 0; i < LV::kLoads; ++i)
-            if ((lv.first_row(i) & ~15) == at) lv.load(rv, i, row - at, vlds);
+        for (int g = 0; g < ROWS / 16; ++g) {
+            int ahead = 0;
+            row[g] = pg.row + 16 * g;
+            while (row[g] >= pg.page_size) {
+                row[g] -= pg.page_size;
+                ++ahead;
+            }
+            pg.descriptors(ahead, hi - kb - 16 * g + row[g], lk, lv, k[g], v[g]);
+        }
     }
-}
+    template <typename L>
+    __device__ __forceinline__ void load(const L& l, const i32x4 (&r)[ROWS / 16], uint32_t lds) const {
+        if (one) {
+#pragma unroll
+            for (int i = 0; i < L::kLoads; ++i) l.load(r[0], i, row[0], lds);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < L::kLoads; ++i)
+#pragma unroll
+            for (int g = 0; g < ROWS / 16; ++g)
+                if (l.first_row(i) >> 4 == g) l.load(r[g], i, row[g] - 16 * g, lds);
+    }
+};
 
 // ---- one wave's rows against a block of keys ------------------------------------------------------
 
@@ -338,16 +353,20 @@ struct Wave {
         const int lane = threadIdx.x & 63, h = lane >> 5;
         const int r = t.row0 + row_base + (lane & 31);
         const bool in = r < t.rows;
-        const int tok = in ? r / a.G : 0, hd = in ? r - tok * a.G : 0;
+        int tok, hd;
+        row_of(a, t, row_base + (lane & 31), tok, hd);
         pos = in ? t.kv - t.n + tok : -1;
         pos = pos < -1 ? -1 : pos;
         from = a.window > 0 && pos - a.window > -1 ? (int)(pos - a.window) : -1;
         const int r0 = t.row0 + row_base, r1 = r0 + 31 < t.rows ? r0 + 31 : t.rows - 1;
         live = r0 < t.rows;
-        first = uniform(live ? t.kv - t.n + r0 / a.G : -1);
-        last = uniform(live ? t.kv - t.n + r1 / a.G : -1);
-        const bf16_t* p = static_cast<const bf16_t*>(a.q) + (a.packed ? 0 : t.seq * a.sq.b) + (t.first + tok) * a.sq.t +
-                          ((int64_t)t.head * a.G + hd) * a.sq.h + 8 * h;
+        int ta, tb, ignored;
+        row_of(a, t, row_base, ta, ignored);
+        row_of(a, t, r1 - t.row0, tb, ignored);
+        first = uniform(live ? t.kv - t.n + ta : -1);
+        last = uniform(live ? t.kv - t.n + tb : -1);
+        const bf16_t* p = static_cast<const bf16_t*>(a.q) + (a.packed ? 0 : t.seq * a.sq.b) + (t.first + (in ? tok : 0)) * a.sq.t +
+                          ((int64_t)t.head * a.G + (in ? hd : 0)) * a.sq.h + 8 * h;
 #pragma unroll
         for (int ks = 0; ks < kKS; ++ks) {
             uint4 u = make_uint4(0, 0, 0, 0);
@@ -394,9 +413,10 @@ struct Wave {
                 S.s[mt] = mfma32(read16(kp + (sw ^ (32 * ks)) + mt * 32 * TileK<DK>::kRowBytes), Q[ks], ks ? S.s[mt] : zero);
     }
 
-    template <bool MASKED>
-    __device__ __forceinline__ void softmax(const AttnArgs& a, Scores& S, Probs& P, int kb) {
-        if constexpr (MASKED) {
+    // MASKED: 0 no row is masked, 1 some may be, 2 as `masked` says.
+    template <int MASKED>
+    __device__ __forceinline__ void softmax(const AttnArgs& a, Scores& S, Probs& P, int kb, bool masked = true) {
+        if (MASKED == 1 || (MASKED == 2 && masked)) {
             const uint32_t span = (uint32_t)(pos - from);      // keys from + 1 .. pos are seen
             const uint32_t j0 = (uint32_t)(kb + 4 * (fresh_lane() >> 5) - from - 1);
 #pragma unroll
@@ -464,7 +484,7 @@ struct Wave {
                 if (bad) v = split_bad(v, false);
                 O[dt] = mfma32(v, P.p[s], O[dt]);
             }
-        if (bad) mark_bad(vp, piece, kb);
+        if (bad) mark_bad(vs_, kb);
     }
 
     // scores of one block and values of the one before as one stream of products, each operand read from LDS
@@ -497,7 +517,7 @@ struct Wave {
         }
     }
 
-    // The values alone, where nothing is masked.
+    // The values alone, where nothing has to be left out.
     __device__ __forceinline__ void plain_values(const char* vs_, const Probs& P) {
         const int lane = fresh_lane(), l16 = lane & 15;
         const int vrow = 4 * (lane >> 5) + (l16 >> 2);
@@ -507,18 +527,6 @@ struct Wave {
         for (int s = 0; s < 2 * kMT; ++s)
 #pragma unroll
             for (int dt = 0; dt < kDT; ++dt) O[dt] = mfma32(read_v(vp, piece, s, dt), P.p[s], O[dt]);
-    }
-
-    template <bool MASKED>
-    __device__ __forceinline__ void block(const AttnArgs& a, const char* ks_, const char* vs_, int kb) {
-        Scores S;
-        Probs P;
-        scores(ks_, S);
-        softmax<MASKED>(a, S, P, kb);
-        if constexpr (MASKED)
-            values(a, vs_, P, kb);
-        else
-            plain_values(vs_, P);
     }
 
     __device__ static __forceinline__ bf16x8 read_v(const char* vp, int piece, int s, int dt) {
@@ -557,10 +565,23 @@ struct Wave {
         return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
     }
 
+    // Takes them out of a block that no other wave reads.
+    __device__ static __forceinline__ void clear_bad(char* vs_) {
+        const int lane = fresh_lane();
+#pragma unroll 2
+        for (int i = 0; i < KB * DV * 2 / 1024; ++i) {
+            bf16x8* p = reinterpret_cast<bf16x8*>(vs_ + i * 1024 + lane * 16);
+            *p = split_bad(*p, false);
+        }
+    }
+
     // Counts, for every output, the infinities and NaN among the values that its row sees, and makes those
     // outputs NaN.
-    __device__ __forceinline__ void mark_bad(const char* vp, int piece, int kb) {
-        const int h = fresh_lane() >> 5;
+    __device__ __forceinline__ void mark_bad(const char* vs_, int kb) {
+        const int lane = fresh_lane(), l16 = lane & 15, h = lane >> 5;
+        const int vrow = 4 * h + (l16 >> 2);
+        const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
+        const int piece = (2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ TileV<DV>::f(vrow);
         const uint32_t span = (uint32_t)(pos - from), j0 = (uint32_t)(kb + 4 * h - from - 1);
 #pragma unroll
         for (int dt = 0; dt < kDT; ++dt) {
@@ -605,7 +626,8 @@ struct Wave {
             if (h == 0) *reinterpret_cast<float2*>(p + DV) = make_float2(m, l);
             return;
         }
-        const int tok = r / a.G, hd = r - tok * a.G;
+        int tok, hd;
+        row_of(a, t, row_base + n, tok, hd);
         const int64_t head = (int64_t)t.head * a.G + hd;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : t.seq * a.so.b) + (t.first + tok) * a.so.t + head * a.so.h;
@@ -633,17 +655,25 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, Tile& t) {
     t.n = uniform(p.n);
     t.kv = uniform(p.kv);
     t.rows = t.n * a.G;
-    const int tiles = (int)tiles_of(a, t.n, NARROW);
-    t.head = uniform(p.index % a.Hk);
-    const int rest = uniform(p.index / a.Hk);
+    const int rest = uniform(div_by(p.index, a.mHk));
+    t.head = uniform(p.index - rest * a.Hk);
     t.chunks = uniform(p.chunks);
-    t.chunk = uniform(rest % t.chunks);
-    const int tile = uniform(tiles - 1 - rest / t.chunks);        // the tiles with the most keys first
     constexpr int R = NARROW ? kNarrowRows : kWideRows;
+    int tile = 0;                                   // a narrow tile is its sequence's only one
+    t.chunk = rest;
+    if constexpr (!NARROW) {
+        const int q = uniform(rest / t.chunks);
+        t.chunk = rest - q * t.chunks;
+        tile = tiles_of(a, t.n, false) - 1 - q;     // the tiles with the most keys first
+    }
     t.row0 = tile * R;
+    t.tok0 = NARROW ? 0 : uniform(t.row0 / a.G);
+    t.rem0 = t.row0 - t.tok0 * a.G;
     t.slot = p.slot + ((int64_t)tile * a.Hk + t.head) * t.chunks + t.chunk;
     const int r1 = t.row0 + R < t.rows ? t.row0 + R : t.rows;
-    const int p0 = t.kv - t.n + t.row0 / a.G, p1 = t.kv - t.n + (r1 - 1) / a.G;
+    int tok1, hd1;
+    row_of(a, t, r1 - 1 - t.row0, tok1, hd1);
+    const int p0 = t.kv - t.n + t.tok0, p1 = t.kv - t.n + tok1;
     t.hi = uniform(p1 + 1 > 0 ? p1 + 1 : 0);
     const int64_t w0 = a.window > 0 ? (int64_t)p0 - a.window + 1 : 0;
     t.lo = uniform(w0 > 0 ? (int)w0 : 0);
@@ -699,7 +729,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
         auto ask = [&]() {
             if (asked >= nb) return;
             const uint32_t at = lds + (asked & 3) * (KBYTES + VBYTES);
-            load_block<KB>(pg, lk, lv, from + asked * KB, t.hi, at, at + KBYTES);
+            Block<KB> b;
+            b.find(pg, lk, lv, from + asked * KB, t.hi);
+            b.load(lk, b.k, at);
+            b.load(lv, b.v, at + KBYTES);
             pg.advance(KB);
             ++asked;
         };
@@ -722,41 +755,37 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
         if (second) ask();
         typename W::Scores S;
         typename W::Probs P;
-        even(0);
-        if (second) odd();
-        bool seen = wave.sees(a, from);
-        if (seen) wave.scores(smem[0], S);
-        if (second) even(1); else odd();
-        ask();
-        if (seen) wave.template softmax<true>(a, S, P, from);
-        // blocks that all rows see whole, the one before too, and the others, in loops of their own (the waves
-        // change over at different blocks, but pass the same barriers): O stays in one place through either
-        int i = 1;
-        while (i < nb) {
-            for (; i < nb && !wave.masks(a, from + i * KB) && !wave.masks(a, from + (i - 1) * KB); ++i) {
+        if (second) even(0);
+        bool seen = false;
+        // steps whose blocks i and i - 1 every row sees whole, and the others (the first and the last among them),
+        // in loops of their own (the waves change over at different steps, but pass the same barriers): O stays
+        // in one place through either
+        int i = 0;
+        while (i <= nb) {
+            for (; i > 0 && i < nb && !wave.masks(a, from + i * KB) && !wave.masks(a, from + (i - 1) * KB); ++i) {
                 if (second) odd(); else even(i);
                 wave.scores_values(smem[i & 3], S, smem[(i - 1) & 3] + KBYTES, P);
                 if (second) even(i + 1); else odd();
                 ask();
-                wave.template softmax<false>(a, S, P, 0);
+                wave.template softmax<0>(a, S, P, 0);
                 seen = true;
             }
-            for (; i < nb && (wave.masks(a, from + i * KB) || wave.masks(a, from + (i - 1) * KB)); ++i) {
+            for (; i <= nb && (i == 0 || i == nb || wave.masks(a, from + i * KB) || wave.masks(a, from + (i - 1) * KB)); ++i) {
                 if (second) odd(); else even(i);
                 const int kb = from + i * KB;
-                const bool sees = wave.sees(a, kb);
-                const char* vs = smem[(i - 1) & 3] + KBYTES;
+                const bool sees = i < nb && wave.sees(a, kb);
                 if (sees) wave.scores(smem[i & 3], S);
-                if (seen) wave.values(a, vs, P, kb - KB);
-                if (second) even(i + 1); else odd();
-                ask();
-                if (sees) wave.template softmax<true>(a, S, P, kb);
+                if (seen) wave.values(a, smem[(i - 1) & 3] + KBYTES, P, kb - KB);
+                if (i < nb) {
+                    if (second) even(i + 1); else odd();
+                    ask();
+                    if (sees) wave.template softmax<1>(a, S, P, kb);
+                } else if (!second) {
+                    odd();
+                }
                 seen = sees;
             }
         }
-        if (second) odd(); else even(nb);
-        if (seen) wave.values(a, smem[(nb - 1) & 3] + KBYTES, P, from + (nb - 1) * KB);
-        if (!second) odd();
     }
     wave.finish(a, t, 32 * w, partials(a, false), kWideRows);
 }
@@ -781,23 +810,43 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
     const Loader<TileK<DK>, KB, 1> lk(a.skc, a.page_size, 0);
     const Loader<TileV<DV>, KB, 1> lv(a.svc, a.page_size, 0);
     const uint32_t lds = lds_address(smem[w]);
-    int kb = mine;
-    auto arrive = [&]() {
-        wave_lds_sync();        // the last block's reads are through before the next loads land
-        load_block<KB>(pg, lk, lv, kb, t.hi, lds, lds + KBYTES);
-        pg.advance(KB * kWaves);
-        wait_vm<0>();
+    // A wave's keys of the next block are asked for once its scores are through with LDS, its values once the
+    // products are: one block of LDS a wave, and loads under way all the time.
+    Block<KB> b;
+    if (mine < to) {
+        b.find(pg, lk, lv, mine, t.hi);
+        b.load(lk, b.k, lds);
+        b.load(lv, b.v, lds + KBYTES);
+    }
+#pragma unroll 1
+    for (int kb = mine; kb < to; kb += KB * kWaves) {
+        const bool more = kb + KB * kWaves < to, sees = wave.sees(a, kb), masked = wave.masks(a, kb);
+        typename Wave<DK, DV, KB>::Scores S;
+        typename Wave<DK, DV, KB>::Probs P;
+        wait_vm<Loader<TileV<DV>, KB, 1>::kLoads>();           // the keys; the values may be on their way
+        if (sees) wave.scores(smem[w], S);
         wave_lds_sync();
-    };
-    while (kb < to) {
-        for (; kb < to && !wave.masks(a, kb); kb += KB * kWaves) {
-            arrive();
-            wave.template block<false>(a, smem[w], smem[w] + KBYTES, kb);
+        if (more) {
+            pg.advance(KB * kWaves);
+            b.find(pg, lk, lv, kb + KB * kWaves, t.hi);
+            b.load(lk, b.k, lds);
         }
-        for (; kb < to && wave.masks(a, kb); kb += KB * kWaves) {
-            arrive();
-            if (wave.sees(a, kb)) wave.template block<true>(a, smem[w], smem[w] + KBYTES, kb);
+        if (sees) wave.template softmax<2>(a, S, P, kb, masked);
+        if (more)
+            wait_vm<Loader<TileK<DK>, KB, 1>::kLoads>();
+        else
+            wait_vm<0>();
+        if (sees) {
+            if (masked && wave.bad_values(a, smem[w] + KBYTES, kb)) {
+                wave.mark_bad(smem[w] + KBYTES, kb);
+                wave_lds_sync();
+                wave.clear_bad(smem[w] + KBYTES);
+                wave_lds_sync();
+            }
+            wave.plain_values(smem[w] + KBYTES, P);
         }
+        wave_lds_sync();
+        if (more) b.load(lv, b.v, lds + KBYTES);
     }
     // join the waves: every wave leaves m, l, O in LDS; wave w takes the rows' channels in turn
     lds_barrier();
@@ -848,7 +897,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
             }
             continue;
         }
-        const int tok = r / a.G, hd = r - tok * a.G;
+        int tok, hd;
+        row_of(a, t, r, tok, hd);
         const int64_t head = (int64_t)t.head * a.G + hd;
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : t.seq * a.so.b) + (t.first + tok) * a.so.t + head * a.so.h;
@@ -873,7 +923,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int row
     int all_cuts;
     if (!find_place<NARROW, true>(a, blockIdx.x, p, all_cuts)) return;
     const int rows = p.n * a.G, C = p.chunks;
-    const int head_k = p.index % a.Hk, tile = p.index / a.Hk;
+    const int tile = NARROW ? 0 : div_by(p.index, a.mHk), head_k = p.index - tile * a.Hk;
     const int64_t slot = p.slot + ((int64_t)tile * a.Hk + head_k) * C;
     const int lane = threadIdx.x & 63, g = lane / LPR, ch = lane % LPR;
     const int64_t step = (int64_t)R * (DV + 2);

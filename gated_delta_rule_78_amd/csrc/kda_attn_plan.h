@@ -25,6 +25,20 @@ constexpr int kMinUnits = 1;           // of a chunk
 // Chunks: as many workgroups of a kind as the GPU's 256 CUs hold.
 __host__ __device__ constexpr int64_t target(bool narrow) { return narrow ? 512 : 256; }
 
+// What the kernels divide by, and a window's reach.
+inline uint32_t magic_of(int32_t d) { return d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0; }
+inline void set_divisors(AttnArgs& a) {
+    a.mG = magic_of(a.G);
+    a.mHk = magic_of(a.Hk);
+    for (int k = 0; k < 2; ++k) {
+        const int64_t s = a.window + ((k ? kNarrowRows : kWideRows) + a.G - 1) / a.G + kUnit;
+        a.span[k] = a.window > 0 && s < 0x7fffffff ? (int32_t)s : 0x7fffffff;
+    }
+    a.page_shift = -1;
+    for (int i = 0; i <= 20; ++i)
+        if (a.page_size == 1 << i) a.page_shift = i;
+}
+
 // Workspace: two counts, how many (tile, head)s of either kind are cut (the first workgroup of a kind
 // writes its one), then the partial results, per kind slots_most() of rows x (DV + 2) floats.
 constexpr int64_t kHeadBytes = 256;

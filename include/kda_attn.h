@@ -146,8 +146,8 @@ kda_status kda_kv_append(const kda_kv_append_desc* desc, const void* q, const vo
 
 typedef struct kda_paged_attn_desc {
     int64_t N;            /* sequences, >= 1                                                    */
-    int64_t Hq, Hk;       /* query heads and key heads; Hq a multiple of Hk: query head h reads
-                             key head h / (Hq / Hk)                                             */
+    int64_t Hq, Hk;       /* query heads, up to 512, and key heads; Hq a multiple of Hk: query head
+                             h reads key head h / (Hq / Hk)                                     */
     int64_t T;            /* packed: rows per head; else new tokens per sequence                */
     int64_t dk, dv;       /* 64 or 128 each                                                     */
     int64_t pages;        /* pages of the cache, 1 .. 2^31 - 1                                  */
