@@ -42,10 +42,11 @@ __device__ __forceinline__ float both_sum(float x) {
 // 16 bytes a lane from a raw buffer straight into LDS, to lds + 16 lane. Offsets at or past the
 // descriptor's size store zeros. The compiler does not count these loads: whoever reads the LDS waits
 // with wait_vm first.
-__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t off, uint32_t lds) {
+// The uniform offset `more` is added behind the check.
+__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t off, uint32_t lds, uint32_t more = 0) {
     const i32x4 rsrc = {uniform(r[0]), uniform(r[1]), uniform(r[2]), uniform(r[3])};
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(uniform((int)lds)), "v"(off), "s"(rsrc));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(uniform((int)lds)), "v"(off), "s"(rsrc), "s"(uniform((int)more)));
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -243,7 +244,10 @@ struct Pages {
     template <typename LK, typename LV>
     __device__ __forceinline__ void descriptors(int ahead, int valid, const LK& lk, const LV& lv, i32x4& k, i32x4& v) {
         if (pg + ahead - base >= 64) fetch();
-        const int i = pg + ahead - base;
+        held_descriptors(pg + ahead - base, valid, lk, lv, k, v);
+    }
+    template <typename LK, typename LV>
+    __device__ __forceinline__ void held_descriptors(int i, int valid, const LK& lk, const LV& lv, i32x4& k, i32x4& v) const {
         const bool all = valid >= page_size, none = valid <= 0;
         const int khi_ = __builtin_amdgcn_readlane(khi, i), vhi_ = __builtin_amdgcn_readlane(vhi, i);
         const bool bad = khi_ < 0 || none;
@@ -290,6 +294,12 @@ struct Loader {
     __device__ __forceinline__ void load(i32x4 r, int i, int row, uint32_t lds) const {
         load_to_lds(r, (lane_piece ^ (uint32_t)(16 * L::f(i * kStep))) + lane_row + (uint32_t)(row + i * kStep) * row_bytes,
                     lds + (i * WAVES + w) * 1024);
+    }
+    // The same for a tile whose rows the page holds all, from byte `at` of the head's rows on: nothing to
+    // check but the page itself.
+    __device__ __forceinline__ void load_whole(i32x4 r, int i, uint32_t at, uint32_t lds) const {
+        load_to_lds(r, (lane_piece ^ (uint32_t)(16 * L::f(i * kStep))) + lane_row, lds + (i * WAVES + w) * 1024,
+                    at + i * kStep * row_bytes);
     }
     __device__ __forceinline__ int first_row(int i) const { return i * kStep + w * L::kRows; }
 };
@@ -736,6 +746,25 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
             pg.advance(KB);
             ++asked;
         };
+        // The next block where that takes no branch: whole pages of whole blocks, whose addresses are held.
+        const bool even_pages = a.page_size % KB == 0;
+        auto ask_plain_ok = [&]() {
+            return even_pages && asked < nb && from + (asked + 1) * KB <= t.hi && pg.pg - pg.base < 64;
+        };
+        auto ask_plain = [&]() {
+            const uint32_t at = lds + (asked & 3) * (KBYTES + VBYTES);
+            i32x4 k, v;
+            pg.held_descriptors(pg.pg - pg.base, pg.page_size, lk, lv, k, v);
+            const uint32_t ko = pg.row * lk.row_bytes, vo = pg.row * lv.row_bytes;
+#pragma unroll
+            for (int i = 0; i < LK::kLoads; ++i) lk.load_whole(k, i, ko, at);
+#pragma unroll
+            for (int i = 0; i < LV::kLoads; ++i) lv.load_whole(v, i, vo, at + KBYTES);
+            const bool wrap = pg.row + KB == pg.page_size;
+            pg.row = wrap ? 0 : pg.row + KB;
+            pg.pg += wrap;
+            ++asked;
+        };
         // before phase 2i: this wave's share of block i has landed (block i + 1 may be on its way), then everyone's
         auto even = [&](int i) {
             if (i + 1 < nb)
@@ -760,9 +789,22 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
         // steps whose blocks i and i - 1 every row sees whole, and the others (the first and the last among them),
         // in loops of their own (the waves change over at different steps, but pass the same barriers): O stays
         // in one place through either
+        // blocks plain0 .. plain1 - 1 every row sees whole
+        const int64_t w0 = a.window > 0 ? (int64_t)wave.last - a.window + 1 - from : 0;
+        const int plain0 = uniform(w0 > 0 ? (int)((w0 + KB - 1) / KB) : 0);
+        const int plain1 = uniform(wave.first - KB + 1 >= from ? (wave.first - KB + 1 - from) / KB + 1 : 0);
+        auto plain = [&](int i) { return i > plain0 && i < plain1 && i < nb; };
         int i = 0;
         while (i <= nb) {
-            for (; i > 0 && i < nb && !wave.masks(a, from + i * KB) && !wave.masks(a, from + (i - 1) * KB); ++i) {
+            for (; plain(i) && ask_plain_ok(); ++i) {
+                if (second) odd(); else even(i);
+                wave.scores_values(smem[i & 3], S, smem[(i - 1) & 3] + KBYTES, P);
+                if (second) even(i + 1); else odd();
+                ask_plain();
+                wave.template softmax<0>(a, S, P, 0);
+                seen = true;
+            }
+            for (; plain(i) && !ask_plain_ok(); ++i) {
                 if (second) odd(); else even(i);
                 wave.scores_values(smem[i & 3], S, smem[(i - 1) & 3] + KBYTES, P);
                 if (second) even(i + 1); else odd();
@@ -770,7 +812,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
                 wave.template softmax<0>(a, S, P, 0);
                 seen = true;
             }
-            for (; i <= nb && (i == 0 || i == nb || wave.masks(a, from + i * KB) || wave.masks(a, from + (i - 1) * KB)); ++i) {
+            for (; i <= nb && !plain(i); ++i) {
                 if (second) odd(); else even(i);
                 const int kb = from + i * KB;
                 const bool sees = i < nb && wave.sees(a, kb);
