@@ -24,6 +24,11 @@ Rows rows(const void* p, int64_t B, int64_t H, int64_t T, int64_t d, const kda_r
     return Rows{H > 0 ? p : nullptr, {B, H, T}, {s.b, s.h, s.t}, d, e};
 }
 
+// Kernels take strides of heads and tokens in 32 bits.
+bool strides_fit(const Rows& r) {
+    return r.empty() || ((r.n[1] <= 1 || r.s[1] < (int64_t)1 << 32) && (r.n[2] <= 1 || r.s[2] < (int64_t)1 << 32));
+}
+
 // What norm and rotation need, whoever applies them.
 kda_status check_rotation(int64_t d, int64_t rot, int32_t interleaved, int32_t norm, float eps, float scale) {
     if (d < 2 || (d & 1) || rot < 0 || (rot & 1) || rot > d || !flag(interleaved) || !flag(norm)) return KDA_ERR_INVALID_ARG;
@@ -80,6 +85,8 @@ kda_status kda_head_rope_fwd(const kda_head_rope_desc* d, const void* q, const v
     const Rows oq = rows(q_out, d->B, d->Hq, d->T, d->d, d->q_out, e), ok = rows(k_out, d->B, d->Hk, d->T, d->d, d->k_out, e);
     if (!rows_ok(rq) || !rows_ok(rk) || !rows_ok(oq) || !rows_ok(ok) || !oq.distinct() || !ok.distinct())
         return KDA_ERR_INVALID_ARG;
+    for (const Rows* r : {&rq, &rk, &oq, &ok})
+        if (!strides_fit(*r)) return KDA_ERR_UNSUPPORTED;
     const Range in[] = {rq.range(), rk.range(), range_of(q_weight, q_weight ? w : 0), range_of(k_weight, k_weight ? w : 0),
                         range_of(inv_freq, d->rot * 2), range_of(positions, positions ? d->B * d->T * 4 : 0)};
     const Range out[] = {oq.range(), ok.range()};
@@ -119,6 +126,8 @@ kda_status kda_head_rope_bwd(const kda_head_rope_desc* d, const void* q, const v
     const Rows oq = rows(dq, B, d->Hq, T, d->d, d->dq, e), ok = rows(dk, B, d->Hk, T, d->d, d->dk, e);
     if (!rows_ok(rq) || !rows_ok(rk) || !rows_ok(zq) || !rows_ok(zk) || !rows_ok(oq) || !rows_ok(ok) || (any && (!oq.distinct() || !ok.distinct())))
         return KDA_ERR_INVALID_ARG;
+    for (const Rows* r : {&rq, &rk, &zq, &zk, &oq, &ok})
+        if (!strides_fit(*r)) return KDA_ERR_UNSUPPORTED;
     const Range in[] = {rq.range(), rk.range(), zq.range(), zk.range(), range_of(q_weight, q_weight ? w : 0),
                         range_of(k_weight, k_weight ? w : 0), range_of(inv_freq, d->rot * 2),
                         range_of(positions, positions ? B * T * 4 : 0)};
@@ -159,6 +168,8 @@ kda_status kda_kv_append(const kda_kv_append_desc* d, const void* q, const void*
     for (const Rows* r : {&rq, &rk, &rv, &oq, &kc, &vc})
         if (!rows_ok(*r)) return KDA_ERR_INVALID_ARG;
     if (!oq.distinct() || !kc.distinct() || !vc.distinct()) return KDA_ERR_INVALID_ARG;
+    for (const Rows* r : {&rq, &rk, &rv, &oq})
+        if (!strides_fit(*r)) return KDA_ERR_UNSUPPORTED;
     const Range in[] = {rq.range(), rk.range(), rv.range(), range_of(q_weight, q_weight ? w : 0),
                         range_of(k_weight, k_weight ? w : 0), range_of(inv_freq, d->rot * 2),
                         range_of(cu_seqlens, cu_seqlens ? (d->N + 1) * 4 : 0), range_of(kv_lens, d->N * 4),

@@ -8,8 +8,9 @@
  *
  *  - Heads' rows have the core's shapes, [B,H,T,d] or packed [H,T,d], with the strides the caller
  *    gives: slices of one projection's output [T, (Hq + 2 Hk) d] are read where they are. The last
- *    dimension is contiguous. Strides are in elements and not negative; an input's may be 0 (a
- *    tensor expanded along that dimension), an output's rows must not share elements.
+ *    dimension is contiguous. Strides are in elements and not negative, those of heads and tokens
+ *    below 2^32; an input's may be 0 (a tensor expanded along that dimension), an output's rows
+ *    must not share elements.
  *  - Bases are aligned to their element unless a call says more; rows on 16 bytes take wide accesses.
  *  - No output may overlap an input or another output, taken as the ranges from a tensor's first
  *    element to its last (k_cache and v_cache may interleave in one buffer).
