@@ -923,9 +923,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
             const float* src = reinterpret_cast<const float*>(smem[i]) + r * (DV + 2);
-            const float f = mw[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw[i] - mm);
-            if (mw[i] == -INFINITY) continue;      // saw nothing: its O is 0
-            ll = fmaf(f, src[DV + 1], ll);
+            const float lw = src[DV + 1], f = __builtin_amdgcn_exp2f(mw[i] - mm);
+            if (lw == 0.f) continue;               // saw nothing: its O is 0
+            ll = fmaf(f, lw, ll);
 #pragma unroll
             for (int k = 0; k < DV / 64; ++k) acc[k] = fmaf(f, src[lane + 64 * k], acc[k]);
         }
@@ -981,8 +981,8 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int row
             float f = 0.f;
             if (c0 + lane < C) {
                 const float2 ml = *reinterpret_cast<const float2*>(base + (c0 + lane) * step + DV);
-                f = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - mm);
-                if (ml.x != -INFINITY) ll = fmaf(f, ml.y, ll);
+                f = ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - mm);      // a sum of 0: saw no key
+                ll = fmaf(f, ml.y, ll);
             }
             const int left = C - c0 < 64 ? C - c0 : 64;
             for (int b = 0; b < left; b += 8 * NG) {      // 8 loads in flight; past the last chunk weights of 0

@@ -342,3 +342,41 @@ def test_streams_of_another_device_are_refused():
     x = make(c)
     with pytest.raises(ValueError, match="stream is on"):
         call(c, x, stream=Other())
+
+
+@pytest.mark.parametrize("c", [
+    ([1], [40], 4, 2, 128, 128, 16, 0, False),          # one chunk
+    ([1], [6000], 2, 1, 64, 64, 16, 0, False),          # many chunks of a narrow tile, more than a wave joins
+    ([1, 1, 1], [900, 64, 1], 4, 2, 128, 64, 16, 64, False),
+    ([40, 1, 20], [3000, 500, 3], 8, 2, 64, 128, 64, 0, True),
+    ([150], [20000], 2, 1, 128, 128, 512, 0, False),    # many chunks of a wide tile
+])
+def test_nan_queries(c):
+    """A query that holds a NaN has NaN outputs, also where every score of a wave's keys is one; no other row is
+    touched."""
+    x = make(c)
+    clean, clean_l = call(c, x)
+    q = x["q"].clone()
+    q[..., 1, -1, 5] = float("nan")             # head 1, the last token (of every sequence, or of the last one)
+    if not c[8]:
+        q[0, 0, 0, 0] = float("nan")
+    o, lse = call(c, dict(x, q=q))
+    hit = torch.isnan(q).any(-1)
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_l[~hit])
+    check(c, x, clean, clean_l)
+
+
+@pytest.mark.parametrize("c", [
+    ([1], [50000], 16, 1, 64, 64, 16, 0, False),
+    ([2, 1, 1], [30000, 100, 0], 4, 2, 64, 128, 64, 0, True),
+    ([1, 1], [20000, 15], 8, 1, 128, 64, 16, 0, False),
+    ([300, 30, 5], [9000, 10, 200], 2, 1, 128, 128, 64, 0, True),
+    ([520, 3], [1500, 0], 3, 3, 64, 64, 32, 0, True),
+])
+def test_long_caches_cut_into_many_chunks(c):
+    x = make(c)
+    o, lse = call(c, x)
+    check(c, x, o, lse)
+    a, al = call(c, x)
+    assert torch.equal(a, o) and torch.equal(al, lse)
