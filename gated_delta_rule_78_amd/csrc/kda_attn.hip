@@ -20,13 +20,10 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
         if (!(narrow ? has_narrow(a) : has_wide(a))) continue;
         e = launch_main<DK, DV>(a, narrow, groups_most(a, narrow), st);
         if (e != hipSuccess || !may_cut(a)) continue;
-        const int64_t all = a.T * a.G, most = narrow ? kNarrowRows : kWideRows;
-        const int rows = (int)(all < most ? all : most), each = narrow ? 4 : 16;
-        const dim3 grid((unsigned)target(narrow), (unsigned)((rows + each - 1) / each));
         if (narrow)
-            hipLaunchKernelGGL((attn_join_kernel<DV, true>), grid, dim3(kThreads), 0, st, a, each);
+            hipLaunchKernelGGL((attn_join_kernel<DV, true>), dim3(kJoinGroups), dim3(kJoinThreads), 0, st, a);
         else
-            hipLaunchKernelGGL((attn_join_kernel<DV, false>), grid, dim3(kThreads), 0, st, a, each);
+            hipLaunchKernelGGL((attn_join_kernel<DV, false>), dim3(kJoinGroups), dim3(kJoinThreads), 0, st, a);
         e = hipGetLastError();
     }
     return e;

@@ -60,8 +60,6 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 __device__ __forceinline__ int div_by(int n, uint32_t magic) { return magic ? (int)__umulhi((uint32_t)n, magic) : n; }
 
 // One tile's place: which sequence, rows and keys.
-struct Tile;
-__device__ __forceinline__ void row_of(const AttnArgs& a, const Tile& t, int r, int& tok, int& hd);
 struct Tile {
     int64_t seq, first;     // sequence, first token of it in the rows' T (packed) or 0
     int n, kv;              // its new tokens, its keys
@@ -954,70 +952,114 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
 
 // ---- the chunks of cut tiles joined ---------------------------------------------------------------
 
-// Workgroup x: the x-th (tile, head) that is cut; y: a run of its rows, a wave a row. A lane holds 4
-// channels, so that a wave reads several chunks at a time.
+// kJoinGroups workgroups share out the rows of all cut (tile, head)s: a wave a row or, where a row has more
+// chunks than a wave keeps loads under way for, a workgroup a row. A lane holds 4 channels, so that a wave
+// reads kJoinAhead * (256 / DV) chunks at a time.
+constexpr int kJoinAhead = 8;
+
+// Chunks [c0, c1) of a row: their reference, sum and this lane's channels, the same in all lanes that hold them.
+template <int DV>
+__device__ __forceinline__ void join_chunks(const float* base, int64_t step, int c0, int c1, float& mm, float& ll, float4& acc) {
+    constexpr int LPR = DV / 4, NG = 64 / LPR, AT = kJoinAhead * NG;
+    const int lane = threadIdx.x & 63, g = lane / LPR, ch = lane % LPR;
+    mm = -INFINITY;
+    ll = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (; c0 < c1; c0 += AT) {
+        const int left = c1 - c0;
+        float2 ml = make_float2(-INFINITY, 0.f), u[kJoinAhead], v[kJoinAhead];
+        if (lane < AT && lane < left) ml = *reinterpret_cast<const float2*>(base + (c0 + lane) * step + DV);
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {      // past the last chunk weights of 0
+            const int c = k * NG + g;
+            const float2* q = reinterpret_cast<const float2*>(base + (c0 + (c < left ? c : left - 1)) * step + 4 * ch);
+            u[k] = q[0];
+            v[k] = q[1];
+        }
+        float top = fmaxf(ml.x, mm);
+#pragma unroll
+        for (int k = 1; k < 64; k <<= 1) top = fmaxf(top, __shfl_xor(top, k));
+        const float old = mm == top ? 1.f : __builtin_amdgcn_exp2f(mm - top);
+        mm = top;
+        const float f = ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);     // a sum of 0: saw no key
+        ll = fmaf(ll, old, f * ml.y);
+        acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const int c = k * NG + g;
+            const float wf = __shfl(f, c);
+            if (c < left) {
+                acc.x = fmaf(wf, u[k].x, acc.x); acc.y = fmaf(wf, u[k].y, acc.y);
+                acc.z = fmaf(wf, v[k].x, acc.z); acc.w = fmaf(wf, v[k].y, acc.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) ll += __shfl_xor(ll, k);
+#pragma unroll
+    for (int k = LPR; k < 64; k <<= 1) {
+        acc.x += __shfl_xor(acc.x, k); acc.y += __shfl_xor(acc.y, k);
+        acc.z += __shfl_xor(acc.z, k); acc.w += __shfl_xor(acc.w, k);
+    }
+}
+
 template <int DV, bool NARROW>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, int rows_each) {
-    constexpr int R = NARROW ? kNarrowRows : kWideRows;
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
+    constexpr int R = NARROW ? kNarrowRows : kWideRows, NW = kJoinThreads / 64;
     constexpr int LPR = DV / 4, NG = 64 / LPR;
-    if ((int)blockIdx.x >= static_cast<const int*>(a.ws)[NARROW ? 0 : 1]) return;
+    __shared__ __align__(16) float all[NW][DV + 4];
+    const int cuts = static_cast<const int*>(a.ws)[NARROW ? 0 : 1];
+    if (cuts <= 0) return;
+    const int share = uniform(kJoinGroups / cuts > 0 ? kJoinGroups / cuts : 1), cut = uniform(blockIdx.x / share);   // workgroups of a cut
+    const int part = blockIdx.x - cut * share;
     Place p;
     int all_cuts;
-    if (!find_place<NARROW, true>(a, blockIdx.x, p, all_cuts)) return;
-    const int rows = p.n * a.G, C = p.chunks;
-    const int tile = NARROW ? 0 : div_by(p.index, a.mHk), head_k = p.index - tile * a.Hk;
-    const int64_t slot = p.slot + ((int64_t)tile * a.Hk + head_k) * C;
-    const int lane = threadIdx.x & 63, g = lane / LPR, ch = lane % LPR;
-    const int64_t step = (int64_t)R * (DV + 2);
-    const int y0 = blockIdx.y * rows_each, y1 = y0 + rows_each < R ? y0 + rows_each : R;
-    for (int rr = y0 + uniform(threadIdx.x >> 6); rr < y1 && tile * R + rr < rows; rr += kWaves) {
-        const float* base = partials(a, NARROW) + (slot * R + rr) * (DV + 2);
-        float mm = -INFINITY, ll = 0.f;
-        for (int c = lane; c < C; c += 64) mm = fmaxf(mm, base[c * step + DV]);
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) mm = fmaxf(mm, __shfl_xor(mm, k));
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = 0; c0 < C; c0 += 64) {
-            float f = 0.f;
-            if (c0 + lane < C) {
-                const float2 ml = *reinterpret_cast<const float2*>(base + (c0 + lane) * step + DV);
-                f = ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - mm);      // a sum of 0: saw no key
-                ll = fmaf(f, ml.y, ll);
+    if (cut >= cuts || !find_place<NARROW, true>(a, cut, p, all_cuts)) return;
+    const int C = p.chunks, tile = NARROW ? 0 : div_by(p.index, a.mHk), head_k = p.index - tile * a.Hk;
+    const int rows = p.n * a.G - tile * R < R ? p.n * a.G - tile * R : R;
+    const int64_t slot = p.slot + ((int64_t)tile * a.Hk + head_k) * C, step = (int64_t)R * (DV + 2);
+    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+    const bool shared = C > kJoinAhead * NG;
+    const int per = shared ? uniform((C + NW - 1) / NW) : C, c0 = shared ? w * per : 0, c1 = c0 + per < C ? c0 + per : C;
+    for (int rr = shared ? part : part * NW + w; rr < rows; rr += shared ? share : share * NW) {
+        float mm, ll;
+        float4 acc;
+        join_chunks<DV>(partials(a, NARROW) + (slot * R + rr) * (DV + 2), step, c0, c1, mm, ll, acc);
+        if (shared) {
+            __syncthreads();
+            if (lane < LPR) *reinterpret_cast<float4*>(&all[w][4 * lane]) = acc;
+            if (lane == 0) {
+                all[w][DV] = mm;
+                all[w][DV + 1] = ll;
             }
-            const int left = C - c0 < 64 ? C - c0 : 64;
-            for (int b = 0; b < left; b += 8 * NG) {      // 8 loads in flight; past the last chunk weights of 0
-                float wf[8];
-                float2 u[8], v[8];
+            __syncthreads();
+            if (w > 0) continue;
+            const float mw = all[lane % NW][DV];
+            ll = all[lane % NW][DV + 1];
+            mm = mw;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int c = b + k * NG + g;
-                    wf[k] = __shfl(f, c & 63);
-                    wf[k] = c < left ? wf[k] : 0.f;
-                    const float2* q = reinterpret_cast<const float2*>(base + (c0 + (c < left ? c : left - 1)) * step + 4 * ch);
-                    u[k] = q[0];
-                    v[k] = q[1];
-                }
+            for (int k = 1; k < NW; k <<= 1) mm = fmaxf(mm, __shfl_xor(mm, k));
+            const float f = ll == 0.f ? 0.f : __builtin_amdgcn_exp2f(mw - mm);
+            ll *= f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    acc.x = fmaf(wf[k], u[k].x, acc.x); acc.y = fmaf(wf[k], u[k].y, acc.y);
-                    acc.z = fmaf(wf[k], v[k].x, acc.z); acc.w = fmaf(wf[k], v[k].y, acc.w);
-                }
+            for (int k = 1; k < NW; k <<= 1) ll += __shfl_xor(ll, k);
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                const float wf = __shfl(f, i);
+                const float4 x = *reinterpret_cast<const float4*>(&all[i][4 * (lane % LPR)]);
+                acc.x = fmaf(wf, x.x, acc.x); acc.y = fmaf(wf, x.y, acc.y);
+                acc.z = fmaf(wf, x.z, acc.z); acc.w = fmaf(wf, x.w, acc.w);
             }
         }
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) ll += __shfl_xor(ll, k);
-#pragma unroll
-        for (int k = LPR; k < 64; k <<= 1) {
-            acc.x += __shfl_xor(acc.x, k); acc.y += __shfl_xor(acc.y, k);
-            acc.z += __shfl_xor(acc.z, k); acc.w += __shfl_xor(acc.w, k);
-        }
-        if (g == 0) {
+        if (lane < LPR) {
             const int r = tile * R + rr, tok = r / a.G, hd = r - tok * a.G;
             const int64_t head = (int64_t)head_k * a.G + hd;
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
             bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : p.seq * a.so.b) + (p.first + tok) * a.so.t + head * a.so.h;
-            store4(o + 4 * ch, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (a.lse && ch == 0)
+            store4(o + 4 * lane, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (a.lse && lane == 0)
                 a.lse[(a.packed ? 0 : p.seq * a.Hq * a.T) + head * a.T + p.first + tok] =
                     ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
         }

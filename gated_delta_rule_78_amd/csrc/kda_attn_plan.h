@@ -19,6 +19,7 @@ namespace attn {
 
 constexpr int kThreads = 256, kWaves = 4;          // narrow tiles
 constexpr int kWideThreads = 512, kWideWaves = 8;  // wide tiles
+constexpr int kJoinThreads = 512, kJoinGroups = 1024;   // at least the (tile, head)s that can be cut
 constexpr int kNarrowRows = 32, kWideRows = 256;
 constexpr int kUnit = 128;             // keys: what L counts in
 constexpr int kMinUnits = 1;           // of a chunk
