@@ -102,8 +102,8 @@ __device__ __forceinline__ int tile_units(const AttnArgs& a, int kv, bool narrow
 
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, bool narrow) {
     const uint32_t rows = (uint32_t)n * (uint32_t)a.G;
-    if (rows <= kNarrowRows) return narrow ? 1 : 0;
-    return narrow ? 0 : (int)((rows + kWideRows - 1) / kWideRows);
+    const uint32_t each = narrow ? kNarrowRows : kWideRows;
+    return (rows <= (uint32_t)narrow_most(a)) == narrow ? (int)((rows + each - 1) / each) : 0;
 }
 
 // ---- which sequence, tile and chunk a workgroup has ------------------------------------------------
@@ -667,15 +667,10 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, Tile& t) {
     t.head = uniform(p.index - rest * a.Hk);
     t.chunks = uniform(p.chunks);
     constexpr int R = NARROW ? kNarrowRows : kWideRows;
-    int tile = 0;                                   // a narrow tile is its sequence's only one
-    t.chunk = rest;
-    if constexpr (!NARROW) {
-        const int q = uniform(rest / t.chunks);
-        t.chunk = rest - q * t.chunks;
-        tile = tiles_of(a, t.n, false) - 1 - q;     // the tiles with the most keys first
-    }
+    const int q = uniform(rest / t.chunks), tile = tiles_of(a, t.n, NARROW) - 1 - q;     // the tiles with the most keys first
+    t.chunk = rest - q * t.chunks;
     t.row0 = tile * R;
-    t.tok0 = NARROW ? 0 : uniform(t.row0 / a.G);
+    t.tok0 = uniform(t.row0 / a.G);
     t.rem0 = t.row0 - t.tok0 * a.G;
     t.slot = p.slot + ((int64_t)tile * a.Hk + t.head) * t.chunks + t.chunk;
     const int r1 = t.row0 + R < t.rows ? t.row0 + R : t.rows;
@@ -906,7 +901,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
     }
     lds_barrier();
     float* part = partials(a, true);
-    const int rows = t.rows < kNarrowRows ? t.rows : kNarrowRows;
+    const int rows = t.rows - t.row0 < kNarrowRows ? t.rows - t.row0 : kNarrowRows;
     for (int r = w; r < rows; r += kWaves) {
         const int lane = threadIdx.x & 63;
         float mw[kWaves], mm = -INFINITY;
@@ -1016,7 +1011,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     Place p;
     int all_cuts;
     if (cut >= cuts || !find_place<NARROW, true>(a, cut, p, all_cuts)) return;
-    const int C = p.chunks, tile = NARROW ? 0 : div_by(p.index, a.mHk), head_k = p.index - tile * a.Hk;
+    const int C = p.chunks, tile = div_by(p.index, a.mHk), head_k = p.index - tile * a.Hk;
     const int rows = p.n * a.G - tile * R < R ? p.n * a.G - tile * R : R;
     const int64_t slot = p.slot + ((int64_t)tile * a.Hk + head_k) * C, step = (int64_t)R * (DV + 2);
     const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);

@@ -2,7 +2,7 @@
 //
 // The G query heads of a key head are rows of one matrix: row r of a sequence is token r / G, head
 // r % G of the group, so that all of them read each key once. A sequence's rows make tiles, narrow
-// ones where it has at most kNarrowRows rows (the waves of a workgroup then share out the keys), wide
+// ones where it has at most narrow_most() rows (the waves of a workgroup then share out the keys), wide
 // ones else (the waves share out the rows). A tile's keys are cut into C chunks, C the same for every
 // tile of a sequence: ceil(keys / L), L such that the keys of all tiles make about target() chunks.
 // Chunks of a cut tile leave their sums in the workspace and a second launch joins them. Every wave
@@ -40,20 +40,26 @@ inline void set_divisors(AttnArgs& a) {
         if (a.page_size == 1 << i) a.page_shift = i;
 }
 
+// Rows of a sequence that make narrow tiles. Heads of 64: up to 128, each tile reading the keys again (out of
+// L2; 32 sequences of 64, 96, 128 rows over 8000 keys: 56, 70, 84 us against 79, 85, 88 with wide tiles). Larger
+// heads: one tile's (64, 128 rows in narrow tiles: 115, 180 us against 111, 123).
+__host__ __device__ inline int narrow_most(const AttnArgs& a) { return a.dk + a.dv <= 128 ? 128 : kNarrowRows; }
+
 // Workspace: two counts, how many (tile, head)s of either kind are cut (the first workgroup of a kind
 // writes its one), then the partial results, per kind slots_most() of rows x (DV + 2) floats.
 constexpr int64_t kHeadBytes = 256;
 __host__ __device__ inline int64_t tiles_most(const AttnArgs& a, int rows, bool narrow) {
     const int64_t all = (a.packed ? a.T : a.N * a.T) * a.G, seqs = a.packed && a.T < a.N ? a.T : a.N;
-    return narrow ? seqs : all / rows + seqs;
+    const int64_t most = all / rows + seqs, each = narrow_most(a) / kNarrowRows * seqs;
+    return narrow && each < most ? each : most;
 }
 // cut chunks: ceil(k / L) <= 2 k / L of each tile with k > L
 __host__ __device__ inline int64_t slots_most(bool narrow) { return 2 * target(narrow); }
 __host__ __device__ inline int64_t partial_bytes(int rows, int dv) { return (int64_t)rows * (dv + 2) * 4; }
 
 // Which kinds a call can hold, from what the host knows.
-__host__ __device__ inline bool has_narrow(const AttnArgs& a) { return a.packed || a.T * a.G <= kNarrowRows; }
-__host__ __device__ inline bool has_wide(const AttnArgs& a) { return a.T * a.G > kNarrowRows; }
+__host__ __device__ inline bool has_narrow(const AttnArgs& a) { return a.packed || a.T * a.G <= narrow_most(a); }
+__host__ __device__ inline bool has_wide(const AttnArgs& a) { return a.T * a.G > narrow_most(a); }
 // No tile has more keys than the table holds: none is cut when a chunk takes them all.
 __host__ __device__ inline bool may_cut(const AttnArgs& a) { return (int64_t)a.max_pages * a.page_size > kUnit * kMinUnits; }
 

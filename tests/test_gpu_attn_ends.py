@@ -380,3 +380,15 @@ def test_long_caches_cut_into_many_chunks(c):
     check(c, x, o, lse)
     a, al = call(c, x)
     assert torch.equal(a, o) and torch.equal(al, lse)
+
+
+@pytest.mark.parametrize("c", [
+    ([33, 128, 129, 64, 32, 1], [0, 70, 300, 2000, 9000, 128], 2, 2, 64, 64, 16, 0, True),
+    ([16, 9, 5], [4000, 100, 0], 8, 1, 64, 64, 64, 0, True),
+    ([12] * 3, [1500, 31, 700], 10, 1, 64, 64, 32, 40, False),
+    ([43], [9000], 3, 1, 64, 64, 16, 0, False),
+])
+def test_heads_of_64_around_the_widths_of_tiles(c):
+    x = make(c)
+    o, lse = call(c, x)
+    check(c, x, o, lse)
