@@ -153,7 +153,8 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
     }
     // chunk length; the sum's rounding may not make it too small: chunks would pass the workspace's slots
     units = lane_value(wave_prefix_sum(units), 63) * 1.01f;
-    const float inv = 1.f / fminf(fmaxf(ceilf(units / (float)target(NARROW)), (float)kMinUnits), 16777216.f);
+    const float share = units * (1.f / (float)target(NARROW)), whole = fminf(whole_units(share), kWholeMost);
+    const float inv = 1.f / fminf(fmaxf(ceilf(share), 1.f), 16777216.f);
     Counts base = {0, 0, 0};
     int lo = 0, left = N;
     for (bool held = k == 1;; held = false) {
@@ -165,7 +166,8 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
             if (!held) sequence(a, s, first, n, kv);
             if (n <= 0) continue;
             const int tiles = tiles_of(a, n, NARROW) * a.Hk;
-            chunks = (int)fmaxf(ceilf((float)tile_units(a, kv, NARROW) * inv - 0.001f), 1.f);
+            const float most = (float)tile_units(a, kv, NARROW);
+            chunks = most <= whole ? 1 : (int)fmaxf(ceilf(most * inv - 0.001f), 1.f);
             c.items += tiles * chunks;
             if (chunks > 1) {
                 c.slots += tiles * chunks;

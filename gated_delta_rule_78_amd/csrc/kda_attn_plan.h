@@ -22,7 +22,13 @@ constexpr int kWideThreads = 512, kWideWaves = 8;  // wide tiles
 constexpr int kJoinThreads = 512, kJoinGroups = 1024;   // at least the (tile, head)s that can be cut
 constexpr int kNarrowRows = 32, kWideRows = 256;
 constexpr int kUnit = 128;             // keys: what L counts in
-constexpr int kMinUnits = 1;           // of a chunk
+// A tile of at most so many units is not cut, where a chunk's even share of all the work is `share` units: with
+// little to do the saved keys outweigh the join early, with more the chunks of cut tiles no longer run at once.
+// Whole against cut, heads of 128, us: share 0.1, 5 units 13.4 : 12.4 (narrow), 6 units 29.9 : 24.3 (wide); 0.5,
+// 4 units 26.7 : 28.5 (wide), 9 units 20 : 17; 2.3, 9 units 20.5 : 25.1; 3.5, 6 units 40 : 52 (wide); 3.8, 15
+// units 28.7 : 32.0.
+constexpr float kWholeLeast = 3.f, kWholeMost = 16.f;
+__host__ __device__ constexpr float whole_units(float share) { return kWholeLeast + 4.f * share; }
 // Chunks: as many workgroups of a kind as the GPU's 256 CUs hold.
 __host__ __device__ constexpr int64_t target(bool narrow) { return narrow ? 512 : 256; }
 
@@ -61,7 +67,7 @@ __host__ __device__ inline int64_t partial_bytes(int rows, int dv) { return (int
 __host__ __device__ inline bool has_narrow(const AttnArgs& a) { return a.packed || a.T * a.G <= narrow_most(a); }
 __host__ __device__ inline bool has_wide(const AttnArgs& a) { return a.T * a.G > narrow_most(a); }
 // No tile has more keys than the table holds: none is cut when a chunk takes them all.
-__host__ __device__ inline bool may_cut(const AttnArgs& a) { return (int64_t)a.max_pages * a.page_size > kUnit * kMinUnits; }
+__host__ __device__ inline bool may_cut(const AttnArgs& a) { return (int64_t)a.max_pages * a.page_size > (int64_t)(kUnit * kWholeLeast); }
 
 }  // namespace attn
 }  // namespace kda
