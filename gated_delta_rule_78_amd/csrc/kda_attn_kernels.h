@@ -143,18 +143,17 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
     const int lane = threadIdx.x & 63, N = (int)a.N;
     int64_t first = 0;
     int n = 0, kv = 0, k = (N + 63) / 64;
-    float units = 0.f;
-    if (k == 1) {
-        if (lane < N && sequence(a, lane, first, n, kv))
-            units = (float)(tiles_of(a, n, NARROW) * a.Hk) * (float)tile_units(a, kv, NARROW);
-    } else {
-        for (int s = lane * k; s < N && s < (lane + 1) * k; ++s)
-            if (sequence(a, s, first, n, kv)) units += (float)(tiles_of(a, n, NARROW) * a.Hk) * (float)tile_units(a, kv, NARROW);
-    }
+    float tiles = 0.f, units = 0.f;
+    for (int s = lane * k; s < N && s < (lane + 1) * k; ++s)
+        if (sequence(a, s, first, n, kv)) {
+            const float t = (float)(tiles_of(a, n, NARROW) * a.Hk);
+            tiles += t;
+            units = fmaf(t, (float)tile_units(a, kv, NARROW), units);
+        }
     // chunk length; the sum's rounding may not make it too small: chunks would pass the workspace's slots
     units = lane_value(wave_prefix_sum(units), 63) * 1.01f;
-    const float share = units * (1.f / (float)target(NARROW)), whole = fminf(whole_units(share), kWholeMost);
-    const float inv = 1.f / fminf(fmaxf(ceilf(share), 1.f), 16777216.f);
+    const float whole = fminf(whole_units(lane_value(wave_prefix_sum(tiles), 63)), kWholeMost);
+    const float inv = 1.f / fminf(fmaxf(ceilf(units / (float)target(NARROW)), 1.f), 16777216.f);
     Counts base = {0, 0, 0};
     int lo = 0, left = N;
     for (bool held = k == 1;; held = false) {

@@ -22,13 +22,13 @@ constexpr int kWideThreads = 512, kWideWaves = 8;  // wide tiles
 constexpr int kJoinThreads = 512, kJoinGroups = 1024;   // at least the (tile, head)s that can be cut
 constexpr int kNarrowRows = 32, kWideRows = 256;
 constexpr int kUnit = 128;             // keys: what L counts in
-// A tile of at most so many units is not cut, where a chunk's even share of all the work is `share` units: with
-// little to do the saved keys outweigh the join early, with more the chunks of cut tiles no longer run at once.
-// Whole against cut, heads of 128, us: share 0.1, 5 units 13.4 : 12.4 (narrow), 6 units 29.9 : 24.3 (wide); 0.5,
-// 4 units 26.7 : 28.5 (wide), 9 units 20 : 17; 2.3, 9 units 20.5 : 25.1; 3.5, 6 units 40 : 52 (wide); 3.8, 15
-// units 28.7 : 32.0.
+// A tile of at most so many units is not cut, of `tiles` (tile, head)s in all: with few of them the keys that
+// each chunk saves outweigh the partial results and the join early, with more the chunks of cut tiles no longer
+// run at once. Whole against cut, heads of 128, us: 8 tiles of 5 units 13.4 : 12.4 (narrow), 6 units 29.9 : 24.3
+// (wide); 32 tiles, 4 units 26.7 : 28.5 (wide), 9 units 20 : 17, 10 units 43 : 32 (wide); 128 tiles, 9 units
+// 20.5 : 25.1, 15 units 28.1 : 31.9, 10 units 44 : 50 (wide), 16 units 64 : 62 (wide).
 constexpr float kWholeLeast = 3.f, kWholeMost = 16.f;
-__host__ __device__ constexpr float whole_units(float share) { return kWholeLeast + 4.f * share; }
+__host__ __device__ constexpr float whole_units(float tiles) { return kWholeLeast + (3.f / 32.f) * tiles; }
 // Chunks: as many workgroups of a kind as the GPU's 256 CUs hold.
 __host__ __device__ constexpr int64_t target(bool narrow) { return narrow ? 512 : 256; }
 
