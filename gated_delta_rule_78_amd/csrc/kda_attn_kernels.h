@@ -277,7 +277,7 @@ struct Loader {
     static constexpr int kLoads = ROWS / (L::kRows * WAVES), kStep = L::kRows * WAVES, kRowBytes = L::kRowBytes;
     uint32_t row_bytes;
     int full;               // bytes from a page's first row of the head to behind its last
-    uint32_t lane_row, lane_piece;      // offsets of this lane's row and piece in the first load
+    uint32_t lane_row, lane_piece;      // this lane's row's offset within a load's, its piece's in the first load
     int w;
 
     __device__ __forceinline__ Loader(const kda_page_strides& st, int page_size, int wave) {
@@ -285,20 +285,19 @@ struct Loader {
         full = (page_size - 1) * (int)row_bytes + kRowBytes;
         w = wave;
         const int lane = threadIdx.x & 63, lr = lane / L::kPieces;
-        lane_row = (uint32_t)(w * L::kRows + lr) * row_bytes;
+        lane_row = (uint32_t)lr * row_bytes;
         lane_piece = 16 * ((lane % L::kPieces) ^ L::f(w * L::kRows) ^ L::f(lr));
     }
     // Load i from the page of descriptor r whose row `row` is the tile's row 0. The piece permutation
     // differs from the first load's by a constant.
     __device__ __forceinline__ void load(i32x4 r, int i, int row, uint32_t lds) const {
-        load_to_lds(r, (lane_piece ^ (uint32_t)(16 * L::f(i * kStep))) + lane_row + (uint32_t)(row + i * kStep) * row_bytes,
+        load_to_lds(r, (lane_piece ^ (uint32_t)(16 * L::f(i * kStep))) + lane_row + (uint32_t)(row + first_row(i)) * row_bytes,
                     lds + (i * WAVES + w) * 1024);
     }
-    // The same for a tile whose rows the page holds all, from byte `at` of the head's rows on: nothing to
-    // check but the page itself.
-    __device__ __forceinline__ void load_whole(i32x4 r, int i, uint32_t at, uint32_t lds) const {
+    // The same where the page holds all of this load's rows, `row` its first: nothing to check but the page.
+    __device__ __forceinline__ void load_whole(i32x4 r, int i, int row, uint32_t lds) const {
         load_to_lds(r, (lane_piece ^ (uint32_t)(16 * L::f(i * kStep))) + lane_row, lds + (i * WAVES + w) * 1024,
-                    at + i * kStep * row_bytes);
+                    (uint32_t)row * row_bytes);
     }
     __device__ __forceinline__ int first_row(int i) const { return i * kStep + w * L::kRows; }
 };
@@ -740,23 +739,33 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
             pg.advance(KB);
             ++asked;
         };
-        // The next block where that takes no branch: whole pages of whole blocks, whose addresses are held.
-        const bool even_pages = a.page_size % KB == 0;
+        // The next block where that takes no branch: pages of a power of two rows, whose addresses are held. Each
+        // load's rows are in one page.
         auto ask_plain_ok = [&]() {
-            return even_pages && asked < nb && from + (asked + 1) * KB <= t.hi && pg.pg - pg.base < 64;
+            const int end = from + (asked + 1) * KB;
+            return a.page_shift >= 0 && asked < nb && end <= t.hi && ((end - 1) >> a.page_shift) - pg.base < 64;
         };
         auto ask_plain = [&]() {
             const uint32_t at = lds + (asked & 3) * (KBYTES + VBYTES);
+            const int kb = from + asked * KB, mask = pg.page_size - 1;
             i32x4 k, v;
-            pg.held_descriptors(pg.pg - pg.base, pg.page_size, lk, lv, k, v);
-            const uint32_t ko = pg.row * lk.row_bytes, vo = pg.row * lv.row_bytes;
 #pragma unroll
-            for (int i = 0; i < LK::kLoads; ++i) lk.load_whole(k, i, ko, at);
+            for (int i = 0; i < LK::kLoads; ++i) {
+                const int key = kb + lk.first_row(i);
+                if (i == 0 || a.page_shift < 6)      // a page of 64 rows holds the block
+                    pg.held_descriptors((key >> a.page_shift) - pg.base, pg.page_size, lk, lv, k, v);
+                lk.load_whole(k, i, key & mask, at);
+                if (LK::kLoads == LV::kLoads) lv.load_whole(v, i, key & mask, at + KBYTES);
+            }
+            if (LK::kLoads != LV::kLoads)
 #pragma unroll
-            for (int i = 0; i < LV::kLoads; ++i) lv.load_whole(v, i, vo, at + KBYTES);
-            const bool wrap = pg.row + KB == pg.page_size;
-            pg.row = wrap ? 0 : pg.row + KB;
-            pg.pg += wrap;
+                for (int i = 0; i < LV::kLoads; ++i) {
+                    const int key = kb + lv.first_row(i);
+                    pg.held_descriptors((key >> a.page_shift) - pg.base, pg.page_size, lk, lv, k, v);
+                    lv.load_whole(v, i, key & mask, at + KBYTES);
+                }
+            pg.pg = (kb + KB) >> a.page_shift;
+            pg.row = (kb + KB) & mask;
             ++asked;
         };
         // before phase 2i: this wave's share of block i has landed (block i + 1 may be on its way), then everyone's

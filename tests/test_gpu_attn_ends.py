@@ -392,3 +392,15 @@ def test_heads_of_64_around_the_widths_of_tiles(c):
     x = make(c)
     o, lse = call(c, x)
     check(c, x, o, lse)
+
+
+@pytest.mark.parametrize("c", [
+    ([1500], [0], 16, 8, 128, 128, 16, 0, False),       # more pages in one chunk than a wave holds addresses of
+    ([700, 900], [650, 300], 16, 8, 64, 128, 32, 0, True),
+    ([600, 600], [500, 700], 16, 8, 128, 64, 16, 0, False),
+    ([1300], [200], 16, 8, 64, 64, 16, 700, False),
+])
+def test_small_pages_in_wide_tiles(c):
+    x = make(c)
+    o, lse = call(c, x)
+    check(c, x, o, lse)
