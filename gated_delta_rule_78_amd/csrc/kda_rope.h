@@ -31,7 +31,7 @@ enum Kind { kQueries = 0, kKeys = 1, kValues = 2 };
 // of a kind.
 struct Shape {
     int lpr;                // lanes a row
-    int v_wide;             // append: v in 16-byte accesses
+    int v_wide, v_lanes;    // append: v in 16-byte accesses, by so many lanes a row (a power of two)
     int tokens[3];
     int64_t group0[4];
     uint32_t magic[3];      // ceil(2^32 / heads), 0 for one head

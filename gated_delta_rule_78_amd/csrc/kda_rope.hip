@@ -105,6 +105,8 @@ hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
                       rows_on8(a.k, a.sk, a.B, a.Hk, a.T) && pages_on8(a.k_out, a.skc);
     Shape s = shape(a, 4, true, kNoLimit);
     s.v_wide = a.dv % 8 == 0 && rows_on8(a.v, a.sv, a.B, a.Hk, a.T) && pages_on8(a.v_out, a.svc);
+    s.v_lanes = 1;
+    while (s.v_lanes < kThreads && s.v_lanes * (s.v_wide ? 8 : 1) < a.dv) s.v_lanes *= 2;
     if (too_many(s)) return hipErrorInvalidConfiguration;
     const int lay = layout(a, wide);
     return a.in_bf16 ? launch_rows<bf16_t, bf16_t, true>(a, s, lay, st) : launch_rows<float, bf16_t, true>(a, s, lay, st);

@@ -7,70 +7,94 @@
 namespace kda {
 namespace rope {
 
-// Positions of a workgroup's tokens, and for the append their places in the cache; a wave a token.
+// Positions of a workgroup's tokens, and for the append their places in the cache; a lane of the first wave a
+// token.
 template <bool APPEND>
 __device__ __forceinline__ void fill_tokens(const RopeArgs& a, Token* tok, int64_t u0, int ntok, int kind) {
-    const int lane = threadIdx.x & 63;
-    for (int i = threadIdx.x >> 6; i < ntok; i += kWaves) {
-        const int64_t u = u0 + i, b = a.B == 1 ? 0 : u / a.T, t = u - b * a.T;
-        Token x;
-        x.on = 1;
-        x.dst = 0;
-        int64_t pos;
-        if constexpr (APPEND) {
-            int64_t s = b, first = 0, n = a.T;
-            bool live = true;
-            if (a.packed) {
-                s = find_sequence(a.cu, a.N, t);
-                live = s >= 0 && s < a.N;
-                s = live ? s : 0;
-                first = a.cu[s];
-                n = (int64_t)a.cu[s + 1] - first;
+    const int i = threadIdx.x;
+    if (i >= 64) return;
+    const int64_t u = u0 + (i < ntok ? i : 0), b = a.B == 1 ? 0 : u / a.T, t = u - b * a.T;
+    Token x;
+    x.on = 1;
+    x.dst = 0;
+    int64_t pos;
+    if constexpr (APPEND) {
+        int64_t s = b, first = 0, n = a.T;
+        bool live = true;
+        if (a.packed) {
+            // the first token's sequence is that of all tokens before its end, and so on from there
+            for (int from = 0; from < ntok;) {
+                const int f = find_sequence(a.cu, a.N, u0 + from);
+                const int64_t end = (f >= a.N ? a.T : (int64_t)a.cu[f + 1]) - u0;
+                if (i >= from) s = f;
+                from = end > from ? (end < ntok ? (int)end : ntok) : from + 1;
             }
-            pos = (int64_t)a.kv_lens[s] - n + (t - first);
-            x.on = live;
-            if (kind != kQueries) {
-                x.on = 0;
-                if (live && pos >= 0 && pos < (int64_t)a.max_pages * a.page_size) {
-                    const int32_t pg = (int32_t)pos / a.page_size, row = (int32_t)pos - pg * a.page_size;
-                    const int32_t page = a.table[s * a.table_stride + pg];
-                    const kda_page_strides& st = kind == kKeys ? a.skc : a.svc;
-                    x.on = page >= 0 && page < a.pages;
-                    x.dst = page * st.p + row * st.t;
-                }
-            }
-        } else {
-            pos = a.positions ? a.positions[u] : t;
+            live = s >= 0 && s < a.N;
+            s = live ? s : 0;
+            first = a.cu[s];
+            n = (int64_t)a.cu[s + 1] - first;
         }
-        x.pos = (int32_t)pos;
-        if (lane == 0) tok[i] = x;
+        pos = (int64_t)a.kv_lens[s] - n + (t - first);
+        x.on = live;
+        if (kind != kQueries) {
+            x.on = 0;
+            if (live && pos >= 0 && pos < (int64_t)a.max_pages * a.page_size) {
+                const int32_t pg = (int32_t)pos / a.page_size, row = (int32_t)pos - pg * a.page_size;
+                const int32_t page = a.table[s * a.table_stride + pg];
+                const kda_page_strides& st = kind == kKeys ? a.skc : a.svc;
+                x.on = page >= 0 && page < a.pages;
+                x.dst = page * st.p + row * st.t;
+            }
+        }
+    } else {
+        pos = a.positions ? a.positions[u] : t;
     }
+    x.pos = (int32_t)pos;
+    if (i < ntok) tok[i] = x;
 }
 
-// The new tokens' values into the cache: 8 channels an access where rows lie on 16 bytes.
+// The new tokens' values into the cache: 8 channels an access where rows lie on 16 bytes, v_lanes lanes a row
+// and four rows a thread under way.
 template <typename TI, bool WIDE>
-__device__ __forceinline__ void copy_values(const RopeArgs& a, const Rows3& rows, const Token* tok) {
-    constexpr int V = WIDE ? 8 : 1;
-    const int per = a.dv / V, total = rows.count * per;
-    for (int e = threadIdx.x; e < total; e += kThreads) {
-        const int r = e / per, c = (e - r * per) * V;
-        const Row x = rows.row(r);
-        if (!tok[x.t].on) continue;
-        const TI* p = static_cast<const TI*>(a.v) + (x.at(a.sv) + c);
-        bf16_t* o = static_cast<bf16_t*>(a.v_out) + (tok[x.t].dst + x.h * a.svc.h + c);
-        if constexpr (WIDE) {
-            if constexpr (sizeof(TI) == 2) {
-                *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(p);
-            } else {
-                float f[8];
-                unpack16(*reinterpret_cast<const uint4*>(p), p, f);
-                unpack16(*reinterpret_cast<const uint4*>(p + 4), p, f + 4);
-                store8(o, f);
+__device__ __forceinline__ void copy_values(const RopeArgs& a, const Rows3& rows, const Token* tok, int lanes) {
+    constexpr int V = WIDE ? 8 : 1, AT = 4;
+    const int rg = kThreads / lanes, shift = __builtin_ctz(lanes);
+    const TI* src = static_cast<const TI*>(a.v);
+    bf16_t* dst = static_cast<bf16_t*>(a.v_out);
+#pragma unroll 1
+    for (int c = (threadIdx.x & (lanes - 1)) * V; c < a.dv; c += lanes * V)
+#pragma unroll 1
+        for (int r0 = threadIdx.x >> shift; r0 < rows.count; r0 += AT * rg) {
+            uint4 u[AT], u1[AT];
+            float f[AT];
+            Row x[AT];
+#pragma unroll
+            for (int k = 0; k < AT; ++k) {
+                x[k] = rows.row(r0 + k * rg < rows.count ? r0 + k * rg : r0);
+                const TI* p = src + (x[k].at(a.sv) + c);
+                if constexpr (WIDE) {
+                    u[k] = *reinterpret_cast<const uint4*>(p);
+                    if constexpr (sizeof(TI) == 4) u1[k] = *reinterpret_cast<const uint4*>(p + 4);
+                } else {
+                    f[k] = ld_f(p);
+                }
             }
-        } else {
-            st_f(o, ld_f(p));
+#pragma unroll
+            for (int k = 0; k < AT; ++k) {
+                if (r0 + k * rg >= rows.count || !tok[x[k].t].on) continue;
+                bf16_t* o = dst + (tok[x[k].t].dst + x[k].h * a.svc.h + c);
+                if constexpr (!WIDE) {
+                    st_f(o, f[k]);
+                } else if constexpr (sizeof(TI) == 2) {
+                    *reinterpret_cast<uint4*>(o) = u[k];
+                } else {
+                    float g[8];
+                    unpack16(u[k], src, g);
+                    unpack16(u1[k], src, g + 4);
+                    store8(o, g);
+                }
+            }
         }
-    }
 }
 
 // The rows of workgroup `group` of a kind.
@@ -91,7 +115,8 @@ template <typename TI, typename TO, int LAY, bool APPEND>
 __global__ __launch_bounds__(kThreads, kLaysWide<LAY> ? 5 : 3) void rope_kernel(RopeArgs a, Shape s) {
     extern __shared__ __align__(16) float2 cs[];
     __shared__ Token tok[kMaxTokens];
-    const int64_t wg = blockIdx.x;
+    // the append's values and keys first: they wait longest, for their places
+    const int64_t wg = APPEND ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
     const int kind = wg < s.group0[1] ? kQueries : wg < s.group0[2] ? kKeys : kValues;
     int ntok;
     const Rows3 rows = rows_of(a, s, kind, wg - s.group0[kind], ntok);
@@ -100,9 +125,9 @@ __global__ __launch_bounds__(kThreads, kLaysWide<LAY> ? 5 : 3) void rope_kernel(
             fill_tokens<true>(a, tok, rows.u0, ntok, kind);
             lds_barrier();
             if (s.v_wide)
-                copy_values<TI, true>(a, rows, tok);
+                copy_values<TI, true>(a, rows, tok, s.v_lanes);
             else
-                copy_values<TI, false>(a, rows, tok);
+                copy_values<TI, false>(a, rows, tok, s.v_lanes);
             return;
         }
     }
