@@ -6,12 +6,6 @@ namespace attn {
 
 namespace {
 
-// Workgroups at most: every tile once, and the chunks beyond the first of each.
-int64_t groups_most(const AttnArgs& a, bool narrow) {
-    const int64_t tiles = tiles_most(a, narrow ? kNarrowRows : kWideRows, narrow) * a.Hk;
-    return tiles + (may_cut(a) ? target(narrow) : 0);
-}
-
 template <int DK, int DV>
 hipError_t launch(const AttnArgs& a, hipStream_t st) {
     hipError_t e = hipSuccess;
@@ -44,8 +38,6 @@ hipError_t launch_paged_attn(const AttnArgs& args, hipStream_t st) {
     using namespace attn;
     AttnArgs a = args;
     set_divisors(a);
-    for (int k = 0; k < 2; ++k)     // a launch has fewer than 2^32 threads
-        if (groups_most(a, k == 0) >= (int64_t)1 << 23) return hipErrorInvalidConfiguration;
     if (a.dk == 128) return a.dv == 128 ? launch<128, 128>(a, st) : launch<128, 64>(a, st);
     return a.dv == 128 ? launch<64, 128>(a, st) : launch<64, 64>(a, st);
 }

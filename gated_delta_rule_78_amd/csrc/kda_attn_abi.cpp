@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "kda_attn_internal.h"
+#include "kda_attn_plan.h"
 #include "kda_rows.h"
 
 namespace {
@@ -14,7 +15,8 @@ using kda::Rows;
 using kda::aligned;
 using kda::range_of;
 
-constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxRows = (int64_t)1 << 31, kMaxKeys = (int64_t)1 << 30;
+constexpr int64_t kMaxSequences = 1 << 16;     // every workgroup reads all their lengths
 
 kda_status check_desc(const kda_paged_attn_desc* d) {
     if (!d || d->N < 1 || d->Hq < 1 || d->Hk < 1 || d->Hq % d->Hk || d->T < 0 || d->window < 0 ||
@@ -24,10 +26,10 @@ kda_status check_desc(const kda_paged_attn_desc* d) {
     if (!(d->scale >= -3.4028234e38f && d->scale <= 3.4028234e38f)) return KDA_ERR_INVALID_ARG;
     if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128) || d->page_size % 16 || d->page_size > 1 << 20)
         return KDA_ERR_UNSUPPORTED;
-    if (d->Hq > 512 || d->N >= kMaxRows || d->T >= kMaxRows || d->T * d->Hq >= kMaxRows * 64 || d->window >= kMaxRows)
+    if (d->Hq > 512 || d->N > kMaxSequences || d->T >= kMaxRows || d->T * d->Hq >= kMaxRows * 64 || d->window >= kMaxRows)
         return KDA_ERR_UNSUPPORTED;
     if (d->T * (d->Hq / d->Hk) >= kMaxRows || (!d->packed && d->N * d->T * (d->Hq / d->Hk) >= kMaxRows)) return KDA_ERR_UNSUPPORTED;
-    if (d->pages >= kMaxRows || d->max_pages >= kMaxRows || d->max_pages * d->page_size >= kMaxRows ||
+    if (d->pages >= kMaxRows || d->max_pages >= kMaxRows || d->max_pages * d->page_size > kMaxKeys ||
         d->table_stride >= (int64_t)1 << 40)
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
@@ -56,7 +58,8 @@ extern "C" {
 
 size_t kda_paged_attn_workspace_bytes(const kda_paged_attn_desc* d) {
     if (check_desc(d) != KDA_OK || d->T == 0) return 0;
-    return kda::attn_ws_bytes(to_args(d));
+    const AttnArgs a = to_args(d);
+    return kda::attn::too_many(a) ? 0 : kda::attn_ws_bytes(a);
 }
 
 kda_status kda_paged_attn(const kda_paged_attn_desc* d, const void* q, const void* k_cache, const void* v_cache,
@@ -84,8 +87,10 @@ kda_status kda_paged_attn(const kda_paged_attn_desc* d, const void* q, const voi
     if (!ro.distinct()) return KDA_ERR_INVALID_ARG;
     // a page's rows are reached by 32-bit offsets
     for (const Rows* r : {&kc, &vc})
-        if (r->s[0] >= (int64_t)1 << 31 || r->s[2] >= (int64_t)1 << 30 || ((d->page_size - 1) * r->s[2] + r->d) * 2 >= (int64_t)1 << 31) return KDA_ERR_UNSUPPORTED;
+        if (r->s[0] >= (int64_t)1 << 31 || r->s[2] >= (int64_t)1 << 30 || ((d->page_size - 1) * r->s[2] + r->d) * 2 >= (int64_t)1 << 31)
+            return KDA_ERR_UNSUPPORTED;
     const AttnArgs plan = to_args(d);
+    if (kda::attn::too_many(plan)) return KDA_ERR_UNSUPPORTED;
     const size_t need = kda::attn_ws_bytes(plan);
     if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return KDA_ERR_INVALID_ARG;

@@ -178,7 +178,8 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
                   cuts = wave_scan(c.cuts) + base.cuts - c.cuts;
         if (lo == 0 && left == N) all_cuts = lane_read(cuts + c.cuts, 63);
         const int at = CUT ? cuts : items, count = CUT ? c.cuts : c.items;
-        const uint64_t mine = __ballot(at <= idx && idx < at + count);
+        // (sums that lengths which break the rules drive past 2^31 find nothing)
+        const uint64_t mine = __ballot((uint32_t)at <= (uint32_t)idx && idx - at < count);
         if (mine == 0) return false;
         const int w = __builtin_ctzll(mine);
         base = Counts{lane_read(items, w), lane_read(slots, w), lane_read(cuts, w)};

@@ -69,5 +69,16 @@ __host__ __device__ inline bool has_wide(const AttnArgs& a) { return a.T * a.G >
 // No tile has more keys than the table holds: none is cut when a chunk takes them all.
 __host__ __device__ inline bool may_cut(const AttnArgs& a) { return (int64_t)a.max_pages * a.page_size > (int64_t)(kUnit * kWholeLeast); }
 
+
+// Workgroups at most: every tile once, and the chunks beyond the first of each.
+inline int64_t groups_most(const AttnArgs& a, bool narrow) {
+    const int64_t tiles = tiles_most(a, narrow ? kNarrowRows : kWideRows, narrow) * a.Hk;
+    return tiles + (may_cut(a) ? target(narrow) : 0);
+}
+// A launch has fewer than 2^32 threads.
+inline bool too_many(const AttnArgs& a) {
+    return (has_narrow(a) && groups_most(a, true) >= (int64_t)1 << 23) || (has_wide(a) && groups_most(a, false) >= (int64_t)1 << 23);
+}
+
 }  // namespace attn
 }  // namespace kda

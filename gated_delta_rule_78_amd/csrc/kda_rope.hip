@@ -97,7 +97,7 @@ hipError_t launch_rope_fwd(const RopeArgs& a, hipStream_t st) {
     const bool wide = (!a.Hq || (rows_on8(a.q, a.sq, a.B, a.Hq, a.T) && rows_on8(a.q_out, a.sqo, a.B, a.Hq, a.T))) &&
                       (!a.Hk || (rows_on8(a.k, a.sk, a.B, a.Hk, a.T) && rows_on8(a.k_out, a.sko, a.B, a.Hk, a.T)));
     const Shape s = shape(a, 4, false, kNoLimit);
-    if (too_many(s)) return hipErrorInvalidConfiguration;
+    if (too_many(s)) return hipErrorNotSupported;
     const int lay = layout(a, wide);
     return a.in_bf16 ? launch_rows<bf16_t, bf16_t, false>(a, s, lay, st) : launch_rows<float, float, false>(a, s, lay, st);
 }
@@ -110,7 +110,7 @@ hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
     s.v_wide = a.dv % 8 == 0 && rows_on8(a.v, a.sv, a.B, a.Hk, a.T) && pages_on8(a.v_out, a.svc);
     s.v_lanes = 1;
     while (s.v_lanes < kThreads && s.v_lanes * (s.v_wide ? 8 : 1) < a.dv) s.v_lanes *= 2;
-    if (too_many(s)) return hipErrorInvalidConfiguration;
+    if (too_many(s)) return hipErrorNotSupported;
     const int lay = layout(a, wide);
     return a.in_bf16 ? launch_rows<bf16_t, bf16_t, true>(a, s, lay, st) : launch_rows<float, bf16_t, true>(a, s, lay, st);
 }
@@ -123,7 +123,7 @@ hipError_t launch_rope_bwd(const RopeArgs& a, hipStream_t st) {
                       (!a.Hk || (rows_on8(a.dko, a.sko, a.B, a.Hk, a.T) && rows_on8(a.dk, a.sdk, a.B, a.Hk, a.T) &&
                                  (!a.norm || rows_on8(a.k, a.sk, a.B, a.Hk, a.T))));
     const Shape s = shape(a, 4, false, sums ? kMaxGroups : kNoLimit);
-    if (too_many(s)) return hipErrorInvalidConfiguration;
+    if (too_many(s)) return hipErrorNotSupported;
     if (a.B * a.T > 0) {
         const int lay = layout(a, wide);
         const hipError_t e = a.in_bf16 ? launch_grads<bf16_t>(a, s, lay, sums, st) : launch_grads<float>(a, s, lay, sums, st);

@@ -67,6 +67,9 @@ RopeArgs to_args(const kda_head_rope_desc* d, const void* q, const void* k, cons
     return a;
 }
 
+// hipErrorNotSupported: more workgroups than a launch can have.
+kda_status status(hipError_t e) { return e == hipSuccess ? KDA_OK : e == hipErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_HIP; }
+
 }  // namespace
 
 extern "C" {
@@ -93,7 +96,7 @@ kda_status kda_head_rope_fwd(const kda_head_rope_desc* d, const void* q, const v
     if (!kda::rows_apart(in, out)) return KDA_ERR_INVALID_ARG;
     RopeArgs a = to_args(d, q, k, q_weight, k_weight, inv_freq, positions);
     a.q_out = q_out; a.k_out = k_out;
-    return kda::launch_rope_fwd(a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return status(kda::launch_rope_fwd(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t kda_head_rope_bwd_workspace_bytes(const kda_head_rope_desc* d) {
@@ -138,7 +141,7 @@ kda_status kda_head_rope_bwd(const kda_head_rope_desc* d, const void* q, const v
     RopeArgs a = to_args(d, q, k, q_weight, k_weight, inv_freq, positions);
     a.dqo = dq_out; a.dko = dk_out; a.dq = dq; a.dk = dk;
     a.dwq = dq_weight; a.dwk = dk_weight; a.ws = static_cast<float*>(workspace);
-    return kda::launch_rope_bwd(a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return status(kda::launch_rope_bwd(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 kda_status kda_kv_append(const kda_kv_append_desc* d, const void* q, const void* k, const void* v, const float* q_weight,
@@ -190,7 +193,7 @@ kda_status kda_kv_append(const kda_kv_append_desc* d, const void* q, const void*
     a.sq = d->q; a.sk = d->k; a.sv = d->v; a.sqo = d->q_out; a.skc = d->k_cache; a.svc = d->v_cache;
     a.cu = cu_seqlens; a.kv_lens = kv_lens; a.table = block_table; a.table_stride = d->table_stride;
     a.pages = (int32_t)d->pages; a.page_size = (int32_t)d->page_size; a.max_pages = (int32_t)d->max_pages;
-    return kda::launch_rope_append(a, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return status(kda::launch_rope_append(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

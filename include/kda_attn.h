@@ -15,6 +15,10 @@
  *  - No output may overlap an input or another output, taken as the ranges from a tensor's first
  *    element to its last (k_cache and v_cache may interleave in one buffer).
  *  - Everything between inputs and outputs is fp32 or wider; every output is rounded once.
+ *  - A launch has fewer than 2^32 threads. A call that would need more is refused with
+ *    KDA_ERR_UNSUPPORTED, and its workspace query answers 0 in the attention: from 2^24 workgroups of
+ *    a few tokens of one tensor in the norm and the append, from 2^23 tiles of a key head (256 rows of
+ *    one sequence, or 32 where it has few) in the attention.
  */
 #ifndef KDA_ATTN_H
 #define KDA_ATTN_H
@@ -52,7 +56,7 @@ typedef struct kda_page_strides {
  */
 typedef struct kda_head_rope_desc {
     int64_t B;            /* blocks of rows, >= 1                                               */
-    int64_t Hq, Hk;       /* heads of q and of k, >= 0 (0: that tensor is absent)               */
+    int64_t Hq, Hk;       /* heads of q and of k, 0 .. 4096 (0: that tensor is absent)          */
     int64_t T;            /* tokens per block, >= 0; B * T < 2^31                               */
     int64_t d;            /* channels per head, even, 2 .. KDA_ROPE_MAX_D                       */
     int64_t rot;          /* channels rotated, even, 0 .. d                                     */
@@ -111,7 +115,7 @@ kda_status kda_head_rope_bwd(const kda_head_rope_desc* desc, const void* q, cons
  */
 typedef struct kda_kv_append_desc {
     int64_t N;            /* sequences, >= 1                                                    */
-    int64_t Hq, Hk;       /* heads of q (0: no q) and of k and v (>= 1)                         */
+    int64_t Hq, Hk;       /* heads of q (0: no q) and of k and v (>= 1), up to 4096             */
     int64_t T;            /* packed: rows per head; else new tokens per sequence; >= 0, all
                              rows together < 2^31                                               */
     int64_t dk, dv;       /* channels of k (and q): even, 2 .. KDA_ROPE_MAX_D; of v: from 1     */
@@ -146,14 +150,14 @@ kda_status kda_kv_append(const kda_kv_append_desc* desc, const void* q, const vo
                          void* q_out, void* k_cache, void* v_cache, void* stream);
 
 typedef struct kda_paged_attn_desc {
-    int64_t N;            /* sequences, >= 1                                                    */
+    int64_t N;            /* sequences, 1 .. 65536                                              */
     int64_t Hq, Hk;       /* query heads, up to 512, and key heads; Hq a multiple of Hk: query head
                              h reads key head h / (Hq / Hk)                                     */
     int64_t T;            /* packed: rows per head; else new tokens per sequence                */
     int64_t dk, dv;       /* 64 or 128 each                                                     */
     int64_t pages;        /* pages of the cache, 1 .. 2^31 - 1                                  */
     int64_t page_size;    /* rows of a page, a multiple of 16, up to 2^20                       */
-    int64_t max_pages;    /* as kda_kv_append_desc                                              */
+    int64_t max_pages;    /* as kda_kv_append_desc, but max_pages * page_size <= 2^30           */
     int64_t table_stride;
     int64_t window;       /* keys that a query sees, its own among them; 0: all before it       */
     kda_row_strides q, o;
@@ -175,7 +179,8 @@ size_t kda_paged_attn_workspace_bytes(const kda_paged_attn_desc* desc);
  * A token that sees no position (one at a negative position) has o = 0 and lse = -inf. What stands in
  * rows that a token does not see, NaN among it, does not reach its output.
  *   q           : [N,Hq,T,dk] (packed [Hq,T,dk]) bf16; k_cache, v_cache as above. Bases on 16 bytes,
- *                 strides multiples of 8 elements; the rows of one page within 2^31 bytes
+ *                 strides multiples of 8 elements; from page to page less than 2^31
+ *                 elements, the rows of one page and head within 2^31 bytes
  *   o           : [N,Hq,T,dv] (packed [Hq,T,dv]) bf16 (written), base on 16 bytes, strides as q's
  *   lse         : fp32 [N,Hq,T] (packed [Hq,T]), dense (written), or NULL to skip
  *   workspace   : kda_paged_attn_workspace_bytes(desc) bytes, 16-byte aligned; calls that overlap in

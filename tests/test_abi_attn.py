@@ -281,3 +281,21 @@ def test_bindings_refuse():
     with pytest.raises(ValueError, match="lse must be"):
         kda.paged_attn(qb, kc, vc, table, lens, lse=z(2, 4, 6))
 
+
+
+# ---- calls past what a launch, an index or a scan of the lengths can hold ----
+
+def test_limits(lib):
+    big = (1 << 31) - 1
+    one = dict(B=1, Hq=1, Hk=0, T=big, d=2, rot=2)
+    assert rfwd(lib, rdesc(**one), k=None, ko=None) == UNSUPPORTED            # 2^27 workgroups
+    assert rbwd(lib, rdesc(**one), k=None, zk=None, dk=None) == UNSUPPORTED
+    assert rfwd(lib, rdesc(Hq=4097, q=RowStrides(0, 0, 0)), ko=p(9)) == UNSUPPORTED
+    assert rfwd(lib, rdesc(q=RowStrides(0, 1 << 32, 64))) == UNSUPPORTED
+    a = adesc(N=1, Hq=0, Hk=1, T=big, dk=2, dv=1, rot=2, most=1, stride=1)
+    assert app(lib, a, q=None, qo=None) == UNSUPPORTED
+    for bad in (dict(N=65537), dict(pg=1, most=(1 << 26) + 1, stride=1 << 27), dict(N=1, Hq=8, Hk=8, T=1 << 28), dict(N=2, T=1 << 30)):
+        d = tdesc(**bad)
+        assert att(lib, d, o=p(30)) == UNSUPPORTED and lib.kda_paged_attn_workspace_bytes(d) == 0, bad
+    assert lib.kda_paged_attn_workspace_bytes(tdesc(N=65536)) > 0
+    assert lib.kda_paged_attn_workspace_bytes(tdesc(most=1 << 26, stride=1 << 26)) > 0
