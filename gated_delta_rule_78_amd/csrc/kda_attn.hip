@@ -14,10 +14,11 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
         if (!(narrow ? has_narrow(a) : has_wide(a))) continue;
         e = launch_main<DK, DV>(a, narrow, groups_most(a, narrow), st);
         if (e != hipSuccess || !may_cut(a)) continue;
+        const dim3 grid((unsigned)join_groups(a, narrow));
         if (narrow)
-            hipLaunchKernelGGL((attn_join_kernel<DV, true>), dim3(kJoinGroups), dim3(kJoinThreads), 0, st, a);
+            hipLaunchKernelGGL((attn_join_kernel<DV, true>), grid, dim3(kJoinThreads), 0, st, a);
         else
-            hipLaunchKernelGGL((attn_join_kernel<DV, false>), dim3(kJoinGroups), dim3(kJoinThreads), 0, st, a);
+            hipLaunchKernelGGL((attn_join_kernel<DV, false>), grid, dim3(kJoinThreads), 0, st, a);
         e = hipGetLastError();
     }
     return e;

@@ -1017,7 +1017,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     __shared__ __align__(16) float all[NW][DV + 4];
     const int cuts = static_cast<const int*>(a.ws)[NARROW ? 0 : 1];
     if (cuts <= 0) return;
-    const int share = uniform(kJoinGroups / cuts > 0 ? kJoinGroups / cuts : 1), cut = uniform(blockIdx.x / share);   // workgroups of a cut
+    const int share = uniform((int)gridDim.x / cuts), cut = uniform(blockIdx.x / share);   // workgroups of a cut
     const int part = blockIdx.x - cut * share;
     Place p;
     int all_cuts;

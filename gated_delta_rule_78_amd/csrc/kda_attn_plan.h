@@ -19,16 +19,17 @@ namespace attn {
 
 constexpr int kThreads = 256, kWaves = 4;          // narrow tiles
 constexpr int kWideThreads = 512, kWideWaves = 8;  // wide tiles
-constexpr int kJoinThreads = 512, kJoinGroups = 1024;   // at least the (tile, head)s that can be cut
+constexpr int kJoinThreads = 256, kJoinGroups = 1024;   // workgroups at most: at least the (tile, head)s that can be cut
 constexpr int kNarrowRows = 32, kWideRows = 256;
 constexpr int kUnit = 128;             // keys: what L counts in
 // A tile of at most so many units is not cut, of `tiles` (tile, head)s in all: with few of them the keys that
 // each chunk saves outweigh the partial results and the join early, with more the chunks of cut tiles no longer
-// run at once. Whole against cut, heads of 128, us: 8 tiles of 5 units 13.4 : 12.4 (narrow), 6 units 29.9 : 24.3
-// (wide); 32 tiles, 4 units 26.7 : 28.5 (wide), 9 units 20 : 17, 10 units 43 : 32 (wide); 128 tiles, 9 units
-// 20.5 : 25.1, 15 units 28.1 : 31.9, 10 units 44 : 50 (wide), 16 units 64 : 62 (wide).
+// run at once. Whole against cut, heads of 128, us: 8 tiles of 3 units 11.1 : 13.7; 32 tiles, 5 units 16.1 : 14.8;
+// 128 tiles, 5, 9 units 14.6 : 17.7, 19.8 : 22.2; 384 tiles, 15 units 71 : 75; wide ones, 8 and 32 tiles of 3 units
+// 25.0 : 23.6, 25.4 : 28.3; 128 tiles, 5, 9 units 31 : 40, 43 : 46. Unequal lengths, 75 tiles of up to 12 units
+// beside a longer one: 40 : 31.
 constexpr float kWholeLeast = 3.f, kWholeMost = 16.f;
-__host__ __device__ constexpr float whole_units(float tiles) { return kWholeLeast + (3.f / 32.f) * tiles; }
+__host__ __device__ constexpr float whole_units(float tiles) { return kWholeLeast + (1.f / 16.f) * tiles; }
 // Chunks: as many workgroups of a kind as the GPU's 256 CUs hold.
 __host__ __device__ constexpr int64_t target(bool narrow) { return narrow ? 512 : 256; }
 
@@ -78,6 +79,14 @@ inline int64_t groups_most(const AttnArgs& a, bool narrow) {
 // A launch has fewer than 2^32 threads.
 inline bool too_many(const AttnArgs& a) {
     return (has_narrow(a) && groups_most(a, true) >= (int64_t)1 << 23) || (has_wide(a) && groups_most(a, false) >= (int64_t)1 << 23);
+}
+
+// Workgroups of the join: one a row of all (tile, head)s that can be cut, up to kJoinGroups.
+inline int64_t join_groups(const AttnArgs& a, bool narrow) {
+    const int rows = narrow ? kNarrowRows : kWideRows;
+    const int64_t tiles = tiles_most(a, rows, narrow) * a.Hk, each = a.T * a.G < rows ? a.T * a.G : rows;
+    const int64_t cuts = tiles < target(narrow) ? tiles : target(narrow);
+    return cuts * each < kJoinGroups ? cuts * each : kJoinGroups;
 }
 
 }  // namespace attn
