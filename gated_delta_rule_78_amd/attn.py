@@ -117,6 +117,13 @@ def _rope_desc(q, k, q_strides, k_strides, qo, ko, dq, dk, rot, dtype, interleav
                         eps, rope_scale)
 
 
+@functools.lru_cache(maxsize=1024)
+def _rope_bwd_desc(*shape):
+    """The backward's descriptor and the workspace that weight gradients need."""
+    desc = _rope_desc(*shape)
+    return desc, _library().kda_head_rope_bwd_workspace_bytes(desc)
+
+
 def _rope_inputs(fn, q, k, inv_freq, positions, q_weight, k_weight, norm):
     """Checks the inputs that both directions share; returns (shapes and strides of q and k, GPU, rot)."""
     x = q if q is not None else k
@@ -218,29 +225,43 @@ def head_rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, *, interleaved
     strides. Returns (dq, dk, dq_weight, dk_weight): rows in their input's type, weight gradients [d]
     fp32; None for each input that was not given."""
     qs, ks, qst, kst, index, rot = _rope_inputs("head_rope_bwd", q, k, inv_freq, positions, q_weight, k_weight, norm)
-    for name, g, t in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        if (g is None) != (t is None):
-            raise ValueError("%s goes with %s" % (name, name[1]))
-        if g is not None:
-            _check_rows(name, g, index, t.dtype, t.shape)
-    x = q if q is not None else k
+    x = q if qs is not None else k
+    dt = x.dtype
+    zqs, zks = dq_out.stride() if dq_out is not None else (), dk_out.stride() if dk_out is not None else ()
+    if not ((dq_out is None if qs is None else dq_out is not None and dq_out.shape == qs and dq_out.dtype is dt and zqs[-1] == 1
+             and dq_out.get_device() == index)
+            and (dk_out is None if ks is None else dk_out is not None and dk_out.shape == ks and dk_out.dtype is dt
+                 and zks[-1] == 1 and dk_out.get_device() == index)):
+        for name, g, t in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
+            if (g is None) != (t is None):
+                raise ValueError("%s goes with %s" % (name, name[1]))
+            if g is not None:
+                _check_rows(name, g, index, dt, t.shape)
     if workspace is not None:
         _check_workspace(workspace, x.device)
-    sums = q_weight is not None or k_weight is not None
-    lib = _lib or _library()
     with scope(index, stream):
-        dq = torch.empty_like(q) if q is not None else None
-        dk = torch.empty_like(k) if k is not None else None
-        dwq = torch.empty_like(q_weight) if q_weight is not None and q is not None else None
-        dwk = torch.empty_like(k_weight) if k_weight is not None and k is not None else None
-        st = lambda t: t.stride() if t is not None else ()
-        desc = _rope_desc(qs, ks, qst, kst, st(dq_out), st(dk_out), st(dq), st(dk), rot, x.dtype, bool(interleaved), bool(norm),
-                          float(eps), float(rope_scale))
-        workspace = _workspace(lib.kda_head_rope_bwd_workspace_bytes(desc) if sums else 0, workspace, x.device)
-        st = lib.kda_head_rope_bwd(desc, ptr(q), ptr(k), ptr(q_weight), ptr(k_weight), ptr(inv_freq), ptr(positions),
-                                   ptr(dq_out), ptr(dk_out), ptr(dq), ptr(dk), ptr(dwq), ptr(dwk), ptr(workspace),
-                                   _nbytes(workspace), raw_stream(index, stream))
-    _check("kda_head_rope_bwd", st)
+        dq = dk = dwq = dwk = None
+        dqs = dks = ()
+        if qs is not None:
+            dq = torch.empty_like(q)
+            dqs = dq.stride()
+            if q_weight is not None:
+                dwq = torch.empty_like(q_weight)
+        if ks is not None:
+            dk = torch.empty_like(k)
+            dks = dk.stride()
+            if k_weight is not None:
+                dwk = torch.empty_like(k_weight)
+        desc, need = _rope_bwd_desc(qs, ks, qst, kst, zqs, zks, dqs, dks, rot, dt, bool(interleaved), bool(norm), float(eps),
+                                    float(rope_scale))
+        if dwq is None and dwk is None:
+            need = 0
+        workspace = _workspace(need, workspace, x.device)
+        st = (_lib or _library()).kda_head_rope_bwd(
+            desc, ptr(q), ptr(k), ptr(q_weight), ptr(k_weight), ptr(inv_freq), ptr(positions), ptr(dq_out), ptr(dk_out), ptr(dq),
+            ptr(dk), ptr(dwq), ptr(dwk), ptr(workspace), _nbytes(workspace), raw_stream(index, stream))
+    if st:
+        _check("kda_head_rope_bwd", st)
     return dq, dk, dwq, dwk
 
 
