@@ -35,7 +35,9 @@ __global__ __launch_bounds__(1024) void rope_colsum_kernel(RopeArgs a, Shape s) 
 
 namespace {
 
-constexpr int64_t kMaxGroups = 1024;      // workgroups of a tensor that keep weight sums
+// Workgroups of a tensor that keep weight sums, two a CU: 8192 tokens of 32 + 8 bf16 heads of 128, both directions,
+// 77.4 us; 1024 of them 82.1, 256 90.7.
+constexpr int64_t kMaxGroups = 512;
 
 bool on8(int64_t v) { return (v & 7) == 0; }
 bool on16b(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -44,6 +46,9 @@ bool rows_on8(const void* p, const kda_row_strides& s, int64_t B, int64_t H, int
 }
 bool pages_on8(const void* p, const kda_page_strides& s) { return on16b(p) && on8(s.p) && on8(s.h) && on8(s.t); }
 
+// 16-byte accesses where rows start on them and runs of 8 channels stay whole, else element by element: 8192
+// tokens of 32 + 8 heads of 128 34 and 62 us in bf16, 68 and 86 in fp32 (appended with 8 value heads 40 and 72, 56
+// and 81).
 int layout(const RopeArgs& a, bool wide) {
     // runs of 8 pairs inside the rotated half and inside the rest; interleaved whole pairs of runs
     wide = wide && (a.interleaved ? a.d % 16 == 0 : a.rot % 16 == 0 && (a.d - a.rot) % 16 == 0);
