@@ -713,8 +713,8 @@ __device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
 // 3846 to 3989 us (from card to card; 1.07 to 1.11 PFLOP/s where a large matrix product reaches 1.38), an 8K prompt 545 to
 // 569. The matrix units are busy 55 % of the time, the vector units 55 %, at a clock that this load takes down from 2.4 to
 // 1.82 GHz. 256 rows: every key that is read from L2 serves as many rows as the registers of eight waves hold; the causal
-// edge costs half a tile. Both groups in step (each wave multiplying, then all of them exponentiating) 590 us for the
-// prompt, asking for blocks while multiplying 674.
+// edge costs half a tile. Tiles of four waves, all in step, took 4208 and 590 us; blocks asked for in the product phase
+// instead of the softmax leave the prompt at 815 TFLOP/s.
 
 template <int DK, int DV>
 __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) {
