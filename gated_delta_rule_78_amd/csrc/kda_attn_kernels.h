@@ -71,20 +71,49 @@ struct Tile {
     int64_t slot;           // partial result, when chunks > 1
 };
 
-// New tokens and keys of a sequence; false where it has no rows of this kind.
-__device__ __forceinline__ bool sequence(const AttnArgs& a, int64_t s, int64_t& first, int& n, int& kv) {
-    first = 0;
-    n = (int)a.T;
-    if (a.packed) {
-        const int64_t c0 = a.cu[s], c1 = a.cu[s + 1];
-        const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.T;
-        first = ok ? c0 : 0;
-        n = ok ? (int)(c1 - c0) : 0;
-    }
+// First token, new tokens and keys of a sequence from its lengths as they stand (c0, c1 with a.packed only); false
+// where it has no rows.
+__device__ __forceinline__ bool lengths(const AttnArgs& a, int c0, int c1, int kv_len, int64_t& first, int& n, int& kv) {
+    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.T;
+    first = a.packed && ok ? c0 : 0;
+    n = a.packed ? (ok ? c1 - c0 : 0) : (int)a.T;
     const int most = a.max_pages * a.page_size;
-    kv = a.kv_lens[s];
-    kv = kv < 0 ? 0 : kv > most ? most : kv;
+    kv = kv_len < 0 ? 0 : kv_len > most ? most : kv_len;
     return n > 0;
+}
+__device__ __forceinline__ bool sequence(const AttnArgs& a, int64_t s, int64_t& first, int& n, int& kv) {
+    int c0 = 0, c1 = 0;
+    if (a.packed) {
+        c0 = a.cu[s];
+        c1 = a.cu[s + 1];
+    }
+    return lengths(a, c0, c1, a.kv_lens[s], first, n, kv);
+}
+// f(new tokens, keys) for the sequences s, s + step, .. below `end` that have rows, four of them loaded at a time.
+template <typename F>
+__device__ __forceinline__ void for_sequences(const AttnArgs& a, int s, int step, int end, const F& f) {
+    constexpr int AT = 4;
+#pragma unroll 1
+    for (; s < end; s += AT * step) {
+        int c0[AT], c1[AT], v[AT];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) c0[i] = c1[i] = 0;
+        if (a.packed)
+#pragma unroll
+            for (int i = 0; i < AT; ++i) {
+                const int x = s + i * step < end ? s + i * step : s;
+                c0[i] = a.cu[x];
+                c1[i] = a.cu[x + 1];
+            }
+#pragma unroll
+        for (int i = 0; i < AT; ++i) v[i] = a.kv_lens[s + i * step < end ? s + i * step : s];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            int64_t first;
+            int n, kv;
+            if (lengths(a, c0[i], c1[i], v[i], first, n, kv) && s + i * step < end) f(n, kv);
+        }
+    }
 }
 
 // Row row0 + r of a tile: its token and its head in the group.
@@ -144,12 +173,15 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
     int64_t first = 0;
     int n = 0, kv = 0, k = (N + 63) / 64;
     float tiles = 0.f, units = 0.f;
-    for (int s = lane * k; s < N && s < (lane + 1) * k; ++s)
-        if (sequence(a, s, first, n, kv)) {
-            const float t = (float)(tiles_of(a, n, NARROW) * a.Hk);
-            tiles += t;
-            units = fmaf(t, (float)tile_units(a, kv, NARROW), units);
-        }
+    auto add = [&](int n_, int kv_) {
+        const float t = (float)(tiles_of(a, n_, NARROW) * a.Hk);
+        tiles += t;
+        units = fmaf(t, (float)tile_units(a, kv_, NARROW), units);
+    };
+    if (k > 1)
+        for_sequences(a, lane, 64, N, add);
+    else if (lane < N && sequence(a, lane, first, n, kv))
+        add(n, kv);
     // chunk length; the sum's rounding may not make it too small: chunks would pass the workspace's slots
     units = lane_value(wave_prefix_sum(units), 63) * 1.01f;
     const float whole = fminf(whole_units(lane_value(wave_prefix_sum(tiles), 63)), kWholeMost);
@@ -161,19 +193,22 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
         Counts c = {0, 0, 0};
         int chunks = 1;
         const int s0 = lo + lane * k, s1 = s0 + k < lo + left ? s0 + k : lo + left;
-        for (int s = s0; s < s1; ++s) {
-            if (!held) sequence(a, s, first, n, kv);
-            if (n <= 0) continue;
-            const int tiles = tiles_of(a, n, NARROW) * a.Hk;
-            const float most = (float)tile_units(a, kv, NARROW);
+        auto tally = [&](int n_, int kv_) {
+            const int own = tiles_of(a, n_, NARROW) * a.Hk;
+            const float most = (float)tile_units(a, kv_, NARROW);
             chunks = most <= whole ? 1 : (int)fmaxf(ceilf(most * inv - 0.001f), 1.f);
-            c.items += tiles * chunks;
+            c.items += own * chunks;
             if (chunks > 1) {
-                c.slots += tiles * chunks;
-                c.cuts += tiles;
+                c.slots += own * chunks;
+                c.cuts += own;
             }
+        };
+        if (k > 1) {
+            for_sequences(a, s0, 1, s1, tally);
+        } else if (s0 < s1) {
+            if (!held) sequence(a, s0, first, n, kv);
+            if (n > 0) tally(n, kv);
         }
-        if (s0 >= s1) n = 0;
         const int items = wave_scan(c.items) + base.items - c.items, slots = wave_scan(c.slots) + base.slots - c.slots,
                   cuts = wave_scan(c.cuts) + base.cuts - c.cuts;
         if (lo == 0 && left == N) all_cuts = lane_read(cuts + c.cuts, 63);

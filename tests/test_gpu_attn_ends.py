@@ -404,3 +404,16 @@ def test_small_pages_in_wide_tiles(c):
     x = make(c)
     o, lse = call(c, x)
     check(c, x, o, lse)
+
+
+@pytest.mark.parametrize("n", [65, 256, 257, 4097, 4500])
+def test_numbers_of_sequences_around_the_scan(n):
+    """Rounds of 64 sequences, four lengths a lane at a time: every row against the same call in pieces, and cut
+    sequences among them."""
+    new = [(s * 5) % 4 if s % 7 else 1 for s in range(n)]
+    past = [(s * 13) % 40 for s in range(n)]
+    past[n // 3], past[n - 1], new[n - 1] = 3000, 5000, 2
+    c = (new, past, 2, 1, 64, 64, 16, 0, True)
+    x = make(c)
+    o, lse = call(c, x)
+    check(c, x, o, lse)
