@@ -745,7 +745,7 @@ __device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
 // asked for is awaited at the barrier before phase 2j, three or four phases later.
 //
 // The products bound it, 4 G dk + 4 G dv flops a token and key: 4096 tokens of 32 + 8 heads of 128 over 65536 keys take
-// 3846 to 3989 us (from card to card; 1.07 to 1.11 PFLOP/s where a large matrix product reaches 1.38), an 8K prompt 545 to
+// 3705 to 3989 us (from card to card; 1.07 to 1.15 PFLOP/s where a large matrix product reaches 1.38), an 8K prompt 534 to
 // 569. The matrix units are busy 55 % of the time, the vector units 55 %, at a clock that this load takes down from 2.4 to
 // 1.82 GHz. 256 rows: every key that is read from L2 serves as many rows as the registers of eight waves hold; the causal
 // edge costs half a tile. Tiles of four waves, all in step, took 4208 and 590 us; blocks asked for in the product phase
