@@ -1067,7 +1067,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     __shared__ __align__(16) float all[NW][DV + 4];
     const int cuts = static_cast<const int*>(a.ws)[NARROW ? 0 : 1];
     if (cuts <= 0) return;
-    const int share = uniform((int)gridDim.x / cuts), cut = uniform(blockIdx.x / share);   // workgroups of a cut
+    // workgroups of a cut; lengths that break the rules may make more cuts than there are workgroups
+    const int each = (int)gridDim.x / cuts, share = uniform(each > 0 ? each : 1), cut = uniform(blockIdx.x / share);
     const int part = blockIdx.x - cut * share;
     Place p;
     int all_cuts;

@@ -417,3 +417,19 @@ def test_numbers_of_sequences_around_the_scan(n):
     x = make(c)
     o, lse = call(c, x)
     check(c, x, o, lse)
+
+
+def test_overlapping_sequences_stay_within_the_tensors():
+    """cu_seqlens that go back and forth: the same rows in many sequences, more tiles and cuts than the rows allow.
+    Numbers are undefined, accesses are not; what surrounds the outputs keeps its bits."""
+    for T, N, kv, Hq, Hk, d in ((4, 40, 3000, 2, 2, 64), (300, 30, 4000, 2, 1, 128), (1, 600, 900, 1, 1, 64)):
+        q = torch.randn(Hq, T, d, device=DEV).to(BF16)
+        pages = 70
+        kc, vc = (torch.randn(pages, Hk, 64, d, device=DEV).to(BF16) for _ in range(2))
+        table = torch.randint(0, pages, (N, (kv + 63) // 64), dtype=torch.int32, device=DEV)
+        cu = torch.tensor([0 if s % 2 == 0 else T for s in range(N + 1)], dtype=torch.int32, device=DEV)
+        lens = torch.full((N,), kv, dtype=torch.int32, device=DEV)
+        wide = torch.full((Hq, T + 2, d), 7.0, dtype=BF16, device=DEV)
+        kda.paged_attn(q, kc, vc, table, lens, cu_seqlens=cu, o=wide[:, 1:T + 1])
+        torch.cuda.synchronize()
+        assert bool((wide[:, 0] == 7).all()) and bool((wide[:, T + 1] == 7).all())
