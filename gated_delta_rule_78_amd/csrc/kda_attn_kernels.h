@@ -1023,12 +1023,13 @@ __device__ __forceinline__ void join_chunks(const float* base, int64_t step, int
     acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (; c0 < c1; c0 += AT) {
-        const int left = c1 - c0;
+        const int left = uniform(c1 - c0);
         float2 ml = make_float2(-INFINITY, 0.f), u[kJoinAhead], v[kJoinAhead];
         if (lane < AT && lane < left) ml = *reinterpret_cast<const float2*>(base + (c0 + lane) * step + DV);
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {      // past the last chunk weights of 0
+        for (int k = 0; k < kJoinAhead; ++k) {
             const int c = k * NG + g;
+            if (k * NG >= left) continue;
             const float2* q = reinterpret_cast<const float2*>(base + (c0 + (c < left ? c : left - 1)) * step + 4 * ch);
             u[k] = q[0];
             v[k] = q[1];
@@ -1044,6 +1045,7 @@ __device__ __forceinline__ void join_chunks(const float* base, int64_t step, int
 #pragma unroll
         for (int k = 0; k < kJoinAhead; ++k) {
             const int c = k * NG + g;
+            if (k * NG >= left) continue;
             const float wf = __shfl(f, c);
             if (c < left) {
                 acc.x = fmaf(wf, u[k].x, acc.x); acc.y = fmaf(wf, u[k].y, acc.y);
