@@ -508,9 +508,12 @@ struct Wave {
     }
 
     // A key that some rows do not see reaches them as a probability of 0 times its value: whether the block
-    // at kb has such keys and V holds an infinity or a NaN.
+    // at kb has such keys and V holds an infinity or a NaN. A block holds keys up to the tile's last row's (zeros
+    // behind them), which a wave of a wide tile may not see though all its rows are one token's; OWN: this wave's
+    // rows are all of the tile's, so that rows of one token see the block whole but for the window.
+    template <bool OWN>
     __device__ __forceinline__ bool bad_values(const AttnArgs& a, const char* vs_, int kb) const {
-        return (last != first || a.window > 0) && masks(a, kb) && any_bad(vs_);
+        return (!OWN || last != first || a.window > 0) && masks(a, kb) && any_bad(vs_);
     }
 
     // O^T += V^T P^T. Bad values are left out, and the outputs that they belong to become NaN.
@@ -519,7 +522,7 @@ struct Wave {
         const int vrow = 4 * (lane >> 5) + (l16 >> 2);
         const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
         const int piece = (2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ TileV<DV>::f(vrow);
-        const bool bad = bad_values(a, vs_, kb);
+        const bool bad = bad_values<false>(a, vs_, kb);
 #pragma unroll
         for (int s = 0; s < 2 * kMT; ++s)
 #pragma unroll
@@ -932,7 +935,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
         else
             wait_vm<0>();
         if (sees) {
-            if (masked && wave.bad_values(a, smem[w] + KBYTES, kb)) {
+            if (masked && wave.template bad_values<true>(a, smem[w] + KBYTES, kb)) {
                 wave.mark_bad(smem[w] + KBYTES, kb);
                 wave_lds_sync();
                 wave.clear_bad(smem[w] + KBYTES);
