@@ -516,7 +516,7 @@ struct Wave {
         return (!OWN || last != first || a.window > 0) && masks(a, kb) && any_bad(vs_);
     }
 
-    // O^T += V^T P^T. Bad values are left out, and the outputs that they belong to become NaN.
+    // O^T += V^T P^T. Bad values are left out of the product; the outputs that they belong to get them after it.
     __device__ __forceinline__ void values(const AttnArgs& a, const char* vs_, const Probs& P, int kb) {
         const int lane = fresh_lane(), l16 = lane & 15;
         const int vrow = 4 * (lane >> 5) + (l16 >> 2);
@@ -528,7 +528,7 @@ struct Wave {
 #pragma unroll
             for (int dt = 0; dt < kDT; ++dt) {
                 bf16x8 v = read_v(vp, piece, s, dt);
-                if (bad) v = split_bad(v, false);
+                if (bad) v = without_bad(v);
                 O[dt] = mfma32(v, P.p[s], O[dt]);
             }
         if (bad) mark_bad(vs_, kb);
@@ -597,17 +597,26 @@ struct Wave {
         return __any(hit);
     }
 
-    // V without its infinities and NaN (zeros there), or ones where it holds them and zeros elsewhere.
-    __device__ static __forceinline__ bf16x8 split_bad(bf16x8 x, bool ones) {
+    // V without its infinities and NaN, zeros there.
+    __device__ static __forceinline__ bf16x8 without_bad(bf16x8 x) {
         const uint4 u = __builtin_bit_cast(uint4, x);
         uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
-            if (ones)
-                w[k] = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
-            else
-                w[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+            w[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+        }
+        return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+
+    // Ones where V holds the infinity of this sign bit or a NaN, zeros elsewhere.
+    __device__ static __forceinline__ bf16x8 only_bad(bf16x8 x, uint32_t sign) {
+        const uint4 u = __builtin_bit_cast(uint4, x);
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = w[k] & 0xffffu, hi = w[k] >> 16, inf = 0x7f80u | sign;
+            w[k] = (lo == inf || (lo & 0x7fffu) > 0x7f80u ? 0x3f80u : 0u) | (hi == inf || (hi & 0x7fffu) > 0x7f80u ? 0x3f800000u : 0u);
         }
         return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
     }
@@ -618,36 +627,40 @@ struct Wave {
 #pragma unroll 2
         for (int i = 0; i < KB * DV * 2 / 1024; ++i) {
             bf16x8* p = reinterpret_cast<bf16x8*>(vs_ + i * 1024 + lane * 16);
-            *p = split_bad(*p, false);
+            *p = without_bad(*p);
         }
     }
 
-    // Counts, for every output, the infinities and NaN among the values that its row sees, and makes those
-    // outputs NaN.
+    // Counts, for every output, the infinities of either sign and NaN among the values that its row sees, and adds
+    // such an infinity to it: both where there is a NaN, so that it becomes one.
     __device__ __forceinline__ void mark_bad(const char* vs_, int kb) {
         const int lane = fresh_lane(), l16 = lane & 15, h = lane >> 5;
         const int vrow = 4 * h + (l16 >> 2);
         const char* vp = vs_ + vrow * TileV<DV>::kRowBytes + 8 * (l16 & 1);
         const int piece = (2 * ((lane >> 4) & 1) + ((l16 & 3) >> 1)) ^ TileV<DV>::f(vrow);
         const uint32_t span = (uint32_t)(pos - from), j0 = (uint32_t)(kb + 4 * h - from - 1);
+#pragma unroll 1
+        for (uint32_t sign = 0; sign <= 0x8000u; sign += 0x8000u) {
+            const float inf = __uint_as_float(0x7f800000u | sign << 16);
 #pragma unroll
-        for (int dt = 0; dt < kDT; ++dt) {
-            f32x16 C = {};
+            for (int dt = 0; dt < kDT; ++dt) {
+                f32x16 C = {};
 #pragma unroll
-            for (int s = 0; s < 2 * kMT; ++s) {
-                uint32_t seen[4];
+                for (int s = 0; s < 2 * kMT; ++s) {
+                    uint32_t seen[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t j = j0 + (uint32_t)(16 * s + 2 * (k & 1) + 8 * (k >> 1));
-                    asm volatile("" : "+v"(j));      // formed anew for each product: a rare path, few registers
-                    seen[k] = (j < span ? 0x3f80u : 0u) | (j + 1 < span ? 0x3f800000u : 0u);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t j = j0 + (uint32_t)(16 * s + 2 * (k & 1) + 8 * (k >> 1));
+                        asm volatile("" : "+v"(j));      // formed anew for each product: a rare path, few registers
+                        seen[k] = (j < span ? 0x3f80u : 0u) | (j + 1 < span ? 0x3f800000u : 0u);
+                    }
+                    C = mfma32(only_bad(read_v(vp, piece, s, dt), sign),
+                               __builtin_bit_cast(bf16x8, make_uint4(seen[0], seen[1], seen[2], seen[3])), C);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                C = mfma32(split_bad(read_v(vp, piece, s, dt), true),
-                           __builtin_bit_cast(bf16x8, make_uint4(seen[0], seen[1], seen[2], seen[3])), C);
-                __builtin_amdgcn_sched_barrier(0);
-            }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) O[dt][r] = C[r] > 0.f ? NAN : O[dt][r];
+                for (int r = 0; r < 16; ++r) O[dt][r] = C[r] > 0.f ? O[dt][r] + inf : O[dt][r];
+            }
         }
     }
 
