@@ -380,7 +380,7 @@ def paged_attn(q, k_cache, v_cache, block_table, kv_lens, *, cu_seqlens=None, sc
         o = softmax(scale * q k^T) v,   lse = log sum exp(scale * q k^T)     (scale: default 1 / sqrt(dk))
     Query head h reads key head h // (Hq / Hk). Returns o [N,Hq,T,dv] (packed [Hq,T,dv]) bf16, its
     dimensions in memory in q's order; with ``return_lse`` (o, lse), lse fp32 [N,Hq,T] (packed [Hq,T]).
-    A token that sees nothing has o = 0 and lse = -inf."""
+    A token that sees nothing has o = 0 and lse = -inf; one that sees scores of -inf alone NaN and -inf."""
     BF16 = torch.bfloat16
     N = _rows_dims(q, cu_seqlens)
     index, qs, qst = q.get_device(), q.shape, q.stride()

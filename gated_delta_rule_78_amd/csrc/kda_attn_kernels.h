@@ -135,6 +135,10 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, bool narrow) {
     return (rows <= (uint32_t)narrow_most(a)) == narrow ? (int)((rows + each - 1) / each) : 0;
 }
 
+// 1 / l for a row's sum l. A sum of 0 is that of a token at a negative position, which sees nothing (o = 0), or of
+// one that sees scores of -inf alone (0 / 0); else l is at least the probability of the key that set the reference.
+__device__ __forceinline__ float inv_sum(float l, int pos) { return l == 0.f ? (pos < 0 ? 0.f : NAN) : 1.f / l; }
+
 // ---- which sequence, tile and chunk a workgroup has ------------------------------------------------
 
 // Running sums over the sequences.
@@ -689,7 +693,7 @@ struct Wave {
         int tok, hd;
         row_of(a, t, row_base + n, tok, hd);
         const int64_t head = (int64_t)t.head * a.G + hd;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = inv_sum(l, pos);
         bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : t.seq * a.so.b) + (t.first + tok) * a.so.t + head * a.so.h;
 #pragma unroll
         for (int dt = 0; dt < kDT; ++dt)
@@ -1011,7 +1015,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
         int tok, hd;
         row_of(a, t, r, tok, hd);
         const int64_t head = (int64_t)t.head * a.G + hd;
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        const float inv = inv_sum(ll, t.kv - t.n + tok);
         bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : t.seq * a.so.b) + (t.first + tok) * a.so.t + head * a.so.h;
 #pragma unroll
         for (int k = 0; k < DV / 64; ++k) st_f(o + lane + 64 * k, acc[k] * inv);
@@ -1131,7 +1135,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
         if (lane < LPR) {
             const int r = tile * R + rr, tok = r / a.G, hd = r - tok * a.G;
             const int64_t head = (int64_t)head_k * a.G + hd;
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            const float inv = inv_sum(ll, p.kv - p.n + tok);
             bf16_t* o = static_cast<bf16_t*>(a.o) + (a.packed ? 0 : p.seq * a.so.b) + (p.first + tok) * a.so.t + head * a.so.h;
             store4(o + 4 * lane, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
             if (a.lse && lane == 0)

@@ -176,8 +176,9 @@ size_t kda_paged_attn_workspace_bytes(const kda_paged_attn_desc* desc);
  *
  *     o = sum_j softmax_j(scale * q . k_j) v_j,     lse = log sum_j exp(scale * q . k_j).
  *
- * A token that sees no position (one at a negative position) has o = 0 and lse = -inf. What stands in
- * rows that a token does not see, NaN among it, does not reach its output.
+ * A token that sees no position (one at a negative position) has o = 0 and lse = -inf. One that sees
+ * scores of -inf alone (keys with an infinity) has lse = -inf and o = 0 / 0, NaN. What stands in rows
+ * that a token does not see, NaN among it, does not reach its output.
  *   q           : [N,Hq,T,dk] (packed [Hq,T,dk]) bf16; k_cache, v_cache as above. Bases on 16 bytes,
  *                 strides multiples of 8 elements; from page to page less than 2^31
  *                 elements, the rows of one page and head within 2^31 bytes
