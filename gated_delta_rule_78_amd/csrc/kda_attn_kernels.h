@@ -996,8 +996,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_narrow_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
             const float* src = reinterpret_cast<const float*>(smem[i]) + r * (DV + 2);
-            const float lw = src[DV + 1], f = __builtin_amdgcn_exp2f(mw[i] - mm);
-            if (lw == 0.f) continue;               // saw nothing: its O is 0
+            // 1 where no wave has a reference: sums are 0 then, or NaN, and O is 0, or NaN from values
+            const float lw = src[DV + 1], f = mw[i] == mm ? 1.f : __builtin_amdgcn_exp2f(mw[i] - mm);
             ll = fmaf(f, lw, ll);
 #pragma unroll
             for (int k = 0; k < DV / 64; ++k) acc[k] = fmaf(f, src[lane + 64 * k], acc[k]);

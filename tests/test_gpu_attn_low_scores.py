@@ -75,3 +75,20 @@ def test_low_scores_beside_others(c):
     sees = seen_by(x, c, s, j)
     assert torch.isnan(b[sees][..., 3]).all()
     assert torch.equal(b[~sees].nan_to_num(7.0), a[~sees].nan_to_num(7.0)) and torch.equal(lb, la)
+
+
+@pytest.mark.parametrize("c", [([1], [40], 4, 2, 128, 128, 16, 0, False), ([4, 2], [300, 120], 4, 1, 64, 64, 16, 0, True),
+                               ([3], [6000], 2, 1, 64, 128, 16, 0, False), ([90], [100], 8, 2, 64, 128, 32, 0, False)], ids=ids)
+def test_a_nan_value_where_a_whole_wave_has_low_scores(c):
+    """The key of a NaN value and all those near it have scores of -inf: 0 times NaN all the same."""
+    s = int(np.argmax(c[1]))
+    n, kv = c[0][s], c[0][s] + c[1][s]
+    x = all_low(make(c), c, keep=(kv - n,))
+    clean, lse = (torch.from_numpy(tokens(t, c[8])) for t in call(c, x))
+    own = seen_by(x, c, s, 5)
+    assert torch.isfinite(clean[own]).all()
+    v = x["vc"].clone()
+    p, r = position(x, c, s, 5)
+    v[p, :, r, 3] = float("nan")
+    o, l2 = (torch.from_numpy(tokens(t, c[8])) for t in call(c, dict(x, vc=v)))
+    assert torch.isnan(o[own][..., 3]).all() and torch.equal(o[own][..., 4:], clean[own][..., 4:]) and torch.equal(l2, lse)
