@@ -364,7 +364,7 @@ def _attn_desc(q, q_strides, o_strides, kc, kcs, vc, vcs, N, max_pages, table_st
     """The call's descriptor and the workspace it needs."""
     desc = PagedAttnDesc(N, q[-3], vc[1], q[-2], q[-1], vc[3], vc[0], vc[2], max_pages, table_stride, window,
                          _strides(q_strides), _strides(o_strides), PageStrides(*kcs[:3]), PageStrides(*vcs[:3]), packed,
-                         float(q[-1] ** -0.5 if scale is None else scale))
+                         q[-1] ** -0.5 if scale is None else scale)
     return desc, _library().kda_paged_attn_workspace_bytes(desc)
 
 
@@ -414,7 +414,7 @@ def paged_attn(q, k_cache, v_cache, block_table, kv_lens, *, cu_seqlens=None, sc
         if lse is None and return_lse:
             lse = torch.empty(qs[:-1], dtype=torch.float32, device=q.device)
         desc, need = _attn_desc(qs, qst, o.stride(), kc, kcs, vc, vcs, N, block_table.shape[1], block_table.stride(0), int(window),
-                                cu_seqlens is not None, scale)
+                                cu_seqlens is not None, None if scale is None else float(scale))
         workspace = _workspace(need, workspace, q.device)
         st = (_lib or _library()).kda_paged_attn(
             desc, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ptr(cu_seqlens), kv_lens.data_ptr(),
