@@ -304,8 +304,8 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, inv_freq=None, *,
     q, k, v: [N,Hq,T,dk], [N,Hk,T,dk], [N,Hk,T,dv], T new tokens of each of N sequences, or packed
     [H,T,d] with cu_seqlens (int32 [N+1]); bf16 or fp32, any strides with contiguous channels.
     k_cache, v_cache: [pages,Hk,page_size,dk], [pages,Hk,page_size,dv] bf16, written in place, any
-    strides with contiguous channels. block_table: int32 [N,max_pages]; position j of sequence s is
-    row j % page_size of page block_table[s, j // page_size]. kv_lens: int32 [N], positions in use
+    strides with contiguous channels. block_table: int32 [N,max_pages], or one row expanded to that; position
+    j of sequence s is row j % page_size of page block_table[s, j // page_size]. kv_lens: int32 [N], positions in use
     with the new tokens, which are each sequence's last. Norm and rotation as ``head_rope_fwd``."""
     BF16 = torch.bfloat16
     N = _rows_dims(k, cu_seqlens)

@@ -22,7 +22,7 @@ kda_status check_desc(const kda_paged_attn_desc* d) {
     if (!d || d->N < 1 || d->Hq < 1 || d->Hk < 1 || d->Hq % d->Hk || d->T < 0 || d->window < 0 ||
         (d->packed != 0 && d->packed != 1))
         return KDA_ERR_INVALID_ARG;
-    if (d->pages < 1 || d->page_size < 1 || d->max_pages < 1 || d->table_stride < d->max_pages) return KDA_ERR_INVALID_ARG;
+    if (d->pages < 1 || d->page_size < 1 || d->max_pages < 1 || !kda::table_ok(d->table_stride, d->max_pages)) return KDA_ERR_INVALID_ARG;
     if (!(d->scale >= -3.4028234e38f && d->scale <= 3.4028234e38f)) return KDA_ERR_INVALID_ARG;
     if ((d->dk != 64 && d->dk != 128) || (d->dv != 64 && d->dv != 128) || d->page_size % 16 || d->page_size > 1 << 20)
         return KDA_ERR_UNSUPPORTED;

@@ -149,7 +149,7 @@ kda_status kda_kv_append(const kda_kv_append_desc* d, const void* q, const void*
                          const int32_t* block_table, void* q_out, void* k_cache, void* v_cache, void* stream) {
     if (!d || d->N < 1 || d->Hq < 0 || d->Hk < 1 || d->T < 0 || d->dv < 1 || !kda::valid_dtype(d->in_dtype) || !flag(d->packed))
         return KDA_ERR_INVALID_ARG;
-    if (d->pages < 1 || d->page_size < 1 || d->max_pages < 1 || d->table_stride < d->max_pages) return KDA_ERR_INVALID_ARG;
+    if (d->pages < 1 || d->page_size < 1 || d->max_pages < 1 || !kda::table_ok(d->table_stride, d->max_pages)) return KDA_ERR_INVALID_ARG;
     const kda_status rs = check_rotation(d->dk, d->rot, d->interleaved, d->norm, d->eps, d->rope_scale);
     if (rs != KDA_OK) return rs;
     if (d->Hq > kMaxHeads || d->Hk > kMaxHeads || d->dv > KDA_ROPE_MAX_D || d->N >= kMaxRows || d->T >= kMaxRows ||

@@ -91,6 +91,9 @@ inline bool interleaved(const Rows& a, const Rows& b) {
     return gap >= lo.d && k == 0;
 }
 
+// A block table's rows: apart, or one row for every sequence.
+inline bool table_ok(int64_t stride, int64_t max_pages) { return stride == 0 || stride >= max_pages; }
+
 template <int NI, int NO>
 bool rows_apart(const Range (&in)[NI], const Range (&out)[NO]) {
     for (int i = 0; i < NO; ++i) {

@@ -123,7 +123,8 @@ typedef struct kda_kv_append_desc {
     int64_t pages;        /* pages of the cache, 1 .. 2^31 - 1                                  */
     int64_t page_size;    /* rows of a page, 1 .. 2^20                                          */
     int64_t max_pages;    /* entries of a sequence in block_table; max_pages * page_size < 2^31 */
-    int64_t table_stride; /* from a sequence's entries to the next one's, >= max_pages          */
+    int64_t table_stride; /* from a sequence's entries to the next one's, >= max_pages, or 0:
+                             the same pages for every sequence                                  */
     kda_row_strides q, k, v, q_out;
     kda_page_strides k_cache, v_cache;
     int32_t in_dtype;     /* kda_dtype of q, k, v; q_out and the cache are bf16                 */

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from tests.test_gpu_paged_attn import call, make
+import gated_delta_rule_78_amd as kda
+from tests.test_gpu_paged_attn import DEV, call, make
 
 pytestmark = pytest.mark.gpu
 
@@ -16,3 +17,25 @@ def test_a_scale_held_in_a_tensor_is_read_at_every_call():
         o, lse = call(c, x, scale=held)
         a, al = call(c, x, scale=value)
         assert torch.equal(o, a) and torch.equal(lse, al), value
+
+
+def test_one_table_row_for_every_sequence():
+    """Sequences that share all pages: a table expanded over them."""
+    for c in (([1], [300], 4, 2, 64, 64, 16, 0, False), ([40], [100], 4, 2, 128, 128, 16, 0, False)):
+        x = make(c)
+        n = c[0][0]
+        q = torch.cat([x["q"], 0.5 * x["q"], -x["q"]]).transpose(1, 2).contiguous().transpose(1, 2)
+        row = x["table"].expand(3, -1)
+        assert row.stride(0) == 0
+        lens = x["kv_lens"] - torch.tensor([0, 7, 16], dtype=torch.int32, device=DEV)
+        a = kda.paged_attn(q, x["kc"], x["vc"], row, lens, return_lse=True)
+        b = kda.paged_attn(q, x["kc"], x["vc"], row.contiguous(), lens, return_lse=True)
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+        # the append: three sequences' tokens, one behind the other in the same pages
+        outs = []
+        for t in (row, row.contiguous()):
+            kc, vc = torch.zeros_like(x["kc"]), torch.zeros_like(x["vc"])
+            at = torch.tensor([n, 2 * n, 3 * n], dtype=torch.int32, device=DEV)
+            kda.kv_append(None, q[:, :2], q[:, 2:, :, :c[5]], kc, vc, t, at, norm=False)
+            outs.append((kc, vc))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1]) and bool(outs[0][0].any())
