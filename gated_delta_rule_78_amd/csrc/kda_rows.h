@@ -63,32 +63,34 @@ inline bool rows_ok(const Rows& r) {
     return r.empty() || (aligned(r.p, (uintptr_t)r.e) && r.extent(&m));
 }
 
-// a and b, both distinct and of one element type, share no element though their ranges may overlap:
-// with the same sizes and strides, some stride has b's rows in the gaps that a's leave (or the
-// other way round), as the two halves of one buffer.
+// a and b, both distinct, of one element type and the same sizes, share no element though their ranges may
+// overlap: some outer stride that both have sets b's rows into the gaps that a's leave (or the other way round),
+// as the two halves of one buffer. The strides below it may differ, as those of unequal widths do.
 inline bool interleaved(const Rows& a, const Rows& b) {
     for (int i = 0; i < 3; ++i)
-        if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.s[i] != b.s[i])) return false;
-    int o[3];
-    const int k = a.order(o);
+        if (a.n[i] != b.n[i]) return false;
+    int oa[3], ob[3];
+    const int k = a.order(oa);
+    b.order(ob);
     const intptr_t pa = reinterpret_cast<intptr_t>(a.p), pb = reinterpret_cast<intptr_t>(b.p);
-    const Rows &lo = pa <= pb ? a : b, &hi = pa <= pb ? b : a;
-    const int64_t bytes = pa <= pb ? pb - pa : pa - pb;
+    const bool a_first = pa <= pb;
+    const int64_t bytes = a_first ? pb - pa : pa - pb;
     if (bytes % a.e) return false;
     int64_t gap = bytes / a.e;
     for (int i = 0; i < k; ++i) {
+        const int64_t step = a.s[oa[i]];
+        if (ob[i] != oa[i] || b.s[ob[i]] != step || step < 1) return false;
+        if (i > 0 && a.s[oa[i - 1]] % step) return false;    // rows of different outer indices at different places
         // what the dimensions of smaller strides reach
-        int64_t rl = lo.d, rh = hi.d;
+        int64_t ra = a.d, rb = b.d;
         for (int j = i + 1; j < k; ++j) {
-            rl += (lo.n[o[j]] - 1) * lo.s[o[j]];
-            rh += (hi.n[o[j]] - 1) * hi.s[o[j]];
+            ra += (a.n[oa[j]] - 1) * a.s[oa[j]];
+            rb += (b.n[ob[j]] - 1) * b.s[ob[j]];
         }
-        const int64_t step = a.s[o[i]];
-        if (i > 0 && a.s[o[i - 1]] % step) return false;    // rows of different outer indices at different places
         gap %= step;
-        if (gap >= rl && gap + rh <= step) return true;
+        if (gap >= (a_first ? ra : rb) && gap + (a_first ? rb : ra) <= step) return true;
     }
-    return gap >= lo.d && k == 0;
+    return false;
 }
 
 // A block table's rows: apart, or one row for every sequence.

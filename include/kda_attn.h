@@ -13,7 +13,8 @@
  *    must not share elements.
  *  - Bases are aligned to their element unless a call says more; rows on 16 bytes take wide accesses.
  *  - No output may overlap an input or another output, taken as the ranges from a tensor's first
- *    element to its last (k_cache and v_cache may interleave in one buffer).
+ *    element to its last (k_cache and v_cache may interleave in one buffer: a page's keys and values, or a
+ *    row's, side by side, of whatever widths).
  *  - Everything between inputs and outputs is fp32 or wider; every output is rounded once.
  *  - A launch has fewer than 2^32 threads. A call that would need more is refused with
  *    KDA_ERR_UNSUPPORTED, and its workspace query answers 0 in the attention: from 2^24 workgroups of

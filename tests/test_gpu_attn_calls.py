@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import gated_delta_rule_78_amd as kda
-from tests.test_gpu_paged_attn import DEV, call, make
+from tests.test_gpu_paged_attn import BF16, DEV, call, make
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,26 @@ def test_one_table_row_for_every_sequence():
             kda.kv_append(None, q[:, :2], q[:, 2:, :, :c[5]], kc, vc, t, at, norm=False)
             outs.append((kc, vc))
         assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1]) and bool(outs[0][0].any())
+
+
+@pytest.mark.parametrize("heads_first", [True, False])
+def test_caches_of_unequal_widths_in_one_buffer(heads_first):
+    """A page's keys and, behind them, its narrower values."""
+    pages, Hk, page, dk, dv, N = 9, 2, 16, 128, 64, 3
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)
+    k, v, q = rn(N, Hk, 20, dk), rn(N, Hk, 20, dv), rn(N, 4, 20, dk)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(N, 3)
+    lens = torch.tensor([20, 41, 33], dtype=torch.int32, device=DEV)
+    plain = torch.zeros(pages, Hk, page, dk, dtype=BF16, device=DEV), torch.zeros(pages, Hk, page, dv, dtype=BF16, device=DEV)
+    one = torch.zeros(pages, Hk * page * (dk + dv), dtype=BF16, device=DEV)
+    if heads_first:         # [pages, (Hk, page, dk) then (Hk, page, dv)]
+        kc, vc = one[:, :Hk * page * dk].view(pages, Hk, page, dk), one[:, Hk * page * dk:].view(pages, Hk, page, dv)
+    else:                   # [pages, page, (Hk, dk) then (Hk, dv)]
+        rows = one.view(pages, page, Hk * (dk + dv))
+        kc, vc = (t.unflatten(2, (Hk, -1)).transpose(1, 2) for t in (rows[..., :Hk * dk], rows[..., Hk * dk:]))
+    want = kda.kv_append(q, k, v, *plain, table, lens, norm=True)
+    got = kda.kv_append(q, k, v, kc, vc, table, lens, norm=True)
+    assert torch.equal(got, want) and torch.equal(kc, plain[0]) and torch.equal(vc, plain[1])
+    assert torch.equal(kda.paged_attn(got, kc, vc, table, lens), kda.paged_attn(want, *plain, table, lens))
