@@ -87,7 +87,7 @@ kda_status kda_paged_attn(const kda_paged_attn_desc* d, const void* q, const voi
     if (!ro.distinct()) return KDA_ERR_INVALID_ARG;
     // a page's rows are reached by 32-bit offsets
     for (const Rows* r : {&kc, &vc})
-        if (r->s[0] >= (int64_t)1 << 31 || r->s[2] >= (int64_t)1 << 30 || ((d->page_size - 1) * r->s[2] + r->d) * 2 >= (int64_t)1 << 31)
+        if ((r->n[0] > 1 && r->s[0] >= (int64_t)1 << 31) || r->s[2] >= (int64_t)1 << 30 || ((d->page_size - 1) * r->s[2] + r->d) * 2 >= (int64_t)1 << 31)
             return KDA_ERR_UNSUPPORTED;
     const AttnArgs plan = to_args(d);
     if (kda::attn::too_many(plan)) return KDA_ERR_UNSUPPORTED;

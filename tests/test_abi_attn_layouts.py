@@ -3,7 +3,8 @@ and a call that passes it answers KDA_ERR_HIP for want of a device."""
 import pytest
 import torch
 
-from tests.test_abi_attn import INVALID, adesc, app, att, lib, tdesc  # noqa: F401  (lib is the fixture)
+from gated_delta_rule_78_amd.attn import PageStrides
+from tests.test_abi_attn import INVALID, UNSUPPORTED, adesc, app, att, lib, p, tdesc  # noqa: F401  (lib is the fixture)
 
 # with a device a call that passes validation would launch on addresses that are none
 no_device = pytest.mark.skipif(torch.cuda.is_available(), reason="would launch on addresses that are none")
@@ -14,3 +15,10 @@ no_device = pytest.mark.skipif(torch.cuda.is_available(), reason="would launch o
 def test_tables_of_one_row_for_every_sequence(lib, stride, ok):  # noqa: F811
     assert (att(lib, tdesc(stride=stride)) != INVALID) == ok
     assert (app(lib, adesc(stride=stride)) != INVALID) == ok
+
+
+@no_device
+@pytest.mark.parametrize("pages, ok", [(1, True), (2, False)])
+def test_strides_between_pages_that_there_are(lib, pages, ok):  # noqa: F811
+    far = PageStrides(1 << 32, 1024, 64)
+    assert (att(lib, tdesc(pg=pages, kc=far, vc=far), kc=p(10), vc=p(20)) not in (INVALID, UNSUPPORTED)) == ok

@@ -62,3 +62,14 @@ def test_caches_of_unequal_widths_in_one_buffer(heads_first):
     got = kda.kv_append(q, k, v, kc, vc, table, lens, norm=True)
     assert torch.equal(got, want) and torch.equal(kc, plain[0]) and torch.equal(vc, plain[1])
     assert torch.equal(kda.paged_attn(got, kc, vc, table, lens), kda.paged_attn(want, *plain, table, lens))
+
+
+def test_a_cache_of_one_page_may_have_any_stride_between_pages():
+    c = ([3], [9], 4, 2, 64, 64, 16, 0, False)
+    x = make(c)
+    p = int(x["table"][0, 0])
+    kc, vc = (x[t][p:p + 1].clone() for t in ("kc", "vc"))
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    o = kda.paged_attn(x["q"], kc, vc, table, x["kv_lens"])
+    far = [t.as_strided(t.shape, (1 << 33,) + t.stride()[1:]) for t in (kc, vc)]
+    assert torch.equal(kda.paged_attn(x["q"], *far, table, x["kv_lens"]), o)
