@@ -42,10 +42,12 @@ __device__ __forceinline__ float both_sum(float x) {
 // 16 bytes a lane from a raw buffer straight into LDS, to lds + 16 lane. Offsets at or past the
 // descriptor's size store zeros. The compiler does not count these loads: whoever reads the LDS waits
 // with wait_vm first.
-// The uniform offset `more` is added behind the check. The LDS address stands in m0, a wait state ahead (s_nop).
+// The uniform offset `more` is added behind the check. The LDS address stands in m0, a wait state ahead; scalar
+// operands that a vector instruction wrote (lane reads, among them those of spilled registers) need five, which the
+// compiler does not keep before an asm: s_nop 4.
 __device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t off, uint32_t lds, uint32_t more = 0) {
     const i32x4 rsrc = {uniform(r[0]), uniform(r[1]), uniform(r[2]), uniform(r[3])};
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "{m0}"(uniform((int)lds)), "v"(off), "s"(rsrc), "s"(uniform((int)more)) : "memory");
 }
 template <int N>

@@ -12,3 +12,18 @@ __global__ void lds_loads(const float* in, kda::attn::i32x4 r, unsigned off, uns
     kda::lds_barrier();
     out[threadIdx.x] = lds[threadIdx.x];
 }
+
+// Loads whose descriptors are read from lanes right before them.
+__global__ void lane_descriptors(const int* in, unsigned off, unsigned at, float* out) {
+    __shared__ __align__(1024) float lds[4096];
+    int w[4], n = (int)at;
+    for (int k = 0; k < 4; ++k) w[k] = in[threadIdx.x + 64 * k];
+    for (int i = 0; i < n; ++i) {
+        kda::attn::i32x4 r;
+        for (int k = 0; k < 4; ++k) r[k] = __builtin_amdgcn_readlane(w[k], i);
+        kda::attn::load_to_lds(r, off, kda::attn::lds_address(lds) + 1024 * (i & 3), (unsigned)__builtin_amdgcn_readlane(w[0], i + 1));
+    }
+    kda::attn::wait_vm<0>();
+    kda::lds_barrier();
+    out[threadIdx.x] = lds[threadIdx.x];
+}
