@@ -125,18 +125,6 @@ __device__ __forceinline__ void row_of(const AttnArgs& a, const Tile& t, int r, 
     hd = x - q * a.G;
 }
 
-// Keys that the longest tile of a sequence reads, in units.
-__device__ __forceinline__ int tile_units(const AttnArgs& a, int kv, bool narrow) {
-    const int k = kv < a.span[narrow] ? kv : a.span[narrow];
-    return k > 0 ? (int)(((uint32_t)k + kUnit - 1) / kUnit) : 1;
-}
-
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, bool narrow) {
-    const uint32_t rows = (uint32_t)n * (uint32_t)a.G;
-    const uint32_t each = narrow ? kNarrowRows : kWideRows;
-    return (rows <= (uint32_t)narrow_most(a)) == narrow ? (int)((rows + each - 1) / each) : 0;
-}
-
 // 1 / l for a row's sum l. A sum of 0 is that of a token at a negative position, which sees nothing (o = 0), or of
 // one that sees scores of -inf alone (0 / 0); else l is at least the probability of the key that set the reference.
 __device__ __forceinline__ float inv_sum(float l, int pos) { return l == 0.f ? (pos < 0 ? 0.f : NAN) : 1.f / l; }
@@ -188,10 +176,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
         for_sequences(a, lane, 64, N, add);
     else if (lane < N && sequence(a, lane, first, n, kv))
         add(n, kv);
-    // chunk length; the sum's rounding may not make it too small: chunks would pass the workspace's slots
-    units = lane_value(wave_prefix_sum(units), 63) * 1.01f;
-    const float whole = fminf(whole_units(lane_value(wave_prefix_sum(tiles), 63)), kWholeMost);
-    const float inv = 1.f / fminf(fmaxf(ceilf(units / (float)target(NARROW)), 1.f), 16777216.f);
+    const Cut cut = cut_of(lane_value(wave_prefix_sum(tiles), 63), lane_value(wave_prefix_sum(units), 63), NARROW);
     Counts base = {0, 0, 0};
     int lo = 0, left = N;
     for (bool held = k == 1;; held = false) {
@@ -201,8 +186,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, int idx, Place& ou
         const int s0 = lo + lane * k, s1 = s0 + k < lo + left ? s0 + k : lo + left;
         auto tally = [&](int n_, int kv_) {
             const int own = tiles_of(a, n_, NARROW) * a.Hk;
-            const float most = (float)tile_units(a, kv_, NARROW);
-            chunks = most <= whole ? 1 : (int)fmaxf(ceilf(most * inv - 0.001f), 1.f);
+            chunks = chunks_of(cut, tile_units(a, kv_, NARROW));
             c.items += own * chunks;
             if (chunks > 1) {
                 c.slots += own * chunks;

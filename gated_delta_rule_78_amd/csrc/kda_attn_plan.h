@@ -10,6 +10,7 @@
 // of loads and a scan over the lanes, as long as it would take to read a list made by another launch.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #include "kda_attn_internal.h"
@@ -54,6 +55,33 @@ inline void set_divisors(AttnArgs& a) {
 // L2; 32 sequences of 64, 96, 128 rows over 8000 keys: 56, 70, 84 us against 79, 85, 88 with wide tiles). Larger
 // heads: one tile's (64, 128 rows in narrow tiles: 115, 180 us against 111, 123).
 __host__ __device__ inline int narrow_most(const AttnArgs& a) { return a.dk + a.dv <= 128 ? 128 : kNarrowRows; }
+
+// Keys that the longest tile of a sequence of kv keys reads, in units, and the tiles of its n new tokens.
+__host__ __device__ inline int tile_units(const AttnArgs& a, int kv, bool narrow) {
+    const int k = kv < a.span[narrow] ? kv : a.span[narrow];
+    return k > 0 ? (int)(((uint32_t)k + kUnit - 1) / kUnit) : 1;
+}
+__host__ __device__ inline int tiles_of(const AttnArgs& a, int n, bool narrow) {
+    const uint32_t rows = (uint32_t)n * (uint32_t)a.G;
+    const uint32_t each = narrow ? kNarrowRows : kWideRows;
+    return (rows <= (uint32_t)narrow_most(a)) == narrow ? (int)((rows + each - 1) / each) : 0;
+}
+
+// The chunk length L from the sums over all (tile, head)s: up to `whole` units stay in one chunk, inv = 1 / L. The
+// units' sum is taken a hundredth larger, since its rounding may not make L too small: chunks would pass the
+// workspace's slots. A tile cut has k > L units in ceil(k / L - 0.001) < 2 k / L chunks, all of them together
+// below 2 target(); so there are below target() of them.
+struct Cut {
+    float whole, inv;
+};
+__host__ __device__ inline Cut cut_of(float tiles, float units, bool narrow) {
+    const float length = fminf(fmaxf(ceilf(units * 1.01f / (float)target(narrow)), 1.f), 16777216.f);
+    return {fminf(whole_units(tiles), kWholeMost), 1.f / length};
+}
+// The main launch and the join both work it out: one rounding, whatever the compiler makes of either.
+__host__ __device__ inline int chunks_of(Cut c, int units) {
+    return (float)units <= c.whole ? 1 : (int)fmaxf(ceilf(fmaf((float)units, c.inv, -0.001f)), 1.f);
+}
 
 // Workspace: two counts, how many (tile, head)s of either kind are cut (the first workgroup of a kind
 // writes its one), then the partial results, per kind slots_most() of rows x (DV + 2) floats.

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import gated_delta_rule_78_amd as kda
-from tests.test_gpu_paged_attn import BF16, DEV, call, make
+from tests.test_gpu_paged_attn import BF16, DEV, call, ids, make
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,51 @@ def test_a_cache_of_one_page_may_have_any_stride_between_pages():
     o = kda.paged_attn(x["q"], kc, vc, table, x["kv_lens"])
     far = [t.as_strided(t.shape, (1 << 33,) + t.stride()[1:]) for t in (kc, vc)]
     assert torch.equal(kda.paged_attn(x["q"], *far, table, x["kv_lens"]), o)
+
+
+@pytest.mark.parametrize("c", [
+    ([1], [9000], 8, 2, 128, 128, 64, 0, False),
+    ([1], [50000], 16, 1, 64, 64, 16, 0, False),
+    ([40, 1, 20], [3000, 500, 3], 8, 2, 64, 128, 64, 0, True),
+    ([300, 30, 5], [9000, 10, 200], 2, 1, 128, 128, 64, 0, True),
+    ([520, 3], [1500, 0], 3, 3, 64, 64, 32, 700, True),
+    ([3], [3000], 512, 1, 128, 64, 64, 0, False),
+], ids=ids)
+def test_a_workspace_of_just_its_size(c):
+    """What stands behind the bytes that the call asks for keeps its bits."""
+    from gated_delta_rule_78_amd import attn
+    x = make(c)
+    o, lse = call(c, x)
+    asked = []
+    real = attn._workspace
+    try:
+        attn._workspace = lambda need, ws, dev: asked.append(need) or real(need, ws, dev)
+        call(c, x)
+    finally:
+        attn._workspace = real
+    need = asked[0]
+    ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
+    a, al = call(c, x, workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert torch.equal(a, o) and torch.equal(al, lse)
+    assert bool((ws[need:] == 0x5A).all())
+
+
+def test_overlapping_sequences_stay_within_the_workspace():
+    """cu_seqlens that go back and forth make more tiles and cuts than the rows allow: what stands behind the
+    workspace keeps its bits."""
+    from gated_delta_rule_78_amd import attn
+    for T, N, kv, Hq, Hk, d in ((4, 40, 3000, 2, 2, 64), (300, 30, 4000, 2, 1, 128), (1, 600, 900, 1, 1, 64)):
+        q = torch.randn(Hq, T, d, device=DEV).to(BF16)
+        pages = 70
+        kc, vc = (torch.randn(pages, Hk, 64, d, device=DEV).to(BF16) for _ in range(2))
+        table = torch.randint(0, pages, (N, (kv + 63) // 64), dtype=torch.int32, device=DEV)
+        cu = torch.tensor([0 if s % 2 == 0 else T for s in range(N + 1)], dtype=torch.int32, device=DEV)
+        lens = torch.full((N,), kv, dtype=torch.int32, device=DEV)
+        o = torch.zeros(Hq, T, d, dtype=BF16, device=DEV)
+        _, need = attn._attn_desc(q.shape, q.stride(), o.stride(), kc.shape, kc.stride(), vc.shape, vc.stride(), N,
+                                  table.shape[1], table.stride(0), 0, True, None)
+        ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
+        kda.paged_attn(q, kc, vc, table, lens, cu_seqlens=cu, o=o, workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert bool((ws[need:] == 0x5A).all()), (T, N)
