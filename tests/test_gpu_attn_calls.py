@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import gated_delta_rule_78_amd as kda
-from tests.test_gpu_paged_attn import BF16, DEV, call, ids, make
+from tests.test_gpu_paged_attn import BF16, DEV, U16, call, ids, make
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,29 @@ def test_overlapping_sequences_stay_within_the_workspace():
         kda.paged_attn(q, kc, vc, table, lens, cu_seqlens=cu, o=o, workspace=ws[:need])
         torch.cuda.synchronize()
         assert bool((ws[need:] == 0x5A).all()), (T, N)
+
+
+@pytest.mark.parametrize("n", [65, 257, 4097])
+def test_a_batch_against_its_sequences_alone(n):
+    """Sequences of up to 384 keys are never cut, so that in a batch of many (rounds of 64 lengths, four a lane) they
+    get the bits that they get alone; longer ones lie within the rounding of their probabilities."""
+    new = [(s * 5) % 4 if s % 7 else 1 for s in range(n)]
+    past = [(s * 13) % 40 for s in range(n)]
+    past[n // 3], past[n - 1], new[n - 1], new[n // 2], past[n // 2] = 3000, 5000, 2, 40, 300
+    c = (new, past, 2, 1, 64, 64, 16, 0, True)
+    x = make(c)
+    o, lse = call(c, x)
+    for s in list(range(0, n, max(1, n // 60))) + [n // 3, n // 2, n - 1]:
+        a, b = x["cu_host"][s], x["cu_host"][s + 1]
+        if a == b:
+            continue
+        alone, l1 = kda.paged_attn(x["q"][:, a:b], x["kc"], x["vc"], x["table"][s:s + 1], x["kv_lens"][s:s + 1],
+                                   cu_seqlens=torch.tensor([0, b - a], dtype=torch.int32, device=DEV), return_lse=True)
+        if new[s] + past[s] <= 384:
+            assert torch.equal(alone, o[:, a:b]) and torch.equal(l1, lse[:, a:b]), s
+        else:
+            # each within 2^-8 of sum p |v| (below max |v|) by its probabilities and half a step of bf16 by its rounding
+            top = float(x["vc"][x["table"][s, :(new[s] + past[s]) // 16].long()].float().abs().max())
+            assert float((alone.float() - o[:, a:b].float()).abs().max()) <= 4 * U16 * top
+            # the same scores; sums of some 100 roundings a lane, and a few of |lse| < 16: below 300 times 2^-24 each
+            assert bool(((l1 - lse[:, a:b]).abs() <= 600 * 2.0 ** -24).all())
