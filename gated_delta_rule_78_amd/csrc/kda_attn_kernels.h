@@ -750,10 +750,12 @@ __device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
 // share of block i + 2 (first group) or i + 3 (second): a block's place is free by then, and what is
 // asked for is awaited at the barrier before phase 2j, three or four phases later.
 //
-// The products bound it, 4 G dk + 4 G dv flops a token and key: 4096 tokens of 32 + 8 heads of 128 over 65536 keys take
-// 3705 to 3989 us (from card to card; 1.07 to 1.15 PFLOP/s where a large matrix product reaches 1.38), an 8K prompt 534 to
-// 569. The matrix units are busy 55 % of the time, the vector units 55 %, at a clock that this load takes down from 2.4 to
-// 1.82 GHz. 256 rows: every key that is read from L2 serves as many rows as the registers of eight waves hold; the causal
+// Products and their operands bound it, 4 G dk + 4 G dv flops a token and key: 4096 tokens of 32 + 8 heads of 128 over
+// 65536 keys take 3720 to 3970 us (from card to card; 1.07 to 1.15 PFLOP/s where a large matrix product reaches 1.38), an 8K
+// prompt 532 to 567. A wave has 32 queries, so that each operand of K or V is read from LDS for one product, 1 KB in 32
+// cycles of a SIMD: at full rate the four SIMDs would read the 128 bytes a cycle that LDS gives. The matrix units (and
+// so LDS) are busy 54 % of the time, the vector units 54 %, little of it at once (45 and 49 % for the prompt), at
+// a clock that this load takes down from 2.4 to 1.86 GHz. 256 rows: every key that is read from L2 serves as many rows as the registers of eight waves hold; the causal
 // edge costs half a tile. Tiles of four waves, all in step, took 4208 and 590 us; blocks asked for in the product phase
 // instead of the softmax leave the prompt at 815 TFLOP/s.
 
@@ -887,8 +889,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) 
 // ---- narrow tiles: four waves with the same 32 rows, each its own blocks of 32 keys ----------------
 //
 // The bytes of the keys and values bound it, where there is enough of them: 256 sequences of one token over up to 16384
-// keys (8.62 GB) take 1490 us, 5.8 TB/s, at 8 key heads of 128; one token over 8192 14 us (34 MB; 9.6 + 4.0 for the join
-// and the launches), which is the latency from the lengths to the table to the keys to the join. Rows that G and the new
+// keys (8.62 GB) take 1490 us, 5.8 TB/s, at 8 key heads of 128; one token over 8192 15.2 us (34 MB; 11.1 of it here, 4.4
+// in the join), which is the latency from the lengths to the table to the keys to the join. Rows that G and the new
 // tokens do not fill (28 of 32 there) cost products that HBM hides: the matrix units are busy 8 % of the time. Eight waves
 // and half as many workgroups: 48 us against 37 for 34 sequences over up to 31333 keys of pages of 16, 26.6 against 28.8
 // for 16 sequences over 1900.

@@ -18,6 +18,8 @@
 namespace kda {
 namespace attn {
 
+// Times of both sides of a rule are of calls over one set of inputs, which the caches may hold: one token over 8192 keys
+// takes 13.7 to 14.1 us then, 15.2 with inputs in turn.
 constexpr int kThreads = 256, kWaves = 4;          // narrow tiles
 constexpr int kWideThreads = 512, kWideWaves = 8;  // wide tiles
 constexpr int kJoinThreads = 256, kJoinGroups = 1024;   // workgroups at most: at least the (tile, head)s that can be cut

@@ -52,8 +52,9 @@ typedef struct kda_page_strides {
  *
  * over the pairs (a, b) of the first rot channels: (i, i + rot/2), or (2i, 2i + 1) interleaved.
  * Channels from rot on are y. Frequencies that a longer context scales come in inv_freq, the factor
- * that goes with them in rope_scale. Angles are formed and reduced in fp64 from the fp32 frequency:
- * far positions lose nothing. The sum of a row's squares must be finite in fp32.
+ * that goes with them in rope_scale. Angles are formed and reduced in fp64 from the fp32 frequency
+ * and are off by at most 2^-51 of their size: 2^-31 at a million radians, 2^-20 at 2^31. The sum of a
+ * row's squares must be finite in fp32.
  */
 typedef struct kda_head_rope_desc {
     int64_t B;            /* blocks of rows, >= 1                                               */
@@ -110,9 +111,9 @@ kda_status kda_head_rope_bwd(const kda_head_rope_desc* desc, const void* q, cons
  * New tokens come packed, sequence s the rows cu_seqlens[s] .. cu_seqlens[s+1]-1 of every head, or
  * as T rows of every sequence. cu_seqlens, kv_lens and block_table are read on the device only.
  * cu_seqlens must not decrease nor leave [0, T]. Rows before cu_seqlens[0] and from cu_seqlens[N] on
- * are in no sequence: they are not read and their outputs are left as they were. Values that break
- * these rules, lengths past max_pages * page_size and page numbers outside [0, pages) give undefined
- * numbers but no access outside the tensors.
+ * are in no sequence: they may be read but are not used, and their outputs are left as they were.
+ * Values that break these rules, lengths past max_pages * page_size and page numbers outside
+ * [0, pages) give undefined numbers but no access outside the tensors.
  */
 typedef struct kda_kv_append_desc {
     int64_t N;            /* sequences, >= 1                                                    */
@@ -155,13 +156,16 @@ typedef struct kda_paged_attn_desc {
     int64_t N;            /* sequences, 1 .. 65536                                              */
     int64_t Hq, Hk;       /* query heads, up to 512, and key heads; Hq a multiple of Hk: query head
                              h reads key head h / (Hq / Hk)                                     */
-    int64_t T;            /* packed: rows per head; else new tokens per sequence                */
-    int64_t dk, dv;       /* 64 or 128 each                                                     */
+    int64_t T;            /* packed: rows per head; else new tokens per sequence; the rows of
+                             a key head's queries, all sequences together, < 2^31              */
+    int64_t dk, dv;       /* 64 or 128 each: other widths, which the append takes, are refused
+                             with KDA_ERR_UNSUPPORTED                                          */
     int64_t pages;        /* pages of the cache, 1 .. 2^31 - 1                                  */
     int64_t page_size;    /* rows of a page, a multiple of 16, up to 2^20                       */
     int64_t max_pages;    /* as kda_kv_append_desc, but max_pages * page_size <= 2^30           */
     int64_t table_stride;
-    int64_t window;       /* keys that a query sees, its own among them; 0: all before it       */
+    int64_t window;       /* keys that a query sees, its own among them, below 2^31; 0: all
+                             before it                                                         */
     kda_row_strides q, o;
     kda_page_strides k_cache, v_cache;
     int32_t packed;
