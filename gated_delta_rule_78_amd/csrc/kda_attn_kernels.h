@@ -754,10 +754,10 @@ __device__ __forceinline__ float* partials(const AttnArgs& a, bool narrow) {
 // 65536 keys take 3720 to 3970 us (from card to card; 1.07 to 1.15 PFLOP/s where a large matrix product reaches 1.38), an 8K
 // prompt 532 to 567. A wave has 32 queries, so that each operand of K or V is read from LDS for one product, 1 KB in 32
 // cycles of a SIMD: at full rate the four SIMDs would read the 128 bytes a cycle that LDS gives. The matrix units (and
-// so LDS) are busy 54 % of the time, the vector units 54 %, little of it at once (45 and 49 % for the prompt), at
-// a clock that this load takes down from 2.4 to 1.86 GHz. 256 rows: every key that is read from L2 serves as many rows as the registers of eight waves hold; the causal
-// edge costs half a tile. Tiles of four waves, all in step, took 4208 and 590 us; blocks asked for in the product phase
-// instead of the softmax leave the prompt at 815 TFLOP/s.
+// so LDS) are busy 54 % of the time, the vector units 54 %, little of it at once (45 and 49 % for the prompt), at a
+// clock that this load takes down from 2.4 to 1.86 GHz. 256 rows: every key that is read from L2 serves as many rows as
+// the registers of eight waves hold; the causal edge costs half a tile. Tiles of four waves, all in step, took 4208 and
+// 590 us; blocks asked for in the product phase instead of the softmax leave the prompt at 815 TFLOP/s.
 
 template <int DK, int DV>
 __global__ __launch_bounds__(kWideThreads, 2) void attn_wide_kernel(AttnArgs a) {
